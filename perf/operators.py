@@ -262,7 +262,7 @@ def _calls(s):
     if kind == "plan":
         return ro.rowops_expert_plan(s["indices"], s["experts"], values=s["values"])
     if kind == "gather":
-        rows = ro.rowops_expert_gather(s["x"], s["order"], s["k"], out=s["rows"])
+        rows = ro.rowops_expert_gather(s["x"], s["slot"], out=s["rows"])
         if not s["grad"]:
             return rows
         return rows, ro.rowops_expert_combine(s["y"], s["slot"], dtype=torch.float32)
