@@ -387,6 +387,142 @@ int rowops_teacher_ce(const float *student, const float *teacher, float *grad, f
                       double *mean_loss, int64_t rows, int64_t cols, float grad_scale,
                       rowops_stream stream);
 
+/*
+ * The mixture-of-experts layer behind the router: the plan that groups
+ * (token, choice) pairs by expert, the rows moved to their experts and back,
+ * and the experts' matrix products.  The pages have no counterpart; these
+ * entry points take what rowops_top_k_rows and rowops_router_masked_topk
+ * answer.  Beyond the common contract:
+ *   - Matrices marked `void` hold the element type that their rowops_dtype
+ *     argument names.  An argument that names no type, or one that the entry
+ *     point does not take, is ROWOPS_ERR_SHAPE.  Sums are fp32; each result is
+ *     rounded once, to nearest even.
+ *   - `slots` (rows of a matrix grouped by expert) and rows * k are at most
+ *     2^30, experts is 1..1024 and k at least 1, else ROWOPS_ERR_SHAPE.
+ *   - offsets, slot and indices are device data that no host check sees.  Their
+ *     use is checked on the device: a slot outside [0, slots) is skipped, and
+ *     offsets are clamped to 0..slots with no group ending before it starts.
+ *     Rows that no group or slot names are not read, and output rows that none
+ *     names are left as they were.
+ */
+typedef enum {
+    ROWOPS_F32 = 0,
+    ROWOPS_F16 = 1,
+    ROWOPS_BF16 = 2
+} rowops_dtype;
+
+/* Bytes of device workspace rowops_expert_plan needs (a function of the sizes
+ * and the current device's SM count; 0 for up to 4096 pairs and for sizes that
+ * the call refuses). */
+size_t rowops_expert_plan_workspace(int64_t rows, int64_t k, int64_t experts);
+
+/*
+ * Plan of a routed batch: the pairs p = t * k + j (token t, choice j) sorted by
+ * expert, in the order of p within an expert.
+ *   e_p = trunc(indices_p); pair p takes part when 0 <= indices_p < experts and
+ *         values is NULL or values_p != 0 (NaN takes part)
+ *   offsets_e = number of pairs of the experts before e  (offsets[experts]: all)
+ *   slot_p  = the pair's rank in the sorted order, -1 for a pair left out
+ *   order_s = the pair at rank s, -1 for s >= offsets[experts]
+ * indices, values: rows x k fp32 as rowops_top_k_rows writes them on
+ * probabilities (a masked expert has probability +0.0, so a token whose mask
+ * leaves fewer than k experts, or none, loses those pairs); offsets: experts + 1;
+ * order, slot: rows * k.  rows == 0 writes offsets (all 0).  `workspace` holds at
+ * least rowops_expert_plan_workspace(...) bytes, 16-byte aligned; concurrent
+ * calls need separate workspaces.  No output may overlap another buffer.
+ */
+int rowops_expert_plan(const float *indices, const float *values, int32_t *offsets, int32_t *order,
+                       int32_t *slot, int64_t rows, int64_t k, int64_t experts, void *workspace,
+                       size_t workspace_bytes, rowops_stream stream);
+
+/*
+ * Token rows to their experts' slots: out[slot[t][j]] = x[t], rounded to
+ * out_type.  x: rows x cols of x_type; slot: rows x k; out: slots x cols.  A slot
+ * named twice gets one of its rows.  Its gradient is rowops_expert_combine of
+ * the slots' gradients with weights NULL.  cols == 0 is a no-op.
+ */
+int rowops_expert_gather(const void *x, const int32_t *slot, void *out, int64_t rows, int64_t k,
+                         int64_t cols, int64_t slots, int x_type, int out_type,
+                         rowops_stream stream);
+
+/*
+ * Expert rows back to their tokens: out[t] = sum_j w[t][j] * y[slot[t][j]], the
+ * choices in order, skipped slots adding nothing; a token with none is all +0.0.
+ * y: slots x cols of y_type; slot, weights: rows x k (weights NULL: all 1);
+ * out: rows x cols of out_type.  cols == 0 is a no-op.
+ */
+int rowops_expert_combine(const void *y, const int32_t *slot, const float *weights, void *out,
+                          int64_t rows, int64_t k, int64_t cols, int64_t slots, int y_type,
+                          int out_type, rowops_stream stream);
+
+/*
+ * Backward of rowops_expert_combine.
+ *   dy[slot[t][j]] = w[t][j] * dout[t]
+ *   dweights[t][j] = sum_c dout[t][c] * y[slot[t][j]][c]   (0 for a skipped slot)
+ * dout: rows x cols of out_type; y, dy: slots x cols of y_type; slot, weights,
+ * dweights: rows x k.  cols == 0 writes dweights (all 0).
+ */
+int rowops_expert_combine_bwd(const void *dout, const void *y, const int32_t *slot,
+                              const float *weights, void *dy, float *dweights, int64_t rows,
+                              int64_t k, int64_t cols, int64_t slots, int out_type, int y_type,
+                              rowops_stream stream);
+
+/*
+ * Matrix product of each expert's rows with its weights.
+ *   y[s][n] = sum_k x[s][k] * w[e][n][k]     for offsets[e] <= s < offsets[e + 1]
+ *             (transposed != 0: w[e][k][n])
+ * x: slots x in_cols; w: experts x out_cols x in_cols (transposed: experts x
+ * in_cols x out_cols); y: slots x out_cols; all of `dtype`, ROWOPS_F16 or
+ * ROWOPS_BF16.  offsets: experts + 1, or NULL with experts == 1 for one dense
+ * product.  The gradient with respect to x is the same call on dy with the
+ * other `transposed`.  in_cols == 0 or out_cols == 0 is ROWOPS_ERR_SHAPE.
+ * Waits of the pipelined kernel are bounded: see rowops_pipeline_timeouts().
+ */
+int rowops_expert_matmul(const void *x, const void *w, const int32_t *offsets, void *y,
+                         int64_t slots, int64_t in_cols, int64_t out_cols, int64_t experts,
+                         int transposed, int dtype, rowops_stream stream);
+
+/*
+ * Gradient of rowops_expert_matmul with respect to the weights.
+ *   dw[e][n][k] = sum_{s of expert e} dy[s][n] * x[s][k]   (overwritten; an
+ *   expert without rows gets zeros)
+ * dy: slots x out_cols; x: slots x in_cols; both of `dtype` (ROWOPS_F16 or
+ * ROWOPS_BF16); dw: experts x out_cols x in_cols of `dw_type`, which is `dtype`
+ * or ROWOPS_F32.  For transposed weights swap dy and x (and their widths).
+ * slots == 0 writes zeros.
+ */
+int rowops_expert_matmul_wgrad(const void *dy, const void *x, const int32_t *offsets, void *dw,
+                               int64_t slots, int64_t in_cols, int64_t out_cols, int64_t experts,
+                               int dtype, int dw_type, rowops_stream stream);
+
+/*
+ * Quantises to e4m3 (four exponent bits, no infinity, largest value 448) with
+ * one scale for each block of 128 columns of a row (block_rows == 1) or of 128
+ * rows by 128 columns (block_rows == 128); the last blocks may be smaller.
+ *   a = max(max |x| over the block's finite x, 2^-100)
+ *   scale = a / 448,  q = e4m3(448 * x / a)      (ties to even)
+ * so that x is about q * scale.  An infinite or NaN x becomes e4m3 NaN.
+ * x: batches x rows x cols of x_type; q: the same shape, one byte a value;
+ * scale: batches x ceil(rows / block_rows) x ceil(cols / 128).  Blocks do not
+ * cross matrices.  Any other block_rows is ROWOPS_ERR_SHAPE; cols == 0 is a no-op.
+ */
+int rowops_quantize_blocks(const void *x, uint8_t *q, float *scale, int64_t batches, int64_t rows,
+                           int64_t cols, int64_t block_rows, int x_type, rowops_stream stream);
+
+/*
+ * rowops_expert_matmul (not transposed) on e4m3 operands with a scale for each
+ * block of 128.
+ *   y[s][n] = sum_b xs[s][b] * ws[e][n / 128][b] * sum_{k in block b} xq[s][k] * wq[e][n][k]
+ * xq: slots x in_cols with xs: slots x ceil(in_cols / 128); wq: experts x
+ * out_cols x in_cols with ws: experts x ceil(out_cols / 128) x ceil(in_cols / 128),
+ * as rowops_quantize_blocks writes them with block_rows 1 and 128; y: slots x
+ * out_cols of y_type.  offsets as for rowops_expert_matmul.
+ */
+int rowops_expert_matmul_fp8(const uint8_t *xq, const float *xs, const uint8_t *wq,
+                             const float *ws, const int32_t *offsets, void *y, int64_t slots,
+                             int64_t in_cols, int64_t out_cols, int64_t experts, int y_type,
+                             rowops_stream stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,7 +1,9 @@
 """rowops on GB300: row-wise normalise-and-reduce ops (softmax and its backward,
 scaled causal attention softmax, hard-masked softmax, logsumexp, fused softmax
-cross-entropy, LayerNorm forward/backward, top-k kept mask) as hand-written
-sm_103a CUDA kernels behind a C ABI (include/rowops.h).
+cross-entropy, LayerNorm forward/backward, top-k kept mask) and the
+mixture-of-experts layer behind the router (plan, gather, combine, the experts'
+matrix products) as hand-written sm_103a CUDA kernels behind a C ABI
+(include/rowops.h).
 
 The functions below are the ctypes binding of that ABI; ``inputs`` holds the
 seeded synthetic workloads and ``build`` compiles the library.
@@ -13,6 +15,14 @@ from .binding import (  # noqa: F401
     rowops_attn_softmax_bwd,
     rowops_attn_softmax_fwd,
     rowops_column_sums,
+    rowops_expert_combine,
+    rowops_expert_combine_bwd,
+    rowops_expert_gather,
+    rowops_expert_matmul,
+    rowops_expert_matmul_fp8,
+    rowops_expert_matmul_wgrad,
+    rowops_expert_plan,
+    rowops_expert_plan_workspace,
     rowops_kernel_launches,
     rowops_layernorm_bwd,
     rowops_layernorm_bwd_workspace,
@@ -21,6 +31,7 @@ from .binding import (  # noqa: F401
     rowops_lrp_softmax_rows,
     rowops_masked_softmax,
     rowops_masked_softmax_fmask,
+    rowops_quantize_blocks,
     rowops_rmsnorm_bwd,
     rowops_rmsnorm_fwd,
     rowops_router_masked_topk,

@@ -437,4 +437,184 @@ int rowops_teacher_ce(const float* student, const float* teacher, float* grad, f
                                                grad_scale, vec4, st(stream)));
 }
 
+// ------------------------------------------------------- the expert operators
+
+}  // extern "C"
+
+namespace {
+
+constexpr int64_t kMaxSlots = int64_t(1) << 30;
+constexpr int64_t kMaxExperts = 1024;
+
+int64_t type_bytes(int dtype) { return dtype == ROWOPS_F32 ? 4 : 2; }
+bool any_type(int dtype) { return dtype == ROWOPS_F32 || dtype == ROWOPS_F16 || dtype == ROWOPS_BF16; }
+bool half_type(int dtype) { return dtype == ROWOPS_F16 || dtype == ROWOPS_BF16; }
+
+// No output overlaps an input or another output.
+int check_overlap(std::initializer_list<Buf> in, std::initializer_list<Buf> out) {
+    for (const Buf* o = out.begin(); o != out.end(); ++o) {
+        for (const Buf& i : in)
+            if (overlap(*o, i)) return ROWOPS_ERR_ALIAS;
+        for (const Buf* p = out.begin(); p != o; ++p)
+            if (overlap(*o, *p)) return ROWOPS_ERR_ALIAS;
+    }
+    return ROWOPS_OK;
+}
+
+// Sizes of the operators that move token rows.
+int check_token_rows(int64_t rows, int64_t k, int64_t cols, int64_t slots, int a_type, int b_type) {
+    if (!any_type(a_type) || !any_type(b_type)) return ROWOPS_ERR_SHAPE;
+    if (rows < 0 || k < 1 || slots < 0 || slots > kMaxSlots || rows > kMaxSlots / k) return ROWOPS_ERR_SHAPE;
+    if (int e = check_dims(rows, cols)) return e;
+    return check_dims(slots, cols);
+}
+
+// Sizes of the experts' products.  Every matrix has at most 2^60 elements.
+int check_product(const int32_t* offsets, int64_t slots, int64_t in_cols, int64_t out_cols, int64_t experts) {
+    if (slots < 0 || slots > kMaxSlots || experts < 1 || experts > kMaxExperts) return ROWOPS_ERR_SHAPE;
+    if (in_cols < 1 || out_cols < 1 || in_cols > INT32_MAX - 256 || out_cols > INT32_MAX - 256) return ROWOPS_ERR_SHAPE;
+    if (int e = check_dims(slots, in_cols)) return e;
+    if (int e = check_dims(slots, out_cols)) return e;
+    if (int e = check_dims(experts * out_cols, in_cols)) return e;
+    if (offsets == nullptr && experts != 1) return ROWOPS_ERR_NULL;
+    return ROWOPS_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t rowops_expert_plan_workspace(int64_t rows, int64_t k, int64_t experts) {
+    if (rows <= 0 || k < 1 || rows > kMaxSlots / k || experts < 1 || experts > kMaxExperts) return 0;
+    return rowops::expert_plan_workspace(rows * k, experts);
+}
+
+int rowops_expert_plan(const float* indices, const float* values, int32_t* offsets, int32_t* order, int32_t* slot,
+                       int64_t rows, int64_t k, int64_t experts, void* workspace, size_t workspace_bytes,
+                       rowops_stream stream) {
+    if (rows < 0 || k < 1 || rows > kMaxSlots / k || experts < 1 || experts > kMaxExperts) return ROWOPS_ERR_SHAPE;
+    const int64_t n = rows * k * 4;
+    if (!offsets || (n && (!indices || !order || !slot))) return ROWOPS_ERR_NULL;
+    if (!elems_aligned({{indices, 4}, {values, 4}, {offsets, 4}, {order, 4}, {slot, 4}})) return ROWOPS_ERR_ALIGN;
+    if (int e = check_overlap({{indices, n}, {values, n}}, {{offsets, (experts + 1) * 4}, {order, n}, {slot, n}}))
+        return e;
+    const size_t need = rowops::expert_plan_workspace(rows * k, experts);
+    if (need && (!workspace || workspace_bytes < need || !aligned(workspace, 16))) return ROWOPS_ERR_WORKSPACE;
+    if (need) {
+        const Buf ws = {workspace, int64_t(need)};
+        for (const Buf& b : {Buf{indices, n}, Buf{values, n}, Buf{offsets, (experts + 1) * 4}, Buf{order, n}, Buf{slot, n}})
+            if (overlap(ws, b)) return ROWOPS_ERR_ALIAS;
+    }
+    return to_status(
+        rowops::launch_expert_plan(indices, values, offsets, order, slot, rows * k, experts, workspace, st(stream)));
+}
+
+int rowops_expert_gather(const void* x, const int32_t* slot, void* out, int64_t rows, int64_t k, int64_t cols,
+                         int64_t slots, int x_type, int out_type, rowops_stream stream) {
+    if (int e = check_token_rows(rows, k, cols, slots, x_type, out_type)) return e;
+    if (rows == 0 || cols == 0 || slots == 0) return ROWOPS_OK;
+    if (!x || !slot || !out) return ROWOPS_ERR_NULL;
+    const int64_t xb = type_bytes(x_type), ob = type_bytes(out_type);
+    if (!elems_aligned({{x, xb}, {slot, 4}, {out, ob}})) return ROWOPS_ERR_ALIGN;
+    if (int e = check_overlap({{x, rows * cols * xb}, {slot, rows * k * 4}}, {{out, slots * cols * ob}})) return e;
+    return to_status(rowops::launch_expert_gather(x, slot, out, rows, k, cols, slots, x_type, out_type, st(stream)));
+}
+
+int rowops_expert_combine(const void* y, const int32_t* slot, const float* weights, void* out, int64_t rows, int64_t k,
+                          int64_t cols, int64_t slots, int y_type, int out_type, rowops_stream stream) {
+    if (int e = check_token_rows(rows, k, cols, slots, y_type, out_type)) return e;
+    if (rows == 0 || cols == 0) return ROWOPS_OK;
+    if ((slots && !y) || !slot || !out) return ROWOPS_ERR_NULL;
+    const int64_t yb = type_bytes(y_type), ob = type_bytes(out_type), n = rows * k * 4;
+    if (!elems_aligned({{y, yb}, {slot, 4}, {weights, 4}, {out, ob}})) return ROWOPS_ERR_ALIGN;
+    if (int e = check_overlap({{y, slots * cols * yb}, {slot, n}, {weights, n}}, {{out, rows * cols * ob}})) return e;
+    return to_status(
+        rowops::launch_expert_combine(y, slot, weights, out, rows, k, cols, slots, y_type, out_type, st(stream)));
+}
+
+int rowops_expert_combine_bwd(const void* dout, const void* y, const int32_t* slot, const float* weights, void* dy,
+                              float* dweights, int64_t rows, int64_t k, int64_t cols, int64_t slots, int out_type,
+                              int y_type, rowops_stream stream) {
+    if (int e = check_token_rows(rows, k, cols, slots, out_type, y_type)) return e;
+    if (rows == 0) return ROWOPS_OK;
+    const int64_t yb = type_bytes(y_type), ob = type_bytes(out_type), n = rows * k * 4, m = slots * cols * yb;
+    if ((cols && !dout) || (m && (!y || !dy)) || !slot || !weights || !dweights) return ROWOPS_ERR_NULL;
+    if (!elems_aligned({{dout, ob}, {y, yb}, {slot, 4}, {weights, 4}, {dy, yb}, {dweights, 4}}))
+        return ROWOPS_ERR_ALIGN;
+    if (int e = check_overlap({{dout, rows * cols * ob}, {y, m}, {slot, n}, {weights, n}}, {{dy, m}, {dweights, n}}))
+        return e;
+    return to_status(rowops::launch_expert_combine_bwd(dout, y, slot, weights, dy, dweights, rows, k, cols, slots,
+                                                       out_type, y_type, st(stream)));
+}
+
+int rowops_expert_matmul(const void* x, const void* w, const int32_t* offsets, void* y, int64_t slots,
+                         int64_t in_cols, int64_t out_cols, int64_t experts, int transposed, int dtype,
+                         rowops_stream stream) {
+    if (!half_type(dtype)) return ROWOPS_ERR_SHAPE;
+    if (int e = check_product(offsets, slots, in_cols, out_cols, experts)) return e;
+    if (slots == 0) return ROWOPS_OK;
+    if (!x || !w || !y) return ROWOPS_ERR_NULL;
+    if (!elems_aligned({{x, 2}, {w, 2}, {offsets, 4}, {y, 2}})) return ROWOPS_ERR_ALIGN;
+    const int64_t wb = experts * out_cols * in_cols * 2;
+    if (int e = check_overlap({{x, slots * in_cols * 2}, {w, wb}, {offsets, (experts + 1) * 4}},
+                              {{y, slots * out_cols * 2}}))
+        return e;
+    return to_status(rowops::launch_expert_matmul(x, w, offsets, y, slots, in_cols, out_cols, experts, transposed != 0,
+                                                  dtype, st(stream)));
+}
+
+int rowops_expert_matmul_wgrad(const void* dy, const void* x, const int32_t* offsets, void* dw, int64_t slots,
+                               int64_t in_cols, int64_t out_cols, int64_t experts, int dtype, int dw_type,
+                               rowops_stream stream) {
+    if (!half_type(dtype) || (dw_type != dtype && dw_type != ROWOPS_F32)) return ROWOPS_ERR_SHAPE;
+    if (int e = check_product(offsets, slots, in_cols, out_cols, experts)) return e;
+    if ((slots && (!dy || !x)) || !dw) return ROWOPS_ERR_NULL;
+    if (!elems_aligned({{dy, 2}, {x, 2}, {offsets, 4}, {dw, type_bytes(dw_type)}})) return ROWOPS_ERR_ALIGN;
+    const int64_t wb = experts * out_cols * in_cols * type_bytes(dw_type);
+    if (int e = check_overlap({{dy, slots * out_cols * 2}, {x, slots * in_cols * 2}, {offsets, (experts + 1) * 4}},
+                              {{dw, wb}}))
+        return e;
+    return to_status(rowops::launch_expert_matmul_wgrad(dy, x, offsets, dw, slots, in_cols, out_cols, experts, dtype,
+                                                        dw_type, st(stream)));
+}
+
+int rowops_quantize_blocks(const void* x, uint8_t* q, float* scale, int64_t batches, int64_t rows, int64_t cols,
+                           int64_t block_rows, int x_type, rowops_stream stream) {
+    if (!any_type(x_type) || (block_rows != 1 && block_rows != 128) || batches < 0 || rows < 0) return ROWOPS_ERR_SHAPE;
+    if (rows > kMaxSlots || batches > kMaxSlots || rows * batches > kMaxSlots) return ROWOPS_ERR_SHAPE;
+    const int64_t n = rows * batches;
+    if (int e = check_dims(n, cols)) return e;
+    if (cols > INT32_MAX - 256) return ROWOPS_ERR_SHAPE;
+    if (n == 0 || cols == 0) return ROWOPS_OK;
+    const int64_t scales = batches * ((rows + block_rows - 1) / block_rows) * ((cols + 127) / 128);
+    if (scales > INT32_MAX) return ROWOPS_ERR_SHAPE;  // one block of threads, or a part of one, for each
+    if (!x || !q || !scale) return ROWOPS_ERR_NULL;
+    const int64_t xb = type_bytes(x_type);
+    if (!elems_aligned({{x, xb}, {scale, 4}})) return ROWOPS_ERR_ALIGN;
+    if (int e = check_overlap({{x, n * cols * xb}}, {{q, n * cols}, {scale, scales * 4}})) return e;
+    return to_status(
+        rowops::launch_quantize_blocks(x, q, scale, batches, rows, cols, block_rows, x_type, st(stream)));
+}
+
+int rowops_expert_matmul_fp8(const uint8_t* xq, const float* xs, const uint8_t* wq, const float* ws,
+                             const int32_t* offsets, void* y, int64_t slots, int64_t in_cols, int64_t out_cols,
+                             int64_t experts, int y_type, rowops_stream stream) {
+    if (!any_type(y_type)) return ROWOPS_ERR_SHAPE;
+    if (int e = check_product(offsets, slots, in_cols, out_cols, experts)) return e;
+    if (slots == 0) return ROWOPS_OK;
+    if (!xq || !xs || !wq || !ws || !y) return ROWOPS_ERR_NULL;
+    const int64_t yb = type_bytes(y_type);
+    if (!elems_aligned({{xs, 4}, {ws, 4}, {offsets, 4}, {y, yb}})) return ROWOPS_ERR_ALIGN;
+    const int64_t kb = (in_cols + 127) / 128, nb = (out_cols + 127) / 128;
+    if (int e = check_overlap({{xq, slots * in_cols},
+                               {xs, slots * kb * 4},
+                               {wq, experts * out_cols * in_cols},
+                               {ws, experts * nb * kb * 4},
+                               {offsets, (experts + 1) * 4}},
+                              {{y, slots * out_cols * yb}}))
+        return e;
+    return to_status(rowops::launch_expert_matmul_fp8(xq, xs, wq, ws, offsets, y, slots, in_cols, out_cols, experts,
+                                                      y_type, st(stream)));
+}
+
 }  // extern "C"

@@ -1,0 +1,227 @@
+// expert_rows.cu - token rows to their experts' slots and back.
+//
+//   gather       out[slot[t][j]] = x[t]
+//   combine      out[t] = sum_j w[t][j] y[slot[t][j]]
+//   combine_bwd  dy[slot[t][j]] = w[t][j] dout[t],  dw[t][j] = sum_c dout[t][c] y[slot[t][j]][c]
+//
+// All three are bound by HBM.  They go token by token, so a token's row is read
+// (or written) once however many experts it has, and an expert row is touched
+// once; the plan's order decides only where the rows lie.  A slot outside the
+// expert matrix is skipped.  Sums are fp32 in the order of the choices (and of
+// the columns, for dw), so results repeat bit for bit.
+#include "types.cuh"
+
+namespace rowops {
+namespace {
+
+constexpr int kRowThreads = 256;
+constexpr int kRowWarps = kRowThreads / 32;
+
+// One warp per (token, tile of 32 * V * U columns).
+template <typename TI, typename TO, int V, int U>
+__global__ void __launch_bounds__(kRowThreads)
+    gather_rows(const TI* __restrict__ x, const int32_t* __restrict__ slot, TO* __restrict__ out, int64_t items,
+                int tiles, int k, int64_t cols, int64_t slots) {
+    const int64_t item = int64_t(blockIdx.x) * kRowWarps + (threadIdx.x >> 5);
+    if (item >= items) return;
+    const int64_t t = item / tiles, c0 = (item % tiles) * (32 * V * U) + (threadIdx.x & 31) * V;
+    Chunk<TI, V> in[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int64_t c = c0 + u * (32 * V);
+        if (c < cols) in[u].load(x + t * cols + c);
+    }
+    Chunk<TO, V> o[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int i = 0; i < V; ++i) o[u].set(i, in[u].get(i));
+    for (int j = 0; j < k; ++j) {
+        const int64_t s = __ldg(slot + t * k + j);
+        if (s < 0 || s >= slots) continue;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t c = c0 + u * (32 * V);
+            if (c < cols) o[u].store(out + s * cols + c);
+        }
+    }
+}
+
+template <typename TI, typename TO, int V, int U>
+__global__ void __launch_bounds__(kRowThreads)
+    combine_rows(const TI* __restrict__ y, const int32_t* __restrict__ slot, const float* __restrict__ weights,
+                 TO* __restrict__ out, int64_t items, int tiles, int k, int64_t cols, int64_t slots) {
+    const int64_t item = int64_t(blockIdx.x) * kRowWarps + (threadIdx.x >> 5);
+    if (item >= items) return;
+    const int64_t t = item / tiles, c0 = (item % tiles) * (32 * V * U) + (threadIdx.x & 31) * V;
+    float acc[U][V];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[u][i] = 0.f;
+#pragma unroll 4
+    for (int j = 0; j < k; ++j) {
+        const int64_t s = __ldg(slot + t * k + j);
+        if (s < 0 || s >= slots) continue;
+        const float w = weights == nullptr ? 1.0f : __ldg(weights + t * k + j);
+        Chunk<TI, V> in[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t c = c0 + u * (32 * V);
+            if (c < cols) in[u].load(y + s * cols + c);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int i = 0; i < V; ++i) acc[u][i] = fmaf(w, in[u].get(i), acc[u][i]);
+    }
+    Chunk<TO, V> o[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int64_t c = c0 + u * (32 * V);
+#pragma unroll
+        for (int i = 0; i < V; ++i) o[u].set(i, acc[u][i]);
+        if (c < cols) o[u].store(out + t * cols + c);
+    }
+}
+
+// WARPS warps per pair (t, j); pairs of one token are neighbours, so its dout
+// row comes from the L1 after the first.
+template <typename TO, typename TY, int V, int WARPS>
+__global__ void __launch_bounds__(kRowThreads)
+    combine_rows_bwd(const TO* __restrict__ dout, const TY* __restrict__ y, const int32_t* __restrict__ slot,
+                     const float* __restrict__ weights, TY* __restrict__ dy, float* __restrict__ dweights,
+                     int64_t pairs, int k, int64_t cols, int64_t slots) {
+    __shared__ float part[kRowWarps];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t p = int64_t(blockIdx.x) * (kRowWarps / WARPS) + warp / WARPS;
+    const int64_t s = p < pairs ? int64_t(__ldg(slot + p)) : -1;
+    float dot = 0.f;
+    if (s >= 0 && s < slots) {
+        const float w = __ldg(weights + p);
+        const TO* d = dout + (p / k) * cols;
+#pragma unroll 4
+        for (int64_t c = ((warp % WARPS) * 32 + lane) * V; c < cols; c += WARPS * 32 * V) {
+            Chunk<TO, V> a;
+            Chunk<TY, V> b, o;
+            a.load(d + c);
+            b.load(y + s * cols + c);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                dot = fmaf(a.get(i), b.get(i), dot);
+                o.set(i, w * a.get(i));
+            }
+            o.store(dy + s * cols + c);
+        }
+    }
+    dot = group_sum<32>(dot);
+    if constexpr (WARPS > 1) {
+        if (lane == 0) part[warp] = dot;
+        __syncthreads();
+        if (threadIdx.x == 0 && p < pairs) {
+            float sum = part[0];
+            for (int i = 1; i < WARPS; ++i) sum += part[i];
+            dweights[p] = sum;
+        }
+    } else if (lane == 0 && p < pairs) {
+        dweights[p] = dot;
+    }
+}
+
+bool chunked(const void* p, int64_t cols, int v, size_t size) {
+    return cols % v == 0 && reinterpret_cast<uintptr_t>(p) % (v * size) == 0;
+}
+
+struct Items {
+    int64_t items;
+    int tiles;
+    unsigned grid;
+};
+inline Items row_items(int64_t rows, int64_t cols, int tile) {
+    Items r;
+    r.tiles = int((cols + tile - 1) / tile);
+    r.items = rows * r.tiles;
+    r.grid = unsigned((r.items + kRowWarps - 1) / kRowWarps);
+    return r;
+}
+
+}  // namespace
+
+cudaError_t launch_expert_gather(const void* x, const int32_t* slot, void* out, int64_t rows, int64_t k,
+                                 int64_t cols, int64_t slots, int x_type, int out_type, cudaStream_t stream) {
+    with_type(x_type, [&](auto ti) {
+        with_type(out_type, [&](auto to) {
+            using TI = decltype(ti);
+            using TO = decltype(to);
+            constexpr int V = chunk_of<TI, TO>();
+            const TI* xp = static_cast<const TI*>(x);
+            TO* op = static_cast<TO*>(out);
+            if (chunked(x, cols, V, sizeof(TI)) && chunked(out, cols, V, sizeof(TO))) {
+                const Items n = row_items(rows, cols, 32 * V * 2);
+                gather_rows<TI, TO, V, 2><<<n.grid, kRowThreads, 0, stream>>>(xp, slot, op, n.items, n.tiles, int(k),
+                                                                              cols, slots);
+            } else {
+                const Items n = row_items(rows, cols, 32 * 4);
+                gather_rows<TI, TO, 1, 4><<<n.grid, kRowThreads, 0, stream>>>(xp, slot, op, n.items, n.tiles, int(k),
+                                                                              cols, slots);
+            }
+        });
+    });
+    note_launches(1);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_expert_combine(const void* y, const int32_t* slot, const float* weights, void* out, int64_t rows,
+                                  int64_t k, int64_t cols, int64_t slots, int y_type, int out_type,
+                                  cudaStream_t stream) {
+    with_type(y_type, [&](auto ti) {
+        with_type(out_type, [&](auto to) {
+            using TI = decltype(ti);
+            using TO = decltype(to);
+            constexpr int V = chunk_of<TI, TO>();
+            const TI* yp = static_cast<const TI*>(y);
+            TO* op = static_cast<TO*>(out);
+            if (chunked(y, cols, V, sizeof(TI)) && chunked(out, cols, V, sizeof(TO))) {
+                const Items n = row_items(rows, cols, 32 * V * 2);
+                combine_rows<TI, TO, V, 2><<<n.grid, kRowThreads, 0, stream>>>(yp, slot, weights, op, n.items,
+                                                                               n.tiles, int(k), cols, slots);
+            } else {
+                const Items n = row_items(rows, cols, 32 * 4);
+                combine_rows<TI, TO, 1, 4><<<n.grid, kRowThreads, 0, stream>>>(yp, slot, weights, op, n.items,
+                                                                               n.tiles, int(k), cols, slots);
+            }
+        });
+    });
+    note_launches(1);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_expert_combine_bwd(const void* dout, const void* y, const int32_t* slot, const float* weights,
+                                      void* dy, float* dweights, int64_t rows, int64_t k, int64_t cols,
+                                      int64_t slots, int out_type, int y_type, cudaStream_t stream) {
+    const int64_t pairs = rows * k;
+    const bool wide = pairs < 16 * int64_t(sm_count());  // few pairs: a block each
+    with_type(out_type, [&](auto to) {
+        with_type(y_type, [&](auto ty) {
+            using TO = decltype(to);
+            using TY = decltype(ty);
+            constexpr int V = chunk_of<TO, TY>();
+            auto go = [&](auto kernel, int warps) {
+                const int64_t per = kRowWarps / warps;
+                kernel<<<unsigned((pairs + per - 1) / per), kRowThreads, 0, stream>>>(
+                    static_cast<const TO*>(dout), static_cast<const TY*>(y), slot, weights, static_cast<TY*>(dy),
+                    dweights, pairs, int(k), cols, slots);
+            };
+            const bool vec = chunked(dout, cols, V, sizeof(TO)) && chunked(y, cols, V, sizeof(TY)) &&
+                             chunked(dy, cols, V, sizeof(TY));
+            if (vec && wide) go(combine_rows_bwd<TO, TY, V, kRowWarps>, kRowWarps);
+            else if (vec) go(combine_rows_bwd<TO, TY, V, 1>, 1);
+            else if (wide) go(combine_rows_bwd<TO, TY, 1, kRowWarps>, kRowWarps);
+            else go(combine_rows_bwd<TO, TY, 1, 1>, 1);
+        });
+    });
+    note_launches(1);
+    return cudaGetLastError();
+}
+
+}  // namespace rowops

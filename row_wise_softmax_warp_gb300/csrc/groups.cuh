@@ -1,0 +1,60 @@
+// groups.cuh - rows grouped by expert: expert e owns rows offsets[e] ..
+// offsets[e + 1] - 1 of a matrix of `slots` rows.
+//
+// The offsets are device data that no host check has seen, so every read of
+// them is clamped to 0 .. slots with ends not before starts: bad offsets give
+// wrong rows, never an access out of bounds.
+#pragma once
+
+#include "common.cuh"
+
+namespace rowops {
+
+constexpr int kMaxExperts = 1024;
+
+struct RowRange {
+    int first, count;
+};
+
+__device__ __forceinline__ RowRange group_rows(const int32_t* offsets, int e, int slots) {
+    if (offsets == nullptr) return {0, slots};  // one dense group
+    const int lo = min(max(__ldg(offsets + e), 0), slots);
+    const int hi = min(max(__ldg(offsets + e + 1), lo), slots);
+    return {lo, hi - lo};
+}
+
+// Expert, first row and row count of row tile `tile` (tiles of TILE rows,
+// counted over the experts in order); false past the last tile.  Called by a
+// whole warp, which scans the experts 32 at a time.
+template <int TILE>
+__device__ __forceinline__ bool find_row_tile(const int32_t* offsets, int experts, int slots, int64_t tile,
+                                              int& expert, int& first, int& count) {
+    const int lane = threadIdx.x & 31;
+    int64_t before = 0;
+    for (int base = 0; base < experts; base += 32) {
+        const int e = base + lane;
+        RowRange r{0, 0};
+        if (e < experts) r = group_rows(offsets, e, slots);
+        const int n = r.count / TILE + (r.count % TILE != 0);
+        int upto = n;  // inclusive scan over the warp
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(kFullMask, upto, o);
+            if (lane >= o) upto += v;
+        }
+        const unsigned past = __ballot_sync(kFullMask, before + upto > tile);
+        if (past) {
+            const int src = __ffs(past) - 1;
+            const int in_group = int(tile - before) - (__shfl_sync(kFullMask, upto, src) - __shfl_sync(kFullMask, n, src));
+            const int at = in_group * TILE;
+            expert = base + src;
+            first = __shfl_sync(kFullMask, r.first, src) + at;
+            count = min(TILE, __shfl_sync(kFullMask, r.count, src) - at);
+            return true;
+        }
+        before += __shfl_sync(kFullMask, upto, 31);
+    }
+    return false;
+}
+
+}  // namespace rowops

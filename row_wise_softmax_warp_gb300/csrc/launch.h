@@ -203,4 +203,38 @@ cudaError_t launch_teacher_ce(const float* s, const float* t, float* grad, float
 cudaError_t launch_topk_kept(const float* x, float* kept, int64_t rows, int64_t cols, int64_t k,
                              bool vec4, cudaStream_t stream);
 
+// The expert operators (types are rowops_dtype values).
+size_t expert_plan_workspace(int64_t pairs, int64_t experts);
+cudaError_t launch_expert_plan(const float* indices, const float* values, int32_t* offsets, int32_t* order,
+                               int32_t* slot, int64_t pairs, int64_t experts, void* workspace, cudaStream_t stream);
+cudaError_t launch_expert_gather(const void* x, const int32_t* slot, void* out, int64_t rows, int64_t k,
+                                 int64_t cols, int64_t slots, int x_type, int out_type, cudaStream_t stream);
+cudaError_t launch_expert_combine(const void* y, const int32_t* slot, const float* weights, void* out, int64_t rows,
+                                  int64_t k, int64_t cols, int64_t slots, int y_type, int out_type,
+                                  cudaStream_t stream);
+cudaError_t launch_expert_combine_bwd(const void* dout, const void* y, const int32_t* slot, const float* weights,
+                                      void* dy, float* dweights, int64_t rows, int64_t k, int64_t cols,
+                                      int64_t slots, int out_type, int y_type, cudaStream_t stream);
+cudaError_t launch_quantize_blocks(const void* x, uint8_t* q, float* scale, int64_t batches, int64_t rows,
+                                   int64_t cols, int64_t block_rows, int x_type, cudaStream_t stream);
+cudaError_t launch_expert_matmul(const void* x, const void* w, const int32_t* offsets, void* y, int64_t slots,
+                                 int64_t in, int64_t out, int64_t experts, bool transposed, int dtype,
+                                 cudaStream_t stream);
+cudaError_t launch_expert_matmul_wgrad(const void* dy, const void* x, const int32_t* offsets, void* dw,
+                                       int64_t slots, int64_t in, int64_t out, int64_t experts, int dtype,
+                                       int dw_type, cudaStream_t stream);
+cudaError_t launch_expert_matmul_fp8(const uint8_t* x, const float* x_scale, const uint8_t* w, const float* w_scale,
+                                     const int32_t* offsets, void* y, int64_t slots, int64_t in, int64_t out,
+                                     int64_t experts, int y_type, cudaStream_t stream);
+// The same products for matrices of any alignment.
+cudaError_t launch_matmul_any(const void* x, const void* w, const int32_t* offsets, void* y, int64_t slots,
+                              int64_t in, int64_t out, int64_t experts, bool transposed, int dtype,
+                              cudaStream_t stream);
+cudaError_t launch_matmul_wgrad_any(const void* dy, const void* x, const int32_t* offsets, void* dw, int64_t slots,
+                                    int64_t in, int64_t out, int64_t experts, int dtype, int dw_type,
+                                    cudaStream_t stream);
+cudaError_t launch_matmul_fp8_any(const uint8_t* x, const float* x_scale, const uint8_t* w, const float* w_scale,
+                                  const int32_t* offsets, void* y, int64_t slots, int64_t in, int64_t out,
+                                  int64_t experts, int y_type, cudaStream_t stream);
+
 }  // namespace rowops
