@@ -1,18 +1,408 @@
-// expert_matmul.cu - the experts' matrix products.
-#include "launch.h"
+// expert_matmul.cu - the experts' matrix products on tcgen05.
+//
+//   kRows     y[s][n]  = sum_k w[e][n][k] x[s][k]        rows s of expert e
+//   kRowsT    y[s][n]  = sum_k w[e][k][n] x[s][k]
+//   kWeights  dw[e][m][n] = sum_{s of e} dy[s][m] x[s][n]
+//
+// The first operand's side (M) is the weights' output width, or dw's rows; the
+// second's (N) is tokens, or dw's columns.  Weights on the M side leave N free
+// to follow the ragged groups: a group of n rows is cut into ceil(n / 256) even
+// tiles of a multiple of 32 columns, so a group of 40 rows pays for 64 and not
+// for the 256 of a fixed row tile.
+//
+// A cluster of two CTAs computes 256 x N (N <= 256): each holds its 128 rows of
+// the first operand and half of the second in shared memory, 64 of the sum at a
+// time, and its 128 x N accumulators in tensor memory, twice, so the epilogue
+// of one tile runs beside the products of the next.  Both operands together
+// take 64 bytes a clock from the L2 at the full rate of the tensor cores; one
+// CTA alone with 128 x 256 would take 96.
+// Warp 4 copies (one lane), warp 5 issues products (one lane of CTA 0), warps
+// 0..3 write results.
+//
+// Operands whose sum runs along rows in memory are K-major, the others
+// MN-major: both sides of kWeights, the weights of kRowsT.  Sums past the end
+// (k >= in) are zeros that TMA fills in.  The sum of kWeights ends inside a
+// group's last 64 rows, where TMA would read the next group's: its products
+// stop at a multiple of 16 rows, and the rows between are zeroed in shared
+// memory before them (both sides: 0 times a NaN is no zero).
+#include "groups.cuh"
+#include "tensor_core.cuh"
+#include "types.cuh"
 
 namespace rowops {
+namespace {
+
+enum Form { kRows, kRowsT, kWeights };
+
+constexpr int kTileN = 256;                    // most columns of a tile
+constexpr int kStepK = 64;                     // of the sum per stage
+constexpr int kStages = 6;
+constexpr uint32_t kHalfBytes = 128 * 128;     // one operand's share of a CTA and stage
+constexpr uint32_t kStageBytes = 2 * kHalfBytes;
+constexpr int kColumn = 64 * 128;              // bytes of a 64-value column of an MN-major operand
+constexpr int kProductThreads = 192;
+constexpr int kCopyWarp = 4, kProductWarp = 5;
+constexpr uint32_t kTmemColumns = 512;
+
+struct ProductArgs {
+    CUtensorMap a;        // first operand
+    CUtensorMap b;        // second operand; kRows, kRowsT: boxes of 128 rows
+    CUtensorMap b_small;  // kRows, kRowsT: boxes of 16 rows
+    const int32_t* offsets;
+    void* out;
+    int slots, experts;
+    int m, n, k;  // kRows*: m output width, k input width.  kWeights: dw is m x n
+    uint32_t format;  // operand format code
+};
+
+struct Shared {
+    uint64_t full[kStages], empty[kStages];
+    uint64_t acc_full[2], acc_empty[2];
+    uint64_t tail_full[kStages], tail_done[kStages];  // kWeights: a stage whose last rows are zeroed
+    uint32_t tmem;
+    int abort;
+};
+
+struct Tile {
+    int expert;
+    int m0;       // first row of the pair's 256
+    int n0;       // first column: a row of x and y, or a column of dw
+    int n;        // columns to write
+    int width;    // columns the products compute
+    int sum0;     // kWeights: first row of the sum
+    int sum;      // its length
+};
+
+template <Form FORM>
+__device__ __forceinline__ bool tile_at(const ProductArgs& g, const int* table, int64_t t, Tile& w) {
+    const int tiles_m = (g.m + 255) / 256;
+    if constexpr (FORM == kWeights) {
+        const int tiles_n = (g.n + kTileN - 1) / kTileN;
+        const int64_t row = t / tiles_m;
+        if (row >= int64_t(tiles_n) * g.experts) return false;
+        w.expert = int(row / tiles_n);
+        w.m0 = int(t % tiles_m) * 256;
+        w.n0 = int(row % tiles_n) * kTileN;
+        w.n = min(kTileN, g.n - w.n0);
+        w.width = (w.n + 127) & ~127;
+        const RowRange r = group_rows(g.offsets, w.expert, g.slots);
+        w.sum0 = r.first;
+        w.sum = r.count;
+    } else {
+        const int64_t row = t / tiles_m;
+        if (row >= table[g.experts]) return false;
+        w.expert = tile_expert(table, g.experts, int(row));
+        w.m0 = int(t % tiles_m) * 256;
+        const RowRange r = group_rows(g.offsets, w.expert, g.slots);
+        const int tiles = (r.count + kTileN - 1) / kTileN;
+        const int each = ((r.count + tiles - 1) / tiles + 31) & ~31;  // at most 256, and every tile gets a row
+        const int at = (int(row) - table[w.expert]) * each;
+        w.n0 = r.first + at;
+        w.n = min(each, r.count - at);
+        w.width = (w.n + 31) & ~31;
+        w.sum0 = 0;
+        w.sum = g.k;
+    }
+    return true;
+}
+
+// Rows of the last stage of a sum of kWeights that have to be zeroed, or 0.
+__device__ __forceinline__ int ragged_rows(int sum) { return (16 - (sum & 15)) & 15; }
+
+// Zeroes the ragged rows of one CTA's operands in a stage; the whole warp.
+__device__ __forceinline__ void zero_ragged(unsigned char* stage, int sum, int width) {
+    const int valid = (sum - 1) % kStepK + 1, rows = ragged_rows(sum);
+    const int columns = 2 + width / 128;  // 64-value columns of both operands
+    for (int i = threadIdx.x & 31; i < columns * rows * 8; i += 32) {
+        const int c = i / (rows * 8), in = i % (rows * 8);
+        unsigned char* column = stage + (c < 2 ? c * kColumn : int(kHalfBytes) + (c - 2) * kColumn);
+        *reinterpret_cast<uint4*>(column + (valid + in / 8) * 128 + in % 8 * 16) = make_uint4(0, 0, 0, 0);
+    }
+}
+
+template <typename T, typename O, Form FORM>
+__device__ __forceinline__ void write_tile(const ProductArgs& g, const Tile& w, uint32_t tmem, int row, bool zero,
+                                           uint32_t free_bar) {
+    // row: the tile's row of this lane, as every epilogue lane has one
+    const int m = w.m0 + row, lane = threadIdx.x & 31;
+    for (int c = 0; c < w.n; c += 32) {
+        uint32_t r[32] = {};
+        if (!zero) {
+            tmem_load32(tmem + uint32_t(c), r);
+            tmem_wait_load(r);
+            if (c + 32 >= w.n) {  // the accumulators are free
+                tcgen05_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(free_bar);
+            }
+        }
+        if (m < g.m) {
+            if constexpr (FORM == kWeights) {
+                constexpr int V = 16 / int(sizeof(O));
+                O* p = static_cast<O*>(g.out) + (int64_t(w.expert) * g.m + m) * g.n + w.n0 + c;
+#pragma unroll
+                for (int i = 0; i < 32; i += V) {
+                    if (c + i >= w.n) break;
+                    Chunk<O, V> o;
+#pragma unroll
+                    for (int v = 0; v < V; ++v) o.set(v, __uint_as_float(r[i + v]));
+                    o.store(p + i);
+                }
+            } else {
+                O* p = static_cast<O*>(g.out) + int64_t(w.n0 + c) * g.m + m;
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    if (c + i < w.n) p[int64_t(i) * g.m] = from_float<O>(__uint_as_float(r[i]));
+            }
+        }
+        __syncwarp();
+    }
+}
+
+template <typename T, typename O, Form FORM>
+__global__ void __launch_bounds__(kProductThreads, 1)
+    expert_product(const __grid_constant__ ProductArgs g) {
+    extern __shared__ unsigned char raw[];
+    unsigned char* stages = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
+    int* table = reinterpret_cast<int*>(stages + kStages * kStageBytes);
+    __shared__ Shared sh;
+    volatile int* abort_flag = &sh.abort;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&sh.full[i], 1);
+            mbar_init(&sh.empty[i], 1);
+            mbar_init(&sh.tail_full[i], 1);
+            mbar_init(&sh.tail_done[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh.acc_full[i], 1);
+            mbar_init(&sh.acc_empty[i], 8);  // the epilogue warps of both CTAs
+        }
+        sh.abort = 0;
+        fence_barrier_init();
+    }
+    if (warp == kCopyWarp && lane == 0) {
+        prefetch_map(&g.a);
+        prefetch_map(&g.b);
+        if constexpr (FORM != kWeights) prefetch_map(&g.b_small);
+    }
+    if (warp == kProductWarp) tmem_alloc_pair(&sh.tmem, kTmemColumns);
+    if constexpr (FORM != kWeights)
+        if (warp == 0) build_tile_table<kTileN>(g.offsets, g.experts, g.slots, table);
+    tcgen05_fence_before();
+    __syncthreads();
+    cluster_sync_all();
+    tcgen05_fence_after();
+    const uint32_t tmem = sh.tmem;
+
+    const int64_t first = blockIdx.x >> 1, step = gridDim.x >> 1;
+    bool ok = true;
+    if (warp == kCopyWarp) {
+        if (lane == 0) {
+            uint32_t it = 0;
+            Tile w;
+            for (int64_t t = first; ok && tile_at<FORM>(g, table, t, w); t += step) {
+                const int blocks = (w.sum + kStepK - 1) / kStepK;
+                const int half = w.width / 2;
+                const uint32_t mine = kHalfBytes + uint32_t(half) * 128;
+                const bool ragged = FORM == kWeights && ragged_rows(w.sum) != 0;
+                for (int kb = 0; kb < blocks; ++kb, ++it) {
+                    const uint32_t s = it % kStages;
+                    if (!mbar_wait_cluster(&sh.empty[s], ((it / kStages) & 1) ^ 1, abort_flag)) {
+                        raise_abort(abort_flag);
+                        ok = false;
+                        break;
+                    }
+                    // CTA 1 zeroes its ragged rows itself, so it waits for that stage itself
+                    const bool tail = ragged && kb == blocks - 1;
+                    uint32_t bar = map_to_rank(&sh.full[s], 0);
+                    if (rank == 0) mbar_arrive_expect_tx(&sh.full[s], tail ? mine : 2 * mine);
+                    else if (tail) {
+                        mbar_arrive_expect_tx(&sh.tail_full[s], mine);
+                        bar = map_to_rank(&sh.tail_full[s], 1);
+                    }
+                    const uint32_t a = smem_addr(stages + s * kStageBytes), b = a + kHalfBytes;
+                    const int k0 = kb * kStepK;
+                    const int m0 = w.m0 + int(rank) * 128, n0 = w.n0 + int(rank) * half;
+                    if constexpr (FORM == kRows) {
+                        tma_load_3d(a, &g.a, k0, m0, w.expert, bar);
+                    } else if constexpr (FORM == kRowsT) {
+                        tma_load_3d(a, &g.a, m0, k0, w.expert, bar);
+                        tma_load_3d(a + kColumn, &g.a, m0 + 64, k0, w.expert, bar);
+                    } else {
+                        tma_load_2d(a, &g.a, m0, w.sum0 + k0, bar);
+                        tma_load_2d(a + kColumn, &g.a, m0 + 64, w.sum0 + k0, bar);
+                    }
+                    if constexpr (FORM == kWeights) {
+                        for (int i = 0; i < half; i += 64)
+                            tma_load_2d(b + i / 64 * kColumn, &g.b, n0 + i, w.sum0 + k0, bar);
+                    } else if (half == 128) {
+                        tma_load_2d(b, &g.b, k0, n0, bar);
+                    } else {
+                        for (int i = 0; i < half; i += 16) tma_load_2d(b + i * 128, &g.b_small, k0, n0 + i, bar);
+                    }
+                }
+            }
+            // every stage is released in this CTA too before it may leave
+            for (uint32_t i = it > kStages ? it - kStages : 0; ok && i < it; ++i) {
+                ok = mbar_wait_cluster(&sh.empty[i % kStages], (i / kStages) & 1, abort_flag);
+                if (!ok) raise_abort(abort_flag);
+            }
+        }
+    } else if (warp == kProductWarp) {
+        uint32_t it = 0, acc = 0, tails = 0;  // tails: the phases of the tail barriers, a bit a stage
+        Tile w;
+        for (int64_t t = first; ok && tile_at<FORM>(g, table, t, w); t += step) {
+            const int blocks = (w.sum + kStepK - 1) / kStepK;
+            if (blocks == 0) continue;
+            const bool ragged = FORM == kWeights && ragged_rows(w.sum) != 0;
+            if (rank != 0) {  // CTA 1 only zeroes its ragged rows
+                it += blocks;
+                if (!ragged) continue;
+                const uint32_t s = (it - 1) % kStages;
+                ok = warp_wait(&sh.tail_full[s], (tails >> s) & 1, abort_flag);
+                if (!ok) break;
+                zero_ragged(stages + s * kStageBytes, w.sum, w.width);
+                fence_async_shared();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(map_to_rank(&sh.tail_done[s], 0));
+                tails ^= 1u << s;
+                continue;
+            }
+            const uint32_t d = tmem + (acc & 1) * kTileN;
+            const uint32_t desc = with_n(instr_desc(g.format, FORM != kRows, FORM == kWeights), w.width);
+            ok = warp_wait(&sh.acc_empty[acc & 1], ((acc >> 1) & 1) ^ 1, abort_flag);
+            tcgen05_fence_after();
+            for (int kb = 0; ok && kb < blocks; ++kb, ++it) {
+                const uint32_t s = it % kStages;
+                ok = warp_wait(&sh.full[s], (it / kStages) & 1, abort_flag);
+                if (!ok) break;
+                unsigned char* stage = stages + s * kStageBytes;
+                if (ragged && kb == blocks - 1) {
+                    zero_ragged(stage, w.sum, w.width);
+                    fence_async_shared();
+                    __syncwarp();
+                    ok = warp_wait(&sh.tail_done[s], (tails >> s) & 1, abort_flag);
+                    if (!ok) break;
+                    tails ^= 1u << s;
+                }
+                tcgen05_fence_after();
+                if (lane == 0) {
+                    const uint32_t a = smem_addr(stage), b = a + kHalfBytes;
+                    const int left = w.sum - kb * kStepK;
+                    const int steps = left >= kStepK ? kStepK / 16 : (left + 15) / 16;
+                    for (int i = 0; i < steps; ++i) {
+                        const uint64_t da = FORM == kRows ? operand_desc(a + i * 32, 16, 1024)
+                                                          : operand_desc(a + i * 2048, kColumn, 1024);
+                        const uint64_t db = FORM == kWeights ? operand_desc(b + i * 2048, kColumn, 1024)
+                                                             : operand_desc(b + i * 32, 16, 1024);
+                        mma_pair_16bit(d, da, db, desc, kb > 0 || i > 0);
+                    }
+                    mma_commit_pair(&sh.empty[s]);
+                    if (kb == blocks - 1) mma_commit_pair(&sh.acc_full[acc & 1]);
+                }
+                __syncwarp();
+            }
+            ++acc;
+        }
+    } else {
+        uint32_t acc = 0;
+        Tile w;
+        for (int64_t t = first; tile_at<FORM>(g, table, t, w); t += step) {
+            const int row = int(rank) * 128 + warp * 32 + lane;
+            if (w.sum == 0) {
+                write_tile<T, O, FORM>(g, w, 0, row, true, 0);
+                continue;
+            }
+            if (!warp_wait(&sh.acc_full[acc & 1], (acc >> 1) & 1, abort_flag)) break;
+            tcgen05_fence_after();
+            write_tile<T, O, FORM>(g, w, tmem + (uint32_t(warp * 32) << 16) + (acc & 1) * kTileN, row, false,
+                                   map_to_rank(&sh.acc_empty[acc & 1], 0));
+            ++acc;
+        }
+    }
+    __syncwarp();
+    if (*abort_flag) let_copies_land();
+    tcgen05_fence_before();
+    __syncthreads();
+    cluster_sync_all();  // no CTA leaves, or frees tensor memory, while the other still uses it
+    tcgen05_fence_after();
+    if (warp == kProductWarp) tmem_dealloc_pair(tmem, kTmemColumns);
+}
+
+constexpr size_t kMostSmem = 1024 + kStages * size_t(kStageBytes) + (kMaxExperts + 1) * 4;
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+}  // namespace
+
+uint32_t pipeline_timeouts_matmul() { return read_pipeline_timeouts(); }
 
 cudaError_t launch_expert_matmul(const void* x, const void* w, const int32_t* offsets, void* y, int64_t slots,
                                  int64_t in, int64_t out, int64_t experts, bool transposed, int dtype,
                                  cudaStream_t stream) {
-    return launch_matmul_any(x, w, offsets, y, slots, in, out, experts, transposed, dtype, stream);
+    if (in % 8 != 0 || (transposed && out % 8 != 0) || !aligned16(x) || !aligned16(w))
+        return launch_matmul_any(x, w, offsets, y, slots, in, out, experts, transposed, dtype, stream);
+    const CUtensorMapDataType type =
+        dtype == ROWOPS_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    ProductArgs g;
+    if (!make_map(&g.a, type, 2, w, transposed ? out : in, transposed ? in : out, experts, 64, transposed ? 64 : 128,
+                  true) ||
+        !make_map(&g.b, type, 2, x, in, slots, 1, 64, 128, false) ||
+        !make_map(&g.b_small, type, 2, x, in, slots, 1, 64, 16, false))
+        return cudaErrorInvalidValue;
+    g.offsets = offsets;
+    g.out = y;
+    g.slots = int(slots);
+    g.experts = int(experts);
+    g.m = int(out);
+    g.n = 0;
+    g.k = int(in);
+    g.format = dtype == ROWOPS_F16 ? 0 : 1;
+    const int64_t tiles = (slots / kTileN + (experts < slots ? experts : slots)) * ((out + 255) / 256);  // at most
+    const size_t smem = kMostSmem;
+    if (dtype == ROWOPS_F16)
+        return transposed ? launch_pairs<expert_product<__half, __half, kRowsT>>(tiles, kProductThreads, smem, stream, g)
+                          : launch_pairs<expert_product<__half, __half, kRows>>(tiles, kProductThreads, smem, stream, g);
+    return transposed
+               ? launch_pairs<expert_product<__nv_bfloat16, __nv_bfloat16, kRowsT>>(tiles, kProductThreads, smem, stream, g)
+               : launch_pairs<expert_product<__nv_bfloat16, __nv_bfloat16, kRows>>(tiles, kProductThreads, smem, stream, g);
 }
 
 cudaError_t launch_expert_matmul_wgrad(const void* dy, const void* x, const int32_t* offsets, void* dw,
                                        int64_t slots, int64_t in, int64_t out, int64_t experts, int dtype,
                                        int dw_type, cudaStream_t stream) {
-    return launch_matmul_wgrad_any(dy, x, offsets, dw, slots, in, out, experts, dtype, dw_type, stream);
+    if (slots == 0) return cudaMemsetAsync(dw, 0, size_t(experts) * out * in * (dw_type == ROWOPS_F32 ? 4 : 2), stream);
+    if (in % 8 != 0 || out % 8 != 0 || !aligned16(x) || !aligned16(dy) || !aligned16(dw))
+        return launch_matmul_wgrad_any(dy, x, offsets, dw, slots, in, out, experts, dtype, dw_type, stream);
+    const CUtensorMapDataType type =
+        dtype == ROWOPS_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    ProductArgs g;
+    if (!make_map(&g.a, type, 2, dy, out, slots, 1, 64, 64, false) ||
+        !make_map(&g.b, type, 2, x, in, slots, 1, 64, 64, false))
+        return cudaErrorInvalidValue;
+    g.b_small = g.b;
+    g.offsets = offsets;
+    g.out = dw;
+    g.slots = int(slots);
+    g.experts = int(experts);
+    g.m = int(out);
+    g.n = int(in);
+    g.k = 0;
+    g.format = dtype == ROWOPS_F16 ? 0 : 1;
+    const int64_t tiles = experts * ((out + 255) / 256) * ((in + kTileN - 1) / kTileN);
+    const size_t smem = kMostSmem;
+    if (dtype == ROWOPS_F16)
+        return dw_type == ROWOPS_F32
+                   ? launch_pairs<expert_product<__half, float, kWeights>>(tiles, kProductThreads, smem, stream, g)
+                   : launch_pairs<expert_product<__half, __half, kWeights>>(tiles, kProductThreads, smem, stream, g);
+    return dw_type == ROWOPS_F32
+               ? launch_pairs<expert_product<__nv_bfloat16, float, kWeights>>(tiles, kProductThreads, smem, stream, g)
+               : launch_pairs<expert_product<__nv_bfloat16, __nv_bfloat16, kWeights>>(tiles, kProductThreads, smem,
+                                                                                      stream, g);
 }
 
 cudaError_t launch_expert_matmul_fp8(const uint8_t* x, const float* x_scale, const uint8_t* w, const float* w_scale,

@@ -57,4 +57,38 @@ __device__ __forceinline__ bool find_row_tile(const int32_t* offsets, int expert
     return false;
 }
 
+// table[e] = row tiles of the experts before e (table[experts]: all).  Called by
+// one whole warp.
+template <int TILE>
+__device__ __forceinline__ void build_tile_table(const int32_t* offsets, int experts, int slots, int* table) {
+    const int lane = threadIdx.x & 31;
+    int before = 0;
+    for (int base = 0; base < experts; base += 32) {
+        const int e = base + lane;
+        RowRange r{0, 0};
+        if (e < experts) r = group_rows(offsets, e, slots);
+        const int n = r.count / TILE + (r.count % TILE != 0);
+        int upto = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(kFullMask, upto, o);
+            if (lane >= o) upto += v;
+        }
+        if (e < experts) table[e] = before + upto - n;
+        before += __shfl_sync(kFullMask, upto, 31);
+    }
+    if (lane == 0) table[experts] = before;
+}
+
+// The expert of row tile `tile`, 0 <= tile < table[experts].
+__device__ __forceinline__ int tile_expert(const int* table, int experts, int tile) {
+    int lo = 0, hi = experts;  // table[lo] <= tile < table[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (table[mid] <= tile) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
 }  // namespace rowops

@@ -135,6 +135,7 @@ bool launch_teacher_ce_tma(const float* s, const float* t, float* grad, float* r
 uint32_t pipeline_timeouts_rows();
 uint32_t pipeline_timeouts_pairs();
 uint32_t pipeline_timeouts_ln();
+uint32_t pipeline_timeouts_matmul();
 // LayerNorm backward stage 1 on rows of 384..1024 floats on 16-byte
 // boundaries through the bulk-copy ring (one CTA per SM, at most 2^17 / cols
 // and at most max_ctas, 0: no further limit); writes

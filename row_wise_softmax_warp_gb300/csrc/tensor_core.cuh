@@ -1,0 +1,221 @@
+// tensor_core.cuh - tcgen05 and tiled TMA in clusters of two CTAs (sm_103a).
+//
+// The two CTAs of a cluster (SMs of one TPC) work on one 256-row tile: CTA r
+// holds rows r * 128 .. of operand A, half the columns of operand B, and rows
+// r * 128 .. of the accumulator in its tensor memory.  CTA 0 issues the
+// matrix instructions for both.  Operand tiles lie in shared memory in rows of
+// 128 bytes with the 128-byte swizzle, as TMA writes them.
+#pragma once
+
+#include <cuda.h>
+
+#include <atomic>
+
+#include "launch.h"
+#include "pipeline.cuh"
+
+namespace rowops {
+namespace {
+
+// ------------------------------------------------------------ tensor memory
+
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t* slot, uint32_t columns) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(smem_addr(slot)),
+                 "r"(columns)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;\n");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t addr, uint32_t columns) {
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;\n" ::"r"(addr), "r"(columns));
+}
+__device__ __forceinline__ void tcgen05_fence_before() {
+    asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory");
+}
+__device__ __forceinline__ void tcgen05_fence_after() {
+    asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory");
+}
+
+// 32 columns of the warp's 32 lanes: lane i of the warp gets row i.
+__device__ __forceinline__ void tmem_load32(uint32_t addr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr));
+}
+// The registers pass through the wait, so no use of them moves before it.
+__device__ __forceinline__ void tmem_wait_load(uint32_t (&r)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
+}
+
+// ----------------------------------------------------------- matrix products
+
+// Shared-memory operand descriptor, 128-byte swizzle.  K-major (rows of 64
+// 16-bit or 128 8-bit values along the sum): `stride` is the distance of 8-row
+// groups, `lead` unused.  MN-major (rows of 64 values along M or N): `stride`
+// is the distance of groups of 8 along the sum, `lead` that of 64-value columns.
+__device__ __forceinline__ uint64_t operand_desc(uint32_t addr, uint32_t lead, uint32_t stride) {
+    return uint64_t((addr >> 4) & 0x3fff) | (uint64_t((lead >> 4) & 0x3fff) << 16) |
+           (uint64_t((stride >> 4) & 0x3fff) << 32) | (uint64_t(1) << 46) | (uint64_t(2) << 61);
+}
+
+// Instruction descriptor: fp32 accumulators, operand format codes, M = 256.
+constexpr uint32_t instr_desc(uint32_t format, bool a_mn, bool b_mn) {
+    return (1u << 4) | (format << 7) | (format << 10) | (uint32_t(a_mn) << 15) | (uint32_t(b_mn) << 16) |
+           ((256u >> 4) << 24);
+}
+__device__ __forceinline__ uint32_t with_n(uint32_t desc, int n) { return desc | (uint32_t(n >> 3) << 17); }
+
+__device__ __forceinline__ void mma_pair_16bit(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(desc), "r"(uint32_t(add))
+        : "memory");
+}
+__device__ __forceinline__ void mma_pair_8bit(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(desc), "r"(uint32_t(add))
+        : "memory");
+}
+// Arrives on the barrier at this offset in both CTAs when every product issued so far is done.
+__device__ __forceinline__ void mma_commit_pair(uint64_t* bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n" ::"r"(
+            smem_addr(bar)),
+        "h"(uint16_t(3))
+        : "memory");
+}
+
+// ---------------------------------------------------------- tiled TMA, barriers
+
+// `bar`: shared::cluster address of a barrier of either CTA.
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
+        "[%1, {%2, %3}], [%4];\n" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
+        "[%1, {%2, %3, %4}], [%5];\n" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+    asm volatile("prefetch.tensormap [%0];\n" ::"l"(map) : "memory");
+}
+// Arrival on a barrier of either CTA; the releases order this thread's earlier accesses.
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void fence_barrier_init() {
+    asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+}
+// Orders this thread's shared-memory writes before later reads by TMA and tcgen05.
+__device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory"); }
+
+// Gives copies and products in flight time to land before an aborted kernel leaves (about a millisecond).
+__device__ __forceinline__ void let_copies_land() {
+    for (int i = 0; i < 1000; ++i) __nanosleep(1000);
+}
+
+// Bounded wait of a whole warp on a barrier that either CTA arrives on: the same
+// answer in every lane; false (after raising the abort) on timeout or abort.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+    const bool ok = __all_sync(kFullMask, mbar_wait_cluster(bar, parity, abort_flag));
+    if (!ok && (threadIdx.x & 31) == 0) raise_abort(abort_flag);
+    return ok;
+}
+
+// ------------------------------------------------------------------ host side
+
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+inline EncodeTiled tensor_map_encoder() {
+    static const EncodeTiled fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        const cudaError_t e =
+            cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found);
+        return e == cudaSuccess && found == cudaDriverEntryPointSuccess ? reinterpret_cast<EncodeTiled>(p) : nullptr;
+    }();
+    return fn;
+}
+
+// A row-major matrix (or `depth` of them, 3D) of `width`-value rows, read in
+// boxes of box_x x box_y values with the 128-byte swizzle; values outside read as 0.
+inline bool make_map(CUtensorMap* map, CUtensorMapDataType type, int size, const void* base, int64_t width,
+                     int64_t height, int64_t depth, int box_x, int box_y, bool three) {
+    const EncodeTiled encode = tensor_map_encoder();
+    if (encode == nullptr) return false;
+    const cuuint64_t dims[3] = {cuuint64_t(width), cuuint64_t(height), cuuint64_t(depth)};
+    const cuuint64_t strides[2] = {cuuint64_t(width * size), cuuint64_t(width * height * size)};
+    const cuuint32_t box[3] = {cuuint32_t(box_x), cuuint32_t(box_y), 1};
+    const cuuint32_t steps[3] = {1, 1, 1};
+    return encode(map, type, three ? 3 : 2, const_cast<void*>(base), dims, strides, box, steps,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Clusters of two of `kernel` that the current device runs at once (0 if
+// unknown); the first call on a device also allows the kernel its shared memory.
+template <auto kernel>
+int resident_pairs(int threads, size_t smem) {
+    static std::atomic<int> cached[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return 0;
+    if (dev < 64)
+        if (const int c = cached[dev].load(std::memory_order_relaxed)) return c;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) != cudaSuccess) return 0;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim = {2, 1, 1};
+    cfg.gridDim = dim3(2);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) return 0;
+    if (dev < 64) cached[dev].store(n, std::memory_order_relaxed);
+    return n;
+}
+
+template <auto kernel, typename A>
+cudaError_t launch_pairs(int64_t pairs, int threads, size_t smem, cudaStream_t stream, const A& args) {
+    const int resident = resident_pairs<kernel>(threads, smem);
+    if (resident <= 0) {
+        const cudaError_t e = cudaGetLastError();
+        return e == cudaSuccess ? cudaErrorInvalidConfiguration : e;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim = {2, 1, 1};
+    cfg.gridDim = dim3(2 * unsigned(pairs < resident ? pairs : resident));
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args);
+    note_launches(1);
+    return e;
+}
+
+}  // namespace
+}  // namespace rowops
