@@ -16,8 +16,8 @@
 // of one tile runs beside the products of the next.  Both operands together
 // take 64 bytes a clock from the L2 at the full rate of the tensor cores; one
 // CTA alone with 128 x 256 would take 96.
-// Warp 4 copies (one lane), warp 5 issues products (one lane of CTA 0), warps
-// 0..3 write results.
+// Warps 4 and 5 copy an operand each, warp 6 issues products (in CTA 0), warps
+// 0..3 write results, and in kWeights warp 7 zeroes.
 //
 // Operands whose sum runs along rows in memory are K-major, the others
 // MN-major: both sides of kWeights, the weights of kRowsT.  Sums past the end
@@ -40,9 +40,10 @@ constexpr int kStages = 6;
 constexpr uint32_t kHalfBytes = 128 * 128;     // one operand's share of a CTA and stage
 constexpr uint32_t kStageBytes = 2 * kHalfBytes;
 constexpr int kColumn = 64 * 128;              // bytes of a 64-value column of an MN-major operand
-constexpr int kProductThreads = 192;
-constexpr int kCopyWarp = 4, kProductWarp = 5;
+constexpr int kCopyWarpA = 4, kCopyWarpB = 5, kProductWarp = 6, kZeroWarp = 7;  // the last in kWeights only
 constexpr uint32_t kTmemColumns = 512;
+
+constexpr int threads_of(Form form) { return form == kWeights ? 256 : 224; }
 
 struct ProductArgs {
     CUtensorMap a;        // first operand
@@ -160,7 +161,7 @@ __device__ __forceinline__ void write_tile(const ProductArgs& g, const Tile& w, 
 }
 
 template <typename T, typename O, Form FORM>
-__global__ void __launch_bounds__(kProductThreads, 1)
+__global__ void __launch_bounds__(threads_of(FORM), 1)
     expert_product(const __grid_constant__ ProductArgs g) {
     extern __shared__ unsigned char raw[];
     unsigned char* stages = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
@@ -172,10 +173,10 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     const uint32_t rank = cluster_rank();
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(&sh.full[i], 1);
+            mbar_init(&sh.full[i], 2);  // a copying lane per operand
             mbar_init(&sh.empty[i], 1);
-            mbar_init(&sh.tail_full[i], 1);
-            mbar_init(&sh.tail_done[i], 1);
+            mbar_init(&sh.tail_full[i], 2);
+            mbar_init(&sh.tail_done[i], 2);  // the zeroing warps of both CTAs
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.acc_full[i], 1);
@@ -184,7 +185,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         sh.abort = 0;
         fence_barrier_init();
     }
-    if (warp == kCopyWarp && lane == 0) {
+    if (warp == kCopyWarpA && lane == 0) {
         prefetch_map(&g.a);
         prefetch_map(&g.b);
         if constexpr (FORM != kWeights) prefetch_map(&g.b_small);
@@ -196,117 +197,112 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     __syncthreads();
     cluster_sync_all();
     tcgen05_fence_after();
-    const uint32_t tmem = sh.tmem;
+    const uint32_t tmem = uniform(sh.tmem), stage0 = uniform(smem_addr(stages));
 
     const int64_t first = blockIdx.x >> 1, step = gridDim.x >> 1;
     bool ok = true;
-    if (warp == kCopyWarp) {
-        if (lane == 0) {
-            uint32_t it = 0;
-            Tile w;
-            for (int64_t t = first; ok && tile_at<FORM>(g, table, t, w); t += step) {
-                const int blocks = (w.sum + kStepK - 1) / kStepK;
-                const int half = w.width / 2;
-                const uint32_t mine = kHalfBytes + uint32_t(half) * 128;
-                const bool ragged = FORM == kWeights && ragged_rows(w.sum) != 0;
-                for (int kb = 0; kb < blocks; ++kb, ++it) {
-                    const uint32_t s = it % kStages;
-                    if (!mbar_wait_cluster(&sh.empty[s], ((it / kStages) & 1) ^ 1, abort_flag)) {
-                        raise_abort(abort_flag);
-                        ok = false;
-                        break;
-                    }
-                    // CTA 1 zeroes its ragged rows itself, so it waits for that stage itself
-                    const bool tail = ragged && kb == blocks - 1;
-                    uint32_t bar = map_to_rank(&sh.full[s], 0);
-                    if (rank == 0) mbar_arrive_expect_tx(&sh.full[s], tail ? mine : 2 * mine);
-                    else if (tail) {
-                        mbar_arrive_expect_tx(&sh.tail_full[s], mine);
-                        bar = map_to_rank(&sh.tail_full[s], 1);
-                    }
-                    const uint32_t a = smem_addr(stages + s * kStageBytes), b = a + kHalfBytes;
-                    const int k0 = kb * kStepK;
-                    const int m0 = w.m0 + int(rank) * 128, n0 = w.n0 + int(rank) * half;
-                    if constexpr (FORM == kRows) {
-                        tma_load_3d(a, &g.a, k0, m0, w.expert, bar);
-                    } else if constexpr (FORM == kRowsT) {
-                        tma_load_3d(a, &g.a, m0, k0, w.expert, bar);
-                        tma_load_3d(a + kColumn, &g.a, m0 + 64, k0, w.expert, bar);
-                    } else {
-                        tma_load_2d(a, &g.a, m0, w.sum0 + k0, bar);
-                        tma_load_2d(a + kColumn, &g.a, m0 + 64, w.sum0 + k0, bar);
-                    }
-                    if constexpr (FORM == kWeights) {
-                        for (int i = 0; i < half; i += 64)
-                            tma_load_2d(b + i / 64 * kColumn, &g.b, n0 + i, w.sum0 + k0, bar);
-                    } else if (half == 128) {
-                        tma_load_2d(b, &g.b, k0, n0, bar);
-                    } else {
-                        for (int i = 0; i < half; i += 16) tma_load_2d(b + i * 128, &g.b_small, k0, n0 + i, bar);
-                    }
-                }
-            }
-            // every stage is released in this CTA too before it may leave
-            for (uint32_t i = it > kStages ? it - kStages : 0; ok && i < it; ++i) {
-                ok = mbar_wait_cluster(&sh.empty[i % kStages], (i / kStages) & 1, abort_flag);
-                if (!ok) raise_abort(abort_flag);
-            }
-        }
-    } else if (warp == kProductWarp) {
-        uint32_t it = 0, acc = 0, tails = 0;  // tails: the phases of the tail barriers, a bit a stage
+    if (warp == kCopyWarpA || warp == kCopyWarpB) {
+        const bool is_a = warp == kCopyWarpA;
+        const uint32_t to = stage0 + (is_a ? 0 : kHalfBytes);
+        uint32_t it = 0;
         Tile w;
         for (int64_t t = first; ok && tile_at<FORM>(g, table, t, w); t += step) {
-            const int blocks = (w.sum + kStepK - 1) / kStepK;
-            if (blocks == 0) continue;
-            const bool ragged = FORM == kWeights && ragged_rows(w.sum) != 0;
-            if (rank != 0) {  // CTA 1 only zeroes its ragged rows
-                it += blocks;
-                if (!ragged) continue;
-                const uint32_t s = (it - 1) % kStages;
-                ok = warp_wait(&sh.tail_full[s], (tails >> s) & 1, abort_flag);
-                if (!ok) break;
-                zero_ragged(stages + s * kStageBytes, w.sum, w.width);
-                fence_async_shared();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(map_to_rank(&sh.tail_done[s], 0));
-                tails ^= 1u << s;
-                continue;
-            }
-            const uint32_t d = tmem + (acc & 1) * kTileN;
-            const uint32_t desc = with_n(instr_desc(g.format, FORM != kRows, FORM == kWeights), w.width);
-            ok = warp_wait(&sh.acc_empty[acc & 1], ((acc >> 1) & 1) ^ 1, abort_flag);
-            tcgen05_fence_after();
-            for (int kb = 0; ok && kb < blocks; ++kb, ++it) {
+            const int sum = uniform(w.sum), blocks = (sum + kStepK - 1) / kStepK;
+            const int half = uniform(w.width) / 2, expert = uniform(w.expert), sum0 = uniform(w.sum0);
+            const int m0 = uniform(w.m0) + int(rank) * 128, n0 = uniform(w.n0) + int(rank) * half;
+            const uint32_t mine = is_a ? kHalfBytes : uint32_t(half) * 128;
+            const bool ragged = FORM == kWeights && ragged_rows(sum) != 0;
+            for (int kb = 0; kb < blocks; ++kb, ++it) {
                 const uint32_t s = it % kStages;
-                ok = warp_wait(&sh.full[s], (it / kStages) & 1, abort_flag);
+                ok = warp_wait(&sh.empty[s], ((it / kStages) & 1) ^ 1, abort_flag);
                 if (!ok) break;
-                unsigned char* stage = stages + s * kStageBytes;
-                if (ragged && kb == blocks - 1) {
-                    zero_ragged(stage, w.sum, w.width);
-                    fence_async_shared();
-                    __syncwarp();
-                    ok = warp_wait(&sh.tail_done[s], (tails >> s) & 1, abort_flag);
-                    if (!ok) break;
-                    tails ^= 1u << s;
+                uint32_t bar = map_to_rank(&sh.full[s], 0);
+                if (ragged && kb == blocks - 1) {  // each CTA's zeroing warp waits for its own copies
+                    if (rank == 0) elect_arrive(&sh.full[s]);
+                    elect_arrive_expect_tx(&sh.tail_full[s], mine);
+                    bar = map_to_rank(&sh.tail_full[s], rank);
+                } else if (rank == 0) {
+                    elect_arrive_expect_tx(&sh.full[s], 2 * mine);
                 }
-                tcgen05_fence_after();
-                if (lane == 0) {
-                    const uint32_t a = smem_addr(stage), b = a + kHalfBytes;
-                    const int left = w.sum - kb * kStepK;
-                    const int steps = left >= kStepK ? kStepK / 16 : (left + 15) / 16;
-                    for (int i = 0; i < steps; ++i) {
+                const uint32_t dst = to + s * kStageBytes;
+                const int k0 = kb * kStepK;
+                if (is_a) {
+                    if constexpr (FORM == kRows) {
+                        tma_load_3d(dst, &g.a, k0, m0, expert, bar);
+                    } else if constexpr (FORM == kRowsT) {
+                        tma_load_3d(dst, &g.a, m0, k0, expert, bar);
+                        tma_load_3d(dst + kColumn, &g.a, m0 + 64, k0, expert, bar);
+                    } else {
+                        tma_load_2d(dst, &g.a, m0, sum0 + k0, bar);
+                        tma_load_2d(dst + kColumn, &g.a, m0 + 64, sum0 + k0, bar);
+                    }
+                } else if constexpr (FORM == kWeights) {
+                    tma_load_2d(dst, &g.b, n0, sum0 + k0, bar);
+                    if (half == 128) tma_load_2d(dst + kColumn, &g.b, n0 + 64, sum0 + k0, bar);
+                } else if (half == 128) {
+                    tma_load_2d(dst, &g.b, k0, n0, bar);
+                } else {
+                    for (int i = 0; i < half; i += 16) tma_load_2d(dst + i * 128, &g.b_small, k0, n0 + i, bar);
+                }
+            }
+        }
+        // every stage is released in this CTA too before it may leave
+        for (uint32_t i = it > kStages ? it - kStages : 0; ok && i < it; ++i)
+            ok = warp_wait(&sh.empty[i % kStages], (i / kStages) & 1, abort_flag);
+    } else if (warp == kProductWarp) {
+        if (rank == 0) {
+            uint32_t it = 0, acc = 0, tails = 0;  // tails: the phases of tail_done, a bit a stage
+            Tile w;
+            for (int64_t t = first; ok && tile_at<FORM>(g, table, t, w); t += step) {
+                const int sum = uniform(w.sum), blocks = (sum + kStepK - 1) / kStepK;
+                if (blocks == 0) continue;
+                const bool ragged = FORM == kWeights && ragged_rows(sum) != 0;
+                const uint32_t d = tmem + (acc & 1) * kTileN;
+                const uint32_t desc = uniform(with_n(instr_desc(g.format, FORM != kRows, FORM == kWeights), w.width));
+                ok = warp_wait(&sh.acc_empty[acc & 1], ((acc >> 1) & 1) ^ 1, abort_flag);
+                for (int kb = 0; ok && kb < blocks; ++kb, ++it) {
+                    const uint32_t s = it % kStages;
+                    ok = warp_wait(&sh.full[s], (it / kStages) & 1, abort_flag);
+                    if (FORM == kWeights && ragged && kb == blocks - 1) {
+                        ok = ok && warp_wait(&sh.tail_done[s], (tails >> s) & 1, abort_flag);
+                        tails ^= 1u << s;
+                    }
+                    if (!ok) break;
+                    tcgen05_fence_after();
+                    const uint32_t a = stage0 + s * kStageBytes, b = a + kHalfBytes;
+                    const auto product = [&](int i) {
                         const uint64_t da = FORM == kRows ? operand_desc(a + i * 32, 16, 1024)
                                                           : operand_desc(a + i * 2048, kColumn, 1024);
                         const uint64_t db = FORM == kWeights ? operand_desc(b + i * 2048, kColumn, 1024)
                                                              : operand_desc(b + i * 32, 16, 1024);
                         mma_pair_16bit(d, da, db, desc, kb > 0 || i > 0);
+                    };
+                    if (FORM == kWeights && kb == blocks - 1) {
+                        const int steps = (sum - kb * kStepK + 15) / 16;
+                        for (int i = 0; i < steps; ++i) product(i);
+                    } else {  // past the end of a sum of kRows and kRowsT are zeros
+#pragma unroll
+                        for (int i = 0; i < kStepK / 16; ++i) product(i);
                     }
                     mma_commit_pair(&sh.empty[s]);
-                    if (kb == blocks - 1) mma_commit_pair(&sh.acc_full[acc & 1]);
                 }
-                __syncwarp();
+                if (ok) mma_commit_pair(&sh.acc_full[acc & 1]);
+                ++acc;
             }
-            ++acc;
+        }
+    } else if (FORM == kWeights && warp == kZeroWarp) {
+        uint32_t it = 0, tails = 0;  // tails: the phases of tail_full
+        Tile w;
+        for (int64_t t = first; tile_at<FORM>(g, table, t, w); t += step) {
+            it += (w.sum + kStepK - 1) / kStepK;
+            if (ragged_rows(w.sum) == 0) continue;
+            const uint32_t s = (it - 1) % kStages;
+            if (!warp_wait(&sh.tail_full[s], (tails >> s) & 1, abort_flag)) break;
+            tails ^= 1u << s;
+            zero_ragged(stages + s * kStageBytes, w.sum, w.width);
+            fence_async_shared();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(map_to_rank(&sh.tail_done[s], 0));
         }
     } else {
         uint32_t acc = 0;
@@ -365,11 +361,11 @@ cudaError_t launch_expert_matmul(const void* x, const void* w, const int32_t* of
     const int64_t tiles = (slots / kTileN + (experts < slots ? experts : slots)) * ((out + 255) / 256);  // at most
     const size_t smem = kMostSmem;
     if (dtype == ROWOPS_F16)
-        return transposed ? launch_pairs<expert_product<__half, __half, kRowsT>>(tiles, kProductThreads, smem, stream, g)
-                          : launch_pairs<expert_product<__half, __half, kRows>>(tiles, kProductThreads, smem, stream, g);
+        return transposed ? launch_pairs<expert_product<__half, __half, kRowsT>>(tiles, threads_of(kRowsT), smem, stream, g)
+                          : launch_pairs<expert_product<__half, __half, kRows>>(tiles, threads_of(kRows), smem, stream, g);
     return transposed
-               ? launch_pairs<expert_product<__nv_bfloat16, __nv_bfloat16, kRowsT>>(tiles, kProductThreads, smem, stream, g)
-               : launch_pairs<expert_product<__nv_bfloat16, __nv_bfloat16, kRows>>(tiles, kProductThreads, smem, stream, g);
+               ? launch_pairs<expert_product<__nv_bfloat16, __nv_bfloat16, kRowsT>>(tiles, threads_of(kRowsT), smem, stream, g)
+               : launch_pairs<expert_product<__nv_bfloat16, __nv_bfloat16, kRows>>(tiles, threads_of(kRows), smem, stream, g);
 }
 
 cudaError_t launch_expert_matmul_wgrad(const void* dy, const void* x, const int32_t* offsets, void* dw,
@@ -397,11 +393,11 @@ cudaError_t launch_expert_matmul_wgrad(const void* dy, const void* x, const int3
     const size_t smem = kMostSmem;
     if (dtype == ROWOPS_F16)
         return dw_type == ROWOPS_F32
-                   ? launch_pairs<expert_product<__half, float, kWeights>>(tiles, kProductThreads, smem, stream, g)
-                   : launch_pairs<expert_product<__half, __half, kWeights>>(tiles, kProductThreads, smem, stream, g);
+                   ? launch_pairs<expert_product<__half, float, kWeights>>(tiles, threads_of(kWeights), smem, stream, g)
+                   : launch_pairs<expert_product<__half, __half, kWeights>>(tiles, threads_of(kWeights), smem, stream, g);
     return dw_type == ROWOPS_F32
-               ? launch_pairs<expert_product<__nv_bfloat16, float, kWeights>>(tiles, kProductThreads, smem, stream, g)
-               : launch_pairs<expert_product<__nv_bfloat16, __nv_bfloat16, kWeights>>(tiles, kProductThreads, smem,
+               ? launch_pairs<expert_product<__nv_bfloat16, float, kWeights>>(tiles, threads_of(kWeights), smem, stream, g)
+               : launch_pairs<expert_product<__nv_bfloat16, __nv_bfloat16, kWeights>>(tiles, threads_of(kWeights), smem,
                                                                                       stream, g);
 }
 

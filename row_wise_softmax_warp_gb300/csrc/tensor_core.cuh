@@ -72,24 +72,30 @@ constexpr uint32_t instr_desc(uint32_t format, bool a_mn, bool b_mn) {
 }
 __device__ __forceinline__ uint32_t with_n(uint32_t desc, int n) { return desc | (uint32_t(n >> 3) << 17); }
 
+// The products below are called by a whole warp, of which one lane issues them
+// (the same each time).  The elected lane's predicate, and operands that the
+// compiler sees to be alike in all lanes, keep descriptors in uniform registers;
+// from a branch of one lane each product took about 95 clocks to issue, a stage
+// of four 760 with its barriers, against 512 in which the tensor cores do them.
 __device__ __forceinline__ void mma_pair_16bit(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, bool add) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
         "l"(a), "l"(b), "r"(desc), "r"(uint32_t(add))
         : "memory");
 }
 __device__ __forceinline__ void mma_pair_8bit(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, bool add) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
         "l"(a), "l"(b), "r"(desc), "r"(uint32_t(add))
         : "memory");
 }
 // Arrives on the barrier at this offset in both CTAs when every product issued so far is done.
 __device__ __forceinline__ void mma_commit_pair(uint64_t* bar) {
     asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n" ::"r"(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n}\n" ::"r"(
             smem_addr(bar)),
         "h"(uint16_t(3))
         : "memory");
@@ -97,20 +103,44 @@ __device__ __forceinline__ void mma_commit_pair(uint64_t* bar) {
 
 // ---------------------------------------------------------- tiled TMA, barriers
 
-// `bar`: shared::cluster address of a barrier of either CTA.
+constexpr uint32_t kQuickPolls = 1u << 22;  // some seconds at most
+
+// Called by a whole warp; the elected lane acts.
+__device__ __forceinline__ void elect_arrive(uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e mbarrier.arrive.shared::cta.b64 _, [%0];\n}\n" ::"r"(smem_addr(bar))
+        : "memory");
+}
+__device__ __forceinline__ void elect_arrive_expect_tx(uint64_t* bar, uint32_t bytes) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n}\n" ::"r"(smem_addr(bar)),
+        "r"(bytes)
+        : "memory");
+}
+
+// `bar`: shared::cluster address of a barrier of either CTA.  Called by a whole warp.
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
     asm volatile(
-        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
-        "[%1, {%2, %3}], [%4];\n" ::"r"(dst),
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
+        "[%1, {%2, %3}], [%4];\n}\n" ::"r"(dst),
         "l"(map), "r"(x), "r"(y), "r"(bar)
         : "memory");
 }
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
     asm volatile(
-        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
-        "[%1, {%2, %3, %4}], [%5];\n" ::"r"(dst),
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
+        "[%1, {%2, %3, %4}], [%5];\n}\n" ::"r"(dst),
         "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
         : "memory");
+}
+// A value that every lane of the warp holds, as lane 0 has it.
+template <typename T>
+__device__ __forceinline__ T uniform(T v) {
+    return __shfl_sync(kFullMask, v, 0);
 }
 __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
     asm volatile("prefetch.tensormap [%0];\n" ::"l"(map) : "memory");
@@ -130,10 +160,28 @@ __device__ __forceinline__ void let_copies_land() {
     for (int i = 0; i < 1000; ++i) __nanosleep(1000);
 }
 
-// Bounded wait of a whole warp on a barrier that either CTA arrives on: the same
-// answer in every lane; false (after raising the abort) on timeout or abort.
+// Bounded wait on a barrier that either CTA arrives on, without a suspend hint:
+// between two stages of products the wait's own latency is what counts.
+__device__ __forceinline__ bool quick_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+    for (uint32_t i = 0; i < kQuickPolls; ++i) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n}\n"
+            : "=r"(ok)
+            : "r"(smem_addr(bar)), "r"(parity)
+            : "memory");
+        if (ok) return true;
+        if (*abort_flag) return false;
+    }
+    return false;
+}
+
+// The same for a whole warp: one answer in every lane; false (after raising the
+// abort) on timeout or abort.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
-    const bool ok = __all_sync(kFullMask, mbar_wait_cluster(bar, parity, abort_flag));
+    const bool ok = __all_sync(kFullMask, quick_wait(bar, parity, abort_flag));
     if (!ok && (threadIdx.x & 31) == 0) raise_abort(abort_flag);
     return ok;
 }
