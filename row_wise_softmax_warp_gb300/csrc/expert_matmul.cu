@@ -34,7 +34,7 @@ namespace {
 
 enum Form { kRows, kRowsT, kWeights };
 
-constexpr int kTileN = 256;                    // most columns of a tile
+constexpr int kTileN = kMostRows;              // most columns of a tile
 constexpr int kStepK = 64;                     // of the sum per stage
 constexpr int kStages = 6;
 constexpr uint32_t kHalfBytes = 128 * 128;     // one operand's share of a CTA and stage
@@ -92,14 +92,11 @@ __device__ __forceinline__ bool tile_at(const ProductArgs& g, const int* table, 
     } else {
         const int64_t row = t / tiles_m;
         if (row >= table[g.experts]) return false;
-        w.expert = tile_expert(table, g.experts, int(row));
+        const RowTile r = row_tile(g.offsets, g.experts, g.slots, table, int(row));
+        w.expert = r.expert;
         w.m0 = int(t % tiles_m) * 256;
-        const RowRange r = group_rows(g.offsets, w.expert, g.slots);
-        const int tiles = (r.count + kTileN - 1) / kTileN;
-        const int each = ((r.count + tiles - 1) / tiles + 31) & ~31;  // at most 256, and every tile gets a row
-        const int at = (int(row) - table[w.expert]) * each;
-        w.n0 = r.first + at;
-        w.n = min(each, r.count - at);
+        w.n0 = r.first;
+        w.n = r.count;
         w.width = (w.n + 31) & ~31;
         w.sum0 = 0;
         w.sum = g.k;
@@ -192,7 +189,7 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
     }
     if (warp == kProductWarp) tmem_alloc_pair(&sh.tmem, kTmemColumns);
     if constexpr (FORM != kWeights)
-        if (warp == 0) build_tile_table<kTileN>(g.offsets, g.experts, g.slots, table);
+        if (warp == 0) build_tile_table<kMostRows>(g.offsets, g.experts, g.slots, table);
     tcgen05_fence_before();
     __syncthreads();
     cluster_sync_all();
@@ -358,7 +355,7 @@ cudaError_t launch_expert_matmul(const void* x, const void* w, const int32_t* of
     g.n = 0;
     g.k = int(in);
     g.format = dtype == ROWOPS_F16 ? 0 : 1;
-    const int64_t tiles = (slots / kTileN + (experts < slots ? experts : slots)) * ((out + 255) / 256);  // at most
+    const int64_t tiles = most_row_tiles(slots, experts) * ((out + 255) / 256);
     const size_t smem = kMostSmem;
     if (dtype == ROWOPS_F16)
         return transposed ? launch_pairs<expert_product<__half, __half, kRowsT>>(tiles, threads_of(kRowsT), smem, stream, g)
@@ -399,12 +396,6 @@ cudaError_t launch_expert_matmul_wgrad(const void* dy, const void* x, const int3
                ? launch_pairs<expert_product<__nv_bfloat16, float, kWeights>>(tiles, threads_of(kWeights), smem, stream, g)
                : launch_pairs<expert_product<__nv_bfloat16, __nv_bfloat16, kWeights>>(tiles, threads_of(kWeights), smem,
                                                                                       stream, g);
-}
-
-cudaError_t launch_expert_matmul_fp8(const uint8_t* x, const float* x_scale, const uint8_t* w, const float* w_scale,
-                                     const int32_t* offsets, void* y, int64_t slots, int64_t in, int64_t out,
-                                     int64_t experts, int y_type, cudaStream_t stream) {
-    return launch_matmul_fp8_any(x, x_scale, w, w_scale, offsets, y, slots, in, out, experts, y_type, stream);
 }
 
 }  // namespace rowops

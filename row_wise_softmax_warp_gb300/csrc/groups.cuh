@@ -91,4 +91,31 @@ __device__ __forceinline__ int tile_expert(const int* table, int experts, int ti
     return lo;
 }
 
+// Groups cut into even tiles for the tcgen05 products: a group of n rows into
+// ceil(n / kMostRows) tiles of a multiple of 32 rows (the last may be shorter).
+constexpr int kMostRows = 256;
+
+struct RowTile {
+    int expert, first, count;
+};
+
+// table: build_tile_table<kMostRows>; 0 <= tile < table[experts].
+__device__ __forceinline__ RowTile row_tile(const int32_t* offsets, int experts, int slots, const int* table,
+                                            int tile) {
+    RowTile t;
+    t.expert = tile_expert(table, experts, tile);
+    const RowRange r = group_rows(offsets, t.expert, slots);
+    const int tiles = (r.count + kMostRows - 1) / kMostRows;
+    const int each = ((r.count + tiles - 1) / tiles + 31) & ~31;  // at most kMostRows, and every tile gets a row
+    const int at = (tile - table[t.expert]) * each;
+    t.first = r.first + at;
+    t.count = min(each, r.count - at);
+    return t;
+}
+
+// Host: the most row tiles that groups of `slots` rows in all can have.
+inline int64_t most_row_tiles(int64_t slots, int64_t experts) {
+    return slots / kMostRows + (experts < slots ? experts : slots);
+}
+
 }  // namespace rowops

@@ -136,6 +136,7 @@ uint32_t pipeline_timeouts_rows();
 uint32_t pipeline_timeouts_pairs();
 uint32_t pipeline_timeouts_ln();
 uint32_t pipeline_timeouts_matmul();
+uint32_t pipeline_timeouts_fp8();
 // LayerNorm backward stage 1 on rows of 384..1024 floats on 16-byte
 // boundaries through the bulk-copy ring (one CTA per SM, at most 2^17 / cols
 // and at most max_ctas, 0: no further limit); writes

@@ -625,8 +625,9 @@ uint32_t pipeline_timeouts_rows() { return read_pipeline_timeouts(); }
 }  // namespace rowops
 
 extern "C" uint32_t rowops_pipeline_timeouts(void) {
-    const uint32_t parts[4] = {rowops::pipeline_timeouts_rows(), rowops::pipeline_timeouts_pairs(),
-                               rowops::pipeline_timeouts_ln(), rowops::pipeline_timeouts_matmul()};
+    const uint32_t parts[5] = {rowops::pipeline_timeouts_rows(), rowops::pipeline_timeouts_pairs(),
+                               rowops::pipeline_timeouts_ln(), rowops::pipeline_timeouts_matmul(),
+                               rowops::pipeline_timeouts_fp8()};
     uint32_t v = 0;
     for (uint32_t p : parts) {
         if (p == 0xffffffffu) return p;
