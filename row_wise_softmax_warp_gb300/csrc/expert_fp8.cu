@@ -3,19 +3,26 @@
 //
 //   y[s][n] = sum_b xs[s][b] ws[e][n / 128][b] P_b,  P_b = sum_{k in block b} xq[s][k] wq[e][n][k]
 //
-// Tiles, copies and roles are those of expert_matmul.cu: 256 output columns by
-// up to 256 rows of a group, and a stage of 128 bytes along the sum is one block.
-// The tensor cores add up P_b alone; what they cannot do is the pair of scales,
-// which differs from block to block.  So each block's products go to one of two
-// tensor-memory buffers, and sixteen warps a CTA add scale * P_b to sums that stay
-// in registers (64 a thread) while the next block's products run into the other.
+// A cluster computes up to 256 rows of a group (128 a CTA) by 128 output columns;
+// a stage of 128 bytes along the sum is one block.  Copies and roles are those of
+// expert_matmul.cu.  The tensor cores add up P_b alone; what they cannot do is the
+// pair of scales, which differs from block to block.  So each block's products go
+// to one of four tensor-memory buffers, and eight warps a CTA add scale * P_b to
+// sums that stay in registers (64 a thread) while the next blocks' products run
+// into the others.
 //
-// What bounds it: a block's 256 x 256 x 128 products take 512 clocks of the tensor
-// cores; in that time a CTA reads 128 x 256 values from tensor memory (256 clocks)
-// and adds them (128 clocks of two-wide fused multiply-adds), and the buffers
-// change hands twice.  A lane holds one output column and a register one row, so
-// the scale is a row's: warp 19 multiplies xs with ws once for all lanes, eight
-// blocks ahead, and the adding warps read it from shared memory as a broadcast.
+// Rows lie on the lanes of tensor memory here (in expert_matmul.cu the output
+// columns do): a thread's sums then share one scale, read once a block.  With the
+// rows along the columns every value needs its own scale from shared memory, 1024
+// clocks of its bandwidth a block of 256 x 256 against the 512 clocks of the
+// products: that way measured 788 TFLOP/s (16384 x 4096 x 4096).  A row tile is
+// 256 rows whatever the group; groups of fewer rows copy only what they have.
+//
+// What bounds it: a buffer's way from the products to the adding warps and back
+// takes some 1300 clocks, most of them looks at barriers in shared memory, which the
+// operands keep busy.  Two buffers of 256 columns cover less of it than four of
+// 128 (TFLOPS_2x256 against TFLOPS_4x128 TFLOP/s at the size above), though these
+// read the rows' operand twice as often.
 #include <cuda_fp8.h>
 
 #include "groups.cuh"
@@ -26,75 +33,72 @@ namespace rowops {
 namespace {
 
 constexpr int kBlock = 128;                  // values of the sum per scale, and per stage
-constexpr int kStages = 6;
-constexpr uint32_t kHalfBytes = 128 * 128;   // one operand's share of a CTA and stage
-constexpr uint32_t kStageBytes = 2 * kHalfBytes;
-constexpr int kScaleSlots = 8;
-constexpr int kAddWarps = 16;
-constexpr int kWarpColumns = kMostRows / (kAddWarps / 4);  // rows of y that an adding warp holds
-constexpr int kCopyWarpA = 16, kCopyWarpB = 17, kProductWarp = 18, kScaleWarp = 19;
-constexpr int kThreads = 640;
+constexpr int kTileRows = 256, kTileCols = 128;
+constexpr int kStages = 8;
+constexpr uint32_t kXBytes = 128 * 128, kWBytes = 64 * 128;  // a CTA's share of a stage
+constexpr uint32_t kStageBytes = kXBytes + kWBytes;
+constexpr int kBuffers = 4;                  // of a block's products in tensor memory
+constexpr int kScaleSlots = 3;               // of the scales of kAhead blocks
+constexpr int kAhead = 4;
+constexpr int kAddWarps = 8;
+constexpr int kWarpColumns = kTileCols / (kAddWarps / 4);  // columns that an adding warp holds
+constexpr int kCopyWarp = 8, kProductWarp = 9, kScaleWarp = 10;
+constexpr int kThreads = 384;  // 168 registers a thread
 constexpr uint32_t kTmemColumns = 512;
 
 struct Fp8Args {
-    CUtensorMap w;        // boxes of 128 output columns
     CUtensorMap x;        // boxes of 128 rows
     CUtensorMap x_small;  // boxes of 16 rows
+    CUtensorMap w;        // boxes of 64 output columns
     const float* xs;
     const float* ws;
     const int32_t* offsets;
     void* y;
     int slots, experts;
     int in, out;
+    bool vec;
 };
 
 struct Fp8Shared {
-    float scale[kScaleSlots][kMostRows];
+    float scale[kScaleSlots][kAhead][128];  // of this CTA's rows
     uint64_t full[kStages], empty[kStages];
-    uint64_t acc_full[2], acc_empty[2];
+    uint64_t acc_full[kBuffers], acc_empty[kBuffers], peer_empty[kBuffers];
     uint64_t scale_full[kScaleSlots], scale_empty[kScaleSlots];
     uint32_t tmem;
     int abort;
 };
 
 struct Fp8Tile {
-    int expert, m0, n0, n, width;
+    int expert;
+    int row0, rows;  // of the pair
+    int col0;
 };
 
-__device__ __forceinline__ bool tile_at(const Fp8Args& g, const int* table, int64_t t, Fp8Tile& w) {
-    const int tiles_m = (g.out + 255) / 256;
-    const int64_t row = t / tiles_m;
+__device__ __forceinline__ bool tile_at(const Fp8Args& g, const int* table, int t, Fp8Tile& w) {
+    const int across = (g.out + kTileCols - 1) / kTileCols;
+    const int row = t / across;
     if (row >= table[g.experts]) return false;
-    const RowTile r = row_tile(g.offsets, g.experts, g.slots, table, int(row));
-    w.expert = uniform(r.expert);
-    w.m0 = int(t % tiles_m) * 256;
-    w.n0 = uniform(r.first);
-    w.n = uniform(r.count);
-    w.width = (w.n + 31) & ~31;
+    w.expert = uniform(tile_expert(table, g.experts, row));
+    const RowRange r = group_rows(g.offsets, w.expert, g.slots);
+    const int at = (row - table[w.expert]) * kTileRows;
+    w.row0 = uniform(r.first + at);
+    w.rows = uniform(min(kTileRows, r.count - at));
+    w.col0 = t % across * kTileCols;
     return true;
 }
 
-__device__ __forceinline__ void tmem_load16(uint32_t addr, uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(addr));
-}
-__device__ __forceinline__ void tmem_wait_load16(uint32_t (&r)[16]) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
-#pragma unroll
-    for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(r[i]));
+// Rows of the tile that CTA `rank` copies: its share in whole boxes of 16.
+__device__ __forceinline__ int rows_of(const Fp8Tile& w, int rank) {
+    return min(128, (max(0, w.rows - rank * 128) + 15) & ~15);
 }
 
 // acc += s * p, two at a time.
-__device__ __forceinline__ void add_scaled(float2& acc, uint32_t p0, uint32_t p1, float s0, float s1) {
+__device__ __forceinline__ void add_scaled(float2& acc, uint32_t p0, uint32_t p1, float s) {
     asm("{\n\t.reg .b64 a, p, s;\n\t"
-        "mov.b64 a, {%0, %1};\n\tmov.b64 p, {%2, %3};\n\tmov.b64 s, {%4, %5};\n\t"
+        "mov.b64 a, {%0, %1};\n\tmov.b64 p, {%2, %3};\n\tmov.b64 s, {%4, %4};\n\t"
         "fma.rn.f32x2 a, p, s, a;\n\tmov.b64 {%0, %1}, a;\n}\n"
         : "+f"(acc.x), "+f"(acc.y)
-        : "r"(p0), "r"(p1), "f"(s0), "f"(s1));
+        : "r"(p0), "r"(p1), "f"(s));
 }
 
 template <typename O>
@@ -109,12 +113,13 @@ __global__ void __launch_bounds__(kThreads, 1) expert_product_fp8(const __grid_c
     const uint32_t rank = cluster_rank();
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(&sh.full[i], 2);  // a copying warp per operand
+            mbar_init(&sh.full[i], 1);
             mbar_init(&sh.empty[i], 1);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < kBuffers; ++i) {
             mbar_init(&sh.acc_full[i], 1);
-            mbar_init(&sh.acc_empty[i], 2 * kAddWarps);
+            mbar_init(&sh.acc_empty[i], kAddWarps);
+            mbar_init(&sh.peer_empty[i], kAddWarps);  // in CTA 0: CTA 1's adding warps are done
         }
         for (int i = 0; i < kScaleSlots; ++i) {
             mbar_init(&sh.scale_full[i], 1);
@@ -123,45 +128,41 @@ __global__ void __launch_bounds__(kThreads, 1) expert_product_fp8(const __grid_c
         sh.abort = 0;
         fence_barrier_init();
     }
-    if (warp == kCopyWarpA && lane == 0) {
+    if (warp == kCopyWarp && lane == 0) {
         prefetch_map(&g.w);
         prefetch_map(&g.x);
         prefetch_map(&g.x_small);
     }
     if (warp == kProductWarp) tmem_alloc_pair(&sh.tmem, kTmemColumns);
-    if (warp == 0) build_tile_table<kMostRows>(g.offsets, g.experts, g.slots, table);
+    if (warp == 0) build_tile_table<kTileRows>(g.offsets, g.experts, g.slots, table);
     tcgen05_fence_before();
     __syncthreads();
     cluster_sync_all();
     tcgen05_fence_after();
     const uint32_t tmem = uniform(sh.tmem), stage0 = uniform(smem_addr(stages));
 
-    const int64_t first = blockIdx.x >> 1, step = gridDim.x >> 1;
+    const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
     const int blocks = (g.in + kBlock - 1) / kBlock;
     bool ok = true;
-    if (warp == kCopyWarpA || warp == kCopyWarpB) {
-        const bool is_a = warp == kCopyWarpA;
-        const uint32_t to = stage0 + (is_a ? 0 : kHalfBytes);
+    if (warp == kCopyWarp) {
         uint32_t it = 0;
         Fp8Tile w;
-        for (int64_t t = first; ok && tile_at(g, table, t, w); t += step) {
-            const int half = w.width / 2;
-            const int m0 = w.m0 + int(rank) * 128, n0 = w.n0 + int(rank) * half;
-            const uint32_t mine = is_a ? kHalfBytes : uint32_t(half) * 128;
+        for (int t = first; ok && tile_at(g, table, t, w); t += step) {
+            const int mine = rows_of(w, int(rank)), both = rows_of(w, 0) + rows_of(w, 1);
+            const int row0 = w.row0 + int(rank) * 128;
             for (int kb = 0; kb < blocks; ++kb, ++it) {
                 const uint32_t s = it % kStages;
                 ok = warp_wait(&sh.empty[s], ((it / kStages) & 1) ^ 1, abort_flag);
                 if (!ok) break;
                 const uint32_t bar = map_to_rank(&sh.full[s], 0);
-                if (rank == 0) elect_arrive_expect_tx(&sh.full[s], 2 * mine);
-                const uint32_t dst = to + s * kStageBytes;
-                if (is_a) {
-                    tma_load_3d(dst, &g.w, kb * kBlock, m0, w.expert, bar);
-                } else if (half == 128) {
-                    tma_load_2d(dst, &g.x, kb * kBlock, n0, bar);
+                if (rank == 0) elect_arrive_expect_tx(&sh.full[s], 2 * kWBytes + uint32_t(both) * 128);
+                const uint32_t a = stage0 + s * kStageBytes;
+                tma_load_3d(a + kXBytes, &g.w, kb * kBlock, w.col0 + int(rank) * 64, w.expert, bar);
+                if (mine == 128) {
+                    tma_load_2d(a, &g.x, kb * kBlock, row0, bar);
                 } else {
-                    for (int i = 0; i < half; i += 16)
-                        tma_load_2d(dst + i * 128, &g.x_small, kb * kBlock, n0 + i, bar);
+                    for (int i = 0; i < mine; i += 16)
+                        tma_load_2d(a + i * 128, &g.x_small, kb * kBlock, row0 + i, bar);
                 }
             }
         }
@@ -171,22 +172,29 @@ __global__ void __launch_bounds__(kThreads, 1) expert_product_fp8(const __grid_c
     } else if (warp == kProductWarp) {
         if (rank == 0) {
             uint32_t it = 0;
+            bool ready = false;  // the next stage and buffer are
             Fp8Tile w;
-            for (int64_t t = first; ok && tile_at(g, table, t, w); t += step) {
-                const uint32_t desc = with_n(instr_desc(0, false, false), w.width);  // 0: e4m3
+            for (int t = first; ok && tile_at(g, table, t, w); t += step) {
+                const uint32_t desc = with_n(instr_desc(0, false, false), kTileCols);  // 0: e4m3
                 for (int kb = 0; kb < blocks; ++kb, ++it) {
-                    const uint32_t s = it % kStages, d = tmem + (it & 1) * kMostRows;
-                    ok = warp_wait(&sh.acc_empty[it & 1], ((it >> 1) & 1) ^ 1, abort_flag) &&
-                         warp_wait(&sh.full[s], (it / kStages) & 1, abort_flag);
+                    const uint32_t s = it % kStages, buf = it % kBuffers, free = ((it / kBuffers) & 1) ^ 1;
+                    ok = ready || (warp_wait(&sh.full[s], (it / kStages) & 1, abort_flag) &&
+                                   warp_wait(&sh.acc_empty[buf], free, abort_flag) &&
+                                   warp_wait(&sh.peer_empty[buf], free, abort_flag));
                     if (!ok) break;
                     tcgen05_fence_after();
-                    const uint32_t a = stage0 + s * kStageBytes, b = a + kHalfBytes;
+                    const uint32_t next = it + 1, next_free = ((next / kBuffers) & 1) ^ 1;
+                    const uint32_t looks = look(&sh.full[next % kStages], (next / kStages) & 1) &
+                                           look(&sh.acc_empty[next % kBuffers], next_free) &
+                                           look(&sh.peer_empty[next % kBuffers], next_free);
+                    const uint32_t a = stage0 + s * kStageBytes, b = a + kXBytes;
 #pragma unroll
                     for (int i = 0; i < kBlock / 32; ++i)
-                        mma_pair_8bit(d, operand_desc(a + i * 32, 16, 1024), operand_desc(b + i * 32, 16, 1024), desc,
-                                      i > 0);
-                    mma_commit_pair(&sh.acc_full[it & 1]);
+                        mma_pair_8bit(tmem + buf * kTileCols, operand_desc(a + i * 32, 16, 1024),
+                                      operand_desc(b + i * 32, 16, 1024), desc, i > 0);
+                    mma_commit_pair(&sh.acc_full[buf]);
                     mma_commit_pair(&sh.empty[s]);
+                    ready = saw(looks);
                 }
             }
         }
@@ -194,71 +202,94 @@ __global__ void __launch_bounds__(kThreads, 1) expert_product_fp8(const __grid_c
         uint32_t it = 0;
         const int out_blocks = (g.out + kBlock - 1) / kBlock;
         Fp8Tile w;
-        for (int64_t t = first; ok && tile_at(g, table, t, w); t += step) {
-            const int nb = w.m0 / kBlock + int(rank);
-            const float* ws = g.ws + (int64_t(w.expert) * out_blocks + min(nb, out_blocks - 1)) * blocks;
-            const float* xs = g.xs + int64_t(w.n0) * blocks;
-            for (int kb = 0; kb < blocks; ++kb, ++it) {
+        for (int t = first; ok && tile_at(g, table, t, w); t += step) {
+            const int rows = min(128, w.rows - int(rank) * 128);
+            const float* ws = g.ws + (int64_t(w.expert) * out_blocks + w.col0 / kBlock) * blocks;
+            const float* xs = g.xs + (int64_t(w.row0) + rank * 128) * blocks;
+            for (int k0 = 0; ok && k0 < blocks; k0 += kAhead) {
+                float x[kAhead][4], wv[kAhead];
+#pragma unroll
+                for (int j = 0; j < kAhead; ++j) {
+                    const int kb = min(k0 + j, blocks - 1);
+                    wv[j] = __ldg(ws + kb);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        x[j][i] = i * 32 + lane < rows ? __ldg(xs + int64_t(i * 32 + lane) * blocks + kb) : 0.f;
+                }
                 const uint32_t s = it % kScaleSlots;
                 ok = warp_wait(&sh.scale_empty[s], ((it / kScaleSlots) & 1) ^ 1, abort_flag);
                 if (!ok) break;
-                const float wv = __ldg(ws + kb);
-                float v[kMostRows / 32];
 #pragma unroll
-                for (int i = 0; i < kMostRows / 32; ++i) {
-                    const int c = i * 32 + lane;
-                    v[i] = c < w.n ? __ldg(xs + int64_t(c) * blocks + kb) : 0.f;
-                }
+                for (int j = 0; j < kAhead; ++j)
 #pragma unroll
-                for (int i = 0; i < kMostRows / 32; ++i) sh.scale[s][i * 32 + lane] = v[i] * wv;
+                    for (int i = 0; i < 4; ++i) sh.scale[s][j][i * 32 + lane] = x[j][i] * wv[j];
                 __syncwarp();
                 elect_arrive(&sh.scale_full[s]);
+                ++it;
             }
         }
-    } else {
-        const int c0 = warp / 4 * kWarpColumns, row = int(rank) * 128 + (warp & 3) * 32 + lane;
+    } else if (warp < kAddWarps) {
+        const int c0 = warp / 4 * kWarpColumns, row = (warp & 3) * 32 + lane;
         const uint32_t from = tmem + (uint32_t(warp & 3) << 21) + uint32_t(c0);  // lane 32 * (warp % 4)
-        const uint32_t free0 = map_to_rank(&sh.acc_empty[0], 0), free1 = map_to_rank(&sh.acc_empty[1], 0);
-        uint32_t it = 0;
+        const uint32_t freed = map_to_rank(rank == 0 ? sh.acc_empty : sh.peer_empty, 0);  // CTA 0's, of buffer 0
+        uint32_t it = 0, group = 0;
+        bool ready = false;  // the next block's products are there
         Fp8Tile w;
-        for (int64_t t = first; ok && tile_at(g, table, t, w); t += step) {
+        for (int t = first; ok && tile_at(g, table, t, w); t += step) {
             float2 acc[kWarpColumns / 2];
 #pragma unroll
             for (int i = 0; i < kWarpColumns / 2; ++i) acc[i] = make_float2(0.f, 0.f);
-            for (int kb = 0; kb < blocks; ++kb, ++it) {
-                const uint32_t s = it % kScaleSlots;
-                ok = warp_wait(&sh.acc_full[it & 1], (it >> 1) & 1, abort_flag) &&
-                     warp_wait(&sh.scale_full[s], (it / kScaleSlots) & 1, abort_flag);
+            for (int k0 = 0; ok && k0 < blocks; k0 += kAhead, ++group) {
+                const uint32_t s = group % kScaleSlots;
+                ok = warp_wait(&sh.scale_full[s], (group / kScaleSlots) & 1, abort_flag);
                 if (!ok) break;
-                tcgen05_fence_after();
-                const float4* scale = reinterpret_cast<const float4*>(&sh.scale[s][c0]);
+                float scale[kAhead];
 #pragma unroll
-                for (int q = 0; q < kWarpColumns / 16; ++q) {
-                    if (c0 + q * 16 >= w.width) break;
-                    uint32_t r[16];
-                    tmem_load16(from + (it & 1) * kMostRows + q * 16, r);
-                    tmem_wait_load16(r);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float4 v = scale[q * 4 + i];
-                        add_scaled(acc[q * 8 + i * 2], r[i * 4], r[i * 4 + 1], v.x, v.y);
-                        add_scaled(acc[q * 8 + i * 2 + 1], r[i * 4 + 2], r[i * 4 + 3], v.z, v.w);
-                    }
-                }
-                tcgen05_fence_before();
+                for (int j = 0; j < kAhead; ++j) scale[j] = sh.scale[s][j][row];
                 __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive_cluster(it & 1 ? free1 : free0);
-                    mbar_arrive(&sh.scale_empty[s]);
+                elect_arrive(&sh.scale_empty[s]);
+#pragma unroll
+                for (int j = 0; j < kAhead; ++j) {
+                    if (k0 + j >= blocks) break;
+                    const uint32_t buf = it % kBuffers;
+                    ok = ready || warp_wait(&sh.acc_full[buf], (it / kBuffers) & 1, abort_flag);
+                    if (!ok) break;
+                    tcgen05_fence_after();
+                    uint32_t r[2][32];
+                    tmem_load32(from + buf * kTileCols, r[0]);
+                    tmem_load32(from + buf * kTileCols + 32, r[1]);
+                    tmem_wait_load(r[0]);
+                    tmem_wait_load(r[1]);
+                    tcgen05_fence_before();
+                    __syncwarp();
+                    elect_arrive_pair(freed + buf * 8);
+                    const uint32_t looks = look(&sh.acc_full[(it + 1) % kBuffers], ((it + 1) / kBuffers) & 1);
+#pragma unroll
+                    for (int i = 0; i < kWarpColumns / 2; ++i)
+                        add_scaled(acc[i], r[i / 16][i % 16 * 2], r[i / 16][i % 16 * 2 + 1], scale[j]);
+                    ready = saw(looks);
+                    ++it;
                 }
             }
             if (!ok) break;
-            const int m = w.m0 + row;
-            if (m < g.out) {
-                O* p = static_cast<O*>(g.y) + int64_t(w.n0 + c0) * g.out + m;
+            if (int(rank) * 128 + row < w.rows) {
+                const int64_t r = w.row0 + int(rank) * 128 + row;
+                O* p = static_cast<O*>(g.y) + r * g.out + w.col0 + c0;
+                const int cols = g.out - w.col0 - c0;  // that are there
+                if (g.vec) {  // out and y allow 16-byte stores
+                    constexpr int V = 16 / int(sizeof(O));
 #pragma unroll
-                for (int i = 0; i < kWarpColumns; ++i)
-                    if (c0 + i < w.n) p[int64_t(i) * g.out] = from_float<O>(i & 1 ? acc[i / 2].y : acc[i / 2].x);
+                    for (int i = 0; i < kWarpColumns; i += V) {
+                        Chunk<O, V> o;
+#pragma unroll
+                        for (int v = 0; v < V; ++v) o.set(v, (i + v) & 1 ? acc[(i + v) / 2].y : acc[(i + v) / 2].x);
+                        if (i < cols) o.store(p + i);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < kWarpColumns; ++i)
+                        if (i < cols) p[i] = from_float<O>(i & 1 ? acc[i / 2].y : acc[i / 2].x);
+                }
             }
             __syncwarp();
         }
@@ -286,7 +317,7 @@ cudaError_t launch_expert_matmul_fp8(const uint8_t* x, const float* x_scale, con
         return launch_matmul_fp8_any(x, x_scale, w, w_scale, offsets, y, slots, in, out, experts, y_type, stream);
     const CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_UINT8;
     Fp8Args g;
-    if (!make_map(&g.w, type, 1, w, in, out, experts, kBlock, 128, true) ||
+    if (!make_map(&g.w, type, 1, w, in, out, experts, kBlock, 64, true) ||
         !make_map(&g.x, type, 1, x, in, slots, 1, kBlock, 128, false) ||
         !make_map(&g.x_small, type, 1, x, in, slots, 1, kBlock, 16, false))
         return cudaErrorInvalidValue;
@@ -298,8 +329,11 @@ cudaError_t launch_expert_matmul_fp8(const uint8_t* x, const float* x_scale, con
     g.experts = int(experts);
     g.in = int(in);
     g.out = int(out);
-    const int64_t tiles = most_row_tiles(slots, experts) * ((out + 255) / 256);
+    const int y_size = y_type == ROWOPS_F32 ? 4 : 2;
+    g.vec = out * y_size % 16 == 0 && reinterpret_cast<uintptr_t>(y) % 16 == 0;
+    const int64_t tiles = most_row_tiles(slots, experts) * ((out + kTileCols - 1) / kTileCols);
     cudaError_t e = cudaErrorInvalidValue;
+    if (tiles >= (int64_t(1) << 30)) return e;  // more than a device's memory holds
     with_type(y_type, [&](auto o) {
         e = launch_pairs<expert_product_fp8<decltype(o)>>(tiles, kThreads, kMostSmem, stream, g);
     });

@@ -131,7 +131,7 @@ __device__ __forceinline__ void write_tile(const ProductArgs& g, const Tile& w, 
             if (c + 32 >= w.n) {  // the accumulators are free
                 tcgen05_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(free_bar);
+                if (lane == 0) mbar_arrive_pair(free_bar);
             }
         }
         if (m < g.m) {
@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
                     const uint32_t s = it % kStages;
                     ok = warp_wait(&sh.full[s], (it / kStages) & 1, abort_flag);
                     if (FORM == kWeights && ragged && kb == blocks - 1) {
-                        ok = ok && warp_wait(&sh.tail_done[s], (tails >> s) & 1, abort_flag);
+                        ok = ok && warp_wait_cluster(&sh.tail_done[s], (tails >> s) & 1, abort_flag);
                         tails ^= 1u << s;
                     }
                     if (!ok) break;

@@ -145,7 +145,18 @@ __device__ __forceinline__ T uniform(T v) {
 __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
     asm volatile("prefetch.tensormap [%0];\n" ::"l"(map) : "memory");
 }
-// Arrival on a barrier of either CTA; the releases order this thread's earlier accesses.
+// Arrival on a barrier of either CTA that hands over tensor memory: the tcgen05
+// fences around it order the accesses.
+__device__ __forceinline__ void mbar_arrive_pair(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];\n" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void elect_arrive_pair(uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e mbarrier.arrive.shared::cluster.b64 _, [%0];\n}\n" ::"r"(bar)
+        : "memory");
+}
+// Arrival that also releases this thread's shared-memory writes to the other CTA.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(bar) : "memory");
 }
@@ -160,28 +171,52 @@ __device__ __forceinline__ void let_copies_land() {
     for (int i = 0; i < 1000; ++i) __nanosleep(1000);
 }
 
-// Bounded wait on a barrier that either CTA arrives on, without a suspend hint:
-// between two stages of products the wait's own latency is what counts.
-__device__ __forceinline__ bool quick_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+// Bounded wait of a whole warp: one lane polls and a vote tells the others, so the
+// compiler sees one answer for all; false (after raising the abort) on timeout or
+// abort.  No suspend hint: between two stages of products the wait's
+// own latency is what counts.  The acquire is the CTA's: TMA's and tcgen05's
+// arrivals order what they did.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
     for (uint32_t i = 0; i < kQuickPolls; ++i) {
-        uint32_t ok;
+        uint32_t done;
         asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "{\n\t.reg .pred p, e;\n\tsetp.ne.u32 p, 0, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+            "@e mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
             "selp.u32 %0, 1, 0, p;\n}\n"
-            : "=r"(ok)
+            : "=r"(done)
             : "r"(smem_addr(bar)), "r"(parity)
             : "memory");
-        if (ok) return true;
-        if (*abort_flag) return false;
+        if (__any_sync(kFullMask, done)) {
+            __syncwarp();
+            return true;
+        }
+        if (__any_sync(kFullMask, *abort_flag)) return false;
     }
+    if ((threadIdx.x & 31) == 0) raise_abort(abort_flag);
     return false;
 }
-
-// The same for a whole warp: one answer in every lane; false (after raising the
-// abort) on timeout or abort.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
-    const bool ok = __all_sync(kFullMask, quick_wait(bar, parity, abort_flag));
+// A look at barriers without waiting: under the tensor cores' traffic one takes some
+// 280 clocks (55 on an idle SM), so a loop looks at the next stage's before it
+// works on this one's and asks for the answer, saw(), afterwards.  The whole warp.
+__device__ __forceinline__ uint32_t look(uint64_t* bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\tsetp.ne.u32 p, 0, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(done)
+        : "r"(smem_addr(bar)), "r"(parity)
+        : "memory");
+    return done;
+}
+__device__ __forceinline__ bool saw(uint32_t looks) {
+    const bool all = __any_sync(kFullMask, looks);
+    __syncwarp();
+    return all;
+}
+// With a cluster-wide acquire, for what the other CTA wrote by itself.
+__device__ __forceinline__ bool warp_wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+    const bool ok = __all_sync(kFullMask, mbar_wait_cluster(bar, parity, abort_flag));
     if (!ok && (threadIdx.x & 31) == 0) raise_abort(abort_flag);
     return ok;
 }
