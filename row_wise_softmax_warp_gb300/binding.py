@@ -384,22 +384,23 @@ def rowops_layernorm_bwd_noalloc(dy, gamma, xhat, inv_std, dx=None, dgamma=None,
 
 
 # ------------------------------------------------------- the expert operators
-# Outputs left as ``None`` and workspaces are allocated on the call's stream.
+# Outputs left as ``None`` and workspaces are allocated on the call's stream.  A
+# small call takes the device a few microseconds, so arguments that are as they
+# should be pass one short test each; what is wrong is found out afterwards.
 
 _DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}  # rowops_dtype
 _FLOATS = (torch.float32, torch.float16, torch.bfloat16)
 _HALVES = (torch.float16, torch.bfloat16)
+_F32 = (torch.float32,)
+_INT = (torch.int32,)
+_E4M3 = (torch.float8_e4m3fn,)
 
 
 class _Placed:
-    """Makes the tensors' device, and the stream if one is given, current for allocations and the launch."""
-
-    __slots__ = ("guards",)
+    """Makes a tensor's device, and a stream if one is given, current for allocations and the launch."""
 
     def __init__(self, t: torch.Tensor, stream):
-        self.guards = []
-        if t.device.index != torch.cuda.current_device():
-            self.guards.append(torch.cuda.device(t.device))
+        self.guards = [torch.cuda.device(t.device)]
         if stream is not None:
             if not isinstance(stream, torch.cuda.Stream):
                 stream = (torch.cuda.ExternalStream(int(stream), device=t.device) if int(stream)
@@ -415,40 +416,49 @@ class _Placed:
             g.__exit__(*exc)
 
 
-def _typed(t, name: str, dtypes, shape=None, like=None):
-    """A contiguous CUDA tensor of one of `dtypes`, of `shape` and on the device of `like` where they are given."""
+def _elsewhere(t, stream) -> bool:
+    """Whether the call has to make another device or stream current first."""
+    return stream is not None or t.get_device() != _current_device()
+
+
+def _typed(t, name: str, dtypes, shape=None, device=None):
+    """A contiguous CUDA tensor of one of `dtypes`, of `shape` and on device number `device` where they are given."""
+    if (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in dtypes and t.is_contiguous()
+            and (shape is None or t.shape == shape) and (device is None or t.get_device() == device)):
+        return t
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if like is not None and t.device != like.device:
-        raise ValueError(f"{name} is on {t.device}, not on {like.device}")
-    return t
+    raise ValueError(f"{name} is on cuda:{t.get_device()}, not on cuda:{device}")
 
 
 def _dims(t, name: str, n: int):
-    if t.dim() != n:
-        raise ValueError(f"{name} must have {n} dimensions, got {t.dim()}")
-    return t.shape
+    shape = t.shape
+    if len(shape) != n:
+        raise ValueError(f"{name} must have {n} dimensions, got {len(shape)}")
+    return shape
 
 
-def _given(t, name: str, dtype, shape, like):
+def _given(t, name: str, dtype, shape, like, device):
     """An output: the caller's, checked, or a new one."""
     if t is None:
         return torch.empty(shape, dtype=dtype, device=like.device)
-    return _typed(t, name, (dtype,), shape, like)
+    return _typed(t, name, (dtype,), shape, device)
 
 
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _current(t):
-    return torch.cuda.current_stream(t.device).cuda_stream
+# t is a CUDA tensor, so CUDA is initialised
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
 def rowops_expert_plan_workspace(rows: int, k: int, experts: int) -> int:
@@ -460,163 +470,191 @@ def rowops_expert_plan(indices, experts, values=None, offsets=None, order=None, 
     """Returns (offsets, order, slot), int32: the (token, choice) pairs of indices (rows, k) grouped by expert.
 
     values (rows, k): pairs whose value is 0 are left out."""
-    indices = _typed(indices, "indices", (torch.float32,))
-    rows, k = _dims(indices, "indices", 2)
+    _typed(indices, "indices", _F32)
+    if _elsewhere(indices, stream):
+        with _Placed(indices, stream):
+            return rowops_expert_plan(indices, experts, values, offsets, order, slot, workspace)
+    rows, k = shape = _dims(indices, "indices", 2)
+    device = indices.get_device()
     if values is not None:
-        _typed(values, "values", (torch.float32,), (rows, k), indices)
-    with _Placed(indices, stream):
-        offsets = _given(offsets, "offsets", torch.int32, (experts + 1,), indices)
-        order = _given(order, "order", torch.int32, (rows * k,), indices)
-        slot = _given(slot, "slot", torch.int32, (rows, k), indices)
-        if workspace is None:
-            need = rowops_expert_plan_workspace(rows, k, experts)
-            workspace = torch.empty(need, dtype=torch.uint8, device=indices.device) if need else None
-        elif not isinstance(workspace, torch.Tensor) or workspace.device != indices.device:
+        _typed(values, "values", _F32, shape, device)
+    lib = library()
+    pairs, size = rows * k, 0
+    need = lib.rowops_expert_plan_workspace(rows, k, experts)
+    offsets = _given(offsets, "offsets", torch.int32, (max(experts, 0) + 1,), indices, device)
+    order = _given(order, "order", torch.int32, (pairs,), indices, device)
+    slot = _given(slot, "slot", torch.int32, shape, indices, device)
+    if workspace is not None:
+        if not isinstance(workspace, torch.Tensor) or workspace.device != indices.device:
             raise ValueError(f"workspace must be a tensor on {indices.device}")
-        size = 0 if workspace is None else workspace.numel() * workspace.element_size()
-        _check(library().rowops_expert_plan(indices.data_ptr(), _ptr(values), offsets.data_ptr(), order.data_ptr(),
-                                            slot.data_ptr(), rows, k, experts, _ptr(workspace), size,
-                                            _current(indices)))
+        size = workspace.numel() * workspace.element_size()
+    elif need:
+        workspace, size = torch.empty(need, dtype=torch.uint8, device=indices.device), need
+    _check(lib.rowops_expert_plan(indices.data_ptr(), _ptr(values), offsets.data_ptr(), order.data_ptr(),
+                                  slot.data_ptr(), rows, k, experts, _ptr(workspace), size, _raw_stream(device)))
     return offsets, order, slot
 
 
 def rowops_expert_gather(x, slot, out=None, slots=None, dtype=None, stream=None):
     """out[slot[t][j]] = x[t]; x (rows, cols), slot (rows, k).  A new `out` has `slots` rows (default rows * k)
     of `dtype` (default x's); its rows that no slot names are not written."""
-    x = _typed(x, "x", _FLOATS)
+    _typed(x, "x", _FLOATS)
+    if _elsewhere(x, stream):
+        with _Placed(x, stream):
+            return rowops_expert_gather(x, slot, out, slots, dtype)
     rows, cols = _dims(x, "x", 2)
-    slot = _typed(slot, "slot", (torch.int32,), None, x)
-    k = _dims(slot, "slot", 2)[1]
-    _typed(slot, "slot", (torch.int32,), (rows, k))
-    if out is not None:
-        slots = _dims(_typed(out, "out", _FLOATS if dtype is None else (dtype,), None, x), "out", 2)[0]
-    elif slots is None:
-        slots = rows * k
-    with _Placed(x, stream):
-        out = _given(out, "out", (x.dtype if dtype is None else dtype) if out is None else out.dtype, (slots, cols), x)
-        _check(library().rowops_expert_gather(x.data_ptr(), slot.data_ptr(), out.data_ptr(), rows, k, cols, slots,
-                                              _DTYPES[x.dtype], _DTYPES[out.dtype], _current(x)))
+    device = x.get_device()
+    k = _dims(_typed(slot, "slot", _INT, None, device), "slot", 2)[1]
+    if slot.shape[0] != rows:
+        raise ValueError(f"slot must have {rows} rows, got {slot.shape[0]}")
+    if out is None:
+        out = torch.empty((rows * k if slots is None else slots, cols), dtype=x.dtype if dtype is None else dtype,
+                          device=x.device)
+    _typed(out, "out", _FLOATS if dtype is None else (dtype,), None, device)
+    if len(out.shape) != 2 or out.shape[1] != cols or (slots is not None and out.shape[0] != slots):
+        raise ValueError(f"out must have shape ({'slots' if slots is None else slots}, {cols}), got {tuple(out.shape)}")
+    _check(library().rowops_expert_gather(x.data_ptr(), slot.data_ptr(), out.data_ptr(), rows, k, cols, out.shape[0],
+                                          _DTYPES[x.dtype], _DTYPES.get(out.dtype, -1), _raw_stream(device)))
     return out
 
 
 def rowops_expert_combine(y, slot, weights=None, out=None, dtype=None, stream=None):
     """out[t] = sum_j weights[t][j] * y[slot[t][j]] (weights None: all 1); out of `dtype` (default y's)."""
-    y = _typed(y, "y", _FLOATS)
+    _typed(y, "y", _FLOATS)
+    if _elsewhere(y, stream):
+        with _Placed(y, stream):
+            return rowops_expert_combine(y, slot, weights, out, dtype)
     slots, cols = _dims(y, "y", 2)
-    slot = _typed(slot, "slot", (torch.int32,), None, y)
-    rows, k = _dims(slot, "slot", 2)
+    device = y.get_device()
+    rows, k = pairs = _dims(_typed(slot, "slot", _INT, None, device), "slot", 2)
     if weights is not None:
-        _typed(weights, "weights", (torch.float32,), (rows, k), y)
-    if out is not None:
-        _typed(out, "out", _FLOATS if dtype is None else (dtype,), (rows, cols), y)
-    with _Placed(y, stream):
-        if out is None:
-            out = _given(None, "out", y.dtype if dtype is None else dtype, (rows, cols), y)
-        _check(library().rowops_expert_combine(y.data_ptr(), slot.data_ptr(), _ptr(weights), out.data_ptr(), rows, k,
-                                               cols, slots, _DTYPES[y.dtype], _DTYPES[out.dtype], _current(y)))
+        _typed(weights, "weights", _F32, pairs, device)
+    if out is None:
+        out = torch.empty((rows, cols), dtype=y.dtype if dtype is None else dtype, device=y.device)
+    else:
+        _typed(out, "out", _FLOATS if dtype is None else (dtype,), (rows, cols), device)
+    _check(library().rowops_expert_combine(y.data_ptr(), slot.data_ptr(), _ptr(weights), out.data_ptr(), rows, k, cols,
+                                           slots, _DTYPES[y.dtype], _DTYPES.get(out.dtype, -1), _raw_stream(device)))
     return out
 
 
 def rowops_expert_combine_bwd(dout, y, slot, weights, dy=None, dweights=None, stream=None):
     """Returns (dy, dweights) of rowops_expert_combine; rows of a new dy that no slot names are not written."""
-    y = _typed(y, "y", _FLOATS)
-    slots, cols = _dims(y, "y", 2)
-    slot = _typed(slot, "slot", (torch.int32,), None, y)
-    rows, k = _dims(slot, "slot", 2)
-    dout = _typed(dout, "dout", _FLOATS, (rows, cols), y)
-    weights = _typed(weights, "weights", (torch.float32,), (rows, k), y)
-    with _Placed(y, stream):
-        dy = _given(dy, "dy", y.dtype, (slots, cols), y)
-        dweights = _given(dweights, "dweights", torch.float32, (rows, k), y)
-        _check(library().rowops_expert_combine_bwd(dout.data_ptr(), y.data_ptr(), slot.data_ptr(),
-                                                   weights.data_ptr(), dy.data_ptr(), dweights.data_ptr(), rows, k,
-                                                   cols, slots, _DTYPES[dout.dtype], _DTYPES[y.dtype], _current(y)))
+    _typed(y, "y", _FLOATS)
+    if _elsewhere(y, stream):
+        with _Placed(y, stream):
+            return rowops_expert_combine_bwd(dout, y, slot, weights, dy, dweights)
+    slots, cols = shape = _dims(y, "y", 2)
+    device = y.get_device()
+    rows, k = pairs = _dims(_typed(slot, "slot", _INT, None, device), "slot", 2)
+    _typed(dout, "dout", _FLOATS, (rows, cols), device)
+    _typed(weights, "weights", _F32, pairs, device)
+    dy = _given(dy, "dy", y.dtype, shape, y, device)
+    dweights = _given(dweights, "dweights", torch.float32, pairs, y, device)
+    _check(library().rowops_expert_combine_bwd(dout.data_ptr(), y.data_ptr(), slot.data_ptr(), weights.data_ptr(),
+                                               dy.data_ptr(), dweights.data_ptr(), rows, k, cols, slots,
+                                               _DTYPES[dout.dtype], _DTYPES[y.dtype], _raw_stream(device)))
     return dy, dweights
 
 
-def _offsets(offsets, experts: int, like):
+def _offsets(offsets, experts: int, device):
     if offsets is not None:
-        _typed(offsets, "offsets", (torch.int32,), (experts + 1,), like)
+        _typed(offsets, "offsets", _INT, (experts + 1,), device)
     elif experts != 1:
         raise ValueError("offsets may be None for one expert only")
-    return offsets
 
 
 def rowops_expert_matmul(x, w, offsets=None, y=None, transposed=False, stream=None):
     """y[s] = w[e] @ x[s] for the rows offsets[e] <= s < offsets[e + 1] of x (slots, in).
 
     w: (experts, out, in), or (experts, in, out) with transposed.  Rows of a new y that no expert has are not written."""
-    x = _typed(x, "x", _HALVES)
+    _typed(x, "x", _HALVES)
+    if _elsewhere(x, stream):
+        with _Placed(x, stream):
+            return rowops_expert_matmul(x, w, offsets, y, transposed)
     slots, in_cols = _dims(x, "x", 2)
-    w = _typed(w, "w", (x.dtype,), None, x)
-    experts, out_cols = _dims(w, "w", 3)[0], w.shape[2 if transposed else 1]
-    _typed(w, "w", (x.dtype,), (experts, in_cols, out_cols) if transposed else (experts, out_cols, in_cols))
-    offsets = _offsets(offsets, experts, x)
-    with _Placed(x, stream):
-        y = _given(y, "y", x.dtype, (slots, out_cols), x)
-        _check(library().rowops_expert_matmul(x.data_ptr(), w.data_ptr(), _ptr(offsets), y.data_ptr(), slots, in_cols,
-                                              out_cols, experts, 1 if transposed else 0, _DTYPES[x.dtype],
-                                              _current(x)))
+    device, dtype = x.get_device(), x.dtype
+    experts, out_cols, k = _dims(_typed(w, "w", (dtype,), None, device), "w", 3)
+    if transposed:
+        out_cols, k = k, out_cols
+    if k != in_cols:
+        raise ValueError(f"w must take rows of {in_cols} values, got {tuple(w.shape)}")
+    _offsets(offsets, experts, device)
+    y = _given(y, "y", dtype, (slots, out_cols), x, device)
+    _check(library().rowops_expert_matmul(x.data_ptr(), w.data_ptr(), _ptr(offsets), y.data_ptr(), slots, in_cols,
+                                          out_cols, experts, 1 if transposed else 0, _DTYPES[dtype],
+                                          _raw_stream(device)))
     return y
 
 
 def rowops_expert_matmul_wgrad(dy, x, offsets=None, dw=None, dtype=None, stream=None):
     """dw[e] = sum over expert e's rows of dy[s]^T x[s]: (experts, out, in), of x's type or torch.float32."""
-    dy = _typed(dy, "dy", _HALVES)
+    _typed(dy, "dy", _HALVES)
+    if _elsewhere(dy, stream):
+        with _Placed(dy, stream):
+            return rowops_expert_matmul_wgrad(dy, x, offsets, dw, dtype)
     slots, out_cols = _dims(dy, "dy", 2)
-    x = _typed(x, "x", (dy.dtype,), None, dy)
-    in_cols = _dims(x, "x", 2)[1]
-    _typed(x, "x", (dy.dtype,), (slots, in_cols))
-    experts = 1 if offsets is None else offsets.numel() - 1
-    offsets = _offsets(offsets, experts, dy)
-    if dw is not None:
-        _typed(dw, "dw", (dy.dtype, torch.float32) if dtype is None else (dtype,), (experts, out_cols, in_cols), dy)
-    with _Placed(dy, stream):
-        if dw is None:
-            dw = _given(None, "dw", dy.dtype if dtype is None else dtype, (experts, out_cols, in_cols), dy)
-        _check(library().rowops_expert_matmul_wgrad(dy.data_ptr(), x.data_ptr(), _ptr(offsets), dw.data_ptr(), slots,
-                                                    in_cols, out_cols, experts, _DTYPES[dy.dtype],
-                                                    _DTYPES.get(dw.dtype, -1), _current(dy)))
+    device = dy.get_device()
+    in_cols = _dims(_typed(x, "x", (dy.dtype,), None, device), "x", 2)[1]
+    if x.shape[0] != slots:
+        raise ValueError(f"x must have {slots} rows, got {x.shape[0]}")
+    experts = 1
+    if offsets is not None:
+        experts = _typed(offsets, "offsets", _INT, None, device).numel() - 1
+        _offsets(offsets, experts, device)
+    shape = (max(experts, 0), out_cols, in_cols)
+    if dw is None:
+        dw = torch.empty(shape, dtype=dy.dtype if dtype is None else dtype, device=dy.device)
+    else:
+        _typed(dw, "dw", (dy.dtype, torch.float32) if dtype is None else (dtype,), shape, device)
+    _check(library().rowops_expert_matmul_wgrad(dy.data_ptr(), x.data_ptr(), _ptr(offsets), dw.data_ptr(), slots,
+                                                in_cols, out_cols, experts, _DTYPES[dy.dtype],
+                                                _DTYPES.get(dw.dtype, -1), _raw_stream(device)))
     return dw
 
 
 def rowops_quantize_blocks(x, block_rows=1, q=None, scale=None, stream=None):
     """Returns (q, scale): e4m3 values of x (..., rows, cols) and an fp32 scale for each block of
     block_rows (1 or 128) rows by 128 columns, scale: (..., ceil(rows / block_rows), ceil(cols / 128))."""
-    x = _typed(x, "x", _FLOATS)
-    if x.dim() < 2:
+    _typed(x, "x", _FLOATS)
+    if _elsewhere(x, stream):
+        with _Placed(x, stream):
+            return rowops_quantize_blocks(x, block_rows, q, scale)
+    shape = x.shape
+    if len(shape) < 2:
         raise ValueError("x must have rows and columns")
-    rows, cols = x.shape[-2:]
-    batches = math.prod(x.shape[:-2])
-    if block_rows not in (1, 128):
+    if block_rows != 1 and block_rows != 128:
         raise ValueError("block_rows must be 1 or 128")
-    with _Placed(x, stream):
-        q = _given(q, "q", torch.float8_e4m3fn, x.shape, x)
-        scale = _given(scale, "scale", torch.float32,
-                       (*x.shape[:-2], -(-rows // block_rows), -(-cols // 128)), x)
-        _check(library().rowops_quantize_blocks(x.data_ptr(), q.data_ptr(), scale.data_ptr(), batches, rows, cols,
-                                                block_rows, _DTYPES[x.dtype], _current(x)))
+    rows, cols = shape[-2:]
+    device = x.get_device()
+    q = _given(q, "q", torch.float8_e4m3fn, shape, x, device)
+    scale = _given(scale, "scale", torch.float32, (*shape[:-2], -(-rows // block_rows), -(-cols // 128)), x, device)
+    _check(library().rowops_quantize_blocks(x.data_ptr(), q.data_ptr(), scale.data_ptr(), math.prod(shape[:-2]), rows,
+                                            cols, block_rows, _DTYPES[x.dtype], _raw_stream(device)))
     return q, scale
 
 
 def rowops_expert_matmul_fp8(xq, xs, wq, ws, offsets=None, y=None, dtype=torch.bfloat16, stream=None):
     """rowops_expert_matmul on e4m3 operands: xq (slots, in) with xs, wq (experts, out, in) with ws, as
     rowops_quantize_blocks gives them with block_rows 1 and 128; y of `dtype`."""
-    e4m3 = (torch.float8_e4m3fn,)
-    xq = _typed(xq, "xq", e4m3)
+    _typed(xq, "xq", _E4M3)
+    if _elsewhere(xq, stream):
+        with _Placed(xq, stream):
+            return rowops_expert_matmul_fp8(xq, xs, wq, ws, offsets, y, dtype)
     slots, in_cols = _dims(xq, "xq", 2)
-    wq = _typed(wq, "wq", e4m3, None, xq)
-    experts, out_cols, _ = _dims(wq, "wq", 3)
-    _typed(wq, "wq", e4m3, (experts, out_cols, in_cols))
-    kb = -(-in_cols // 128)
-    xs = _typed(xs, "xs", (torch.float32,), (slots, kb), xq)
-    ws = _typed(ws, "ws", (torch.float32,), (experts, -(-out_cols // 128), kb), xq)
-    offsets = _offsets(offsets, experts, xq)
-    if y is not None:
-        dtype = _typed(y, "y", _FLOATS, (slots, out_cols), xq).dtype
-    with _Placed(xq, stream):
-        y = _given(y, "y", dtype, (slots, out_cols), xq)
-        _check(library().rowops_expert_matmul_fp8(xq.data_ptr(), xs.data_ptr(), wq.data_ptr(), ws.data_ptr(),
-                                                  _ptr(offsets), y.data_ptr(), slots, in_cols, out_cols, experts,
-                                                  _DTYPES[dtype], _current(xq)))
+    device = xq.get_device()
+    experts, out_cols, k = _dims(_typed(wq, "wq", _E4M3, None, device), "wq", 3)
+    if k != in_cols:
+        raise ValueError(f"wq must take rows of {in_cols} values, got {tuple(wq.shape)}")
+    blocks = -(-in_cols // 128)
+    _typed(xs, "xs", _F32, (slots, blocks), device)
+    _typed(ws, "ws", _F32, (experts, -(-out_cols // 128), blocks), device)
+    _offsets(offsets, experts, device)
+    if y is None:
+        y = torch.empty((slots, out_cols), dtype=dtype, device=xq.device)
+    else:
+        _typed(y, "y", _FLOATS, (slots, out_cols), device)
+    _check(library().rowops_expert_matmul_fp8(xq.data_ptr(), xs.data_ptr(), wq.data_ptr(), ws.data_ptr(),
+                                              _ptr(offsets), y.data_ptr(), slots, in_cols, out_cols, experts,
+                                              _DTYPES.get(y.dtype, -1), _raw_stream(device)))
     return y
