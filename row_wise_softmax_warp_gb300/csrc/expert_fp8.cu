@@ -26,6 +26,7 @@
 #include <cuda_fp8.h>
 
 #include "groups.cuh"
+#include "row_store.cuh"
 #include "tensor_core.cuh"
 #include "types.cuh"
 
@@ -34,7 +35,7 @@ namespace {
 
 constexpr int kBlock = 128;                  // values of the sum per scale, and per stage
 constexpr int kTileRows = 256, kTileCols = 128;
-constexpr int kStages = 8;
+constexpr int kStages = 7;
 constexpr uint32_t kXBytes = 128 * 128, kWBytes = 64 * 128;  // a CTA's share of a stage
 constexpr uint32_t kStageBytes = kXBytes + kWBytes;
 constexpr int kBuffers = 4;                  // of a block's products in tensor memory
@@ -105,7 +106,8 @@ template <typename O>
 __global__ void __launch_bounds__(kThreads, 1) expert_product_fp8(const __grid_constant__ Fp8Args g) {
     extern __shared__ unsigned char raw[];
     unsigned char* stages = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
-    int* table = reinterpret_cast<int*>(stages + kStages * kStageBytes);
+    unsigned char* turn = stages + kStages * kStageBytes;
+    int* table = reinterpret_cast<int*>(turn + kAddWarps * kTurnBytes);
     __shared__ Fp8Shared sh;
     volatile int* abort_flag = &sh.abort;
 
@@ -272,24 +274,19 @@ __global__ void __launch_bounds__(kThreads, 1) expert_product_fp8(const __grid_c
                 }
             }
             if (!ok) break;
-            if (int(rank) * 128 + row < w.rows) {
-                const int64_t r = w.row0 + int(rank) * 128 + row;
-                O* p = static_cast<O*>(g.y) + r * g.out + w.col0 + c0;
-                const int cols = g.out - w.col0 - c0;  // that are there
-                if (g.vec) {  // out and y allow 16-byte stores
-                    constexpr int V = 16 / int(sizeof(O));
+            const auto sum = [&](int i) { return i & 1 ? acc[i / 2].y : acc[i / 2].x; };
+            const int top = (warp & 3) * 32, rows = w.rows - int(rank) * 128 - top;  // of this warp
+            const int cols = g.out - w.col0 - c0;                                   // that are there
+            O* p = static_cast<O*>(g.y) + (int64_t(w.row0) + rank * 128 + top) * g.out + w.col0 + c0;
+            if (g.vec) {  // out and y allow 16-byte stores
+                constexpr int kCols = 128 / int(sizeof(O));
 #pragma unroll
-                    for (int i = 0; i < kWarpColumns; i += V) {
-                        Chunk<O, V> o;
+                for (int c = 0; c < kWarpColumns; c += kCols)
+                    store_rows(turn + warp * kTurnBytes, p + c, g.out, rows, cols - c, [&](int i) { return sum(c + i); });
+            } else if (lane < rows) {
 #pragma unroll
-                        for (int v = 0; v < V; ++v) o.set(v, (i + v) & 1 ? acc[(i + v) / 2].y : acc[(i + v) / 2].x);
-                        if (i < cols) o.store(p + i);
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < kWarpColumns; ++i)
-                        if (i < cols) p[i] = from_float<O>(i & 1 ? acc[i / 2].y : acc[i / 2].x);
-                }
+                for (int i = 0; i < kWarpColumns; ++i)
+                    if (i < cols) p[int64_t(lane) * g.out + i] = from_float<O>(sum(i));
             }
             __syncwarp();
         }
@@ -303,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_product_fp8(const __grid_c
     if (warp == kProductWarp) tmem_dealloc_pair(tmem, kTmemColumns);
 }
 
-constexpr size_t kMostSmem = 1024 + kStages * size_t(kStageBytes) + (kMaxExperts + 1) * 4;
+constexpr size_t kMostSmem = 1024 + kStages * size_t(kStageBytes) + kAddWarps * kTurnBytes + (kMaxExperts + 1) * 4;
 
 }  // namespace
 

@@ -26,6 +26,7 @@
 // stop at a multiple of 16 rows, and the rows between are zeroed in shared
 // memory before them (both sides: 0 times a NaN is no zero).
 #include "groups.cuh"
+#include "row_store.cuh"
 #include "tensor_core.cuh"
 #include "types.cuh"
 
@@ -118,42 +119,55 @@ __device__ __forceinline__ void zero_ragged(unsigned char* stage, int sum, int w
     }
 }
 
-template <typename T, typename O, Form FORM>
-__device__ __forceinline__ void write_tile(const ProductArgs& g, const Tile& w, uint32_t tmem, int row, bool zero,
-                                           uint32_t free_bar) {
-    // row: the tile's row of this lane, as every epilogue lane has one
-    const int m = w.m0 + row, lane = threadIdx.x & 31;
-    for (int c = 0; c < w.n; c += 32) {
-        uint32_t r[32] = {};
-        if (!zero) {
-            tmem_load32(tmem + uint32_t(c), r);
-            tmem_wait_load(r);
-            if (c + 32 >= w.n) {  // the accumulators are free
-                tcgen05_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_pair(free_bar);
-            }
+// One warp's 32 rows of a tile in tensor memory, 32 columns at a time; after the
+// last load the buffer is given back.
+struct Source {
+    uint32_t tmem, free_bar;
+    bool zero;  // a sum of nothing: no buffer
+    __device__ __forceinline__ void load(int c, int width, uint32_t (&r)[32]) const {
+        if (zero) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) r[i] = 0;
+            return;
         }
+        tmem_load32(tmem + uint32_t(c), r);
+        tmem_wait_load(r);
+        if (c + 32 >= width) {
+            tcgen05_fence_before();
+            __syncwarp();
+            elect_arrive_pair(free_bar);
+        }
+    }
+};
+
+// kRows, kRowsT: a lane holds an output column and a register a row of y.
+template <typename O>
+__device__ __forceinline__ void write_rows(const ProductArgs& g, const Tile& w, const Source& from, int m) {
+    for (int c = 0; c < w.n; c += 32) {
+        uint32_t r[32];
+        from.load(c, w.n, r);
         if (m < g.m) {
-            if constexpr (FORM == kWeights) {
-                constexpr int V = 16 / int(sizeof(O));
-                O* p = static_cast<O*>(g.out) + (int64_t(w.expert) * g.m + m) * g.n + w.n0 + c;
+            O* p = static_cast<O*>(g.out) + int64_t(w.n0 + c) * g.m + m;
 #pragma unroll
-                for (int i = 0; i < 32; i += V) {
-                    if (c + i >= w.n) break;
-                    Chunk<O, V> o;
-#pragma unroll
-                    for (int v = 0; v < V; ++v) o.set(v, __uint_as_float(r[i + v]));
-                    o.store(p + i);
-                }
-            } else {
-                O* p = static_cast<O*>(g.out) + int64_t(w.n0 + c) * g.m + m;
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    if (c + i < w.n) p[int64_t(i) * g.m] = from_float<O>(__uint_as_float(r[i]));
-            }
+            for (int i = 0; i < 32; ++i)
+                if (c + i < w.n) p[int64_t(i) * g.m] = from_float<O>(__uint_as_float(r[i]));
         }
         __syncwarp();
+    }
+}
+
+// kWeights: a lane holds a row of dw.  m: the warp's first row.
+template <typename O>
+__device__ __forceinline__ void write_weights(const ProductArgs& g, const Tile& w, const Source& from, int m,
+                                              unsigned char* turn) {
+    constexpr int kCols = 128 / int(sizeof(O));
+    for (int c = 0; c < w.n; c += kCols) {
+        uint32_t r[kCols / 32][32];
+#pragma unroll
+        for (int h = 0; h < kCols / 32; ++h)
+            if (c + h * 32 < w.n) from.load(c + h * 32, w.n, r[h]);
+        store_rows(turn, static_cast<O*>(g.out) + (int64_t(w.expert) * g.m + m) * g.n + w.n0 + c, g.n, g.m - m,
+                   w.n - c, [&](int i) { return __uint_as_float(r[i / 32][i % 32]); });
     }
 }
 
@@ -162,7 +176,8 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
     expert_product(const __grid_constant__ ProductArgs g) {
     extern __shared__ unsigned char raw[];
     unsigned char* stages = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
-    int* table = reinterpret_cast<int*>(stages + kStages * kStageBytes);
+    unsigned char* turn = stages + kStages * kStageBytes;  // kWeights
+    int* table = reinterpret_cast<int*>(turn);              // the others
     __shared__ Shared sh;
     volatile int* abort_flag = &sh.abort;
 
@@ -305,16 +320,15 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
         uint32_t acc = 0;
         Tile w;
         for (int64_t t = first; tile_at<FORM>(g, table, t, w); t += step) {
-            const int row = int(rank) * 128 + warp * 32 + lane;
-            if (w.sum == 0) {
-                write_tile<T, O, FORM>(g, w, 0, row, true, 0);
-                continue;
-            }
-            if (!warp_wait(&sh.acc_full[acc & 1], (acc >> 1) & 1, abort_flag)) break;
+            const bool zero = uniform(w.sum) == 0;
+            if (!zero && !warp_wait(&sh.acc_full[acc & 1], (acc >> 1) & 1, abort_flag)) break;
             tcgen05_fence_after();
-            write_tile<T, O, FORM>(g, w, tmem + (uint32_t(warp * 32) << 16) + (acc & 1) * kTileN, row, false,
-                                   map_to_rank(&sh.acc_empty[acc & 1], 0));
-            ++acc;
+            const Source from{tmem + (uint32_t(warp * 32) << 16) + (acc & 1) * kTileN,
+                              map_to_rank(&sh.acc_empty[acc & 1], 0), zero};
+            const int m = w.m0 + int(rank) * 128 + warp * 32;
+            if constexpr (FORM == kWeights) write_weights<O>(g, w, from, m, turn + warp * kTurnBytes);
+            else write_rows<O>(g, w, from, m + lane);
+            if (!zero) ++acc;
         }
     }
     __syncwarp();
@@ -326,7 +340,8 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
     if (warp == kProductWarp) tmem_dealloc_pair(tmem, kTmemColumns);
 }
 
-constexpr size_t kMostSmem = 1024 + kStages * size_t(kStageBytes) + (kMaxExperts + 1) * 4;
+constexpr size_t kMostSmem = 1024 + kStages * size_t(kStageBytes) + 4 * kTurnBytes;
+static_assert(4 * kTurnBytes >= (kMaxExperts + 1) * 4, "the table of tiles lies where the others turn rows");
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
