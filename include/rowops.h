@@ -476,11 +476,22 @@ int rowops_expert_combine_bwd(const void *dout, const void *y, const int32_t *sl
  * ROWOPS_BF16.  offsets: experts + 1, or NULL with experts == 1 for one dense
  * product.  The gradient with respect to x is the same call on dy with the
  * other `transposed`.  in_cols == 0 or out_cols == 0 is ROWOPS_ERR_SHAPE.
- * Waits of the pipelined kernel are bounded: see rowops_pipeline_timeouts().
+ * The tensor cores' kernel reads matrices whose first value and rows lie on
+ * 16-byte boundaries.  For others give a workspace: they are copied there first
+ * (rowops_expert_matmul_workspace(...) bytes cover row widths that are no multiple
+ * of 8 values, and are 0 where all are).  Without one, or with too little, a slower
+ * kernel takes them as they are, so NULL and 0 are always allowed; a workspace
+ * that is not 16-byte aligned is ROWOPS_ERR_WORKSPACE.  Concurrent calls need
+ * separate workspaces.
+ * Waits of the pipelined kernel are bounded: one that runs out (a defect) leaves
+ * y incomplete and counts one timeout, see rowops_pipeline_timeouts().
  */
+size_t rowops_expert_matmul_workspace(int64_t slots, int64_t in_cols, int64_t out_cols,
+                                      int64_t experts, int transposed);
 int rowops_expert_matmul(const void *x, const void *w, const int32_t *offsets, void *y,
                          int64_t slots, int64_t in_cols, int64_t out_cols, int64_t experts,
-                         int transposed, int dtype, rowops_stream stream);
+                         int transposed, int dtype, void *workspace, size_t workspace_bytes,
+                         rowops_stream stream);
 
 /*
  * Gradient of rowops_expert_matmul with respect to the weights.
@@ -489,11 +500,13 @@ int rowops_expert_matmul(const void *x, const void *w, const int32_t *offsets, v
  * dy: slots x out_cols; x: slots x in_cols; both of `dtype` (ROWOPS_F16 or
  * ROWOPS_BF16); dw: experts x out_cols x in_cols of `dw_type`, which is `dtype`
  * or ROWOPS_F32.  For transposed weights swap dy and x (and their widths).
- * slots == 0 writes zeros.
+ * slots == 0 writes zeros.  Workspace and timeouts as for rowops_expert_matmul.
  */
+size_t rowops_expert_matmul_wgrad_workspace(int64_t slots, int64_t in_cols, int64_t out_cols);
 int rowops_expert_matmul_wgrad(const void *dy, const void *x, const int32_t *offsets, void *dw,
                                int64_t slots, int64_t in_cols, int64_t out_cols, int64_t experts,
-                               int dtype, int dw_type, rowops_stream stream);
+                               int dtype, int dw_type, void *workspace, size_t workspace_bytes,
+                               rowops_stream stream);
 
 /*
  * Quantises to e4m3 (four exponent bits, no infinity, largest value 448) with
@@ -516,12 +529,15 @@ int rowops_quantize_blocks(const void *x, uint8_t *q, float *scale, int64_t batc
  * xq: slots x in_cols with xs: slots x ceil(in_cols / 128); wq: experts x
  * out_cols x in_cols with ws: experts x ceil(out_cols / 128) x ceil(in_cols / 128),
  * as rowops_quantize_blocks writes them with block_rows 1 and 128; y: slots x
- * out_cols of y_type.  offsets as for rowops_expert_matmul.
+ * out_cols of y_type.  offsets, workspace (for in_cols that are no multiple of 16)
+ * and timeouts as for rowops_expert_matmul.
  */
+size_t rowops_expert_matmul_fp8_workspace(int64_t slots, int64_t in_cols, int64_t out_cols,
+                                          int64_t experts);
 int rowops_expert_matmul_fp8(const uint8_t *xq, const float *xs, const uint8_t *wq,
                              const float *ws, const int32_t *offsets, void *y, int64_t slots,
                              int64_t in_cols, int64_t out_cols, int64_t experts, int y_type,
-                             rowops_stream stream);
+                             void *workspace, size_t workspace_bytes, rowops_stream stream);
 
 #ifdef __cplusplus
 }

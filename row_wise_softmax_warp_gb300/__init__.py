@@ -20,7 +20,10 @@ from .binding import (  # noqa: F401
     rowops_expert_gather,
     rowops_expert_matmul,
     rowops_expert_matmul_fp8,
+    rowops_expert_matmul_fp8_workspace,
     rowops_expert_matmul_wgrad,
+    rowops_expert_matmul_wgrad_workspace,
+    rowops_expert_matmul_workspace,
     rowops_expert_plan,
     rowops_expert_plan_workspace,
     rowops_kernel_launches,

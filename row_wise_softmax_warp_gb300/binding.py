@@ -58,10 +58,15 @@ SIGNATURES = {
     "rowops_expert_gather": ([_P, _P, _P, _I64, _I64, _I64, _I64, _I, _I, _P], ctypes.c_int),
     "rowops_expert_combine": ([_P, _P, _P, _P, _I64, _I64, _I64, _I64, _I, _I, _P], ctypes.c_int),
     "rowops_expert_combine_bwd": ([_P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I, _I, _P], ctypes.c_int),
-    "rowops_expert_matmul": ([_P, _P, _P, _P, _I64, _I64, _I64, _I64, _I, _I, _P], ctypes.c_int),
-    "rowops_expert_matmul_wgrad": ([_P, _P, _P, _P, _I64, _I64, _I64, _I64, _I, _I, _P], ctypes.c_int),
+    "rowops_expert_matmul": ([_P, _P, _P, _P, _I64, _I64, _I64, _I64, _I, _I, _P, ctypes.c_size_t, _P], ctypes.c_int),
+    "rowops_expert_matmul_workspace": ([_I64, _I64, _I64, _I64, _I], ctypes.c_size_t),
+    "rowops_expert_matmul_wgrad": ([_P, _P, _P, _P, _I64, _I64, _I64, _I64, _I, _I, _P, ctypes.c_size_t, _P],
+                                   ctypes.c_int),
+    "rowops_expert_matmul_wgrad_workspace": ([_I64, _I64, _I64], ctypes.c_size_t),
+    "rowops_expert_matmul_fp8_workspace": ([_I64, _I64, _I64, _I64], ctypes.c_size_t),
     "rowops_quantize_blocks": ([_P, _P, _P, _I64, _I64, _I64, _I64, _I, _P], ctypes.c_int),
-    "rowops_expert_matmul_fp8": ([_P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I, _P], ctypes.c_int),
+    "rowops_expert_matmul_fp8": ([_P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I, _P, ctypes.c_size_t, _P],
+                                 ctypes.c_int),
 }
 
 
@@ -451,6 +456,15 @@ def _given(t, name: str, dtype, shape, like, device):
     return _typed(t, name, (dtype,), shape, device)
 
 
+def _scratch(workspace, need: int, like):
+    """(workspace, its bytes): the caller's, or a new one of `need` bytes where that is not 0."""
+    if workspace is not None:
+        if not isinstance(workspace, torch.Tensor) or workspace.device != like.device:
+            raise ValueError(f"workspace must be a tensor on {like.device}")
+        return workspace, workspace.numel() * workspace.element_size()
+    return (torch.empty(need, dtype=torch.uint8, device=like.device), need) if need else (None, 0)
+
+
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
@@ -479,17 +493,12 @@ def rowops_expert_plan(indices, experts, values=None, offsets=None, order=None, 
     if values is not None:
         _typed(values, "values", _F32, shape, device)
     lib = library()
-    pairs, size = rows * k, 0
+    pairs = rows * k
     need = lib.rowops_expert_plan_workspace(rows, k, experts)
     offsets = _given(offsets, "offsets", torch.int32, (max(experts, 0) + 1,), indices, device)
     order = _given(order, "order", torch.int32, (pairs,), indices, device)
     slot = _given(slot, "slot", torch.int32, shape, indices, device)
-    if workspace is not None:
-        if not isinstance(workspace, torch.Tensor) or workspace.device != indices.device:
-            raise ValueError(f"workspace must be a tensor on {indices.device}")
-        size = workspace.numel() * workspace.element_size()
-    elif need:
-        workspace, size = torch.empty(need, dtype=torch.uint8, device=indices.device), need
+    workspace, size = _scratch(workspace, need, indices)
     _check(lib.rowops_expert_plan(indices.data_ptr(), _ptr(values), offsets.data_ptr(), order.data_ptr(),
                                   slot.data_ptr(), rows, k, experts, _ptr(workspace), size, _raw_stream(device)))
     return offsets, order, slot
@@ -564,14 +573,27 @@ def _offsets(offsets, experts: int, device):
         raise ValueError("offsets may be None for one expert only")
 
 
-def rowops_expert_matmul(x, w, offsets=None, y=None, transposed=False, stream=None):
+def rowops_expert_matmul_workspace(slots: int, in_cols: int, out_cols: int, experts: int, transposed=False) -> int:
+    return int(library().rowops_expert_matmul_workspace(slots, in_cols, out_cols, experts, 1 if transposed else 0))
+
+
+def rowops_expert_matmul_wgrad_workspace(slots: int, in_cols: int, out_cols: int) -> int:
+    return int(library().rowops_expert_matmul_wgrad_workspace(slots, in_cols, out_cols))
+
+
+def rowops_expert_matmul_fp8_workspace(slots: int, in_cols: int, out_cols: int, experts: int) -> int:
+    return int(library().rowops_expert_matmul_fp8_workspace(slots, in_cols, out_cols, experts))
+
+
+def rowops_expert_matmul(x, w, offsets=None, y=None, transposed=False, workspace=None, stream=None):
     """y[s] = w[e] @ x[s] for the rows offsets[e] <= s < offsets[e + 1] of x (slots, in).
 
-    w: (experts, out, in), or (experts, in, out) with transposed.  Rows of a new y that no expert has are not written."""
+    w: (experts, out, in), or (experts, in, out) with transposed.  Rows of a new y that no expert has are not written.
+    A workspace (one is made where it is None) takes copies of matrices whose rows are no multiple of 16 bytes."""
     _typed(x, "x", _HALVES)
     if _elsewhere(x, stream):
         with _Placed(x, stream):
-            return rowops_expert_matmul(x, w, offsets, y, transposed)
+            return rowops_expert_matmul(x, w, offsets, y, transposed, workspace)
     slots, in_cols = _dims(x, "x", 2)
     device, dtype = x.get_device(), x.dtype
     experts, out_cols, k = _dims(_typed(w, "w", (dtype,), None, device), "w", 3)
@@ -581,18 +603,21 @@ def rowops_expert_matmul(x, w, offsets=None, y=None, transposed=False, stream=No
         raise ValueError(f"w must take rows of {in_cols} values, got {tuple(w.shape)}")
     _offsets(offsets, experts, device)
     y = _given(y, "y", dtype, (slots, out_cols), x, device)
-    _check(library().rowops_expert_matmul(x.data_ptr(), w.data_ptr(), _ptr(offsets), y.data_ptr(), slots, in_cols,
-                                          out_cols, experts, 1 if transposed else 0, _DTYPES[dtype],
-                                          _raw_stream(device)))
+    lib, flag = library(), 1 if transposed else 0
+    need = 0 if in_cols % 8 == 0 and out_cols % 8 == 0 else lib.rowops_expert_matmul_workspace(
+        slots, in_cols, out_cols, experts, flag)
+    workspace, size = _scratch(workspace, need, x)
+    _check(lib.rowops_expert_matmul(x.data_ptr(), w.data_ptr(), _ptr(offsets), y.data_ptr(), slots, in_cols, out_cols,
+                                    experts, flag, _DTYPES[dtype], _ptr(workspace), size, _raw_stream(device)))
     return y
 
 
-def rowops_expert_matmul_wgrad(dy, x, offsets=None, dw=None, dtype=None, stream=None):
+def rowops_expert_matmul_wgrad(dy, x, offsets=None, dw=None, dtype=None, workspace=None, stream=None):
     """dw[e] = sum over expert e's rows of dy[s]^T x[s]: (experts, out, in), of x's type or torch.float32."""
     _typed(dy, "dy", _HALVES)
     if _elsewhere(dy, stream):
         with _Placed(dy, stream):
-            return rowops_expert_matmul_wgrad(dy, x, offsets, dw, dtype)
+            return rowops_expert_matmul_wgrad(dy, x, offsets, dw, dtype, workspace)
     slots, out_cols = _dims(dy, "dy", 2)
     device = dy.get_device()
     in_cols = _dims(_typed(x, "x", (dy.dtype,), None, device), "x", 2)[1]
@@ -607,9 +632,11 @@ def rowops_expert_matmul_wgrad(dy, x, offsets=None, dw=None, dtype=None, stream=
         dw = torch.empty(shape, dtype=dy.dtype if dtype is None else dtype, device=dy.device)
     else:
         _typed(dw, "dw", (dy.dtype, torch.float32) if dtype is None else (dtype,), shape, device)
-    _check(library().rowops_expert_matmul_wgrad(dy.data_ptr(), x.data_ptr(), _ptr(offsets), dw.data_ptr(), slots,
-                                                in_cols, out_cols, experts, _DTYPES[dy.dtype],
-                                                _DTYPES.get(dw.dtype, -1), _raw_stream(device)))
+    lib = library()
+    workspace, size = _scratch(workspace, lib.rowops_expert_matmul_wgrad_workspace(slots, in_cols, out_cols), dy)
+    _check(lib.rowops_expert_matmul_wgrad(dy.data_ptr(), x.data_ptr(), _ptr(offsets), dw.data_ptr(), slots, in_cols,
+                                          out_cols, experts, _DTYPES[dy.dtype], _DTYPES.get(dw.dtype, -1),
+                                          _ptr(workspace), size, _raw_stream(device)))
     return dw
 
 
@@ -634,13 +661,13 @@ def rowops_quantize_blocks(x, block_rows=1, q=None, scale=None, stream=None):
     return q, scale
 
 
-def rowops_expert_matmul_fp8(xq, xs, wq, ws, offsets=None, y=None, dtype=torch.bfloat16, stream=None):
+def rowops_expert_matmul_fp8(xq, xs, wq, ws, offsets=None, y=None, dtype=torch.bfloat16, workspace=None, stream=None):
     """rowops_expert_matmul on e4m3 operands: xq (slots, in) with xs, wq (experts, out, in) with ws, as
     rowops_quantize_blocks gives them with block_rows 1 and 128; y of `dtype`."""
     _typed(xq, "xq", _E4M3)
     if _elsewhere(xq, stream):
         with _Placed(xq, stream):
-            return rowops_expert_matmul_fp8(xq, xs, wq, ws, offsets, y, dtype)
+            return rowops_expert_matmul_fp8(xq, xs, wq, ws, offsets, y, dtype, workspace)
     slots, in_cols = _dims(xq, "xq", 2)
     device = xq.get_device()
     experts, out_cols, k = _dims(_typed(wq, "wq", _E4M3, None, device), "wq", 3)
@@ -654,7 +681,10 @@ def rowops_expert_matmul_fp8(xq, xs, wq, ws, offsets=None, y=None, dtype=torch.b
         y = torch.empty((slots, out_cols), dtype=dtype, device=xq.device)
     else:
         _typed(y, "y", _FLOATS, (slots, out_cols), device)
-    _check(library().rowops_expert_matmul_fp8(xq.data_ptr(), xs.data_ptr(), wq.data_ptr(), ws.data_ptr(),
-                                              _ptr(offsets), y.data_ptr(), slots, in_cols, out_cols, experts,
-                                              _DTYPES.get(y.dtype, -1), _raw_stream(device)))
+    lib = library()
+    workspace, size = _scratch(
+        workspace, lib.rowops_expert_matmul_fp8_workspace(slots, in_cols, out_cols, experts), xq)
+    _check(lib.rowops_expert_matmul_fp8(xq.data_ptr(), xs.data_ptr(), wq.data_ptr(), ws.data_ptr(), _ptr(offsets),
+                                        y.data_ptr(), slots, in_cols, out_cols, experts, _DTYPES.get(y.dtype, -1),
+                                        _ptr(workspace), size, _raw_stream(device)))
     return y

@@ -470,15 +470,41 @@ int check_token_rows(int64_t rows, int64_t k, int64_t cols, int64_t slots, int a
 }
 
 // Sizes of the experts' products.  Every matrix has at most 2^60 elements.
-int check_product(const int32_t* offsets, int64_t slots, int64_t in_cols, int64_t out_cols, int64_t experts) {
+int check_sizes(int64_t slots, int64_t in_cols, int64_t out_cols, int64_t experts) {
     if (slots < 0 || slots > kMaxSlots || experts < 1 || experts > kMaxExperts) return ROWOPS_ERR_SHAPE;
     if (in_cols < 1 || out_cols < 1 || in_cols > INT32_MAX - 256 || out_cols > INT32_MAX - 256) return ROWOPS_ERR_SHAPE;
     if (int e = check_dims(slots, in_cols)) return e;
     if (int e = check_dims(slots, out_cols)) return e;
-    if (int e = check_dims(experts * out_cols, in_cols)) return e;
+    return check_dims(experts * out_cols, in_cols);
+}
+int check_product(const int32_t* offsets, int64_t slots, int64_t in_cols, int64_t out_cols, int64_t experts) {
+    if (int e = check_sizes(slots, in_cols, out_cols, experts)) return e;
     if (offsets == nullptr && experts != 1) return ROWOPS_ERR_NULL;
     return ROWOPS_OK;
 }
+
+// A workspace that may be missing.
+int check_workspace(const void* ws, size_t bytes, std::initializer_list<Buf> others) {
+    if (ws == nullptr || bytes == 0) return ROWOPS_OK;
+    if (!aligned(ws, 16)) return ROWOPS_ERR_WORKSPACE;
+    for (const Buf& b : others)
+        if (overlap({ws, int64_t(bytes)}, b)) return ROWOPS_ERR_ALIAS;
+    return ROWOPS_OK;
+}
+
+// 16-byte aligned part of a workspace that starts on the next 256-byte boundary.
+rowops::Scratch scratch_of(void* ws, size_t bytes) {
+    if (ws == nullptr) return {nullptr, 0};
+    const size_t skip = (256 - (reinterpret_cast<uintptr_t>(ws) & 255)) & 255;
+    if (bytes < skip) return {nullptr, 0};
+    return {static_cast<char*>(ws) + skip, bytes - skip};
+}
+
+// Bytes for a copy of a matrix whose rows are no multiple of 16 bytes, 0 for others.
+size_t copy_bytes(int64_t rows, int64_t row_bytes) {
+    return row_bytes % 16 == 0 ? 0 : rowops::repack_bytes(rows, row_bytes);
+}
+size_t with_slack(size_t bytes) { return bytes ? bytes + 256 : 0; }
 
 }  // namespace
 
@@ -547,9 +573,16 @@ int rowops_expert_combine_bwd(const void* dout, const void* y, const int32_t* sl
                                                        out_type, y_type, st(stream)));
 }
 
+size_t rowops_expert_matmul_workspace(int64_t slots, int64_t in_cols, int64_t out_cols, int64_t experts,
+                                      int transposed) {
+    if (slots <= 0 || check_sizes(slots, in_cols, out_cols, experts)) return 0;
+    return with_slack(copy_bytes(slots, in_cols * 2) + (transposed ? copy_bytes(experts * in_cols, out_cols * 2)
+                                                                   : copy_bytes(experts * out_cols, in_cols * 2)));
+}
+
 int rowops_expert_matmul(const void* x, const void* w, const int32_t* offsets, void* y, int64_t slots,
                          int64_t in_cols, int64_t out_cols, int64_t experts, int transposed, int dtype,
-                         rowops_stream stream) {
+                         void* workspace, size_t workspace_bytes, rowops_stream stream) {
     if (!half_type(dtype)) return ROWOPS_ERR_SHAPE;
     if (int e = check_product(offsets, slots, in_cols, out_cols, experts)) return e;
     if (slots == 0) return ROWOPS_OK;
@@ -559,13 +592,21 @@ int rowops_expert_matmul(const void* x, const void* w, const int32_t* offsets, v
     if (int e = check_overlap({{x, slots * in_cols * 2}, {w, wb}, {offsets, (experts + 1) * 4}},
                               {{y, slots * out_cols * 2}}))
         return e;
+    if (int e = check_workspace(workspace, workspace_bytes,
+                                {{x, slots * in_cols * 2}, {w, wb}, {offsets, (experts + 1) * 4}, {y, slots * out_cols * 2}}))
+        return e;
     return to_status(rowops::launch_expert_matmul(x, w, offsets, y, slots, in_cols, out_cols, experts, transposed != 0,
-                                                  dtype, st(stream)));
+                                                  dtype, scratch_of(workspace, workspace_bytes), st(stream)));
+}
+
+size_t rowops_expert_matmul_wgrad_workspace(int64_t slots, int64_t in_cols, int64_t out_cols) {
+    if (slots <= 0 || check_sizes(slots, in_cols, out_cols, 1)) return 0;
+    return with_slack(copy_bytes(slots, out_cols * 2) + copy_bytes(slots, in_cols * 2));
 }
 
 int rowops_expert_matmul_wgrad(const void* dy, const void* x, const int32_t* offsets, void* dw, int64_t slots,
                                int64_t in_cols, int64_t out_cols, int64_t experts, int dtype, int dw_type,
-                               rowops_stream stream) {
+                               void* workspace, size_t workspace_bytes, rowops_stream stream) {
     if (!half_type(dtype) || (dw_type != dtype && dw_type != ROWOPS_F32)) return ROWOPS_ERR_SHAPE;
     if (int e = check_product(offsets, slots, in_cols, out_cols, experts)) return e;
     if ((slots && (!dy || !x)) || !dw) return ROWOPS_ERR_NULL;
@@ -574,8 +615,12 @@ int rowops_expert_matmul_wgrad(const void* dy, const void* x, const int32_t* off
     if (int e = check_overlap({{dy, slots * out_cols * 2}, {x, slots * in_cols * 2}, {offsets, (experts + 1) * 4}},
                               {{dw, wb}}))
         return e;
+    if (int e = check_workspace(
+            workspace, workspace_bytes,
+            {{dy, slots * out_cols * 2}, {x, slots * in_cols * 2}, {offsets, (experts + 1) * 4}, {dw, wb}}))
+        return e;
     return to_status(rowops::launch_expert_matmul_wgrad(dy, x, offsets, dw, slots, in_cols, out_cols, experts, dtype,
-                                                        dw_type, st(stream)));
+                                                        dw_type, scratch_of(workspace, workspace_bytes), st(stream)));
 }
 
 int rowops_quantize_blocks(const void* x, uint8_t* q, float* scale, int64_t batches, int64_t rows, int64_t cols,
@@ -596,9 +641,15 @@ int rowops_quantize_blocks(const void* x, uint8_t* q, float* scale, int64_t batc
         rowops::launch_quantize_blocks(x, q, scale, batches, rows, cols, block_rows, x_type, st(stream)));
 }
 
+size_t rowops_expert_matmul_fp8_workspace(int64_t slots, int64_t in_cols, int64_t out_cols, int64_t experts) {
+    if (slots <= 0 || check_sizes(slots, in_cols, out_cols, experts)) return 0;
+    return with_slack(copy_bytes(slots, in_cols) + copy_bytes(experts * out_cols, in_cols));
+}
+
 int rowops_expert_matmul_fp8(const uint8_t* xq, const float* xs, const uint8_t* wq, const float* ws,
                              const int32_t* offsets, void* y, int64_t slots, int64_t in_cols, int64_t out_cols,
-                             int64_t experts, int y_type, rowops_stream stream) {
+                             int64_t experts, int y_type, void* workspace, size_t workspace_bytes,
+                             rowops_stream stream) {
     if (!any_type(y_type)) return ROWOPS_ERR_SHAPE;
     if (int e = check_product(offsets, slots, in_cols, out_cols, experts)) return e;
     if (slots == 0) return ROWOPS_OK;
@@ -606,15 +657,12 @@ int rowops_expert_matmul_fp8(const uint8_t* xq, const float* xs, const uint8_t* 
     const int64_t yb = type_bytes(y_type);
     if (!elems_aligned({{xs, 4}, {ws, 4}, {offsets, 4}, {y, yb}})) return ROWOPS_ERR_ALIGN;
     const int64_t kb = (in_cols + 127) / 128, nb = (out_cols + 127) / 128;
-    if (int e = check_overlap({{xq, slots * in_cols},
-                               {xs, slots * kb * 4},
-                               {wq, experts * out_cols * in_cols},
-                               {ws, experts * nb * kb * 4},
-                               {offsets, (experts + 1) * 4}},
-                              {{y, slots * out_cols * yb}}))
-        return e;
+    const Buf bx{xq, slots * in_cols}, bxs{xs, slots * kb * 4}, bw{wq, experts * out_cols * in_cols},
+        bws{ws, experts * nb * kb * 4}, bo{offsets, (experts + 1) * 4}, by{y, slots * out_cols * yb};
+    if (int e = check_overlap({bx, bxs, bw, bws, bo}, {by})) return e;
+    if (int e = check_workspace(workspace, workspace_bytes, {bx, bxs, bw, bws, bo, by})) return e;
     return to_status(rowops::launch_expert_matmul_fp8(xq, xs, wq, ws, offsets, y, slots, in_cols, out_cols, experts,
-                                                      y_type, st(stream)));
+                                                      y_type, scratch_of(workspace, workspace_bytes), st(stream)));
 }
 
 }  // extern "C"

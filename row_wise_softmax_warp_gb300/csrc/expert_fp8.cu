@@ -57,7 +57,7 @@ struct Fp8Args {
     void* y;
     int slots, experts;
     int in, out;
-    bool vec;
+    bool vec;  // rows of y allow 16-byte stores
 };
 
 struct Fp8Shared {
@@ -278,16 +278,11 @@ __global__ void __launch_bounds__(kThreads, 1) expert_product_fp8(const __grid_c
             const int top = (warp & 3) * 32, rows = w.rows - int(rank) * 128 - top;  // of this warp
             const int cols = g.out - w.col0 - c0;                                   // that are there
             O* p = static_cast<O*>(g.y) + (int64_t(w.row0) + rank * 128 + top) * g.out + w.col0 + c0;
-            if (g.vec) {  // out and y allow 16-byte stores
-                constexpr int kCols = 128 / int(sizeof(O));
+            constexpr int kCols = 128 / int(sizeof(O));
 #pragma unroll
-                for (int c = 0; c < kWarpColumns; c += kCols)
-                    store_rows(turn + warp * kTurnBytes, p + c, g.out, rows, cols - c, [&](int i) { return sum(c + i); });
-            } else if (lane < rows) {
-#pragma unroll
-                for (int i = 0; i < kWarpColumns; ++i)
-                    if (i < cols) p[int64_t(lane) * g.out + i] = from_float<O>(sum(i));
-            }
+            for (int c = 0; c < kWarpColumns; c += kCols)
+                store_rows(turn + warp * kTurnBytes, p + c, g.out, rows, cols - c, g.vec,
+                           [&](int i) { return sum(c + i); });
             __syncwarp();
         }
     }
@@ -308,15 +303,17 @@ uint32_t pipeline_timeouts_fp8() { return read_pipeline_timeouts(); }
 
 cudaError_t launch_expert_matmul_fp8(const uint8_t* x, const float* x_scale, const uint8_t* w, const float* w_scale,
                                      const int32_t* offsets, void* y, int64_t slots, int64_t in, int64_t out,
-                                     int64_t experts, int y_type, cudaStream_t stream) {
-    const bool aligned = in % 16 == 0 && (reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(w)) % 16 == 0;
-    if (!aligned)
+                                     int64_t experts, int y_type, Scratch scratch, cudaStream_t stream) {
+    Matrix mx = matrix_of(x, in, slots, 1, 1), mw = matrix_of(w, in, out, experts, 1);
+    Matrix* ms[2] = {&mx, &mw};
+    cudaError_t err;
+    if (!make_readable(ms, {false, true}, offsets, slots, scratch, stream, &err))
         return launch_matmul_fp8_any(x, x_scale, w, w_scale, offsets, y, slots, in, out, experts, y_type, stream);
+    if (err != cudaSuccess) return err;
     const CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_UINT8;
     Fp8Args g;
-    if (!make_map(&g.w, type, 1, w, in, out, experts, kBlock, 64, true) ||
-        !make_map(&g.x, type, 1, x, in, slots, 1, kBlock, 128, false) ||
-        !make_map(&g.x_small, type, 1, x, in, slots, 1, kBlock, 16, false))
+    if (!make_map(&g.w, type, mw, kBlock, 64, true) || !make_map(&g.x, type, mx, kBlock, 128, false) ||
+        !make_map(&g.x_small, type, mx, kBlock, 16, false))
         return cudaErrorInvalidValue;
     g.xs = x_scale;
     g.ws = w_scale;

@@ -34,6 +34,8 @@ namespace rowops {
 namespace {
 
 enum Form { kRows, kRowsT, kWeights };
+template <Form F>
+using FormOf = std::integral_constant<Form, F>;
 
 constexpr int kTileN = kMostRows;              // most columns of a tile
 constexpr int kStepK = 64;                     // of the sum per stage
@@ -55,6 +57,7 @@ struct ProductArgs {
     int slots, experts;
     int m, n, k;  // kRows*: m output width, k input width.  kWeights: dw is m x n
     uint32_t format;  // operand format code
+    bool vec;         // kWeights: rows of dw allow 16-byte stores
 };
 
 struct Shared {
@@ -167,7 +170,7 @@ __device__ __forceinline__ void write_weights(const ProductArgs& g, const Tile& 
         for (int h = 0; h < kCols / 32; ++h)
             if (c + h * 32 < w.n) from.load(c + h * 32, w.n, r[h]);
         store_rows(turn, static_cast<O*>(g.out) + (int64_t(w.expert) * g.m + m) * g.n + w.n0 + c, g.n, g.m - m,
-                   w.n - c, [&](int i) { return __uint_as_float(r[i / 32][i % 32]); });
+                   w.n - c, g.vec, [&](int i) { return __uint_as_float(r[i / 32][i % 32]); });
     }
 }
 
@@ -343,24 +346,25 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
 constexpr size_t kMostSmem = 1024 + kStages * size_t(kStageBytes) + 4 * kTurnBytes;
 static_assert(4 * kTurnBytes >= (kMaxExperts + 1) * 4, "the table of tiles lies where the others turn rows");
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
-
 }  // namespace
 
 uint32_t pipeline_timeouts_matmul() { return read_pipeline_timeouts(); }
 
 cudaError_t launch_expert_matmul(const void* x, const void* w, const int32_t* offsets, void* y, int64_t slots,
                                  int64_t in, int64_t out, int64_t experts, bool transposed, int dtype,
-                                 cudaStream_t stream) {
-    if (in % 8 != 0 || (transposed && out % 8 != 0) || !aligned16(x) || !aligned16(w))
+                                 Scratch scratch, cudaStream_t stream) {
+    Matrix mx = matrix_of(x, in, slots, 1, 2);
+    Matrix mw = matrix_of(w, transposed ? out : in, transposed ? in : out, experts, 2);
+    Matrix* ms[2] = {&mx, &mw};
+    cudaError_t err;
+    if (!make_readable(ms, {false, true}, offsets, slots, scratch, stream, &err))
         return launch_matmul_any(x, w, offsets, y, slots, in, out, experts, transposed, dtype, stream);
+    if (err != cudaSuccess) return err;
     const CUtensorMapDataType type =
         dtype == ROWOPS_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     ProductArgs g;
-    if (!make_map(&g.a, type, 2, w, transposed ? out : in, transposed ? in : out, experts, 64, transposed ? 64 : 128,
-                  true) ||
-        !make_map(&g.b, type, 2, x, in, slots, 1, 64, 128, false) ||
-        !make_map(&g.b_small, type, 2, x, in, slots, 1, 64, 16, false))
+    if (!make_map(&g.a, type, mw, 64, transposed ? 64 : 128, true) || !make_map(&g.b, type, mx, 64, 128, false) ||
+        !make_map(&g.b_small, type, mx, 64, 16, false))
         return cudaErrorInvalidValue;
     g.offsets = offsets;
     g.out = y;
@@ -370,27 +374,32 @@ cudaError_t launch_expert_matmul(const void* x, const void* w, const int32_t* of
     g.n = 0;
     g.k = int(in);
     g.format = dtype == ROWOPS_F16 ? 0 : 1;
+    g.vec = false;
     const int64_t tiles = most_row_tiles(slots, experts) * ((out + 255) / 256);
-    const size_t smem = kMostSmem;
-    if (dtype == ROWOPS_F16)
-        return transposed ? launch_pairs<expert_product<__half, __half, kRowsT>>(tiles, threads_of(kRowsT), smem, stream, g)
-                          : launch_pairs<expert_product<__half, __half, kRows>>(tiles, threads_of(kRows), smem, stream, g);
-    return transposed
-               ? launch_pairs<expert_product<__nv_bfloat16, __nv_bfloat16, kRowsT>>(tiles, threads_of(kRowsT), smem, stream, g)
-               : launch_pairs<expert_product<__nv_bfloat16, __nv_bfloat16, kRows>>(tiles, threads_of(kRows), smem, stream, g);
+    auto go = [&](auto t, auto form) {
+        using T = decltype(t);
+        constexpr Form kForm = decltype(form)::value;
+        return launch_pairs<expert_product<T, T, kForm>>(tiles, threads_of(kForm), kMostSmem, stream, g);
+    };
+    if (dtype == ROWOPS_F16) return transposed ? go(__half{}, FormOf<kRowsT>{}) : go(__half{}, FormOf<kRows>{});
+    return transposed ? go(__nv_bfloat16{}, FormOf<kRowsT>{}) : go(__nv_bfloat16{}, FormOf<kRows>{});
 }
 
 cudaError_t launch_expert_matmul_wgrad(const void* dy, const void* x, const int32_t* offsets, void* dw,
                                        int64_t slots, int64_t in, int64_t out, int64_t experts, int dtype,
-                                       int dw_type, cudaStream_t stream) {
-    if (slots == 0) return cudaMemsetAsync(dw, 0, size_t(experts) * out * in * (dw_type == ROWOPS_F32 ? 4 : 2), stream);
-    if (in % 8 != 0 || out % 8 != 0 || !aligned16(x) || !aligned16(dy) || !aligned16(dw))
+                                       int dw_type, Scratch scratch, cudaStream_t stream) {
+    const int dw_size = dw_type == ROWOPS_F32 ? 4 : 2;
+    if (slots == 0) return cudaMemsetAsync(dw, 0, size_t(experts) * out * in * dw_size, stream);
+    Matrix mdy = matrix_of(dy, out, slots, 1, 2), mx = matrix_of(x, in, slots, 1, 2);
+    Matrix* ms[2] = {&mdy, &mx};
+    cudaError_t err;
+    if (!make_readable(ms, {false, false}, offsets, slots, scratch, stream, &err))
         return launch_matmul_wgrad_any(dy, x, offsets, dw, slots, in, out, experts, dtype, dw_type, stream);
+    if (err != cudaSuccess) return err;
     const CUtensorMapDataType type =
         dtype == ROWOPS_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     ProductArgs g;
-    if (!make_map(&g.a, type, 2, dy, out, slots, 1, 64, 64, false) ||
-        !make_map(&g.b, type, 2, x, in, slots, 1, 64, 64, false))
+    if (!make_map(&g.a, type, mdy, 64, 64, false) || !make_map(&g.b, type, mx, 64, 64, false))
         return cudaErrorInvalidValue;
     g.b_small = g.b;
     g.offsets = offsets;
@@ -401,16 +410,14 @@ cudaError_t launch_expert_matmul_wgrad(const void* dy, const void* x, const int3
     g.n = int(in);
     g.k = 0;
     g.format = dtype == ROWOPS_F16 ? 0 : 1;
+    g.vec = in * dw_size % 16 == 0 && reinterpret_cast<uintptr_t>(dw) % 16 == 0;
     const int64_t tiles = experts * ((out + 255) / 256) * ((in + kTileN - 1) / kTileN);
-    const size_t smem = kMostSmem;
-    if (dtype == ROWOPS_F16)
-        return dw_type == ROWOPS_F32
-                   ? launch_pairs<expert_product<__half, float, kWeights>>(tiles, threads_of(kWeights), smem, stream, g)
-                   : launch_pairs<expert_product<__half, __half, kWeights>>(tiles, threads_of(kWeights), smem, stream, g);
-    return dw_type == ROWOPS_F32
-               ? launch_pairs<expert_product<__nv_bfloat16, float, kWeights>>(tiles, threads_of(kWeights), smem, stream, g)
-               : launch_pairs<expert_product<__nv_bfloat16, __nv_bfloat16, kWeights>>(tiles, threads_of(kWeights), smem,
-                                                                                      stream, g);
+    auto go = [&](auto t, auto o) {
+        return launch_pairs<expert_product<decltype(t), decltype(o), kWeights>>(tiles, threads_of(kWeights), kMostSmem,
+                                                                                stream, g);
+    };
+    if (dtype == ROWOPS_F16) return dw_type == ROWOPS_F32 ? go(__half{}, float{}) : go(__half{}, __half{});
+    return dw_type == ROWOPS_F32 ? go(__nv_bfloat16{}, float{}) : go(__nv_bfloat16{}, __nv_bfloat16{});
 }
 
 }  // namespace rowops

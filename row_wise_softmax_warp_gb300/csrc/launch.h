@@ -219,16 +219,41 @@ cudaError_t launch_expert_combine_bwd(const void* dout, const void* y, const int
                                       int64_t slots, int out_type, int y_type, cudaStream_t stream);
 cudaError_t launch_quantize_blocks(const void* x, uint8_t* q, float* scale, int64_t batches, int64_t rows,
                                    int64_t cols, int64_t block_rows, int x_type, cudaStream_t stream);
+// Scratch memory of one call: `take` gives 256-byte aligned parts of it in turn.
+struct Scratch {
+    void* p;
+    size_t bytes;
+    void* take(size_t n) {
+        n = (n + 255) & ~size_t(255);
+        if (p == nullptr || n > bytes) return nullptr;
+        void* part = p;
+        p = static_cast<char*>(p) + n;
+        bytes -= n;
+        return part;
+    }
+};
+
+// Rows copied to rows on 16-byte boundaries.  rows_per_expert > 0: rows of
+// experts without a group in `offsets` may be left out.
+struct RepackJob {
+    const void* src;
+    void* dst;
+    int64_t rows, row_bytes, rows_per_expert;
+};
+__host__ __device__ inline int64_t repack_pitch(int64_t row_bytes) { return (row_bytes + 15) & ~int64_t(15); }
+inline size_t repack_bytes(int64_t rows, int64_t row_bytes) { return size_t(rows * repack_pitch(row_bytes) + 255) & ~size_t(255); }
+cudaError_t launch_repack(const RepackJob* jobs, int n, const int32_t* offsets, int64_t slots, cudaStream_t stream);
+
 cudaError_t launch_expert_matmul(const void* x, const void* w, const int32_t* offsets, void* y, int64_t slots,
                                  int64_t in, int64_t out, int64_t experts, bool transposed, int dtype,
-                                 cudaStream_t stream);
+                                 Scratch scratch, cudaStream_t stream);
 cudaError_t launch_expert_matmul_wgrad(const void* dy, const void* x, const int32_t* offsets, void* dw,
                                        int64_t slots, int64_t in, int64_t out, int64_t experts, int dtype,
-                                       int dw_type, cudaStream_t stream);
+                                       int dw_type, Scratch scratch, cudaStream_t stream);
 cudaError_t launch_expert_matmul_fp8(const uint8_t* x, const float* x_scale, const uint8_t* w, const float* w_scale,
                                      const int32_t* offsets, void* y, int64_t slots, int64_t in, int64_t out,
-                                     int64_t experts, int y_type, cudaStream_t stream);
-// The same products for matrices of any alignment.
+                                     int64_t experts, int y_type, Scratch scratch, cudaStream_t stream);
+// The same products for matrices of any alignment, without scratch memory.
 cudaError_t launch_matmul_any(const void* x, const void* w, const int32_t* offsets, void* y, int64_t slots,
                               int64_t in, int64_t out, int64_t experts, bool transposed, int dtype,
                               cudaStream_t stream);

@@ -1,0 +1,88 @@
+// repack.cu - rows that start on any byte copied to rows that start on 16-byte
+// boundaries, so that TMA can read them (an in-width of 773 values of 2 bytes, say).
+//
+// A warp takes a row; a lane makes 16 bytes of the copy from five aligned 4-byte
+// words, shifted together.  Bound by HBM: every byte is read and written once (8 experts of 2003 x
+// 1001 fp16 and 8192 rows of 1001: REPACK_US us, REPACK_GBS GB/s).  What lies between a
+// row's end and the next boundary is whatever the source holds there; the tensor
+// map over the copy ends at the row's true width.
+#include "groups.cuh"
+#include "launch.h"
+
+namespace rowops {
+namespace {
+
+constexpr int kRepackThreads = 256;
+
+constexpr int kRepackRows = 4;  // of a warp, one after another
+
+struct RepackArgs {
+    RepackJob job[2];
+    const int32_t* offsets;
+    int slots;
+};
+
+// The aligned word at `at`, of whose bytes those in [begin, end) are there.
+__device__ __forceinline__ uint32_t word_at(const uint8_t* at, const uint8_t* begin, const uint8_t* end) {
+    if (at >= begin && at + 4 <= end) return __ldg(reinterpret_cast<const uint32_t*>(at));
+    uint32_t w = 0;
+    for (int i = 0; i < 4; ++i)
+        if (at + i >= begin && at + i < end) w |= uint32_t(at[i]) << (8 * i);
+    return w;
+}
+
+__global__ void __launch_bounds__(kRepackThreads) repack(const RepackArgs g) {
+    const int lane = threadIdx.x & 31;
+    const int64_t first = (int64_t(blockIdx.x) * (kRepackThreads / 32) + (threadIdx.x >> 5)) * kRepackRows;
+    for (int64_t r = first; r < first + kRepackRows; ++r) {
+        const bool second = r >= g.job[0].rows;
+        const RepackJob& j = g.job[second];
+        const int64_t row = second ? r - g.job[0].rows : r;
+        if (row >= j.rows) return;
+        // a matrix of weights whose expert has no rows is not read later either
+        if (j.rows_per_expert > 0 && g.offsets != nullptr &&
+            group_rows(g.offsets, int(uint32_t(row) / uint32_t(j.rows_per_expert)), g.slots).count == 0)
+            continue;
+        const uint8_t* begin = static_cast<const uint8_t*>(j.src);
+        const uint8_t* end = begin + j.rows * j.row_bytes;
+        const uint8_t* from = begin + row * j.row_bytes;
+        const int off = int(reinterpret_cast<uintptr_t>(from) & 3);
+        from -= off;
+        uint8_t* to = static_cast<uint8_t*>(j.dst) + row * repack_pitch(j.row_bytes);
+        constexpr int U = 4;
+        for (int64_t c0 = lane * 16; c0 < j.row_bytes; c0 += U * 512) {
+            uint32_t w[U][5];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (c0 + u * 512 < j.row_bytes)
+#pragma unroll
+                    for (int i = 0; i < 5; ++i) w[u][i] = word_at(from + c0 + u * 512 + 4 * i, begin, end);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (c0 + u * 512 >= j.row_bytes) break;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) w[u][i] = __funnelshift_r(w[u][i], w[u][i + 1], 8 * off);
+                *reinterpret_cast<uint4*>(to + c0 + u * 512) = make_uint4(w[u][0], w[u][1], w[u][2], w[u][3]);
+            }
+        }
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_repack(const RepackJob* jobs, int n, const int32_t* offsets, int64_t slots, cudaStream_t stream) {
+    RepackArgs g = {};
+    int64_t rows = 0;
+    for (int i = 0; i < n; ++i) {
+        g.job[i] = jobs[i];
+        rows += jobs[i].rows;
+    }
+    g.offsets = offsets;
+    g.slots = int(slots);
+    constexpr int64_t per = kRepackThreads / 32 * kRepackRows;
+    repack<<<unsigned((rows + per - 1) / per), kRepackThreads, 0, stream>>>(g);
+    note_launches(1);
+    return cudaGetLastError();
+}
+
+}  // namespace rowops

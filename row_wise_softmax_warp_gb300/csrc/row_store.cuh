@@ -13,10 +13,11 @@ namespace rowops {
 constexpr int kTurnBytes = 32 * 128;  // of shared memory per warp, 16-byte aligned
 
 // One warp writes 128 bytes (COLS values) of 32 rows: lane i holds row i's values
-// v(0) .. v(COLS - 1).  p: first value of row 0; pitch: values from row to row;
-// rows, cols: what is there (cols a multiple of 16 bytes, p and pitch 16-byte aligned).
+// v(0) .. v(COLS - 1).  p: first value of row 0; pitch: values from row to row; rows,
+// cols: what is there.  vec: p, pitch and cols are multiples of 16 bytes; else the
+// lines are written value by value.
 template <typename O, typename F>
-__device__ __forceinline__ void store_rows(unsigned char* turn, O* p, int64_t pitch, int rows, int cols, F&& v) {
+__device__ __forceinline__ void store_rows(unsigned char* turn, O* p, int64_t pitch, int rows, int cols, bool vec, F&& v) {
     constexpr int V = 16 / int(sizeof(O));
     const int lane = threadIdx.x & 31;
     __syncwarp();  // the last use's reads are done
@@ -28,6 +29,16 @@ __device__ __forceinline__ void store_rows(unsigned char* turn, O* p, int64_t pi
         o.store(reinterpret_cast<O*>(turn + lane * 128 + ((j ^ (lane & 7)) * 16)));  // no two lanes in a bank
     }
     __syncwarp();
+    if (!vec) {
+        constexpr int kCols = 128 / int(sizeof(O));
+        for (int row = 0; row < min(rows, 32); ++row)
+#pragma unroll
+            for (int c = lane; c < kCols; c += 32)
+                if (c < cols)
+                    p[row * pitch + c] =
+                        reinterpret_cast<const O*>(turn + row * 128 + ((c / V) ^ (row & 7)) * 16)[c % V];
+        return;
+    }
     const int chunk = lane & 7;
     if (chunk * V < cols) {
 #pragma unroll

@@ -238,17 +238,50 @@ inline EncodeTiled tensor_map_encoder() {
     return fn;
 }
 
-// A row-major matrix (or `depth` of them, 3D) of `width`-value rows, read in
-// boxes of box_x x box_y values with the 128-byte swizzle; values outside read as 0.
-inline bool make_map(CUtensorMap* map, CUtensorMapDataType type, int size, const void* base, int64_t width,
-                     int64_t height, int64_t depth, int box_x, int box_y, bool three) {
+// An operand that TMA can read: rows of `width` values of `size` bytes, `pitch`
+// bytes apart, `height` of them, `depth` times.
+struct Matrix {
+    const void* base;
+    int64_t width, height, depth, pitch;
+    int size;
+};
+inline Matrix matrix_of(const void* base, int64_t width, int64_t height, int64_t depth, int size) {
+    return {base, width, height, depth, width * size, size};
+}
+inline bool tma_reads(const Matrix& m) { return m.pitch % 16 == 0 && reinterpret_cast<uintptr_t>(m.base) % 16 == 0; }
+
+// Copies the operands that TMA cannot read into scratch memory and points them
+// there; false where there is too little of it.  by_expert: the operand holds a
+// matrix an expert.
+inline bool make_readable(Matrix* (&ms)[2], const bool (&by_expert)[2], const int32_t* offsets, int64_t slots,
+                          Scratch scratch, cudaStream_t stream, cudaError_t* err) {
+    RepackJob jobs[2];
+    int n = 0;
+    *err = cudaSuccess;
+    for (int i = 0; i < 2; ++i) {
+        Matrix& m = *ms[i];
+        if (tma_reads(m)) continue;
+        const int64_t rows = m.height * m.depth, bytes = m.width * m.size;
+        void* dst = scratch.take(repack_bytes(rows, bytes));
+        if (dst == nullptr) return false;
+        jobs[n++] = {m.base, dst, rows, bytes, by_expert[i] ? m.height : 0};
+        m.base = dst;
+        m.pitch = repack_pitch(bytes);
+    }
+    if (n > 0) *err = launch_repack(jobs, n, offsets, slots, stream);
+    return true;
+}
+
+// A tensor map over m (3D where it has a depth), read in boxes of box_x x box_y
+// values with the 128-byte swizzle; values outside read as 0.
+inline bool make_map(CUtensorMap* map, CUtensorMapDataType type, const Matrix& m, int box_x, int box_y, bool three) {
     const EncodeTiled encode = tensor_map_encoder();
     if (encode == nullptr) return false;
-    const cuuint64_t dims[3] = {cuuint64_t(width), cuuint64_t(height), cuuint64_t(depth)};
-    const cuuint64_t strides[2] = {cuuint64_t(width * size), cuuint64_t(width * height * size)};
+    const cuuint64_t dims[3] = {cuuint64_t(m.width), cuuint64_t(m.height), cuuint64_t(m.depth)};
+    const cuuint64_t strides[2] = {cuuint64_t(m.pitch), cuuint64_t(m.pitch * m.height)};
     const cuuint32_t box[3] = {cuuint32_t(box_x), cuuint32_t(box_y), 1};
     const cuuint32_t steps[3] = {1, 1, 1};
-    return encode(map, type, three ? 3 : 2, const_cast<void*>(base), dims, strides, box, steps,
+    return encode(map, type, three ? 3 : 2, const_cast<void*>(m.base), dims, strides, box, steps,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }

@@ -76,14 +76,19 @@ def test_row_refusals(lib):
 
 
 def test_product_refusals(lib):
-    def matmul(x=A, w=B, offsets=C, y=D, slots=64, cin=32, cout=48, experts=4, transposed=0, dtype=BF16):
-        return lib.rowops_expert_matmul(x, w, offsets, y, slots, cin, cout, experts, transposed, dtype, None)
+    def matmul(x=A, w=B, offsets=C, y=D, slots=64, cin=32, cout=48, experts=4, transposed=0, dtype=BF16, ws=None,
+               size=0):
+        return lib.rowops_expert_matmul(x, w, offsets, y, slots, cin, cout, experts, transposed, dtype, ws, size, None)
 
-    def wgrad(dy=A, x=B, offsets=C, dw=D, slots=64, cin=32, cout=48, experts=4, dtype=BF16, dw_type=BF16):
-        return lib.rowops_expert_matmul_wgrad(dy, x, offsets, dw, slots, cin, cout, experts, dtype, dw_type, None)
+    def wgrad(dy=A, x=B, offsets=C, dw=D, slots=64, cin=32, cout=48, experts=4, dtype=BF16, dw_type=BF16, ws=None,
+              size=0):
+        return lib.rowops_expert_matmul_wgrad(dy, x, offsets, dw, slots, cin, cout, experts, dtype, dw_type, ws,
+                                              size, None)
 
-    def fp8(xq=A, xs=B, wq=C, ws=D, offsets=E, y=F, slots=64, cin=160, cout=48, experts=4, y_type=BF16):
-        return lib.rowops_expert_matmul_fp8(xq, xs, wq, ws, offsets, y, slots, cin, cout, experts, y_type, None)
+    def fp8(xq=A, xs=B, wq=C, ws=D, offsets=E, y=F, slots=64, cin=160, cout=48, experts=4, y_type=BF16, work=None,
+            size=0):
+        return lib.rowops_expert_matmul_fp8(xq, xs, wq, ws, offsets, y, slots, cin, cout, experts, y_type, work, size,
+                                            None)
 
     for op in (matmul, wgrad, fp8):
         for bad in (dict(slots=-1), dict(slots=(1 << 30) + 1), dict(cin=0), dict(cout=0), dict(cin=-4),
@@ -101,6 +106,26 @@ def test_product_refusals(lib):
     assert matmul(x=A + 1) == ALIGN and wgrad(dw=D + 2, dw_type=F32) == ALIGN and fp8(xs=B + 2) == ALIGN
     assert matmul(y=A + 2) == ALIAS and matmul(y=B) == ALIAS and matmul(y=C) == ALIAS
     assert wgrad(dw=B + 2) == ALIAS and fp8(y=D) == ALIAS and fp8(y=A + 64) == ALIAS
+    for op, name in ((matmul, "ws"), (wgrad, "ws"), (fp8, "work")):
+        assert op(**{name: W + 8, "size": 1 << 20}) == WORKSPACE
+        for at in (A, B, C, D):
+            assert op(**{name: at + 16, "size": 1 << 20}) == ALIAS
+
+
+def test_workspace_sizes(lib):
+    """A copy for each matrix whose rows are no multiple of 16 bytes; none for others and for refused sizes."""
+    assert lib.rowops_expert_matmul_workspace(100, 64, 128, 4, 0) == 0
+    assert lib.rowops_expert_matmul_workspace(100, 64, 77, 4, 0) == 0  # rows of in values only
+    assert lib.rowops_expert_matmul_workspace(100, 64, 77, 4, 1) >= 4 * 64 * 160
+    assert lib.rowops_expert_matmul_workspace(100, 33, 128, 4, 0) >= (100 + 4 * 128) * 80
+    assert lib.rowops_expert_matmul_wgrad_workspace(100, 64, 128) == 0
+    assert lib.rowops_expert_matmul_wgrad_workspace(100, 33, 50) >= 100 * (80 + 112)
+    assert lib.rowops_expert_matmul_fp8_workspace(100, 64, 77, 4) == 0
+    assert lib.rowops_expert_matmul_fp8_workspace(100, 65, 77, 4) >= (100 + 4 * 77) * 80
+    for bad in ((-1, 33, 8), (4, 0, 8), (4, 33, 0), (1 << 40, 33, 8)):
+        assert lib.rowops_expert_matmul_workspace(*bad, 4, 0) == 0
+        assert lib.rowops_expert_matmul_wgrad_workspace(*bad) == 0
+        assert lib.rowops_expert_matmul_fp8_workspace(*bad, 4) == 0
 
 
 def test_quantize_refusals(lib):

@@ -109,6 +109,19 @@ def test_product(ro, groups, widths, out):
     assert (y[rows:] == 5).all()
 
 
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("widths", [(33, 50), (257, 130), (1, 1)])
+@pytest.mark.parametrize("groups", sorted(GROUPS))
+def test_product_without_a_workspace(ro, groups, widths, out):
+    sizes, (cin, cout) = GROUPS[groups], widths
+    rng = np.random.default_rng(cin + len(sizes))
+    args, x64, w64 = operands(ro, rng, sizes, cin, cout, 0)
+    offsets = offsets_of(sizes)
+    y = ro.rowops_expert_matmul_fp8(*args, torch.from_numpy(offsets).cuda(), dtype=TYPES[out],
+                                    workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    check(y, expert_ref.matmul(x64, w64, offsets), expert_ref.matmul(abs(x64), abs(w64), offsets), cin, out)
+
+
 @pytest.mark.parametrize("widths", [(1040, 384), (1001, 131)])
 def test_product_long(ro, widths):
     cin, cout = widths

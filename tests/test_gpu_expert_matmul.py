@@ -116,6 +116,53 @@ def test_long_sums(ro, widths):
             == expert_ref.wgrad(dy64, x64, offsets)).all()
 
 
+@pytest.mark.parametrize("widths", [(33, 50), (77, 136), (136, 77), (1, 1)])
+@pytest.mark.parametrize("groups", sorted(GROUPS))
+def test_without_a_workspace(ro, groups, widths):
+    """Rows off 16-byte boundaries with too little room for a copy: the kernel that takes any alignment."""
+    sizes, (cin, cout) = GROUPS[groups], widths
+    rng = np.random.default_rng(13)
+    little = torch.empty(16, dtype=torch.uint8, device="cuda")
+    for dtype in ("bf16", "f16"):
+        (x, w, dy), (x64, w64, dy64) = inputs(rng, "whole", sizes, cin, cout, dtype, 0)
+        offsets = offsets_of(sizes)
+        at = torch.from_numpy(offsets).cuda()
+        y = ro.rowops_expert_matmul(x, w, at, workspace=little)
+        assert (f64(y) == expert_ref.matmul(x64, w64, offsets)).all()
+        dx = ro.rowops_expert_matmul(dy, w, at, transposed=True, workspace=little)
+        assert (f64(dx) == expert_ref.matmul(dy64, w64.transpose(0, 2, 1), offsets)).all()
+        for out in (dtype, "f32"):
+            dw = ro.rowops_expert_matmul_wgrad(dy, x, at, dtype=TYPES[out], workspace=little)
+            assert (f64(dw) == expert_ref.wgrad(dy64, x64, offsets)).all()
+
+
+def test_a_workspace_of_the_callers(ro):
+    """Exactly the bytes that are asked for, with guard bytes around them."""
+    rng = np.random.default_rng(14)
+    sizes, cin, cout = [40, 0, 70], 33, 50
+    (x, w, dy), (x64, w64, dy64) = inputs(rng, "whole", sizes, cin, cout, "f16", 0)
+    offsets = offsets_of(sizes)
+    at = torch.from_numpy(offsets).cuda()
+
+    def room(need):
+        buf = torch.full((need + 512,), 77, dtype=torch.uint8, device="cuda")
+        return buf, buf[256:256 + need]
+
+    calls = [(ro.rowops_expert_matmul_workspace(110, cin, cout, 3),
+              lambda ws: ro.rowops_expert_matmul(x, w, at, workspace=ws), expert_ref.matmul(x64, w64, offsets)),
+             (ro.rowops_expert_matmul_workspace(110, cout, cin, 3, True),
+              lambda ws: ro.rowops_expert_matmul(dy, w, at, transposed=True, workspace=ws),
+              expert_ref.matmul(dy64, w64.transpose(0, 2, 1), offsets)),
+             (ro.rowops_expert_matmul_wgrad_workspace(110, cin, cout),
+              lambda ws: ro.rowops_expert_matmul_wgrad(dy, x, at, workspace=ws), expert_ref.wgrad(dy64, x64, offsets))]
+    for need, call, want in calls:
+        buf, ws = room(need)
+        assert need > 0 and (f64(call(ws)) == want).all()
+        assert (buf[:256] == 77).all() and (buf[256 + need:] == 77).all()
+        buf, ws = room(need)
+        assert (f64(call(ws[16:])) == want).all()  # 16 bytes fewer: another kernel or the slack
+
+
 @pytest.mark.parametrize("widths", [(64, 128), (33, 50)])
 def test_dense_without_offsets(ro, widths):
     cin, cout = widths
