@@ -8,9 +8,11 @@
 // million pairs the launches.  Each block owns a contiguous run of pairs and
 // each of its warps a contiguous run of those, so ranks follow from counts
 // alone and no atomic's order reaches the result.  plan_count writes each
-// block's counts; plan_place adds up the counts of the blocks before it (read
-// from the L2), ranks its own pairs and writes them.  One block needs no
-// counts from others: up to kOneBlockPairs pairs are one launch.
+// block's counts; plan_place, a programmatic dependent that counts its own pairs
+// meanwhile, adds up the counts of the blocks before it (read from the L2, the
+// blocks split among threads: one thread an expert took 8 of 21 us), ranks its
+// pairs and writes them.  One block needs no counts from others: up to
+// kOneBlockPairs pairs are one launch.  262144 x 2 pairs of 64 experts: PLAN_US us.
 #include "groups.cuh"
 #include "launch.h"
 
@@ -49,6 +51,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_count(const float* indices,
     __syncthreads();
     for (int e = threadIdx.x; e < experts; e += kPlanThreads)
         counts[int64_t(blockIdx.x) * experts + e] = hist[e];
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
 }
 
 // Shared memory: total[experts] (all blocks), mine[experts] (blocks before this
@@ -78,20 +81,31 @@ __global__ void __launch_bounds__(kPlanThreads)
     }
     __syncthreads();
     for (int e = tid; e < experts; e += kPlanThreads) {
-        int before = 0, sum = 0;
-        if (blocks > 1) {
-            for (int b = 0; b < blocks; ++b) {
-                const int c = __ldg(counts + int64_t(b) * experts + e);
-                if (b < me) before += c;
-                sum += c;
-            }
-        } else {
+        int sum = 0;
+        if (blocks == 1)
             for (int w = 0; w < kPlanWarps; ++w) sum += at[w * experts + e];
-        }
         total[e] = sum;
-        mine[e] = before;
+        mine[e] = 0;
     }
     __syncthreads();
+    if (blocks > 1) {
+        asm volatile("griddepcontrol.wait;\n" ::: "memory");  // plan_count's writes
+        // `parts` threads per expert add up every parts-th block's counts
+        const int parts = max(1, kPlanThreads / experts);
+        for (int i = tid; i < experts * parts; i += kPlanThreads) {
+            const int e = i % experts;
+            int before = 0, sum = 0;
+#pragma unroll 8
+            for (int b = i / experts; b < blocks; b += parts) {
+                const int c = __ldcg(counts + int64_t(b) * experts + e);
+                before += b < me ? c : 0;
+                sum += c;
+            }
+            atomicAdd(&total[e], sum);
+            atomicAdd(&mine[e], before);
+        }
+        __syncthreads();
+    }
     // exclusive scan of total over the experts (at most 1024: two per thread)
     constexpr int kPer = kMaxExperts / kPlanThreads;
     int v[kPer], sum = 0;
@@ -194,10 +208,20 @@ cudaError_t launch_expert_plan(const float* indices, const float* values, int32_
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
-    plan_place<<<blocks, kPlanThreads, smem, stream>>>(indices, values, counts, offsets, order, slot, int(pairs), ne,
-                                                       run);
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3(kPlanThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = blocks > 1 ? 1 : 0;  // alone it must wait for whatever ran before
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, plan_place, indices, values, static_cast<const int32_t*>(counts),
+                                             offsets, order, slot, int(pairs), ne, run);
     note_launches(1);
-    return cudaGetLastError();
+    return e;
 }
 
 }  // namespace rowops
