@@ -17,18 +17,23 @@ namespace {
 constexpr int kRowThreads = 256;
 constexpr int kRowWarps = kRowThreads / 32;
 
-// One warp per (token, tile of 32 * V * U columns).
-template <typename TI, typename TO, int V, int U>
+// A group of 2^shift lanes (SHORT; else a warp, which the compiler makes better
+// use of) per (token, tile of 2^shift * V * U columns); rows
+// shorter than a warp's tile share a warp (64 columns of 262144 tokens, combine:
+// 68 -> 33 us).
+template <typename TI, typename TO, int V, int U, bool SHORT>
 __global__ void __launch_bounds__(kRowThreads)
     gather_rows(const TI* __restrict__ x, const int32_t* __restrict__ slot, TO* __restrict__ out, int64_t items,
-                int tiles, int k, int64_t cols, int64_t slots) {
-    const int64_t item = int64_t(blockIdx.x) * kRowWarps + (threadIdx.x >> 5);
+                int tiles, int shift, int k, int64_t cols, int64_t slots) {
+    if constexpr (!SHORT) shift = 5;
+    const int lanes = 1 << shift;
+    const int64_t item = int64_t(blockIdx.x) * (kRowThreads >> shift) + (threadIdx.x >> shift);
     if (item >= items) return;
-    const int64_t t = item / tiles, c0 = (item % tiles) * (32 * V * U) + (threadIdx.x & 31) * V;
+    const int64_t t = item / tiles, c0 = (item % tiles) * (lanes * V * U) + (threadIdx.x & (lanes - 1)) * V;
     Chunk<TI, V> in[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        const int64_t c = c0 + u * (32 * V);
+        const int64_t c = c0 + u * (lanes * V);
         if (c < cols) in[u].load(x + t * cols + c);
     }
     Chunk<TO, V> o[U];
@@ -41,25 +46,26 @@ __global__ void __launch_bounds__(kRowThreads)
         if (s < 0 || s >= slots) continue;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int64_t c = c0 + u * (32 * V);
+            const int64_t c = c0 + u * (lanes * V);
             if (c < cols) o[u].store(out + s * cols + c);
         }
     }
 }
 
-template <typename TI, typename TO, int V, int U>
+template <typename TI, typename TO, int V, int U, bool SHORT>
 __global__ void __launch_bounds__(kRowThreads)
     combine_rows(const TI* __restrict__ y, const int32_t* __restrict__ slot, const float* __restrict__ weights,
-                 TO* __restrict__ out, int64_t items, int tiles, int k, int64_t cols, int64_t slots) {
-    const int64_t item = int64_t(blockIdx.x) * kRowWarps + (threadIdx.x >> 5);
+                 TO* __restrict__ out, int64_t items, int tiles, int shift, int k, int64_t cols, int64_t slots) {
+    if constexpr (!SHORT) shift = 5;
+    const int lanes = 1 << shift;
+    const int64_t item = int64_t(blockIdx.x) * (kRowThreads >> shift) + (threadIdx.x >> shift);
     if (item >= items) return;
-    const int64_t t = item / tiles, c0 = (item % tiles) * (32 * V * U) + (threadIdx.x & 31) * V;
+    const int64_t t = item / tiles, c0 = (item % tiles) * (lanes * V * U) + (threadIdx.x & (lanes - 1)) * V;
     float acc[U][V];
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int i = 0; i < V; ++i) acc[u][i] = 0.f;
-#pragma unroll 4
     for (int j = 0; j < k; ++j) {
         const int64_t s = __ldg(slot + t * k + j);
         if (s < 0 || s >= slots) continue;
@@ -67,7 +73,7 @@ __global__ void __launch_bounds__(kRowThreads)
         Chunk<TI, V> in[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int64_t c = c0 + u * (32 * V);
+            const int64_t c = c0 + u * (lanes * V);
             if (c < cols) in[u].load(y + s * cols + c);
         }
 #pragma unroll
@@ -78,30 +84,33 @@ __global__ void __launch_bounds__(kRowThreads)
     Chunk<TO, V> o[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        const int64_t c = c0 + u * (32 * V);
+        const int64_t c = c0 + u * (lanes * V);
 #pragma unroll
         for (int i = 0; i < V; ++i) o[u].set(i, acc[u][i]);
         if (c < cols) o[u].store(out + t * cols + c);
     }
 }
 
-// WARPS warps per pair (t, j); pairs of one token are neighbours, so its dout
+// WARPS warps, or (WARPS == 0) a group of 2^shift lanes, per pair (t, j); pairs of one token are neighbours, so its dout
 // row comes from the L1 after the first.
 template <typename TO, typename TY, int V, int WARPS>
 __global__ void __launch_bounds__(kRowThreads)
     combine_rows_bwd(const TO* __restrict__ dout, const TY* __restrict__ y, const int32_t* __restrict__ slot,
                      const float* __restrict__ weights, TY* __restrict__ dy, float* __restrict__ dweights,
-                     int64_t pairs, int k, int64_t cols, int64_t slots) {
+                     int64_t pairs, int shift, int k, int64_t cols, int64_t slots) {
     __shared__ float part[kRowWarps];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t p = int64_t(blockIdx.x) * (kRowWarps / WARPS) + warp / WARPS;
+    constexpr int kWarps = WARPS > 0 ? WARPS : 1;
+    if constexpr (WARPS > 0) shift = 5;
+    const int warp = threadIdx.x >> 5, lanes = 1 << shift, lane = threadIdx.x & (lanes - 1);
+    const int64_t p = WARPS > 0 ? int64_t(blockIdx.x) * (kRowWarps / kWarps) + warp / kWarps
+                                : int64_t(blockIdx.x) * (kRowThreads >> shift) + (threadIdx.x >> shift);
     const int64_t s = p < pairs ? int64_t(__ldg(slot + p)) : -1;
     float dot = 0.f;
     if (s >= 0 && s < slots) {
         const float w = __ldg(weights + p);
         const TO* d = dout + (p / k) * cols;
 #pragma unroll 4
-        for (int64_t c = ((warp % WARPS) * 32 + lane) * V; c < cols; c += WARPS * 32 * V) {
+        for (int64_t c = ((WARPS > 0 ? warp % kWarps : 0) * lanes + lane) * V; c < cols; c += kWarps * lanes * V) {
             Chunk<TO, V> a;
             Chunk<TY, V> b, o;
             a.load(d + c);
@@ -114,7 +123,9 @@ __global__ void __launch_bounds__(kRowThreads)
             o.store(dy + s * cols + c);
         }
     }
-    dot = group_sum<32>(dot);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        if (o < lanes) dot += __shfl_xor_sync(kFullMask, dot, o);
     if constexpr (WARPS > 1) {
         if (lane == 0) part[warp] = dot;
         __syncthreads();
@@ -132,16 +143,26 @@ bool chunked(const void* p, int64_t cols, int v, size_t size) {
     return cols % v == 0 && reinterpret_cast<uintptr_t>(p) % (v * size) == 0;
 }
 
+// Lanes of a group that covers `cols` columns with `per` columns a lane: a power of two up to 32.
+int group_shift(int64_t cols, int per) {
+    int shift = 0;
+    while (shift < 5 && (int64_t(per) << shift) < cols) ++shift;
+    return shift;
+}
+
 struct Items {
     int64_t items;
-    int tiles;
+    int tiles, shift;
     unsigned grid;
 };
-inline Items row_items(int64_t rows, int64_t cols, int tile) {
+inline Items row_items(int64_t rows, int64_t cols, int per) {
     Items r;
+    r.shift = group_shift(cols, per);
+    const int64_t tile = int64_t(per) << r.shift;
     r.tiles = int((cols + tile - 1) / tile);
     r.items = rows * r.tiles;
-    r.grid = unsigned((r.items + kRowWarps - 1) / kRowWarps);
+    const int64_t block = kRowThreads >> r.shift;
+    r.grid = unsigned((r.items + block - 1) / block);
     return r;
 }
 
@@ -156,14 +177,17 @@ cudaError_t launch_expert_gather(const void* x, const int32_t* slot, void* out, 
             constexpr int V = chunk_of<TI, TO>();
             const TI* xp = static_cast<const TI*>(x);
             TO* op = static_cast<TO*>(out);
+            auto go = [&](auto kernel, const Items& n) {
+                kernel<<<n.grid, kRowThreads, 0, stream>>>(xp, slot, op, n.items, n.tiles, n.shift, int(k), cols, slots);
+            };
             if (chunked(x, cols, V, sizeof(TI)) && chunked(out, cols, V, sizeof(TO))) {
-                const Items n = row_items(rows, cols, 32 * V * 2);
-                gather_rows<TI, TO, V, 2><<<n.grid, kRowThreads, 0, stream>>>(xp, slot, op, n.items, n.tiles, int(k),
-                                                                              cols, slots);
+                const Items n = row_items(rows, cols, V * 2);
+                if (n.shift < 5) go(gather_rows<TI, TO, V, 2, true>, n);
+                else go(gather_rows<TI, TO, V, 2, false>, n);
             } else {
-                const Items n = row_items(rows, cols, 32 * 4);
-                gather_rows<TI, TO, 1, 4><<<n.grid, kRowThreads, 0, stream>>>(xp, slot, op, n.items, n.tiles, int(k),
-                                                                              cols, slots);
+                const Items n = row_items(rows, cols, 4);
+                if (n.shift < 5) go(gather_rows<TI, TO, 1, 4, true>, n);
+                else go(gather_rows<TI, TO, 1, 4, false>, n);
             }
         });
     });
@@ -181,14 +205,18 @@ cudaError_t launch_expert_combine(const void* y, const int32_t* slot, const floa
             constexpr int V = chunk_of<TI, TO>();
             const TI* yp = static_cast<const TI*>(y);
             TO* op = static_cast<TO*>(out);
+            auto go = [&](auto kernel, const Items& n) {
+                kernel<<<n.grid, kRowThreads, 0, stream>>>(yp, slot, weights, op, n.items, n.tiles, n.shift, int(k), cols,
+                                                           slots);
+            };
             if (chunked(y, cols, V, sizeof(TI)) && chunked(out, cols, V, sizeof(TO))) {
-                const Items n = row_items(rows, cols, 32 * V * 2);
-                combine_rows<TI, TO, V, 2><<<n.grid, kRowThreads, 0, stream>>>(yp, slot, weights, op, n.items,
-                                                                               n.tiles, int(k), cols, slots);
+                const Items n = row_items(rows, cols, V * 2);
+                if (n.shift < 5) go(combine_rows<TI, TO, V, 2, true>, n);
+                else go(combine_rows<TI, TO, V, 2, false>, n);
             } else {
-                const Items n = row_items(rows, cols, 32 * 4);
-                combine_rows<TI, TO, 1, 4><<<n.grid, kRowThreads, 0, stream>>>(yp, slot, weights, op, n.items,
-                                                                               n.tiles, int(k), cols, slots);
+                const Items n = row_items(rows, cols, 4);
+                if (n.shift < 5) go(combine_rows<TI, TO, 1, 4, true>, n);
+                else go(combine_rows<TI, TO, 1, 4, false>, n);
             }
         });
     });
@@ -206,17 +234,20 @@ cudaError_t launch_expert_combine_bwd(const void* dout, const void* y, const int
             using TO = decltype(to);
             using TY = decltype(ty);
             constexpr int V = chunk_of<TO, TY>();
-            auto go = [&](auto kernel, int warps) {
-                const int64_t per = kRowWarps / warps;
-                kernel<<<unsigned((pairs + per - 1) / per), kRowThreads, 0, stream>>>(
-                    static_cast<const TO*>(dout), static_cast<const TY*>(y), slot, weights, static_cast<TY*>(dy),
-                    dweights, pairs, int(k), cols, slots);
-            };
             const bool vec = chunked(dout, cols, V, sizeof(TO)) && chunked(y, cols, V, sizeof(TY)) &&
                              chunked(dy, cols, V, sizeof(TY));
+            const int shift = group_shift(cols, vec ? V * 2 : 4);
+            auto go = [&](auto kernel, int warps) {
+                const int64_t per = warps > 0 ? kRowWarps / warps : kRowThreads >> shift;
+                kernel<<<unsigned((pairs + per - 1) / per), kRowThreads, 0, stream>>>(
+                    static_cast<const TO*>(dout), static_cast<const TY*>(y), slot, weights, static_cast<TY*>(dy),
+                    dweights, pairs, shift, int(k), cols, slots);
+            };
             if (vec && wide) go(combine_rows_bwd<TO, TY, V, kRowWarps>, kRowWarps);
+            else if (vec && shift < 5) go(combine_rows_bwd<TO, TY, V, 0>, 0);
             else if (vec) go(combine_rows_bwd<TO, TY, V, 1>, 1);
             else if (wide) go(combine_rows_bwd<TO, TY, 1, kRowWarps>, kRowWarps);
+            else if (shift < 5) go(combine_rows_bwd<TO, TY, 1, 0>, 0);
             else go(combine_rows_bwd<TO, TY, 1, 1>, 1);
         });
     });
