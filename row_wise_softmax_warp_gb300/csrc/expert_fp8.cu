@@ -70,7 +70,7 @@ struct Fp8Shared {
 };
 
 struct Fp8Tile {
-    int expert;
+    int expert = 0;
     int row0, rows;  // of the pair
     int col0;
 };
@@ -79,7 +79,7 @@ __device__ __forceinline__ bool tile_at(const Fp8Args& g, const int* table, int 
     const int across = (g.out + kTileCols - 1) / kTileCols;
     const int row = t / across;
     if (row >= table[g.experts]) return false;
-    w.expert = uniform(tile_expert(table, g.experts, row));
+    w.expert = uniform(tile_expert(table, g.experts, row, w.expert));
     const RowRange r = group_rows(g.offsets, w.expert, g.slots);
     const int at = (row - table[w.expert]) * kTileRows;
     w.row0 = uniform(r.first + at);

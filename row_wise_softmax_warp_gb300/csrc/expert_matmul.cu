@@ -69,7 +69,7 @@ struct Shared {
 };
 
 struct Tile {
-    int expert;
+    int expert = 0;
     int m0;       // first row of the pair's 256
     int n0;       // first column: a row of x and y, or a column of dw
     int n;        // columns to write
@@ -79,26 +79,26 @@ struct Tile {
 };
 
 template <Form FORM>
-__device__ __forceinline__ bool tile_at(const ProductArgs& g, const int* table, int64_t t, Tile& w) {
+__device__ __forceinline__ bool tile_at(const ProductArgs& g, const int* table, int t, Tile& w) {
     const int tiles_m = (g.m + 255) / 256;
     if constexpr (FORM == kWeights) {
         const int tiles_n = (g.n + kTileN - 1) / kTileN;
-        const int64_t row = t / tiles_m;
-        if (row >= int64_t(tiles_n) * g.experts) return false;
-        w.expert = int(row / tiles_n);
-        w.m0 = int(t % tiles_m) * 256;
-        w.n0 = int(row % tiles_n) * kTileN;
+        const int row = t / tiles_m;
+        if (row >= tiles_n * g.experts) return false;
+        w.expert = row / tiles_n;
+        w.m0 = t % tiles_m * 256;
+        w.n0 = row % tiles_n * kTileN;
         w.n = min(kTileN, g.n - w.n0);
         w.width = (w.n + 127) & ~127;
         const RowRange r = group_rows(g.offsets, w.expert, g.slots);
         w.sum0 = r.first;
         w.sum = r.count;
     } else {
-        const int64_t row = t / tiles_m;
+        const int row = t / tiles_m;
         if (row >= table[g.experts]) return false;
-        const RowTile r = row_tile(g.offsets, g.experts, g.slots, table, int(row));
-        w.expert = r.expert;
-        w.m0 = int(t % tiles_m) * 256;
+        const RowTile r = row_tile(g.offsets, g.experts, g.slots, table, row, w.expert);
+        w.expert = uniform(r.expert);
+        w.m0 = t % tiles_m * 256;
         w.n0 = r.first;
         w.n = r.count;
         w.width = (w.n + 31) & ~31;
@@ -214,14 +214,14 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
     tcgen05_fence_after();
     const uint32_t tmem = uniform(sh.tmem), stage0 = uniform(smem_addr(stages));
 
-    const int64_t first = blockIdx.x >> 1, step = gridDim.x >> 1;
+    const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
     bool ok = true;
     if (warp == kCopyWarpA || warp == kCopyWarpB) {
         const bool is_a = warp == kCopyWarpA;
         const uint32_t to = stage0 + (is_a ? 0 : kHalfBytes);
         uint32_t it = 0;
         Tile w;
-        for (int64_t t = first; ok && tile_at<FORM>(g, table, t, w); t += step) {
+        for (int t = first; ok && tile_at<FORM>(g, table, t, w); t += step) {
             const int sum = uniform(w.sum), blocks = (sum + kStepK - 1) / kStepK;
             const int half = uniform(w.width) / 2, expert = uniform(w.expert), sum0 = uniform(w.sum0);
             const int m0 = uniform(w.m0) + int(rank) * 128, n0 = uniform(w.n0) + int(rank) * half;
@@ -268,7 +268,7 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
         if (rank == 0) {
             uint32_t it = 0, acc = 0, tails = 0;  // tails: the phases of tail_done, a bit a stage
             Tile w;
-            for (int64_t t = first; ok && tile_at<FORM>(g, table, t, w); t += step) {
+            for (int t = first; ok && tile_at<FORM>(g, table, t, w); t += step) {
                 const int sum = uniform(w.sum), blocks = (sum + kStepK - 1) / kStepK;
                 if (blocks == 0) continue;
                 const bool ragged = FORM == kWeights && ragged_rows(sum) != 0;
@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
     } else if (FORM == kWeights && warp == kZeroWarp) {
         uint32_t it = 0, tails = 0;  // tails: the phases of tail_full
         Tile w;
-        for (int64_t t = first; tile_at<FORM>(g, table, t, w); t += step) {
+        for (int t = first; tile_at<FORM>(g, table, t, w); t += step) {
             it += (w.sum + kStepK - 1) / kStepK;
             if (ragged_rows(w.sum) == 0) continue;
             const uint32_t s = (it - 1) % kStages;
@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
     } else {
         uint32_t acc = 0;
         Tile w;
-        for (int64_t t = first; tile_at<FORM>(g, table, t, w); t += step) {
+        for (int t = first; tile_at<FORM>(g, table, t, w); t += step) {
             const bool zero = uniform(w.sum) == 0;
             if (!zero && !warp_wait(&sh.acc_full[acc & 1], (acc >> 1) & 1, abort_flag)) break;
             tcgen05_fence_after();
@@ -343,6 +343,7 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
     if (warp == kProductWarp) tmem_dealloc_pair(tmem, kTmemColumns);
 }
 
+constexpr int64_t kMostTiles = int64_t(1) << 30;  // more than a device's memory holds
 constexpr size_t kMostSmem = 1024 + kStages * size_t(kStageBytes) + 4 * kTurnBytes;
 static_assert(4 * kTurnBytes >= (kMaxExperts + 1) * 4, "the table of tiles lies where the others turn rows");
 
@@ -376,6 +377,7 @@ cudaError_t launch_expert_matmul(const void* x, const void* w, const int32_t* of
     g.format = dtype == ROWOPS_F16 ? 0 : 1;
     g.vec = false;
     const int64_t tiles = most_row_tiles(slots, experts) * ((out + 255) / 256);
+    if (tiles >= kMostTiles) return cudaErrorInvalidValue;
     auto go = [&](auto t, auto form) {
         using T = decltype(t);
         constexpr Form kForm = decltype(form)::value;
@@ -412,6 +414,7 @@ cudaError_t launch_expert_matmul_wgrad(const void* dy, const void* x, const int3
     g.format = dtype == ROWOPS_F16 ? 0 : 1;
     g.vec = in * dw_size % 16 == 0 && reinterpret_cast<uintptr_t>(dw) % 16 == 0;
     const int64_t tiles = experts * ((out + 255) / 256) * ((in + kTileN - 1) / kTileN);
+    if (tiles >= kMostTiles) return cudaErrorInvalidValue;
     auto go = [&](auto t, auto o) {
         return launch_pairs<expert_product<decltype(t), decltype(o), kWeights>>(tiles, threads_of(kWeights), kMostSmem,
                                                                                 stream, g);
