@@ -65,6 +65,7 @@ struct Fp8Shared {
     uint64_t full[kStages], empty[kStages];
     uint64_t acc_full[kBuffers], acc_empty[kBuffers], peer_empty[kBuffers];
     uint64_t scale_full[kScaleSlots], scale_empty[kScaleSlots];
+    int warp_tiles[kThreads / 32];
     uint32_t tmem;
     int abort;
 };
@@ -136,7 +137,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_product_fp8(const __grid_c
         prefetch_map(&g.x_small);
     }
     if (warp == kProductWarp) tmem_alloc_pair(&sh.tmem, kTmemColumns);
-    if (warp == 0) build_tile_table<kTileRows>(g.offsets, g.experts, g.slots, table);
+    build_tile_table<kTileRows, kThreads>(g.offsets, g.experts, g.slots, table, sh.warp_tiles);
     tcgen05_fence_before();
     __syncthreads();
     cluster_sync_all();

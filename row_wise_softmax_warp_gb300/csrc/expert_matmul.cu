@@ -64,6 +64,7 @@ struct Shared {
     uint64_t full[kStages], empty[kStages];
     uint64_t acc_full[2], acc_empty[2];
     uint64_t tail_full[kStages], tail_done[kStages];  // kWeights: a stage whose last rows are zeroed
+    int warp_tiles[8];
     uint32_t tmem;
     int abort;
 };
@@ -207,7 +208,7 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
     }
     if (warp == kProductWarp) tmem_alloc_pair(&sh.tmem, kTmemColumns);
     if constexpr (FORM != kWeights)
-        if (warp == 0) build_tile_table<kMostRows>(g.offsets, g.experts, g.slots, table);
+        build_tile_table<kMostRows, threads_of(FORM)>(g.offsets, g.experts, g.slots, table, sh.warp_tiles);
     tcgen05_fence_before();
     __syncthreads();
     cluster_sync_all();
