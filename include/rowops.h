@@ -1,9 +1,11 @@
 /*
  * rowops.h - C ABI of librowops, the GB300 (sm_103a) row-wise
- * normalise-and-reduce ops of a transformer training step.
+ * normalise-and-reduce ops of a transformer training step and the
+ * mixture-of-experts layer behind its router.
  *
- * Every op works on row-major fp32 matrices of `rows` x `cols` with row stride
- * `cols` and launches hand-written CUDA kernels on the caller's stream.
+ * Every op works on row-major matrices of `rows` x `cols` with row stride `cols`
+ * (fp32; the expert operators at the end also fp16, bf16 and e4m3) and launches
+ * hand-written CUDA kernels on the caller's stream.
  *
  * Common contract (applies to every entry point below):
  *   - Pointers are DEVICE pointers on the current CUDA device.  The caller owns
