@@ -414,7 +414,7 @@ typedef enum {
 } rowops_dtype;
 
 /* Bytes of device workspace rowops_expert_plan needs (a function of the sizes
- * and the current device's SM count; 0 for up to 4096 pairs and for sizes that
+ * and the current device's SM count; 0 for up to 2048 pairs and for sizes that
  * the call refuses). */
 size_t rowops_expert_plan_workspace(int64_t rows, int64_t k, int64_t experts);
 

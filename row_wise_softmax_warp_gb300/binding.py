@@ -494,7 +494,7 @@ def rowops_expert_plan(indices, experts, values=None, offsets=None, order=None, 
         _typed(values, "values", _F32, shape, device)
     lib = library()
     pairs = rows * k
-    need = lib.rowops_expert_plan_workspace(rows, k, experts) if workspace is None and pairs > 4096 else 0
+    need = lib.rowops_expert_plan_workspace(rows, k, experts) if workspace is None and pairs > 2048 else 0
     offsets = _given(offsets, "offsets", torch.int32, (max(experts, 0) + 1,), indices, device)
     order = _given(order, "order", torch.int32, (pairs,), indices, device)
     slot = _given(slot, "slot", torch.int32, shape, indices, device)

@@ -12,16 +12,18 @@
 // meanwhile, adds up the counts of the blocks before it (read from the L2, the
 // blocks split among threads: one thread an expert took 8 of 21 us), ranks its
 // pairs and writes them.  One block needs no counts from others: up to
-// kOneBlockPairs pairs are one launch.  262144 x 2 pairs of 64 experts: 15 us.
+// kOneBlockPairs pairs are one launch.  262144 x 2 pairs of 64 experts: 14.7 us.
 #include "groups.cuh"
 #include "launch.h"
 
 namespace rowops {
 namespace {
 
-constexpr int kPlanThreads = 512;
-constexpr int kPlanWarps = kPlanThreads / 32;
-constexpr int kOneBlockPairs = 4096;
+// One block alone is faster with 512 threads (64 pairs: 2.8 against 3.5 us), many
+// with 1024 (524288 pairs of 256 experts: 17.9 against 23.0 us).  2048 pairs: 5.6 us
+// in one block, 6.4 in two launches; 4096 pairs: 8.9 and 6.4.
+constexpr int kOneThreads = 512, kManyThreads = 1024;
+constexpr int kOneBlockPairs = 2048;
 
 // Expert of pair p, or `experts` for a pair that is left out.
 __device__ __forceinline__ int pair_expert(const float* indices, const float* values, int p, int experts) {
@@ -37,53 +39,55 @@ __device__ __forceinline__ void my_run(int pairs, int run, int& begin, int& end)
 }
 
 // counts[block][e]
-__global__ void __launch_bounds__(kPlanThreads) plan_count(const float* indices, const float* values,
+__global__ void __launch_bounds__(kManyThreads) plan_count(const float* indices, const float* values,
                                                            int32_t* counts, int pairs, int experts, int run) {
     extern __shared__ int hist[];
-    for (int e = threadIdx.x; e < experts; e += kPlanThreads) hist[e] = 0;
+    for (int e = threadIdx.x; e < experts; e += kManyThreads) hist[e] = 0;
     __syncthreads();
     int begin, end;
     my_run(pairs, run, begin, end);
-    for (int p = begin + threadIdx.x; p < end; p += kPlanThreads) {
+    for (int p = begin + threadIdx.x; p < end; p += kManyThreads) {
         const int e = pair_expert(indices, values, p, experts);
         if (e < experts) atomicAdd(&hist[e], 1);  // integer counts: the order of the adds does not matter
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < experts; e += kPlanThreads)
+    for (int e = threadIdx.x; e < experts; e += kManyThreads)
         counts[int64_t(blockIdx.x) * experts + e] = hist[e];
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
 }
 
 // Shared memory: total[experts] (all blocks), mine[experts] (blocks before this
-// one), at[kPlanWarps][experts] (each warp's next slot per expert).
-__global__ void __launch_bounds__(kPlanThreads)
+// one), at[warps][experts] (each warp's next slot per expert).
+template <int NT>
+__global__ void __launch_bounds__(NT)
     plan_place(const float* indices, const float* values, const int32_t* counts, int32_t* offsets, int32_t* order,
                int32_t* slot, int pairs, int experts, int run) {
+    constexpr int kWarps = NT / 32;
     extern __shared__ int sh[];
     int* total = sh;
     int* mine = sh + experts;
     int* at = sh + 2 * experts;
-    __shared__ int warp_sum[kPlanWarps];
+    __shared__ int warp_sum[kWarps];
     __shared__ int all;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int blocks = gridDim.x, me = blockIdx.x;
 
     int begin, end;
     my_run(pairs, run, begin, end);
-    const int per = ((end - begin) + kPlanWarps - 1) / kPlanWarps;
+    const int per = ((end - begin) + kWarps - 1) / kWarps;
     const int wb = min(begin + warp * per, end), we = min(wb + per, end);
 
-    for (int i = tid; i < experts * kPlanWarps; i += kPlanThreads) at[i] = 0;
+    for (int i = tid; i < experts * kWarps; i += NT) at[i] = 0;
     __syncthreads();
     for (int p = wb + lane; p < we; p += 32) {
         const int e = pair_expert(indices, values, p, experts);
         if (e < experts) atomicAdd(&at[warp * experts + e], 1);
     }
     __syncthreads();
-    for (int e = tid; e < experts; e += kPlanThreads) {
+    for (int e = tid; e < experts; e += NT) {
         int sum = 0;
         if (blocks == 1)
-            for (int w = 0; w < kPlanWarps; ++w) sum += at[w * experts + e];
+            for (int w = 0; w < kWarps; ++w) sum += at[w * experts + e];
         total[e] = sum;
         mine[e] = 0;
     }
@@ -91,8 +95,8 @@ __global__ void __launch_bounds__(kPlanThreads)
     if (blocks > 1) {
         asm volatile("griddepcontrol.wait;\n" ::: "memory");  // plan_count's writes
         // `parts` threads per expert add up every parts-th block's counts
-        const int parts = max(1, kPlanThreads / experts);
-        for (int i = tid; i < experts * parts; i += kPlanThreads) {
+        const int parts = max(1, NT / experts);
+        for (int i = tid; i < experts * parts; i += NT) {
             const int e = i % experts;
             int before = 0, sum = 0;
 #pragma unroll 8
@@ -106,8 +110,8 @@ __global__ void __launch_bounds__(kPlanThreads)
         }
         __syncthreads();
     }
-    // exclusive scan of total over the experts (at most 1024: two per thread)
-    constexpr int kPer = kMaxExperts / kPlanThreads;
+    // exclusive scan of total over the experts
+    constexpr int kPer = kMaxExperts / NT;
     int v[kPer], sum = 0;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
@@ -134,13 +138,13 @@ __global__ void __launch_bounds__(kPlanThreads)
         }
         base += v[i];
     }
-    if (tid == kPlanThreads - 1) all = base;
+    if (tid == NT - 1) all = base;
     __syncthreads();
     if (me == 0 && tid == 0) offsets[experts] = all;
     // each warp's first slot per expert: this block's, then the warps before it
-    for (int e = tid; e < experts; e += kPlanThreads) {
+    for (int e = tid; e < experts; e += NT) {
         int next = mine[e];
-        for (int w = 0; w < kPlanWarps; ++w) {
+        for (int w = 0; w < kWarps; ++w) {
             const int c = at[w * experts + e];
             at[w * experts + e] = next;
             next += c;
@@ -164,7 +168,7 @@ __global__ void __launch_bounds__(kPlanThreads)
         }
     }
     // the slots past the last pair
-    for (int64_t s = all + int64_t(me) * kPlanThreads + tid; s < pairs; s += int64_t(blocks) * kPlanThreads)
+    for (int64_t s = all + int64_t(me) * NT + tid; s < pairs; s += int64_t(blocks) * NT)
         order[s] = -1;
 }
 
@@ -195,15 +199,16 @@ cudaError_t launch_expert_plan(const float* indices, const float* values, int32_
     int blocks, run;
     plan_shape(pairs, blocks, run);
     const int ne = int(experts);
-    const size_t smem = size_t(ne) * 4 * (2 + kPlanWarps);
+    const auto place = blocks > 1 ? plan_place<kManyThreads> : plan_place<kOneThreads>;
+    const int threads = blocks > 1 ? kManyThreads : kOneThreads;
+    const size_t smem = size_t(ne) * 4 * (2 + threads / 32);
     if (smem > 48 * 1024) {
-        const cudaError_t e =
-            cudaFuncSetAttribute(plan_place, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+        const cudaError_t e = cudaFuncSetAttribute(place, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
         if (e != cudaSuccess) return e;
     }
     int32_t* counts = static_cast<int32_t*>(workspace);
     if (blocks > 1) {
-        plan_count<<<blocks, kPlanThreads, size_t(ne) * 4, stream>>>(indices, values, counts, int(pairs), ne, run);
+        plan_count<<<blocks, kManyThreads, size_t(ne) * 4, stream>>>(indices, values, counts, int(pairs), ne, run);
         note_launches(1);
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
@@ -213,12 +218,12 @@ cudaError_t launch_expert_plan(const float* indices, const float* values, int32_
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.gridDim = dim3(blocks);
-    cfg.blockDim = dim3(kPlanThreads);
+    cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = blocks > 1 ? 1 : 0;  // alone it must wait for whatever ran before
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, plan_place, indices, values, static_cast<const int32_t*>(counts),
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, place, indices, values, static_cast<const int32_t*>(counts),
                                              offsets, order, slot, int(pairs), ne, run);
     note_launches(1);
     return e;

@@ -41,7 +41,7 @@ def test_plan_refusals(lib):
         assert plan(rows=n, experts=64, size=need - 1) == WORKSPACE
         assert plan(rows=n, experts=64, ws=W + 8) == WORKSPACE
         assert plan(rows=n, experts=64, ws=D) == ALIAS
-    assert lib.rowops_expert_plan_workspace(1024, 4, 64) == 0
+    assert lib.rowops_expert_plan_workspace(512, 4, 64) == 0
     for bad in ((-1, 2, 8), (4, 0, 8), (4, 2, 0), (4, 2, 1025), (1 << 40, 2, 8)):
         assert lib.rowops_expert_plan_workspace(*bad) == 0
 

@@ -42,7 +42,7 @@ def routing(rng, tokens, experts, k, blocked=0.2):
 
 
 @pytest.mark.parametrize("tokens,experts,k", [
-    (1, 1, 1), (1, 64, 2), (32, 64, 2), (33, 7, 7), (509, 16, 4), (2048, 64, 2), (2049, 64, 2), (4097, 1, 1),
+    (1, 1, 1), (1, 64, 2), (32, 64, 2), (33, 7, 7), (509, 16, 4), (1024, 64, 2), (1025, 64, 2), (2049, 64, 2), (4097, 1, 1),
     (5000, 1024, 3), (70001, 5, 1), (20000, 256, 8)])
 def test_plan(ro, tokens, experts, k):
     rng = np.random.default_rng(tokens + experts)
