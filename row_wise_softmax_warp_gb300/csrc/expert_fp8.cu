@@ -316,9 +316,10 @@ cudaError_t launch_expert_matmul_fp8(const uint8_t* x, const float* x_scale, con
     if (err != cudaSuccess) return err;
     const CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_UINT8;
     Fp8Args g;
-    if (!make_map(&g.w, type, mw, kBlock, 64, true) || !make_map(&g.x, type, mx, kBlock, 128, false) ||
-        !make_map(&g.x_small, type, mx, kBlock, 16, false))
+    if (!make_map(&g.w, type, mw, kBlock, 64, true) || !make_map(&g.x_small, type, mx, kBlock, 16, false))
         return cudaErrorInvalidValue;
+    g.x = g.x_small;  // a CTA's rows round up to 128 only from 113 on
+    if (slots > 112 && !make_map(&g.x, type, mx, kBlock, 128, false)) return cudaErrorInvalidValue;
     g.xs = x_scale;
     g.ws = w_scale;
     g.offsets = offsets;

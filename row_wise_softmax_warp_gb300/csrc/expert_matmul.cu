@@ -365,9 +365,10 @@ cudaError_t launch_expert_matmul(const void* x, const void* w, const int32_t* of
     const CUtensorMapDataType type =
         dtype == ROWOPS_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     ProductArgs g;
-    if (!make_map(&g.a, type, mw, 64, transposed ? 64 : 128, true) || !make_map(&g.b, type, mx, 64, 128, false) ||
-        !make_map(&g.b_small, type, mx, 64, 16, false))
+    if (!make_map(&g.a, type, mw, 64, transposed ? 64 : 128, true) || !make_map(&g.b_small, type, mx, 64, 16, false))
         return cudaErrorInvalidValue;
+    g.b = g.b_small;  // half a tile is 128 rows only where a tile has more than 224
+    if (slots > 224 && !make_map(&g.b, type, mx, 64, 128, false)) return cudaErrorInvalidValue;
     g.offsets = offsets;
     g.out = y;
     g.slots = int(slots);
