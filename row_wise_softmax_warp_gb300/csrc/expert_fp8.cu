@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_product_fp8(const __grid_c
     volatile int* abort_flag = &sh.abort;
 
     const int warp = uniform(int(threadIdx.x >> 5)), lane = threadIdx.x & 31;
-    const uint32_t rank = cluster_rank();
+    const uint32_t rank = uniform(cluster_rank());
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&sh.full[i], 1);
@@ -151,16 +151,16 @@ __global__ void __launch_bounds__(kThreads, 1) expert_product_fp8(const __grid_c
     const int blocks = (g.in + kBlock - 1) / kBlock;
     bool ok = true;
     if (warp == kCopyWarp) {
-        uint32_t it = 0;
+        const uint32_t full0 = map_to_rank(sh.full, 0);
+        uint32_t s = 0, phase = 1;  // the stage, and the parity of its release
         Fp8Tile w;
         for (int t = first; ok && tile_at(g, table, t, w); t += step) {
             const int mine = rows_of(w, int(rank)), both = rows_of(w, 0) + rows_of(w, 1);
             const int row0 = w.row0 + int(rank) * 128;
-            for (int kb = 0; kb < blocks; ++kb, ++it) {
-                const uint32_t s = it % kStages;
-                ok = warp_wait(&sh.empty[s], ((it / kStages) & 1) ^ 1, abort_flag);
+            for (int kb = 0; kb < blocks; ++kb) {
+                ok = warp_wait(&sh.empty[s], phase, abort_flag);
                 if (!ok) break;
-                const uint32_t bar = map_to_rank(&sh.full[s], 0);
+                const uint32_t bar = full0 + s * 8;
                 if (rank == 0) elect_arrive_expect_tx(&sh.full[s], 2 * kWBytes + uint32_t(both) * 128);
                 const uint32_t a = stage0 + s * kStageBytes;
                 tma_load_3d(a + kXBytes, &g.w, kb * kBlock, w.col0 + int(rank) * 64, w.expert, bar);
@@ -170,36 +170,37 @@ __global__ void __launch_bounds__(kThreads, 1) expert_product_fp8(const __grid_c
                     for (int i = 0; i < mine; i += 16)
                         tma_load_2d(a + i * 128, &g.x_small, kb * kBlock, row0 + i, bar);
                 }
+                next_stage<kStages>(s, phase);
             }
         }
         // every stage is released in this CTA too before it may leave
-        for (uint32_t i = it > kStages ? it - kStages : 0; ok && i < it; ++i)
-            ok = warp_wait(&sh.empty[i % kStages], (i / kStages) & 1, abort_flag);
+        for (int i = 0; ok && i < kStages; ++i) {
+            ok = warp_wait(&sh.empty[s], phase, abort_flag);
+            next_stage<kStages>(s, phase);
+        }
     } else if (warp == kProductWarp) {
         if (rank == 0) {
-            uint32_t it = 0;
-            bool ready = false;  // the next stage and buffer are
+            const uint64_t a0 = operand_desc(stage0, 16, 1024), b0 = operand_desc(stage0 + kXBytes, 16, 1024);
+            constexpr uint32_t desc = instr_desc(0, false, false) | ((kTileCols >> 3) << 17);  // 0: e4m3
+            uint32_t s = 0, phase = 0, buf = 0, free = 1;  // the stage and the buffer, with their parities
+            bool ready = false;                            // they are full and free
             Fp8Tile w;
             for (int t = first; ok && tile_at(g, table, t, w); t += step) {
-                const uint32_t desc = with_n(instr_desc(0, false, false), kTileCols);  // 0: e4m3
-                for (int kb = 0; kb < blocks; ++kb, ++it) {
-                    const uint32_t s = it % kStages, buf = it % kBuffers, free = ((it / kBuffers) & 1) ^ 1;
-                    ok = ready || (warp_wait(&sh.full[s], (it / kStages) & 1, abort_flag) &&
+                for (int kb = 0; kb < blocks; ++kb) {
+                    ok = ready || (warp_wait(&sh.full[s], phase, abort_flag) &&
                                    warp_wait(&sh.acc_empty[buf], free, abort_flag) &&
                                    warp_wait(&sh.peer_empty[buf], free, abort_flag));
                     if (!ok) break;
                     tcgen05_fence_after();
-                    const uint32_t next = it + 1, next_free = ((next / kBuffers) & 1) ^ 1;
-                    const uint32_t looks = look(&sh.full[next % kStages], (next / kStages) & 1) &
-                                           look(&sh.acc_empty[next % kBuffers], next_free) &
-                                           look(&sh.peer_empty[next % kBuffers], next_free);
-                    const uint32_t a = stage0 + s * kStageBytes, b = a + kXBytes;
-#pragma unroll
-                    for (int i = 0; i < kBlock / 32; ++i)
-                        mma_pair_8bit(tmem + buf * kTileCols, operand_desc(a + i * 32, 16, 1024),
-                                      operand_desc(b + i * 32, 16, 1024), desc, i > 0);
-                    mma_commit_pair(&sh.acc_full[buf]);
-                    mma_commit_pair(&sh.empty[s]);
+                    const uint32_t here = s, into = buf;
+                    next_stage<kStages>(s, phase);
+                    next_stage<kBuffers>(buf, free);
+                    const uint32_t looks = look(&sh.full[s], phase) & look(&sh.acc_empty[buf], free) &
+                                           look(&sh.peer_empty[buf], free);
+                    const uint32_t at = here * (kStageBytes >> 4);
+                    mma_pair_8bit_4<32 / 16, 32 / 16>(tmem + into * kTileCols, a0 + at, b0 + at, desc, false);
+                    mma_commit_pair(&sh.acc_full[into]);
+                    mma_commit_pair(&sh.empty[here]);
                     ready = saw(looks);
                 }
             }
@@ -238,43 +239,43 @@ __global__ void __launch_bounds__(kThreads, 1) expert_product_fp8(const __grid_c
         const int c0 = warp / 4 * kWarpColumns, row = (warp & 3) * 32 + lane;
         const uint32_t from = tmem + (uint32_t(warp & 3) << 21) + uint32_t(c0);  // lane 32 * (warp % 4)
         const uint32_t freed = map_to_rank(rank == 0 ? sh.acc_empty : sh.peer_empty, 0);  // CTA 0's, of buffer 0
-        uint32_t it = 0, group = 0;
-        bool ready = false;  // the next block's products are there
+        uint32_t buf = 0, full = 0, group = 0, group_full = 0;  // the buffer and the scales, with their parities
+        bool ready = false;                                     // the next block's products are there
         Fp8Tile w;
         for (int t = first; ok && tile_at(g, table, t, w); t += step) {
             float2 acc[kWarpColumns / 2];
 #pragma unroll
             for (int i = 0; i < kWarpColumns / 2; ++i) acc[i] = make_float2(0.f, 0.f);
-            for (int k0 = 0; ok && k0 < blocks; k0 += kAhead, ++group) {
-                const uint32_t s = group % kScaleSlots;
-                ok = warp_wait(&sh.scale_full[s], (group / kScaleSlots) & 1, abort_flag);
+            for (int k0 = 0; ok && k0 < blocks; k0 += kAhead) {
+                ok = warp_wait(&sh.scale_full[group], group_full, abort_flag);
                 if (!ok) break;
                 float scale[kAhead];
 #pragma unroll
-                for (int j = 0; j < kAhead; ++j) scale[j] = sh.scale[s][j][row];
+                for (int j = 0; j < kAhead; ++j) scale[j] = sh.scale[group][j][row];
                 __syncwarp();
-                elect_arrive(&sh.scale_empty[s]);
+                elect_arrive(&sh.scale_empty[group]);
+                next_stage<kScaleSlots>(group, group_full);
 #pragma unroll
                 for (int j = 0; j < kAhead; ++j) {
                     if (k0 + j >= blocks) break;
-                    const uint32_t buf = it % kBuffers;
-                    ok = ready || warp_wait(&sh.acc_full[buf], (it / kBuffers) & 1, abort_flag);
+                    ok = ready || warp_wait(&sh.acc_full[buf], full, abort_flag);
                     if (!ok) break;
                     tcgen05_fence_after();
-                    const uint32_t looks = look(&sh.acc_full[(it + 1) % kBuffers], ((it + 1) / kBuffers) & 1);
+                    const uint32_t here = buf;
+                    next_stage<kBuffers>(buf, full);
+                    const uint32_t looks = look(&sh.acc_full[buf], full);
                     uint32_t r[2][32];
-                    tmem_load32(from + buf * kTileCols, r[0]);
-                    tmem_load32(from + buf * kTileCols + 32, r[1]);
+                    tmem_load32(from + here * kTileCols, r[0]);
+                    tmem_load32(from + here * kTileCols + 32, r[1]);
                     tmem_wait_load(r[0]);
                     tmem_wait_load(r[1]);
                     tcgen05_fence_before();
                     __syncwarp();
-                    elect_arrive_pair(freed + buf * 8);
+                    elect_arrive_pair(freed + here * 8);
 #pragma unroll
                     for (int i = 0; i < kWarpColumns / 2; ++i)
                         add_scaled(acc[i], r[i / 16][i % 16 * 2], r[i / 16][i % 16 * 2 + 1], scale[j]);
                     ready = saw(looks);
-                    ++it;
                 }
             }
             if (!ok) break;

@@ -185,8 +185,8 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
     __shared__ Shared sh;
     volatile int* abort_flag = &sh.abort;
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = cluster_rank();
+    const int warp = uniform(int(threadIdx.x >> 5)), lane = threadIdx.x & 31;
+    const uint32_t rank = uniform(cluster_rank());
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&sh.full[i], 2);  // a copying lane per operand
@@ -220,7 +220,8 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
     if (warp == kCopyWarpA || warp == kCopyWarpB) {
         const bool is_a = warp == kCopyWarpA;
         const uint32_t to = stage0 + (is_a ? 0 : kHalfBytes);
-        uint32_t it = 0;
+        const uint32_t full0 = map_to_rank(sh.full, 0), tail0 = map_to_rank(sh.tail_full, rank);
+        uint32_t s = 0, phase = 1;  // the stage, and the parity of its release
         Tile w;
         for (int t = first; ok && tile_at<FORM>(g, table, t, w); t += step) {
             const int sum = uniform(w.sum), blocks = (sum + kStepK - 1) / kStepK;
@@ -228,15 +229,14 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
             const int m0 = uniform(w.m0) + int(rank) * 128, n0 = uniform(w.n0) + int(rank) * half;
             const uint32_t mine = is_a ? kHalfBytes : uint32_t(half) * 128;
             const bool ragged = FORM == kWeights && ragged_rows(sum) != 0;
-            for (int kb = 0; kb < blocks; ++kb, ++it) {
-                const uint32_t s = it % kStages;
-                ok = warp_wait(&sh.empty[s], ((it / kStages) & 1) ^ 1, abort_flag);
+            for (int kb = 0; kb < blocks; ++kb) {
+                ok = warp_wait(&sh.empty[s], phase, abort_flag);
                 if (!ok) break;
-                uint32_t bar = map_to_rank(&sh.full[s], 0);
+                uint32_t bar = full0 + s * 8;
                 if (ragged && kb == blocks - 1) {  // each CTA's zeroing warp waits for its own copies
                     if (rank == 0) elect_arrive(&sh.full[s]);
                     elect_arrive_expect_tx(&sh.tail_full[s], mine);
-                    bar = map_to_rank(&sh.tail_full[s], rank);
+                    bar = tail0 + s * 8;
                 } else if (rank == 0) {
                     elect_arrive_expect_tx(&sh.full[s], 2 * mine);
                 }
@@ -260,14 +260,21 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
                 } else {
                     for (int i = 0; i < half; i += 16) tma_load_2d(dst + i * 128, &g.b_small, k0, n0 + i, bar);
                 }
+                next_stage<kStages>(s, phase);
             }
         }
         // every stage is released in this CTA too before it may leave
-        for (uint32_t i = it > kStages ? it - kStages : 0; ok && i < it; ++i)
-            ok = warp_wait(&sh.empty[i % kStages], (i / kStages) & 1, abort_flag);
+        for (int i = 0; ok && i < kStages; ++i) {
+            ok = warp_wait(&sh.empty[s], phase, abort_flag);
+            next_stage<kStages>(s, phase);
+        }
     } else if (warp == kProductWarp) {
         if (rank == 0) {
-            uint32_t it = 0, acc = 0, tails = 0;  // tails: the phases of tail_done, a bit a stage
+            uint32_t s = 0, phase = 0, acc = 0, tails = 0;  // tails: the phases of tail_done, a bit a stage
+            const uint64_t a0 = FORM == kRows ? operand_desc(stage0, 16, 1024) : operand_desc(stage0, kColumn, 1024);
+            const uint64_t b0 = FORM == kWeights ? operand_desc(stage0 + kHalfBytes, kColumn, 1024)
+                                                 : operand_desc(stage0 + kHalfBytes, 16, 1024);
+            constexpr uint32_t kNextA = (FORM == kRows ? 32 : 2048) >> 4, kNextB = (FORM == kWeights ? 2048 : 32) >> 4;
             Tile w;
             for (int t = first; ok && tile_at<FORM>(g, table, t, w); t += step) {
                 const int sum = uniform(w.sum), blocks = (sum + kStepK - 1) / kStepK;
@@ -276,31 +283,24 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
                 const uint32_t d = tmem + (acc & 1) * kTileN;
                 const uint32_t desc = uniform(with_n(instr_desc(g.format, FORM != kRows, FORM == kWeights), w.width));
                 ok = warp_wait(&sh.acc_empty[acc & 1], ((acc >> 1) & 1) ^ 1, abort_flag);
-                for (int kb = 0; ok && kb < blocks; ++kb, ++it) {
-                    const uint32_t s = it % kStages;
-                    ok = warp_wait(&sh.full[s], (it / kStages) & 1, abort_flag);
+                for (int kb = 0; ok && kb < blocks; ++kb) {
+                    ok = warp_wait(&sh.full[s], phase, abort_flag);
                     if (FORM == kWeights && ragged && kb == blocks - 1) {
                         ok = ok && warp_wait_cluster(&sh.tail_done[s], (tails >> s) & 1, abort_flag);
                         tails ^= 1u << s;
                     }
                     if (!ok) break;
                     tcgen05_fence_after();
-                    const uint32_t a = stage0 + s * kStageBytes, b = a + kHalfBytes;
-                    const auto product = [&](int i) {
-                        const uint64_t da = FORM == kRows ? operand_desc(a + i * 32, 16, 1024)
-                                                          : operand_desc(a + i * 2048, kColumn, 1024);
-                        const uint64_t db = FORM == kWeights ? operand_desc(b + i * 2048, kColumn, 1024)
-                                                             : operand_desc(b + i * 32, 16, 1024);
-                        mma_pair_16bit(d, da, db, desc, kb > 0 || i > 0);
-                    };
+                    const uint32_t at = s * (kStageBytes >> 4);
                     if (FORM == kWeights && kb == blocks - 1) {
                         const int steps = (sum - kb * kStepK + 15) / 16;
-                        for (int i = 0; i < steps; ++i) product(i);
+                        for (int i = 0; i < steps; ++i)
+                            mma_pair_16bit(d, a0 + at + i * kNextA, b0 + at + i * kNextB, desc, kb > 0 || i > 0);
                     } else {  // past the end of a sum of kRows and kRowsT are zeros
-#pragma unroll
-                        for (int i = 0; i < kStepK / 16; ++i) product(i);
+                        mma_pair_16bit_4<kNextA, kNextB>(d, a0 + at, b0 + at, desc, kb > 0);
                     }
                     mma_commit_pair(&sh.empty[s]);
+                    next_stage<kStages>(s, phase);
                 }
                 if (ok) mma_commit_pair(&sh.acc_full[acc & 1]);
                 ++acc;

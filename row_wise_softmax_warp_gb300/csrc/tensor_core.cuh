@@ -84,13 +84,29 @@ __device__ __forceinline__ void mma_pair_16bit(uint32_t d, uint64_t a, uint64_t 
         "l"(a), "l"(b), "r"(desc), "r"(uint32_t(add))
         : "memory");
 }
-__device__ __forceinline__ void mma_pair_8bit(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, bool add) {
-    asm volatile(
-        "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "@e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-        "l"(a), "l"(b), "r"(desc), "r"(uint32_t(add))
-        : "memory");
+// Four in a row, whose operands lie NEXT_A and NEXT_B (in units of 16 bytes) apart;
+// all but the first add.
+#define ROWOPS_MMA_PAIR_4(KIND)                                                                              \
+    asm volatile(                                                                                            \
+        "{\n\t.reg .pred p, e;\n\t.reg .b64 a, b;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t" \
+        "@e tcgen05.mma.cta_group::2.kind::" KIND " [%0], %1, %2, %3, p;\n\tsetp.eq.b32 p, 0, 0;\n\t"       \
+        "add.s64 a, %1, %5;\n\tadd.s64 b, %2, %6;\n\t"                                                      \
+        "@e tcgen05.mma.cta_group::2.kind::" KIND " [%0], a, b, %3, p;\n\t"                                  \
+        "add.s64 a, a, %5;\n\tadd.s64 b, b, %6;\n\t"                                                        \
+        "@e tcgen05.mma.cta_group::2.kind::" KIND " [%0], a, b, %3, p;\n\t"                                  \
+        "add.s64 a, a, %5;\n\tadd.s64 b, b, %6;\n\t"                                                        \
+        "@e tcgen05.mma.cta_group::2.kind::" KIND " [%0], a, b, %3, p;\n}\n" ::"r"(d),                        \
+        "l"(a), "l"(b), "r"(desc), "r"(uint32_t(add)), "n"(NEXT_A), "n"(NEXT_B)                              \
+        : "memory")
+template <int NEXT_A, int NEXT_B>
+__device__ __forceinline__ void mma_pair_16bit_4(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, bool add) {
+    ROWOPS_MMA_PAIR_4("f16");
 }
+template <int NEXT_A, int NEXT_B>
+__device__ __forceinline__ void mma_pair_8bit_4(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, bool add) {
+    ROWOPS_MMA_PAIR_4("f8f6f4");
+}
+#undef ROWOPS_MMA_PAIR_4
 // Arrives on the barrier at this offset in both CTAs when every product issued so far is done.
 __device__ __forceinline__ void mma_commit_pair(uint64_t* bar) {
     asm volatile(
@@ -137,7 +153,19 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
         "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
         : "memory");
 }
-// A value that every lane of the warp holds, as lane 0 has it.
+// The next place of a ring of N, and the parity there.
+template <int N>
+__device__ __forceinline__ void next_stage(uint32_t& s, uint32_t& phase) {
+    if (++s == N) {
+        s = 0;
+        phase ^= 1;
+    }
+}
+// A value that every lane of the warp holds, as lane 0 has it.  What decides a
+// warp's role goes through it: in code that the compiler takes to be divergent, uniform
+// registers are out of its reach, and a stage's copies and products took twice as
+// long to issue (32768 rows, 16 experts, 2048 -> 4096 bf16: 326 -> 301 us; one tile of
+// 4096: 21.5 -> 15.2 us).
 template <typename T>
 __device__ __forceinline__ T uniform(T v) {
     return __shfl_sync(kFullMask, v, 0);
