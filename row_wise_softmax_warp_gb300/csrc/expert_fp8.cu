@@ -5,12 +5,11 @@
 //
 // A cluster computes up to 256 rows of a group (128 a CTA) by 128 output columns;
 // a stage of 128 bytes along the sum is one block.  Warps 8, 9 and 10 copy, issue
-// products and prepare scales, otherwise as in
-// expert_matmul.cu.  The tensor cores add up P_b alone; what they cannot do is the
-// pair of scales, which differs from block to block.  So each block's products go
-// to one of four tensor-memory buffers, and eight warps a CTA add scale * P_b to
-// sums that stay in registers (64 a thread) while the next blocks' products run
-// into the others.
+// products and prepare scales, otherwise as in expert_matmul.cu.  The tensor cores
+// add up P_b alone; what they cannot do is the pair of scales, which differs from
+// block to block.  So each block's products go to one of four tensor-memory
+// buffers, and eight warps a CTA add scale * P_b to sums that stay in registers (64
+// a thread) while the next blocks' products run into the others.
 //
 // Rows lie on the lanes of tensor memory here (in expert_matmul.cu the output
 // columns do): a thread's sums then share one scale, read once a block.  With the
@@ -19,13 +18,14 @@
 // products: that way measured 788 TFLOP/s (16384 x 4096 x 4096).  A row tile is
 // 256 rows whatever the group; groups of fewer rows copy only what they have.
 //
-// What bounds it: a stage takes some 515 clocks where its products take 256.  Its
-// 24 KB come from the L2 at some 58 bytes a clock and SM (425 clocks), and a
-// buffer's way from the products to the adding warps and back takes about 1300,
-// most of them looks at barriers in shared memory, which the operands keep busy.
-// Two buffers of 256 columns cover less of that way than four of 128 (1970 against
-// 2150 TFLOP/s at the size above, before results were written in whole lines; now
-// 2400), though these read the rows' operand twice as often.
+// What bounds it: a stage takes some 465 clocks where its products take 256
+// (16384 x 4096 x 4096: 206 us, 2670 TFLOP/s).  Its 24 KB come from the L2 at some 58
+// bytes a clock and SM (425 clocks), and a buffer's way from the products to the
+// adding warps and back takes about 1300, most of them looks at barriers in shared
+// memory, which the operands keep busy.  Two buffers of 256 columns cover less of
+// that way than four of 128 (1970 against 2150 TFLOP/s when that was chosen), though
+// these read the rows' operand twice as often.  Scales read one by one instead of
+// four at once cost 6%.
 #include <cuda_fp8.h>
 
 #include "groups.cuh"
@@ -60,7 +60,8 @@ struct Fp8Args {
     void* y;
     int slots, experts;
     int in, out;
-    bool vec;  // rows of y allow 16-byte stores
+    bool vec;        // rows of y allow 16-byte stores
+    bool scale_vec;  // rows of scales allow 16-byte loads
 };
 
 struct Fp8Shared {
@@ -206,7 +207,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_product_fp8(const __grid_c
             }
         }
     } else if (warp == kScaleWarp) {
-        uint32_t it = 0;
+        uint32_t s = 0, phase = 1;  // the slot, and the parity of its release
         const int out_blocks = (g.out + kBlock - 1) / kBlock;
         Fp8Tile w;
         for (int t = first; ok && tile_at(g, table, t, w); t += step) {
@@ -214,25 +215,35 @@ __global__ void __launch_bounds__(kThreads, 1) expert_product_fp8(const __grid_c
             const float* ws = g.ws + (int64_t(w.expert) * out_blocks + w.col0 / kBlock) * blocks;
             const float* xs = g.xs + (int64_t(w.row0) + rank * 128) * blocks;
             for (int k0 = 0; ok && k0 < blocks; k0 += kAhead) {
-                float x[kAhead][4], wv[kAhead];
+                float x[4][kAhead], wv[kAhead];
+                if (g.scale_vec) {
+                    ld_chunk<kAhead>(ws + k0, wv);
 #pragma unroll
-                for (int j = 0; j < kAhead; ++j) {
-                    const int kb = min(k0 + j, blocks - 1);
-                    wv[j] = __ldg(ws + kb);
+                    for (int i = 0; i < 4; ++i) {
+                        if (i * 32 + lane < rows) ld_chunk<kAhead>(xs + int64_t(i * 32 + lane) * blocks + k0, x[i]);
+                        else
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        x[j][i] = i * 32 + lane < rows ? __ldg(xs + int64_t(i * 32 + lane) * blocks + kb) : 0.f;
+                            for (int j = 0; j < kAhead; ++j) x[i][j] = 0.f;
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < kAhead; ++j) {
+                        const int kb = min(k0 + j, blocks - 1);
+                        wv[j] = __ldg(ws + kb);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            x[i][j] = i * 32 + lane < rows ? __ldg(xs + int64_t(i * 32 + lane) * blocks + kb) : 0.f;
+                    }
                 }
-                const uint32_t s = it % kScaleSlots;
-                ok = warp_wait(&sh.scale_empty[s], ((it / kScaleSlots) & 1) ^ 1, abort_flag);
+                ok = warp_wait(&sh.scale_empty[s], phase, abort_flag);
                 if (!ok) break;
 #pragma unroll
                 for (int j = 0; j < kAhead; ++j)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) sh.scale[s][j][i * 32 + lane] = x[j][i] * wv[j];
+                    for (int i = 0; i < 4; ++i) sh.scale[s][j][i * 32 + lane] = x[i][j] * wv[j];
                 __syncwarp();
                 elect_arrive(&sh.scale_full[s]);
-                ++it;
+                next_stage<kScaleSlots>(s, phase);
             }
         }
     } else if (warp < kAddWarps) {
@@ -331,6 +342,8 @@ cudaError_t launch_expert_matmul_fp8(const uint8_t* x, const float* x_scale, con
     g.out = int(out);
     const int y_size = y_type == ROWOPS_F32 ? 4 : 2;
     g.vec = out * y_size % 16 == 0 && reinterpret_cast<uintptr_t>(y) % 16 == 0;
+    g.scale_vec = (in + kBlock - 1) / kBlock % kAhead == 0 &&
+                  (reinterpret_cast<uintptr_t>(x_scale) | reinterpret_cast<uintptr_t>(w_scale)) % 16 == 0;
     const int64_t tiles = most_row_tiles(slots, experts) * ((out + kTileCols - 1) / kTileCols);
     cudaError_t e = cudaErrorInvalidValue;
     if (tiles >= (int64_t(1) << 30)) return e;  // more than a device's memory holds
