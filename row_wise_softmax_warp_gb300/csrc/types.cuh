@@ -28,9 +28,9 @@ __device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float v) { re
 template <int BYTES>
 struct RawOf;
 template <>
-struct RawOf<2> { using type = uint16_t; };
+struct RawOf<2> { using type = unsigned short; };
 template <>
-struct RawOf<4> { using type = uint32_t; };
+struct RawOf<4> { using type = unsigned int; };
 template <>
 struct RawOf<8> { using type = uint2; };
 template <>
@@ -46,6 +46,9 @@ struct Chunk {
     __device__ __forceinline__ Chunk() : raw() {}
     __device__ __forceinline__ void load(const T* p) { raw = __ldg(reinterpret_cast<const Raw*>(p)); }
     __device__ __forceinline__ void store(T* p) const { *reinterpret_cast<Raw*>(p) = raw; }
+    // for what is touched once: the lines leave the caches first
+    __device__ __forceinline__ void load_once(const T* p) { raw = __ldcs(reinterpret_cast<const Raw*>(p)); }
+    __device__ __forceinline__ void store_once(T* p) const { __stcs(reinterpret_cast<Raw*>(p), raw); }
     __device__ __forceinline__ float get(int i) const { return to_float(v[i]); }
     __device__ __forceinline__ void set(int i, float f) { v[i] = from_float<T>(f); }
 };
