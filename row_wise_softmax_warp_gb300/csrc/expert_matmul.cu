@@ -283,7 +283,7 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
                 const uint32_t d = tmem + (acc & 1) * kTileN;
                 const uint32_t desc = uniform(with_n(instr_desc(g.format, FORM != kRows, FORM == kWeights), w.width));
                 ok = warp_wait(&sh.acc_empty[acc & 1], ((acc >> 1) & 1) ^ 1, abort_flag);
-                bool ready = false;  // kWeights: the stage was seen full
+                bool ready = false;  // the stage was seen full
                 for (int kb = 0; ok && kb < blocks; ++kb) {
                     ok = ready || warp_wait(&sh.full[s], phase, abort_flag);
                     if (FORM == kWeights && ragged && kb == blocks - 1) {
@@ -293,13 +293,10 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
                     if (!ok) break;
                     tcgen05_fence_after();
                     const uint32_t here = s, at = s * (kStageBytes >> 4);
-                    // The look at the next stage overlaps with this one's products (32768 rows,
-                    // 16 experts, 2048 x 4096: 334 -> 313 us; kRows lose up to 6% by it).
-                    uint32_t looks = 0;
-                    if constexpr (FORM == kWeights) {
-                        next_stage<kStages>(s, phase);
-                        if (kb + 1 < blocks) looks = look(&sh.full[s], phase);
-                    }
+                    // The look at the next stage overlaps with this one's products (weights'
+                    // gradient of 32768 rows, 16 experts, 2048 x 4096: 334 -> 313 us).
+                    next_stage<kStages>(s, phase);
+                    const uint32_t looks = kb + 1 < blocks ? look(&sh.full[s], phase) : 0;
                     if (FORM == kWeights && kb == blocks - 1) {
                         const int steps = (sum - kb * kStepK + 15) / 16;
                         for (int i = 0; i < steps; ++i)
@@ -308,8 +305,7 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
                         mma_pair_16bit_4<kNextA, kNextB>(d, a0 + at, b0 + at, desc, kb > 0);
                     }
                     mma_commit_pair(&sh.empty[here]);
-                    if constexpr (FORM == kWeights) ready = saw(looks);
-                    else next_stage<kStages>(s, phase);
+                    ready = saw(looks);
                 }
                 if (ok) mma_commit_pair(&sh.acc_full[acc & 1]);
                 ++acc;
