@@ -51,7 +51,7 @@ constexpr int kThreads = 384;  // 168 registers a thread
 constexpr uint32_t kTmemColumns = 512;
 
 struct Fp8Args {
-    CUtensorMap x;        // boxes of 128 rows
+    CUtensorMap x;        // boxes of 64 rows
     CUtensorMap x_small;  // boxes of 16 rows
     CUtensorMap w;        // boxes of 64 output columns
     const float* xs;
@@ -165,12 +165,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_product_fp8(const __grid_c
                 if (rank == 0) elect_arrive_expect_tx(&sh.full[s], 2 * kWBytes + uint32_t(both) * 128);
                 const uint32_t a = stage0 + s * kStageBytes;
                 tma_load_3d(a + kXBytes, &g.w, kb * kBlock, w.col0 + int(rank) * 64, w.expert, bar);
-                if (mine == 128) {
-                    tma_load_2d(a, &g.x, kb * kBlock, row0, bar);
-                } else {
-                    for (int i = 0; i < mine; i += 16)
-                        tma_load_2d(a + i * 128, &g.x_small, kb * kBlock, row0 + i, bar);
-                }
+                load_rows(a, &g.x, &g.x_small, kb * kBlock, row0, mine, bar);
                 next_stage<kStages>(s, phase);
             }
         }
@@ -330,8 +325,8 @@ cudaError_t launch_expert_matmul_fp8(const uint8_t* x, const float* x_scale, con
     Fp8Args g;
     if (!make_map(&g.w, type, mw, kBlock, 64, true) || !make_map(&g.x_small, type, mx, kBlock, 16, false))
         return cudaErrorInvalidValue;
-    g.x = g.x_small;  // a CTA's rows round up to 128 only from 113 on
-    if (slots > 112 && !make_map(&g.x, type, mx, kBlock, 128, false)) return cudaErrorInvalidValue;
+    g.x = g.x_small;  // a CTA's rows round up to 64 only from 49 on
+    if (slots > 48 && !make_map(&g.x, type, mx, kBlock, 64, false)) return cudaErrorInvalidValue;
     g.xs = x_scale;
     g.ws = w_scale;
     g.offsets = offsets;

@@ -50,7 +50,7 @@ constexpr int threads_of(Form form) { return form == kWeights ? 256 : 224; }
 
 struct ProductArgs {
     CUtensorMap a;        // first operand
-    CUtensorMap b;        // second operand; kRows, kRowsT: boxes of 128 rows
+    CUtensorMap b;        // second operand; kRows, kRowsT: boxes of 64 rows
     CUtensorMap b_small;  // kRows, kRowsT: boxes of 16 rows
     const int32_t* offsets;
     void* out;
@@ -255,10 +255,8 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
                 } else if constexpr (FORM == kWeights) {
                     tma_load_2d(dst, &g.b, n0, sum0 + k0, bar);
                     if (half == 128) tma_load_2d(dst + kColumn, &g.b, n0 + 64, sum0 + k0, bar);
-                } else if (half == 128) {
-                    tma_load_2d(dst, &g.b, k0, n0, bar);
                 } else {
-                    for (int i = 0; i < half; i += 16) tma_load_2d(dst + i * 128, &g.b_small, k0, n0 + i, bar);
+                    load_rows(dst, &g.b, &g.b_small, k0, n0, half, bar);
                 }
                 next_stage<kStages>(s, phase);
             }
@@ -372,8 +370,8 @@ cudaError_t launch_expert_matmul(const void* x, const void* w, const int32_t* of
     ProductArgs g;
     if (!make_map(&g.a, type, mw, 64, transposed ? 64 : 128, true) || !make_map(&g.b_small, type, mx, 64, 16, false))
         return cudaErrorInvalidValue;
-    g.b = g.b_small;  // half a tile is 128 rows only where a tile has more than 224
-    if (slots > 224 && !make_map(&g.b, type, mx, 64, 128, false)) return cudaErrorInvalidValue;
+    g.b = g.b_small;  // half a tile is 64 rows or more only where a tile has more than 96
+    if (slots > 96 && !make_map(&g.b, type, mx, 64, 64, false)) return cudaErrorInvalidValue;
     g.offsets = offsets;
     g.out = y;
     g.slots = int(slots);

@@ -14,12 +14,16 @@ namespace {
 
 constexpr int kRepackThreads = 256;
 
-constexpr int kRepackRows = 4;  // of a warp, one after another
+// Rows of a warp, one after another: four where there are many (a warp whose rows
+// no expert needs costs little then), one where each is a wait of its own.
+constexpr int kRepackRows = 4;
+constexpr int64_t kManyRows = 32768;
 
 struct RepackArgs {
     RepackJob job[2];
     const int32_t* offsets;
     int slots;
+    int each;  // rows of a warp
 };
 
 // The aligned word at `at`, of whose bytes those in [begin, end) are there.
@@ -33,8 +37,8 @@ __device__ __forceinline__ uint32_t word_at(const uint8_t* at, const uint8_t* be
 
 __global__ void __launch_bounds__(kRepackThreads) repack(const RepackArgs g) {
     const int lane = threadIdx.x & 31;
-    const int64_t first = (int64_t(blockIdx.x) * (kRepackThreads / 32) + (threadIdx.x >> 5)) * kRepackRows;
-    for (int64_t r = first; r < first + kRepackRows; ++r) {
+    const int64_t first = (int64_t(blockIdx.x) * (kRepackThreads / 32) + (threadIdx.x >> 5)) * g.each;
+    for (int64_t r = first; r < first + g.each; ++r) {
         const bool second = r >= g.job[0].rows;
         const RepackJob& j = g.job[second];
         const int64_t row = second ? r - g.job[0].rows : r;
@@ -79,7 +83,8 @@ cudaError_t launch_repack(const RepackJob* jobs, int n, const int32_t* offsets, 
     }
     g.offsets = offsets;
     g.slots = int(slots);
-    constexpr int64_t per = kRepackThreads / 32 * kRepackRows;
+    g.each = rows >= kManyRows ? kRepackRows : 1;
+    const int64_t per = kRepackThreads / 32 * g.each;
     repack<<<unsigned((rows + per - 1) / per), kRepackThreads, 0, stream>>>(g);
     note_launches(1);
     return cudaGetLastError();

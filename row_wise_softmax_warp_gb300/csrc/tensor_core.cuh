@@ -153,6 +153,15 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
         "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
         : "memory");
 }
+// `rows` (a multiple of 16) rows of 128 bytes, in as few copies as boxes of 64 and
+// of 16 rows allow: a copy takes some 60 clocks to issue, seven of 16 rows nearly
+// a stage's time.
+__device__ __forceinline__ void load_rows(uint32_t dst, const CUtensorMap* box64, const CUtensorMap* box16, int x, int y,
+                                          int rows, uint32_t bar) {
+    int i = 0;
+    for (; i + 64 <= rows; i += 64) tma_load_2d(dst + i * 128, box64, x, y + i, bar);
+    for (; i < rows; i += 16) tma_load_2d(dst + i * 128, box16, x, y + i, bar);
+}
 // The next place of a ring of N, and the parity there.
 template <int N>
 __device__ __forceinline__ void next_stage(uint32_t& s, uint32_t& phase) {
