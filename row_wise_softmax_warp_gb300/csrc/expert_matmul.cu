@@ -144,7 +144,9 @@ struct Source {
     }
 };
 
-// kRows, kRowsT: a lane holds an output column and a register a row of y.
+// kRows, kRowsT: a lane holds an output column and a register a row of y.  A step
+// from row to row instead of a product a row, and no test where 32 rows are there:
+// 8192 x 768 -> 2048, 30.0 -> 23.5 us.
 template <typename O>
 __device__ __forceinline__ void write_rows(const ProductArgs& g, const Tile& w, const Source& from, int m) {
     for (int c = 0; c < w.n; c += 32) {
@@ -152,9 +154,15 @@ __device__ __forceinline__ void write_rows(const ProductArgs& g, const Tile& w, 
         from.load(c, w.n, r);
         if (m < g.m) {
             O* p = static_cast<O*>(g.out) + int64_t(w.n0 + c) * g.m + m;
+            const int rows = w.n - c;
+            if (rows >= 32) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-                if (c + i < w.n) p[int64_t(i) * g.m] = from_float<O>(__uint_as_float(r[i]));
+                for (int i = 0; i < 32; ++i, p += g.m) *p = from_float<O>(__uint_as_float(r[i]));
+            } else {
+#pragma unroll
+                for (int i = 0; i < 32; ++i, p += g.m)
+                    if (i < rows) *p = from_float<O>(__uint_as_float(r[i]));
+            }
         }
         __syncwarp();
     }
