@@ -19,7 +19,7 @@
 // 256 rows whatever the group; groups of fewer rows copy only what they have.
 //
 // What bounds it: a stage takes some 465 clocks where its products take 256
-// (16384 x 4096 x 4096: 206 us, 2670 TFLOP/s).  Its 24 KB come from the L2 at some 58
+// (16384 x 4096 x 4096: 208 us, 2640 TFLOP/s).  Its 24 KB come from the L2 at some 58
 // bytes a clock and SM (425 clocks), and a buffer's way from the products to the
 // adding warps and back takes about 1300, most of them looks at barriers in shared
 // memory, which the operands keep busy.  Two buffers of 256 columns cover less of

@@ -25,7 +25,7 @@ constexpr int kRowWarps = kRowThreads / 32;
 // A group of 2^shift lanes (SHORT; else a warp, which the compiler makes better
 // use of) per (token, tile of 2^shift * V * U columns); rows
 // shorter than a warp's tile share a warp (64 columns of 262144 tokens, combine:
-// 68 -> 33 us).
+// 68 -> 33 us, 29 since).
 template <typename TI, typename TO, int V, int U, bool SHORT>
 __global__ void __launch_bounds__(kRowThreads)
     gather_rows(const TI* __restrict__ x, const int32_t* __restrict__ slot, TO* __restrict__ out, int64_t items,
