@@ -461,6 +461,8 @@ def _scratch(workspace, need: int, like):
     if workspace is not None:
         if not isinstance(workspace, torch.Tensor) or workspace.device != like.device:
             raise ValueError(f"workspace must be a tensor on {like.device}")
+        if not workspace.is_contiguous():  # its bytes are counted from its values
+            raise ValueError("workspace must be contiguous")
         return workspace, workspace.numel() * workspace.element_size()
     return (torch.empty(need, dtype=torch.uint8, device=like.device), need) if need else (None, 0)
 

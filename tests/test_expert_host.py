@@ -175,3 +175,15 @@ def test_references():
     w2[1, 2, 3] += h
     diff = ((expert_ref.matmul(x, w2, [0, 4, 9]) - y) * dy).sum() / h
     assert abs(diff - expert_ref.wgrad(dy, x, [0, 4, 9])[1, 2, 3]) < 1e-8
+
+
+def test_workspace_has_its_bytes():
+    """A view that names more bytes than it holds, or skips some, is no workspace."""
+    like = torch.empty(1)
+    whole = torch.empty(512, dtype=torch.uint8)
+    assert binding._scratch(whole, 64, like) == (whole, 512)
+    for view in (torch.empty(1, dtype=torch.uint8).expand(1 << 20), whole[::2]):
+        with pytest.raises(ValueError):
+            binding._scratch(view, 64, like)
+    with pytest.raises(ValueError):
+        binding._scratch(bytearray(64), 64, like)
