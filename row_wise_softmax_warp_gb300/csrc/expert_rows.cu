@@ -96,8 +96,10 @@ __global__ void __launch_bounds__(kRowThreads)
     }
 }
 
-// WARPS warps, or (WARPS == 0) a group of 2^shift lanes, per pair (t, j); pairs of one token are neighbours, so its dout
-// row comes from the L1 after the first.
+// WARPS warps, or (WARPS == 0) a group of 2^shift lanes, per pair (t, j); pairs of one
+// token are neighbours, so its dout row comes from the L1 after the first.  A short
+// row's loop makes one or two turns and is not unrolled (262144 x 64: 52.7 -> 41.8 us); the
+// others are (4096 x 4096, k = 4: 60.7 -> 55.2 us).
 template <typename TO, typename TY, int V, int WARPS>
 __global__ void __launch_bounds__(kRowThreads)
     combine_rows_bwd(const TO* __restrict__ dout, const TY* __restrict__ y, const int32_t* __restrict__ slot,
@@ -114,7 +116,7 @@ __global__ void __launch_bounds__(kRowThreads)
     if (s >= 0 && s < slots) {
         const float w = __ldg(weights + p);
         const TO* d = dout + (p / k) * cols;
-#pragma unroll 4
+#pragma unroll (WARPS > 0 ? 4 : 1)
         for (int64_t c = ((WARPS > 0 ? warp % kWarps : 0) * lanes + lane) * V; c < cols; c += kWarps * lanes * V) {
             Chunk<TO, V> a;
             Chunk<TY, V> b, o;
