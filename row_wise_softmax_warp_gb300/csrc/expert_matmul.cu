@@ -66,6 +66,7 @@ struct Shared {
     uint64_t tail_full[kStages], tail_done[kStages];  // kWeights: a stage whose last rows are zeroed
     int warp_tiles[8];
     uint32_t tmem;
+    uint32_t progress;  // stages whose copies are under way, for waits that span many
     int abort;
 };
 
@@ -192,6 +193,7 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
     int* table = reinterpret_cast<int*>(turn);              // the others
     __shared__ Shared sh;
     volatile int* abort_flag = &sh.abort;
+    volatile uint32_t* progress = &sh.progress;
 
     const int warp = uniform(int(threadIdx.x >> 5)), lane = threadIdx.x & 31;
     const uint32_t rank = uniform(cluster_rank());
@@ -206,6 +208,7 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
             mbar_init(&sh.acc_full[i], 1);
             mbar_init(&sh.acc_empty[i], 8);  // the epilogue warps of both CTAs
         }
+        sh.progress = 0;
         sh.abort = 0;
         fence_barrier_init();
     }
@@ -230,6 +233,7 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
         const uint32_t to = stage0 + (is_a ? 0 : kHalfBytes);
         const uint32_t full0 = map_to_rank(sh.full, 0), tail0 = map_to_rank(sh.tail_full, rank);
         uint32_t s = 0, phase = 1;  // the stage, and the parity of its release
+        uint32_t stages_begun = 0;
         Tile w;
         for (int t = first; ok && tile_at<FORM>(g, table, t, w); t += step) {
             const int sum = uniform(w.sum), blocks = (sum + kStepK - 1) / kStepK;
@@ -251,6 +255,7 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
                 const uint32_t dst = to + s * kStageBytes;
                 const int k0 = kb * kStepK;
                 if (is_a) {
+                    *progress = ++stages_begun;
                     if constexpr (FORM == kRows) {
                         tma_load_3d(dst, &g.a, k0, m0, expert, bar);
                     } else if constexpr (FORM == kRowsT) {
@@ -324,7 +329,7 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
             it += (w.sum + kStepK - 1) / kStepK;
             if (ragged_rows(w.sum) == 0) continue;
             const uint32_t s = (it - 1) % kStages;
-            if (!warp_wait(&sh.tail_full[s], (tails >> s) & 1, abort_flag)) break;
+            if (!warp_wait_stages(&sh.tail_full[s], (tails >> s) & 1, abort_flag, progress)) break;
             tails ^= 1u << s;
             zero_ragged(stages + s * kStageBytes, w.sum, w.width);
             fence_async_shared();
@@ -336,7 +341,7 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
         Tile w;
         for (int t = first; tile_at<FORM>(g, table, t, w); t += step) {
             const bool zero = uniform(w.sum) == 0;
-            if (!zero && !warp_wait(&sh.acc_full[acc & 1], (acc >> 1) & 1, abort_flag)) break;
+            if (!zero && !warp_wait_stages(&sh.acc_full[acc & 1], (acc >> 1) & 1, abort_flag, progress)) break;
             tcgen05_fence_after();
             const Source from{tmem + (uint32_t(warp * 32) << 16) + (acc & 1) * kTileN,
                               map_to_rank(&sh.acc_empty[acc & 1], 0), zero};

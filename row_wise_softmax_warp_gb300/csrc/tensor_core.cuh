@@ -119,7 +119,9 @@ __device__ __forceinline__ void mma_commit_pair(uint64_t* bar) {
 
 // ---------------------------------------------------------- tiled TMA, barriers
 
-constexpr uint32_t kQuickPolls = 1u << 22;  // some seconds at most
+// Polls of a wait: a poll takes 35 clocks on an idle SM and some 280 under the tensor
+// cores' traffic, so a wait runs out after 0.07 to some 0.6 s.
+constexpr uint32_t kQuickPolls = 1u << 22;
 
 // Called by a whole warp; the elected lane acts.
 __device__ __forceinline__ void elect_arrive(uint64_t* bar) {
@@ -208,13 +210,13 @@ __device__ __forceinline__ void let_copies_land() {
     for (int i = 0; i < 1000; ++i) __nanosleep(1000);
 }
 
-// Bounded wait of a whole warp: one lane polls and a vote tells the others, so the
-// compiler sees one answer for all; false (after raising the abort) on timeout or
-// abort.  No suspend hint: between two stages of products the wait's
+// Polls of a whole warp: one lane polls and a vote tells the others, so the compiler
+// sees one answer for all.  No suspend hint: between two stages of products the wait's
 // own latency is what counts.  The acquire is the CTA's: TMA's and tcgen05's
 // arrivals order what they did.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
-    for (uint32_t i = 0; i < kQuickPolls; ++i) {
+enum class Polled { kDone, kAborted, kRanOut };
+__device__ __forceinline__ Polled warp_poll(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint32_t polls) {
+    for (uint32_t i = 0; i < polls; ++i) {
         uint32_t done;
         asm volatile(
             "{\n\t.reg .pred p, e;\n\tsetp.ne.u32 p, 0, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
@@ -225,9 +227,31 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
             : "memory");
         if (__any_sync(kFullMask, done)) {
             __syncwarp();
-            return true;
+            return Polled::kDone;
         }
-        if (__any_sync(kFullMask, *abort_flag)) return false;
+        if (__any_sync(kFullMask, *abort_flag)) return Polled::kAborted;
+    }
+    return Polled::kRanOut;
+}
+// Bounded wait of a whole warp; false (after raising the abort) on timeout or abort.
+// For what comes after a stage's or a tile's writing at the latest.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+    const Polled p = warp_poll(bar, parity, abort_flag, kQuickPolls);
+    if (p == Polled::kRanOut && (threadIdx.x & 31) == 0) raise_abort(abort_flag);
+    return p == Polled::kDone;
+}
+// For what comes after a whole sum, or several, which may take seconds: the polls
+// start again as long as `progress` moves, which a copying warp of the same CTA counts
+// up a stage.  Bounded, as there are so many stages and no more.
+__device__ __forceinline__ bool warp_wait_stages(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                                 const volatile uint32_t* progress, uint32_t polls = kQuickPolls) {
+    uint32_t seen = uniform(*progress);
+    for (;;) {
+        const Polled p = warp_poll(bar, parity, abort_flag, polls);
+        if (p != Polled::kRanOut) return p == Polled::kDone;
+        const uint32_t now = uniform(*progress);
+        if (now == seen) break;
+        seen = now;
     }
     if ((threadIdx.x & 31) == 0) raise_abort(abort_flag);
     return false;
