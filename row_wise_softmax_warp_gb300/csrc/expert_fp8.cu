@@ -80,10 +80,10 @@ struct Fp8Tile {
     int col0;
 };
 
-__device__ __forceinline__ bool tile_at(const Fp8Args& g, const int* table, int t, Fp8Tile& w) {
+__device__ __forceinline__ bool tile_at(const Fp8Args& g, const int* table, int t, int tiles, Fp8Tile& w) {
+    if (t >= tiles) return false;
     const int across = (g.out + kTileCols - 1) / kTileCols;
     const int row = t / across;
-    if (row >= table[g.experts]) return false;
     w.expert = uniform(tile_expert(table, g.experts, row, w.expert));
     const RowRange r = group_rows(g.offsets, w.expert, g.slots);
     const int at = (row - table[w.expert]) * kTileRows;
@@ -149,13 +149,14 @@ __global__ void __launch_bounds__(kThreads, 1) expert_product_fp8(const __grid_c
     const uint32_t tmem = uniform(sh.tmem), stage0 = uniform(smem_addr(stages));
 
     const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
+    const int tiles = uniform(all_tiles(table[g.experts], (g.out + kTileCols - 1) / kTileCols));
     const int blocks = (g.in + kBlock - 1) / kBlock;
     bool ok = true;
     if (warp == kCopyWarp) {
         const uint32_t full0 = map_to_rank(sh.full, 0);
         uint32_t s = 0, phase = 1;  // the stage, and the parity of its release
         Fp8Tile w;
-        for (int t = first; ok && tile_at(g, table, t, w); t += step) {
+        for (int t = first; ok && tile_at(g, table, t, tiles, w); t += step) {
             const int mine = rows_of(w, int(rank)), both = rows_of(w, 0) + rows_of(w, 1);
             const int row0 = w.row0 + int(rank) * 128;
             for (int kb = 0; kb < blocks; ++kb) {
@@ -181,7 +182,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_product_fp8(const __grid_c
             uint32_t s = 0, phase = 0, buf = 0, free = 1;  // the stage and the buffer, with their parities
             bool ready = false;                            // they are full and free
             Fp8Tile w;
-            for (int t = first; ok && tile_at(g, table, t, w); t += step) {
+            for (int t = first; ok && tile_at(g, table, t, tiles, w); t += step) {
                 for (int kb = 0; kb < blocks; ++kb) {
                     ok = ready || (warp_wait(&sh.full[s], phase, abort_flag) &&
                                    warp_wait(&sh.acc_empty[buf], free, abort_flag) &&
@@ -205,7 +206,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_product_fp8(const __grid_c
         uint32_t s = 0, phase = 1;  // the slot, and the parity of its release
         const int out_blocks = (g.out + kBlock - 1) / kBlock;
         Fp8Tile w;
-        for (int t = first; ok && tile_at(g, table, t, w); t += step) {
+        for (int t = first; ok && tile_at(g, table, t, tiles, w); t += step) {
             const int rows = min(128, w.rows - int(rank) * 128);
             const float* ws = g.ws + (int64_t(w.expert) * out_blocks + w.col0 / kBlock) * blocks;
             const float* xs = g.xs + (int64_t(w.row0) + rank * 128) * blocks;
@@ -248,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_product_fp8(const __grid_c
         uint32_t buf = 0, full = 0, group = 0, group_full = 0;  // the buffer and the scales, with their parities
         bool ready = false;                                     // the next block's products are there
         Fp8Tile w;
-        for (int t = first; ok && tile_at(g, table, t, w); t += step) {
+        for (int t = first; ok && tile_at(g, table, t, tiles, w); t += step) {
             float2 acc[kWarpColumns / 2];
 #pragma unroll
             for (int i = 0; i < kWarpColumns / 2; ++i) acc[i] = make_float2(0.f, 0.f);
@@ -341,7 +342,7 @@ cudaError_t launch_expert_matmul_fp8(const uint8_t* x, const float* x_scale, con
                   (reinterpret_cast<uintptr_t>(x_scale) | reinterpret_cast<uintptr_t>(w_scale)) % 16 == 0;
     const int64_t tiles = most_row_tiles(slots, experts) * ((out + kTileCols - 1) / kTileCols);
     cudaError_t e = cudaErrorInvalidValue;
-    if (tiles >= (int64_t(1) << 30)) return e;  // more than a device's memory holds
+    if (tiles >= kMostTiles) return e;  // more than a device's memory holds
     with_type(y_type, [&](auto o) {
         e = launch_pairs<expert_product_fp8<decltype(o)>>(tiles, kThreads, kMostSmem, stream, g);
     });

@@ -80,13 +80,22 @@ struct Tile {
     int sum;      // its length
 };
 
+// The number of tiles.
 template <Form FORM>
-__device__ __forceinline__ bool tile_at(const ProductArgs& g, const int* table, int t, Tile& w) {
+__device__ __forceinline__ int tiles_in_all(const ProductArgs& g, const int* table) {
+    const int tiles_m = (g.m + 255) / 256;
+    if constexpr (FORM == kWeights) return (g.n + kTileN - 1) / kTileN * g.experts * tiles_m;  // the host has seen it
+    else return all_tiles(table[g.experts], tiles_m);
+}
+
+// Tile t of `tiles`; false past the last.
+template <Form FORM>
+__device__ __forceinline__ bool tile_at(const ProductArgs& g, const int* table, int t, int tiles, Tile& w) {
+    if (t >= tiles) return false;
     const int tiles_m = (g.m + 255) / 256;
     if constexpr (FORM == kWeights) {
         const int tiles_n = (g.n + kTileN - 1) / kTileN;
         const int row = t / tiles_m;
-        if (row >= tiles_n * g.experts) return false;
         w.expert = row / tiles_n;
         w.m0 = t % tiles_m * 256;
         w.n0 = row % tiles_n * kTileN;
@@ -97,7 +106,6 @@ __device__ __forceinline__ bool tile_at(const ProductArgs& g, const int* table, 
         w.sum = r.count;
     } else {
         const int row = t / tiles_m;
-        if (row >= table[g.experts]) return false;
         const RowTile r = row_tile(g.offsets, g.experts, g.slots, table, row, w.expert);
         w.expert = uniform(r.expert);
         w.m0 = t % tiles_m * 256;
@@ -226,7 +234,7 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
     tcgen05_fence_after();
     const uint32_t tmem = uniform(sh.tmem), stage0 = uniform(smem_addr(stages));
 
-    const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
+    const int first = blockIdx.x >> 1, step = gridDim.x >> 1, tiles = uniform(tiles_in_all<FORM>(g, table));
     bool ok = true;
     if (warp == kCopyWarpA || warp == kCopyWarpB) {
         const bool is_a = warp == kCopyWarpA;
@@ -235,7 +243,7 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
         uint32_t s = 0, phase = 1;  // the stage, and the parity of its release
         uint32_t stages_begun = 0;
         Tile w;
-        for (int t = first; ok && tile_at<FORM>(g, table, t, w); t += step) {
+        for (int t = first; ok && tile_at<FORM>(g, table, t, tiles, w); t += step) {
             const int sum = uniform(w.sum), blocks = (sum + kStepK - 1) / kStepK;
             const int half = uniform(w.width) / 2, expert = uniform(w.expert), sum0 = uniform(w.sum0);
             const int m0 = uniform(w.m0) + int(rank) * 128, n0 = uniform(w.n0) + int(rank) * half;
@@ -287,7 +295,7 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
                                                  : operand_desc(stage0 + kHalfBytes, 16, 1024);
             constexpr uint32_t kNextA = (FORM == kRows ? 32 : 2048) >> 4, kNextB = (FORM == kWeights ? 2048 : 32) >> 4;
             Tile w;
-            for (int t = first; ok && tile_at<FORM>(g, table, t, w); t += step) {
+            for (int t = first; ok && tile_at<FORM>(g, table, t, tiles, w); t += step) {
                 const int sum = uniform(w.sum), blocks = (sum + kStepK - 1) / kStepK;
                 if (blocks == 0) continue;
                 const bool ragged = FORM == kWeights && ragged_rows(sum) != 0;
@@ -325,7 +333,7 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
     } else if (FORM == kWeights && warp == kZeroWarp) {
         uint32_t it = 0, tails = 0;  // tails: the phases of tail_full
         Tile w;
-        for (int t = first; tile_at<FORM>(g, table, t, w); t += step) {
+        for (int t = first; tile_at<FORM>(g, table, t, tiles, w); t += step) {
             it += (w.sum + kStepK - 1) / kStepK;
             if (ragged_rows(w.sum) == 0) continue;
             const uint32_t s = (it - 1) % kStages;
@@ -339,7 +347,7 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
     } else {
         uint32_t acc = 0;
         Tile w;
-        for (int t = first; tile_at<FORM>(g, table, t, w); t += step) {
+        for (int t = first; tile_at<FORM>(g, table, t, tiles, w); t += step) {
             const bool zero = uniform(w.sum) == 0;
             if (!zero && !warp_wait_stages(&sh.acc_full[acc & 1], (acc >> 1) & 1, abort_flag, progress)) break;
             tcgen05_fence_after();
@@ -360,7 +368,6 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
     if (warp == kProductWarp) tmem_dealloc_pair(tmem, kTmemColumns);
 }
 
-constexpr int64_t kMostTiles = int64_t(1) << 30;  // more than a device's memory holds
 constexpr size_t kMostSmem = 1024 + kStages * size_t(kStageBytes) + 4 * kTurnBytes;
 static_assert(4 * kTurnBytes >= (kMaxExperts + 1) * 4, "the table of tiles lies where the others turn rows");
 

@@ -12,6 +12,20 @@ namespace rowops {
 
 constexpr int kMaxExperts = 1024;
 
+// Groups that overlap (offsets that fall and rise again: bad ones, but stay in
+// bounds) can name every row up to 512 times, so counts of tiles are added up
+// unsigned, which holds 512 * 2^30 rows in tiles of 256, and cut at kMostTiles.
+// Groups that do not overlap have fewer: the host refuses more than kMostTiles.
+constexpr int kMostTiles = 1 << 30;
+
+__host__ __device__ constexpr unsigned tiles_of(int rows, int tile) { return unsigned(rows / tile + (rows % tile != 0)); }
+__host__ __device__ constexpr int cut_tiles(unsigned n) { return n < unsigned(kMostTiles) ? int(n) : kMostTiles; }
+// Tiles of `row_tiles` rows of tiles, `across` each: a tile's number plus a grid stays in 32 bits.
+__host__ __device__ constexpr int all_tiles(int row_tiles, int across) {
+    const int64_t n = int64_t(row_tiles) * across;
+    return n < kMostTiles ? int(n) : kMostTiles;
+}
+
 struct RowRange {
     int first, count;
 };
@@ -35,7 +49,7 @@ __device__ __forceinline__ bool find_row_tile(const int32_t* offsets, int expert
         const int e = base + lane;
         RowRange r{0, 0};
         if (e < experts) r = group_rows(offsets, e, slots);
-        const int n = r.count / TILE + (r.count % TILE != 0);
+        const int n = int(tiles_of(r.count, TILE));
         int upto = n;  // inclusive scan over the warp
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -57,40 +71,38 @@ __device__ __forceinline__ bool find_row_tile(const int32_t* offsets, int expert
     return false;
 }
 
-// table[e] = row tiles of the experts before e (table[experts]: all).  Called by
-// the whole block, which synchronises before the table is read; scratch: an int a warp.
+// table[e] = row tiles of the experts before e (table[experts]: all), cut at kMostTiles.
+// Called by the whole block, which synchronises before the table is read; scratch: an int a warp.
 template <int TILE, int NT>
 __device__ __forceinline__ void build_tile_table(const int32_t* offsets, int experts, int slots, int* table,
                                                  int* scratch) {
+    static_assert(TILE >= 256, "512 groups of 2^30 rows have to fit the sum");
     constexpr int kPer = (kMaxExperts + NT - 1) / NT;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int per = (experts + NT - 1) / NT, first = threadIdx.x * per;  // a run of experts each
-    int n[kPer], sum = 0;
+    unsigned n[kPer], sum = 0;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         n[i] = 0;
-        if (i < per && first + i < experts) {
-            const int rows = group_rows(offsets, first + i, slots).count;
-            n[i] = rows / TILE + (rows % TILE != 0);
-        }
+        if (i < per && first + i < experts) n[i] = tiles_of(group_rows(offsets, first + i, slots).count, TILE);
         sum += n[i];
     }
-    int upto = sum;
+    unsigned upto = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(kFullMask, upto, o);
+        const unsigned v = __shfl_up_sync(kFullMask, upto, o);
         if (lane >= o) upto += v;
     }
-    if (lane == 31) scratch[warp] = upto;
+    if (lane == 31) scratch[warp] = int(upto);
     __syncthreads();
-    int before = upto - sum;
-    for (int w = 0; w < warp; ++w) before += scratch[w];
+    unsigned before = upto - sum;
+    for (int w = 0; w < warp; ++w) before += unsigned(scratch[w]);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-        if (i < per && first + i < experts) table[first + i] = before;
+        if (i < per && first + i < experts) table[first + i] = cut_tiles(before);
         before += n[i];
     }
-    if (threadIdx.x == NT - 1) table[experts] = before;
+    if (threadIdx.x == NT - 1) table[experts] = cut_tiles(before);
 }
 
 // The expert of row tile `tile`, 0 <= tile < table[experts], for tiles asked for in

@@ -9,6 +9,8 @@ import numpy as np
 import pytest
 import torch
 
+import expert_ref
+
 pytestmark = pytest.mark.gpu
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -97,3 +99,29 @@ def test_long_sums_of_rows(ro, transposed):
     y = ro.rowops_expert_matmul(x, w, transposed=transposed)
     assert ro.library().rowops_pipeline_timeouts() == before
     assert y.tolist() == [[0.0] * 8, [6.0] * 8, [8.0] * 8]
+
+
+@pytest.mark.parametrize("experts", [225, 449, 1024])
+def test_many_experts(ro, experts):
+    """More experts than a block of the products has threads: whole numbers, so sums are exact."""
+    rng = np.random.default_rng(experts)
+    sizes = rng.choice([0, 0, 1, 2, 7, 33], experts)
+    sizes[0], sizes[-1], sizes[experts // 2] = 3, 5, 300
+    offsets = np.cumsum([0, *sizes]).astype(np.int32)
+    at, rows = torch.from_numpy(offsets).cuda(), int(offsets[-1])
+    x, w, dy = (torch.from_numpy(rng.integers(-1, 2, shape).astype(np.float32)).cuda().half()
+                for shape in ((rows, 128), (experts, 136, 128), (rows, 136)))
+    x64, w64, dy64 = (t.double().cpu().numpy() for t in (x, w, dy))
+    want = expert_ref.matmul(x64, w64, offsets)
+    assert (ro.rowops_expert_matmul(x, w, at).double().cpu().numpy() == want).all()
+    dx = ro.rowops_expert_matmul(dy, w, at, transposed=True)
+    assert (dx.double().cpu().numpy() == expert_ref.matmul(dy64, w64.transpose(0, 2, 1), offsets)).all()
+    dw = ro.rowops_expert_matmul_wgrad(dy, x, at)
+    assert (dw.double().cpu().numpy() == expert_ref.wgrad(dy64, x64, offsets)).all()
+    # -1, 0 and 1 are exact in e4m3; with scales of powers of two so are the products
+    xs = torch.full((rows, 1), 2.0, device="cuda")
+    ws = torch.from_numpy(2.0 ** rng.integers(-2, 3, (experts, 2, 1))).float().cuda()
+    y = ro.rowops_expert_matmul_fp8(x.to(torch.float8_e4m3fn), xs, w.to(torch.float8_e4m3fn), ws, at,
+                                    dtype=torch.float32)
+    scale = 2.0 * expert_ref.spread(ws.double().cpu().numpy(), 128, 136, 1)
+    assert (y.double().cpu().numpy() == expert_ref.matmul(x64, w64 * scale, offsets)).all()
