@@ -245,8 +245,7 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
 // up a stage.  Bounded, as there are so many stages and no more.
 __device__ __forceinline__ bool warp_wait_stages(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
                                                  const volatile uint32_t* progress, uint32_t polls = kQuickPolls) {
-    uint32_t seen = uniform(*progress);
-    for (;;) {
+    for (uint32_t seen = ~0u;;) {  // looked at only when the polls have run out
         const Polled p = warp_poll(bar, parity, abort_flag, polls);
         if (p != Polled::kRanOut) return p == Polled::kDone;
         const uint32_t now = uniform(*progress);
