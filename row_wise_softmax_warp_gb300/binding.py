@@ -405,6 +405,9 @@ class _Placed:
     """Makes a tensor's device, and a stream if one is given, current for allocations and the launch."""
 
     def __init__(self, t: torch.Tensor, stream):
+        device = getattr(stream, "device", None)  # a handle does not say
+        if device is not None and device != t.device:
+            raise ValueError(f"stream is on {device}, the tensors are on {t.device}")
         self.guards = [torch.cuda.device(t.device)]
         if stream is not None:
             if not isinstance(stream, torch.cuda.Stream):
