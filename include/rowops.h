@@ -439,9 +439,11 @@ int rowops_expert_plan(const float *indices, const float *values, int32_t *offse
 
 /*
  * Token rows to their experts' slots: out[slot[t][j]] = x[t], rounded to
- * out_type.  x: rows x cols of x_type; slot: rows x k; out: slots x cols.  A slot
- * named twice gets one of its rows.  Its gradient is rowops_expert_combine of
- * the slots' gradients with weights NULL.  cols == 0 is a no-op.
+ * out_type.  x: rows x cols of x_type; slot: rows x k; out: slots x cols.  No plan
+ * names a slot twice; where the caller's does, each value of that row of out is of
+ * one of the rows, which one may differ from value to value and from call to call.
+ * The gradient is rowops_expert_combine of the slots' gradients with weights NULL.
+ * cols == 0 is a no-op.
  */
 int rowops_expert_gather(const void *x, const int32_t *slot, void *out, int64_t rows, int64_t k,
                          int64_t cols, int64_t slots, int x_type, int out_type,
@@ -462,8 +464,9 @@ int rowops_expert_combine(const void *y, const int32_t *slot, const float *weigh
  *   dy[slot[t][j]] = w[t][j] * dout[t]
  *   dweights[t][j] = sum_c dout[t][c] * y[slot[t][j]][c]   (0 for a skipped slot)
  * dout: rows x cols of out_type; y, dy: slots x cols of y_type; slot, weights,
- * dweights: rows x k.  A row of dy that two pairs name gets one of their rows.
- * cols == 0 writes dweights (all 0).
+ * dweights: rows x k.  A row of dy that two pairs name holds, value by value, one of
+ * theirs and not their sum, as for rowops_expert_gather.  cols == 0 writes dweights
+ * (all 0).
  */
 int rowops_expert_combine_bwd(const void *dout, const void *y, const int32_t *slot,
                               const float *weights, void *dy, float *dweights, int64_t rows,

@@ -8,7 +8,8 @@
 // (or written) once however many experts it has, and an expert row is touched
 // once; the plan's order decides only where the rows lie.  A slot outside the
 // expert matrix is skipped.  Sums are fp32 in the order of the choices (and of
-// the columns, for dw), so results repeat bit for bit.
+// the columns, for dw), so results repeat bit for bit.  A slot that two pairs name
+// is written by both, tile by tile in no fixed order.
 //
 // Blocks of 128 threads were 2..3% faster than of 256 and 5% faster than of 512;
 // combine's rows and results marked to leave the caches first: 19.2 -> 18.0 us (16384 x
