@@ -485,10 +485,11 @@ int rowops_expert_combine_bwd(const void *dout, const void *y, const int32_t *sl
  * The tensor cores' kernel reads matrices whose first value and rows lie on
  * 16-byte boundaries.  For others give a workspace: they are copied there first
  * (rowops_expert_matmul_workspace(...) bytes cover row widths that are no multiple
- * of 8 values, and are 0 where all are).  Without one, or with too little, a slower
- * kernel takes them as they are, so NULL and 0 are always allowed; a workspace
- * that is not 16-byte aligned is ROWOPS_ERR_WORKSPACE.  Concurrent calls need
- * separate workspaces.
+ * of 8 values, and are 0 where all are; a matrix with whole rows that starts off a
+ * 16-byte boundary needs its own bytes and 512 more on top).  Without one, or with
+ * too little, a slower kernel takes them as they are (6 to 16 times), so NULL and 0
+ * are always allowed; a workspace that is not 16-byte aligned is
+ * ROWOPS_ERR_WORKSPACE.  Concurrent calls need separate workspaces.
  * Waits of the pipelined kernel are bounded: one that runs out (a defect) leaves
  * y incomplete and counts one timeout, see rowops_pipeline_timeouts().
  */

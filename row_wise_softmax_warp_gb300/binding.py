@@ -470,6 +470,12 @@ def _scratch(workspace, need: int, like):
     return (torch.empty(need, dtype=torch.uint8, device=like.device), need) if need else (None, 0)
 
 
+def _shifted_room(*operands) -> int:
+    """Bytes for copies of the matrices (tensor, rows, bytes of a row) that start off a 16-byte boundary; the
+    workspace functions of the library see only the widths, and count rows that are no multiple of 16 bytes."""
+    return sum(rows * size + 512 for t, rows, size in operands if t.data_ptr() % 16 and size % 16 == 0)
+
+
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
@@ -594,7 +600,8 @@ def rowops_expert_matmul(x, w, offsets=None, y=None, transposed=False, workspace
     """y[s] = w[e] @ x[s] for the rows offsets[e] <= s < offsets[e + 1] of x (slots, in).
 
     w: (experts, out, in), or (experts, in, out) with transposed.  Rows of a new y that no expert has are not written.
-    A workspace (one is made where it is None) takes copies of matrices whose rows are no multiple of 16 bytes."""
+    A workspace (one is made where it is None) takes copies of matrices whose rows are no multiple of 16 bytes or
+    that start off a 16-byte boundary."""
     _typed(x, "x", _HALVES)
     if _elsewhere(x, stream):
         with _Placed(x, stream):
@@ -611,6 +618,8 @@ def rowops_expert_matmul(x, w, offsets=None, y=None, transposed=False, workspace
     lib, flag = library(), 1 if transposed else 0
     need = 0 if in_cols % 8 == 0 and out_cols % 8 == 0 else lib.rowops_expert_matmul_workspace(
         slots, in_cols, out_cols, experts, flag)
+    if (x.data_ptr() | w.data_ptr()) % 16 and workspace is None:
+        need += _shifted_room((x, slots, 2 * in_cols), (w, experts * w.shape[1], 2 * w.shape[2]))
     workspace, size = _scratch(workspace, need, x)
     _check(lib.rowops_expert_matmul(x.data_ptr(), w.data_ptr(), _ptr(offsets), y.data_ptr(), slots, in_cols, out_cols,
                                     experts, flag, _DTYPES[dtype], _ptr(workspace), size, _raw_stream(device)))
@@ -638,7 +647,10 @@ def rowops_expert_matmul_wgrad(dy, x, offsets=None, dw=None, dtype=None, workspa
     else:
         _typed(dw, "dw", (dy.dtype, torch.float32) if dtype is None else (dtype,), shape, device)
     lib = library()
-    workspace, size = _scratch(workspace, lib.rowops_expert_matmul_wgrad_workspace(slots, in_cols, out_cols), dy)
+    need = lib.rowops_expert_matmul_wgrad_workspace(slots, in_cols, out_cols)
+    if (dy.data_ptr() | x.data_ptr()) % 16 and workspace is None:
+        need += _shifted_room((dy, slots, 2 * out_cols), (x, slots, 2 * in_cols))
+    workspace, size = _scratch(workspace, need, dy)
     _check(lib.rowops_expert_matmul_wgrad(dy.data_ptr(), x.data_ptr(), _ptr(offsets), dw.data_ptr(), slots, in_cols,
                                           out_cols, experts, _DTYPES[dy.dtype], _DTYPES.get(dw.dtype, -1),
                                           _ptr(workspace), size, _raw_stream(device)))
@@ -687,8 +699,10 @@ def rowops_expert_matmul_fp8(xq, xs, wq, ws, offsets=None, y=None, dtype=torch.b
     else:
         _typed(y, "y", _FLOATS, (slots, out_cols), device)
     lib = library()
-    workspace, size = _scratch(
-        workspace, lib.rowops_expert_matmul_fp8_workspace(slots, in_cols, out_cols, experts), xq)
+    need = lib.rowops_expert_matmul_fp8_workspace(slots, in_cols, out_cols, experts)
+    if (xq.data_ptr() | wq.data_ptr()) % 16 and workspace is None:
+        need += _shifted_room((xq, slots, in_cols), (wq, experts * out_cols, in_cols))
+    workspace, size = _scratch(workspace, need, xq)
     _check(lib.rowops_expert_matmul_fp8(xq.data_ptr(), xs.data_ptr(), wq.data_ptr(), ws.data_ptr(), _ptr(offsets),
                                         y.data_ptr(), slots, in_cols, out_cols, experts, _DTYPES.get(y.dtype, -1),
                                         _ptr(workspace), size, _raw_stream(device)))
