@@ -404,8 +404,8 @@ int rowops_teacher_ce(const float *student, const float *teacher, float *grad, f
  *   - offsets, slot and indices are device data that no host check sees.  Their
  *     use is checked on the device: a slot outside [0, slots) is skipped, and
  *     offsets are clamped to 0..slots with no group ending before it starts.
- *     Rows that no group or slot names are not read, and output rows that none
- *     names are left as they were.
+ *     Results do not depend on rows that no group or slot names (the products may
+ *     read them), and output rows that none names are left as they were.
  */
 typedef enum {
     ROWOPS_F32 = 0,
