@@ -538,6 +538,14 @@ int rowops_quantize_blocks(const void *x, uint8_t *q, float *scale, int64_t batc
  * as rowops_quantize_blocks writes them with block_rows 1 and 128; y: slots x
  * out_cols of y_type.  offsets, workspace (for in_cols that are no multiple of 16)
  * and timeouts as for rowops_expert_matmul.
+ * A block's two scales are multiplied first, in fp32: where their product leaves the
+ * range of normal numbers (2^-126 .. 2^128) it loses bits or becomes 0 or infinite,
+ * and y with it.
+ * The gradient with respect to x is this call on dy, quantised by rows, with the
+ * bytes of wq and the scales ws transposed within each expert (blocks of 128 x 128
+ * stay blocks, so nothing is quantised again).  The gradient with respect to the
+ * weights sums over rows, across which these scales differ: take
+ * rowops_expert_matmul_wgrad on fp16 or bf16 rows.
  */
 size_t rowops_expert_matmul_fp8_workspace(int64_t slots, int64_t in_cols, int64_t out_cols,
                                           int64_t experts);
