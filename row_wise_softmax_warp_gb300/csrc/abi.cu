@@ -10,6 +10,7 @@
 #include <cstdint>
 
 #include <initializer_list>
+#include <mutex>
 #include <utility>
 
 #include "rowops.h"
@@ -34,6 +35,33 @@ int sm_count() {
     if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
     if (dev < 64) cached[dev].store(n, std::memory_order_relaxed);
     return n;
+}
+
+cudaError_t allow_smem(const void* kernel, size_t bytes) {
+    struct Allowed {
+        const void* kernel;
+        int dev;
+        size_t bytes;
+    };
+    static std::mutex mu;
+    static Allowed known[256];
+    static int used = 0;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::lock_guard<std::mutex> lock(mu);  // held over the setting, so that no older one comes after it
+    int i = 0;
+    while (i < used && !(known[i].kernel == kernel && known[i].dev == dev)) ++i;
+    if (i < 256) {
+        if (i == used) known[used++] = {kernel, dev, bytes};
+        if (known[i].bytes < bytes) known[i].bytes = bytes;
+        bytes = known[i].bytes;
+    } else {  // no place to remember it: the runtime knows the limit
+        cudaFuncAttributes attr;
+        e = cudaFuncGetAttributes(&attr, kernel);
+        if (e != cudaSuccess || size_t(attr.maxDynamicSharedSizeBytes) >= bytes) return e;
+    }
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
 }
 
 }  // namespace rowops

@@ -13,8 +13,6 @@
 // blocks split among threads: one thread an expert took 8 of 21 us), ranks its
 // pairs and writes them.  One block needs no counts from others: up to
 // kOneBlockPairs pairs are one launch.  262144 x 2 pairs of 64 experts: 14.7 us.
-#include <atomic>
-
 #include "groups.cuh"
 #include "launch.h"
 
@@ -188,24 +186,6 @@ void plan_shape(int64_t pairs, int& blocks, int& run) {
     run = int((pairs + b - 1) / b);
 }
 
-constexpr size_t place_smem(int threads, int experts) { return size_t(experts) * 4 * (2 + threads / 32); }
-
-// Allows plan_place the shared memory of the most experts, whatever this call needs:
-// the limit is the function's on the device and not the call's, so one that followed
-// the calls could be lowered by a second host thread before the first one's launch.
-template <int NT>
-cudaError_t allow_most_smem() {
-    static std::atomic<bool> done[64];
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (dev < 64 && done[dev].load(std::memory_order_relaxed)) return cudaSuccess;
-    e = cudaFuncSetAttribute(plan_place<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             int(place_smem(NT, kMaxExperts)));
-    if (e == cudaSuccess && dev < 64) done[dev].store(true, std::memory_order_relaxed);
-    return e;
-}
-
 }  // namespace
 
 size_t expert_plan_workspace(int64_t pairs, int64_t experts) {
@@ -221,9 +201,9 @@ cudaError_t launch_expert_plan(const float* indices, const float* values, int32_
     const int ne = int(experts);
     const auto place = blocks > 1 ? plan_place<kManyThreads> : plan_place<kOneThreads>;
     const int threads = blocks > 1 ? kManyThreads : kOneThreads;
-    const size_t smem = place_smem(threads, ne);
+    const size_t smem = size_t(ne) * 4 * (2 + threads / 32);
     if (smem > 48 * 1024) {
-        const cudaError_t e = blocks > 1 ? allow_most_smem<kManyThreads>() : allow_most_smem<kOneThreads>();
+        const cudaError_t e = allow_smem(place, smem);
         if (e != cudaSuccess) return e;
     }
     int32_t* counts = static_cast<int32_t*>(workspace);

@@ -19,6 +19,16 @@ namespace rowops {
 void note_launches(int n);  // counts kernels queued (rowops_kernel_launches)
 int sm_count();             // SMs of the current device (cached; 0 if unknown)
 
+// Allows launches of `kernel` on the current device `bytes` of dynamic shared memory.
+// The limit belongs to the function on the device and not to a call, so it is only
+// ever raised: a host thread that needs less must not lower it between another's
+// call of this function and its launch.
+cudaError_t allow_smem(const void* kernel, size_t bytes);
+template <typename... A>
+cudaError_t allow_smem(void (*kernel)(A...), size_t bytes) {
+    return allow_smem(reinterpret_cast<const void*>(kernel), bytes);
+}
+
 template <int L, int N, int V>
 struct Geom {
     static constexpr int LANES = L;

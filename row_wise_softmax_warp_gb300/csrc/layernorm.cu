@@ -1025,7 +1025,7 @@ cudaError_t launch_layernorm_bwd(const float* dy, const float* gamma, const floa
     if (vec4) {
         const LnColsPlan pl = ln_cols_plan(rows, cols, cap);
         if (pl.grid > 0) {
-            err = cudaFuncSetAttribute(ln_bwd_cols, cudaFuncAttributeMaxDynamicSharedMemorySize, int(pl.smem));
+            err = allow_smem(ln_bwd_cols, pl.smem);
             if (err != cudaSuccess) return err;
             ln_bwd_cols<<<unsigned(pl.grid), pl.sets * pl.tp, pl.smem, stream>>>(
                 dy, gamma, xhat, inv_std, dx, ws, rows, int(cols), pl.per_cta, pl.sets, pl.tp, pl.early);
@@ -1048,7 +1048,7 @@ cudaError_t launch_layernorm_bwd(const float* dy, const float* gamma, const floa
         constexpr int GPB = kBlockThreads / G::LANES;
         const size_t smem = size_t(GPB + 1) * 2 * MAXC * sizeof(float);
         auto kern = ln_bwd_group<G::LANES, G::NV, G::VEC>;
-        err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+        err = allow_smem(kern, smem);
         if (err != cudaSuccess) return;
         partials = ln_bwd_partials(rows, cols);
         const int64_t ctas = partials * kLnClusterCtas;
@@ -1074,7 +1074,7 @@ cudaError_t launch_layernorm_bwd(const float* dy, const float* gamma, const floa
         const size_t smem = in_smem ? size_t(2) * size_t(cols) * sizeof(float) : 0;
         auto launch = [&](auto kern) {
             if (smem > 0) {
-                err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+                err = allow_smem(kern, smem);
                 if (err != cudaSuccess) return;
             }
             kern<<<unsigned(partials), kLnLongThreads, smem, stream>>>(dy, gamma, xhat, inv_std, dx, ws, rows,

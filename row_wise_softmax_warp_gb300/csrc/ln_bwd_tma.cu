@@ -239,7 +239,7 @@ bool launch_ln_bwd_tma(const float* dy, const float* gamma, const float* xhat, c
     if (smem > kMaxDynSmem) return false;
     const int64_t per_cta = (rows + grid - 1) / grid;
     auto launch = [&](auto kern) {
-        *err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+        *err = allow_smem(kern, smem);
         if (*err != cudaSuccess) return;
         kern<<<unsigned(grid), kTmaThreads, smem, stream>>>(dy, gamma, xhat, inv_std, dx, ws, rows, int(cols),
                                                             per_cta, int(slot_rows), int(nslot));

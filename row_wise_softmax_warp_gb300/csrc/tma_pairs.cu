@@ -349,7 +349,7 @@ bool launch_tma2(const float* x, const float* w, float* grad, float* row_loss, i
     const int sms = sm_count();
     if (sms <= 0) return false;
     auto kern = tma_rows2<TEACHER>;
-    *err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    *err = allow_smem(kern, smem);
     if (*err != cudaSuccess) return true;
     const int64_t grid = rows < sms ? rows : sms;
     kern<<<unsigned(grid), kTmaThreads, smem, stream>>>(x, w, grad, row_loss, rows, int(cols), chunk, nslot,
@@ -380,7 +380,7 @@ bool launch_softmax_bwd_tma(const float* y, const float* dy, float* dx, int64_t 
     if (!pair_ring(cols, &chunk, &nslot, &smem)) return false;
     const int sms = sm_count();
     if (sms <= 0) return false;
-    *err = cudaFuncSetAttribute(tma_softmax_bwd, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    *err = allow_smem(tma_softmax_bwd, smem);
     if (*err != cudaSuccess) return true;
     const int64_t grid = rows < sms ? rows : sms;
     tma_softmax_bwd<<<unsigned(grid), kTmaThreads, smem, stream>>>(y, dy, dx, rows, int(cols), chunk, nslot,

@@ -497,7 +497,7 @@ bool launch_tma_v(const float* x, float* out, const int32_t* targets, float* aux
     const int64_t grid = rows < sms ? rows : sms;
     if (smem <= kMaxDynSmem && nslot <= kMaxSlots) {
         auto kern = tma_rows<OP, OUT_VEC>;
-        *err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+        *err = allow_smem(kern, smem);
         if (*err != cudaSuccess) return true;
         kern<<<unsigned(grid), kTmaThreads, smem, stream>>>(x, out, targets, aux, rows, int(cols), chunk, nslot,
                                                              grad_scale);
@@ -524,7 +524,7 @@ bool launch_tma_v(const float* x, float* out, const int32_t* targets, float* aux
         // resident at once (one CTA per SM); one CTA per row if the device
         // cannot place them.
         auto kern2 = tma_rows_2pass<OP, 2, OUT_VEC>;
-        *err = cudaFuncSetAttribute(kern2, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+        *err = allow_smem(kern2, smem);
         if (*err != cudaSuccess) return true;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(2);
@@ -576,7 +576,7 @@ bool launch_tma_v(const float* x, float* out, const int32_t* targets, float* aux
             return true;
         }
         auto kern = tma_rows_2pass<OP, 1, OUT_VEC>;
-        *err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+        *err = allow_smem(kern, smem);
         if (*err != cudaSuccess) return true;
         kern<<<unsigned(grid), kTmaThreads, smem, stream>>>(x, out, targets, aux, rows, int(cols), chunk, nslot,
                                                              grad_scale);
