@@ -192,7 +192,7 @@ __device__ __forceinline__ void write_weights(const ProductArgs& g, const Tile& 
     }
 }
 
-template <typename T, typename O, Form FORM>
+template <typename O, Form FORM>  // the operands' type is g.format
 __global__ void __launch_bounds__(threads_of(FORM), 1)
     expert_product(const __grid_constant__ ProductArgs g) {
     extern __shared__ unsigned char raw[];
@@ -404,9 +404,8 @@ cudaError_t launch_expert_matmul(const void* x, const void* w, const int32_t* of
     const int64_t tiles = most_row_tiles(slots, experts) * ((out + 255) / 256);
     if (tiles >= kMostTiles) return cudaErrorInvalidValue;
     auto go = [&](auto t, auto form) {
-        using T = decltype(t);
         constexpr Form kForm = decltype(form)::value;
-        return launch_pairs<expert_product<T, T, kForm>>(tiles, threads_of(kForm), kMostSmem, stream, g);
+        return launch_pairs<expert_product<decltype(t), kForm>>(tiles, threads_of(kForm), kMostSmem, stream, g);
     };
     if (dtype == ROWOPS_F16) return transposed ? go(__half{}, FormOf<kRowsT>{}) : go(__half{}, FormOf<kRows>{});
     return transposed ? go(__nv_bfloat16{}, FormOf<kRowsT>{}) : go(__nv_bfloat16{}, FormOf<kRows>{});
@@ -440,12 +439,11 @@ cudaError_t launch_expert_matmul_wgrad(const void* dy, const void* x, const int3
     g.vec = in * dw_size % 16 == 0 && reinterpret_cast<uintptr_t>(dw) % 16 == 0;
     const int64_t tiles = experts * ((out + 255) / 256) * ((in + kTileN - 1) / kTileN);
     if (tiles >= kMostTiles) return cudaErrorInvalidValue;
-    auto go = [&](auto t, auto o) {
-        return launch_pairs<expert_product<decltype(t), decltype(o), kWeights>>(tiles, threads_of(kWeights), kMostSmem,
-                                                                                stream, g);
+    auto go = [&](auto o) {
+        return launch_pairs<expert_product<decltype(o), kWeights>>(tiles, threads_of(kWeights), kMostSmem, stream, g);
     };
-    if (dtype == ROWOPS_F16) return dw_type == ROWOPS_F32 ? go(__half{}, float{}) : go(__half{}, __half{});
-    return dw_type == ROWOPS_F32 ? go(__nv_bfloat16{}, float{}) : go(__nv_bfloat16{}, __nv_bfloat16{});
+    if (dw_type == ROWOPS_F32) return go(float{});
+    return dtype == ROWOPS_F16 ? go(__half{}) : go(__nv_bfloat16{});
 }
 
 }  // namespace rowops
