@@ -399,6 +399,7 @@ _HALVES = (torch.float16, torch.bfloat16)
 _F32 = (torch.float32,)
 _INT = (torch.int32,)
 _E4M3 = (torch.float8_e4m3fn,)
+_ONE_LAUNCH_PAIRS = 2048  # plans of so many pairs need no workspace, as the header says
 
 
 class _Placed:
@@ -505,7 +506,7 @@ def rowops_expert_plan(indices, experts, values=None, offsets=None, order=None, 
         _typed(values, "values", _F32, shape, device)
     lib = library()
     pairs = rows * k
-    need = lib.rowops_expert_plan_workspace(rows, k, experts) if workspace is None and pairs > 2048 else 0
+    need = lib.rowops_expert_plan_workspace(rows, k, experts) if workspace is None and pairs > _ONE_LAUNCH_PAIRS else 0
     offsets = _given(offsets, "offsets", torch.int32, (max(experts, 0) + 1,), indices, device)
     order = _given(order, "order", torch.int32, (pairs,), indices, device)
     slot = _given(slot, "slot", torch.int32, shape, indices, device)

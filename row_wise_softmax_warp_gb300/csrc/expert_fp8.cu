@@ -18,12 +18,16 @@
 // products: that way measured 788 TFLOP/s (16384 x 4096 x 4096).  A row tile is
 // 256 rows whatever the group; groups of fewer rows copy only what they have.
 //
-// What bounds it: a stage takes some 465 clocks where its products take 256
-// (16384 x 4096 x 4096: 208 us, 2640 TFLOP/s).  Its 24 KB come from the L2 at some 58
-// bytes a clock and SM (425 clocks), and a buffer's way from the products to the
-// adding warps and back takes about 1300, most of them looks at barriers in shared
-// memory, which the operands keep busy.  Two buffers of 256 columns cover less of
-// that way than four of 128 (1970 against 2150 TFLOP/s when that was chosen), though
+// What bounds it: a block takes 0.20 us (some 400 clocks) where its products take 256,
+// and each tile 1.2 to 1.6 us on top, in which the eight warps write their sums and add
+// nothing while the products run only four blocks ahead (from 8192 rows, 768 and 1536 ->
+// 2048: 22 and 30 us in 7 rounds of tiles; 16384 rows, 1024, 2048 and 4096 -> 4096: 77, 120
+// and 210 us in 27).  Sums of 768 are six blocks, so more than half of their time is
+// that fixed part: 32 rows of 64 experts take as long as in bf16.  Within a block, a
+// buffer's way from the products to the adding warps and back takes about 1300 clocks,
+// most of them looks at barriers in shared memory, which the operands keep busy.  Two
+// buffers of 256 columns cover less of that way than four of 128 (1970 against 2150
+// TFLOP/s when that was chosen), though
 // these read the rows' operand twice as often.  Scales read one by one instead of
 // four at once cost 6%.
 #include <cuda_fp8.h>

@@ -1,8 +1,10 @@
 // expert_matmul_any.cu - the experts' matrix products for every alignment.
 //
-// Matrices whose rows start on 16-byte boundaries go through the tcgen05
-// kernels (expert_matmul.cu, expert_fp8.cu); this kernel takes the others,
-// whose rows (773 values of 2 bytes, say) no TMA copy can follow.
+// The tcgen05 kernels (expert_matmul.cu, expert_fp8.cu) read rows that start on
+// 16-byte boundaries; others (of 773 values of 2 bytes, say) are copied to such
+// boundaries in the caller's workspace first (repack.cu).  This kernel takes them as
+// they are where that workspace is missing or too small: 8192 rows of 8 experts, 1001 ->
+// 2003: 395 us, against 56 with the copies.
 //
 //   kRows        y[s][n]  = sum_k x[s][k] w[e][n][k]      rows s of expert e
 //   kRowsT       y[s][n]  = sum_k x[s][k] w[e][k][n]

@@ -12,7 +12,9 @@
 // meanwhile, adds up the counts of the blocks before it (read from the L2, the
 // blocks split among threads: one thread an expert took 8 of 21 us), ranks its
 // pairs and writes them.  One block needs no counts from others: up to
-// kOneBlockPairs pairs are one launch.  262144 x 2 pairs of 64 experts: 14.7 us.
+// kOneBlockPairs pairs are one launch.  262144 x 2 pairs of 64 experts: 14.7 us, of which
+// 2 are the trip to memory for a value that starts only after its index has come back
+// (12.2 without values; 12.9 in a trial that loads both at once).
 #include "groups.cuh"
 #include "launch.h"
 

@@ -15,7 +15,9 @@ namespace {
 constexpr int kRepackThreads = 256;
 
 // Rows of a warp, one after another: four where there are many (a warp whose rows
-// no expert needs costs little then), one where each is a wait of its own.
+// no expert needs costs little then), one where each is a wait of its own.  The product
+// with its copies, four against one row a warp: 3606 rows 17.8 and 15.8 us, 24216 56.5 and
+// 55.8, 41280 53.3 and 54.1; 2 rows of x and 64 experts, 33090 16.5 and 20.6, 128194 27.1 and 56.0.
 constexpr int kRepackRows = 4;
 constexpr int64_t kManyRows = 32768;
 

@@ -214,6 +214,14 @@ __device__ __forceinline__ void let_copies_land() {
 // sees one answer for all.  No suspend hint: between two stages of products the wait's
 // own latency is what counts.  The acquire is the CTA's: TMA's and tcgen05's
 // arrivals order what they did.
+//
+// What this and look() rely on: the whole warp arrives converged (roles, tiles and
+// answers of waits are the same in all lanes), so elect.sync with a full mask picks one
+// lane; p is false before the elected lane's instruction, so the others read a value that
+// was set; the barrier lies in this CTA's shared memory, on 8 bytes, and was initialised
+// before the cluster's first synchronisation; the parity is 0 or 1; and the instructions
+// take their documented operands alone.  A form with the suspend hint as a fourth operand
+// under the elected lane's predicate ended in an illegal instruction and is not used.
 enum class Polled { kDone, kAborted, kRanOut };
 __device__ __forceinline__ Polled warp_poll(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint32_t polls) {
     for (uint32_t i = 0; i < polls; ++i) {

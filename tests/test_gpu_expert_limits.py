@@ -125,3 +125,12 @@ def test_many_experts(ro, experts):
                                     dtype=torch.float32)
     scale = 2.0 * expert_ref.spread(ws.double().cpu().numpy(), 128, 136, 1)
     assert (y.double().cpu().numpy() == expert_ref.matmul(x64, w64 * scale, offsets)).all()
+
+
+def test_plans_that_need_no_workspace(ro):
+    """The binding asks for a workspace only above the pairs that the header names."""
+    from row_wise_softmax_warp_gb300 import binding
+    most = binding._ONE_LAUNCH_PAIRS
+    for k in (1, 2, 8):
+        assert ro.rowops_expert_plan_workspace(most // k, k, 1024) == 0
+        assert ro.rowops_expert_plan_workspace(most // k + 1, k, 1024) > 0
