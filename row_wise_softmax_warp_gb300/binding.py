@@ -131,6 +131,13 @@ def _out(t, like: torch.Tensor, name: str, shape=None, dtype=torch.float32):
     return _mat(t, name, dtype)
 
 
+def _bytes_behind(t: torch.Tensor) -> int:
+    """Bytes of a workspace: those of its values, but none behind the end of its storage (an expanded view names
+    more values than it holds)."""
+    size = t.element_size()
+    return min(t.numel() * size, t.untyped_storage().nbytes() - t.storage_offset() * size)
+
+
 def rowops_kernel_launches() -> int:
     return int(library().rowops_kernel_launches())
 
@@ -245,7 +252,7 @@ def rowops_layernorm_bwd(dy, gamma, xhat, inv_std, dx=None, dgamma=None, dbeta=N
     _check(library().rowops_layernorm_bwd(dy.data_ptr(), gamma.data_ptr(), xhat.data_ptr(),
                                           inv_std.data_ptr(), dx.data_ptr(), dgamma.data_ptr(),
                                           dbeta.data_ptr(), rows, cols, workspace.data_ptr(),
-                                          workspace.numel() * workspace.element_size(),
+                                          _bytes_behind(workspace),
                                           _stream(dy, stream)))
     return dx, dgamma, dbeta
 
