@@ -1,11 +1,12 @@
 /*
  * rowops.h - C ABI of librowops, the GB300 (sm_103a) row-wise
- * normalise-and-reduce ops of a transformer training step and the
- * mixture-of-experts layer behind its router.
+ * normalise-and-reduce ops of a transformer training step, the
+ * mixture-of-experts layer behind its router, and what lies between two
+ * sublayers' products (dropout, the residual's addition and its norm).
  *
  * Every op works on row-major matrices of `rows` x `cols` with row stride `cols`
- * (fp32; the expert operators at the end also fp16, bf16 and e4m3) and launches
- * hand-written CUDA kernels on the caller's stream.
+ * (fp32; the operators behind rowops_dtype also fp16, bf16, e4m3 and e2m1) and
+ * launches hand-written CUDA kernels on the caller's stream.
  *
  * Common contract (applies to every entry point below):
  *   - Pointers are DEVICE pointers on the current CUDA device.  The caller owns
@@ -410,7 +411,9 @@ int rowops_teacher_ce(const float *student, const float *teacher, float *grad, f
 typedef enum {
     ROWOPS_F32 = 0,
     ROWOPS_F16 = 1,
-    ROWOPS_BF16 = 2
+    ROWOPS_BF16 = 2,
+    ROWOPS_E4M3 = 3, /* with one scale for each 128 columns: answers only */
+    ROWOPS_E2M1 = 4  /* with a power of two for each 32 columns: answers only */
 } rowops_dtype;
 
 /* Bytes of device workspace rowops_expert_plan needs (a function of the sizes
@@ -553,6 +556,115 @@ int rowops_expert_matmul_fp8(const uint8_t *xq, const float *xs, const uint8_t *
                              const float *ws, const int32_t *offsets, void *y, int64_t slots,
                              int64_t in_cols, int64_t out_cols, int64_t experts, int y_type,
                              void *workspace, size_t workspace_bytes, rowops_stream stream);
+
+/*
+ * Quantises to microscaled 4-bit values (OCP Microscaling Formats 1.0, MXFP4):
+ * e2m1 (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives) with a power of two for each
+ * block of 32 columns of a row; the last block may be smaller.
+ *   e = max(floor(log2(max |x| over the block)) - 2, -127)
+ *   scale = e + 127 (one byte),  q = e2m1(x / 2^e)   (ties to even, at most 6)
+ * so that x is about q * 2^(scale - 127).  A block with an infinite or NaN x has
+ * scale 255, which stands for NaN, and q = 0.
+ * x: rows x cols of x_type; q: rows x ceil(cols / 2) bytes, the lower column in the
+ * lower four bits, and 0 in the upper bits behind an odd row's end; scale: rows x
+ * ceil(cols / 32) bytes.  cols > 2^31 - 257 is ROWOPS_ERR_SHAPE; cols == 0 is a no-op.
+ */
+int rowops_quantize_mx4(const void *x, uint8_t *q, uint8_t *scale, int64_t rows, int64_t cols,
+                        int x_type, rowops_stream stream);
+
+/*
+ * rowops_expert_matmul (not transposed) on microscaled 4-bit operands.
+ *   y[s][n] = sum_b 2^(xs[s][b] + ws[e][n][b] - 254) * sum_{k in block b} xq[s][k] * wq[e][n][k]
+ * with blocks of 32; a scale of 255 makes its products NaN.  xq: slots x in_cols / 2
+ * bytes with xs: slots x ceil(in_cols / 32); wq: experts x out_cols x in_cols / 2 with
+ * ws: experts x out_cols x ceil(in_cols / 32), as rowops_quantize_mx4 writes them; y:
+ * slots x out_cols of y_type.  in_cols is even (else ROWOPS_ERR_SHAPE): an odd row
+ * counts the four bits behind its end, which are 0.  offsets, workspace (for in_cols
+ * that are no multiple of 32) and timeouts as for rowops_expert_matmul.
+ * The gradient with respect to x is this call on dy, quantised by rows, with the
+ * weights transposed within each expert and quantised from their own values (blocks
+ * run along the sum, so these bytes cannot be transposed).  The gradient with respect
+ * to the weights is rowops_expert_matmul_wgrad on fp16 or bf16 rows.
+ */
+size_t rowops_expert_matmul_mx4_workspace(int64_t slots, int64_t in_cols, int64_t out_cols,
+                                          int64_t experts);
+int rowops_expert_matmul_mx4(const uint8_t *xq, const uint8_t *xs, const uint8_t *wq,
+                             const uint8_t *ws, const int32_t *offsets, void *y, int64_t slots,
+                             int64_t in_cols, int64_t out_cols, int64_t experts, int y_type,
+                             void *workspace, size_t workspace_bytes, rowops_stream stream);
+
+/*
+ * Between two sublayers' products: dropout, the residual's addition and its
+ * root-mean-square norm.  The pages have no counterpart beyond rms_norm_forward and
+ * rms_norm_backward.  `void` matrices, types and roundings as for the expert
+ * operators; cols > 2^31 - 257 is ROWOPS_ERR_SHAPE.
+ *
+ * Dropout drops with probability p, 0 <= p <= 1 (else ROWOPS_ERR_SHAPE), rounded to
+ * t / 65536, and multiplies what stays by 65536 / (65536 - t) (p == 1: nothing stays).
+ * What drops is +0.0, whatever it was.  The mask is not stored: value (i, c) drops
+ * when u < t, where u is the 16-bit half c mod 8 (the lower half of a word first) of
+ * the 128 bits that Philox4x32-10 gives for the key rng[0] and the counter (block,
+ * rng[1]), both low word first, and block = i * ceil(cols / 8) + c / 8.  So the same
+ * rng, rows and cols give the same mask.  rng: two 64-bit numbers in device memory,
+ * 8-byte aligned, read when the call runs: a captured graph whose replays shall drop
+ * anew advances rng[1] in the graph.  rng may be NULL where t is 0 or 65536.
+ */
+
+/*
+ * y = residual + drop(x).  x: rows x cols of x_type; residual (NULL: none) and y:
+ * rows x cols of y_type, any two types.  The gradient with respect to x is this call
+ * on dy without a residual; that of the residual is dy.  y may be exactly residual, or
+ * exactly x where the types are the same; any other overlap is ROWOPS_ERR_ALIAS.
+ * cols == 0 is a no-op.
+ */
+int rowops_dropout(const void *x, const void *residual, const uint64_t *rng, void *y, int64_t rows,
+                   int64_t cols, float p, int x_type, int y_type, rowops_stream stream);
+
+/*
+ * Residual addition and RMSNorm.
+ *   h = residual + drop(x),  rms_i = sqrt(mean_j h_ij^2 + eps),  y_ij = gamma_j * h_ij / rms_i
+ * x: rows x cols of x_type; residual (NULL: none) and h (NULL: not wanted): rows x cols
+ * of h_type, which is x_type or ROWOPS_F32; gamma: cols fp32; row_rms (NULL: not
+ * wanted): rows fp32.  The norm is of the sum before it is rounded to h_type.
+ * out holds y, rows x cols, by out_type:
+ *   x_type        y; scale is not used
+ *   ROWOPS_E4M3   as rowops_quantize_blocks with block_rows 1 writes it, the scales
+ *                 (fp32, rows x ceil(cols / 128)) in scale
+ *   ROWOPS_E2M1   as rowops_quantize_mx4 writes it, the scales (bytes, rows x
+ *                 ceil(cols / 32)) in scale
+ * so that the quantised rows are operands of rowops_expert_matmul_fp8 and
+ * rowops_expert_matmul_mx4.  h may be exactly residual; any other overlap of an
+ * output is ROWOPS_ERR_ALIAS.  cols == 0, eps < 0 and non-finite eps are
+ * ROWOPS_ERR_SHAPE.
+ */
+int rowops_add_rmsnorm_fwd(const void *x, const void *residual, const float *gamma,
+                           const uint64_t *rng, void *h, void *out, void *scale, float *row_rms,
+                           int64_t rows, int64_t cols, float eps, float p, int x_type, int h_type,
+                           int out_type, rowops_stream stream);
+
+/* Bytes of device workspace rowops_add_rmsnorm_bwd needs (a function of the sizes and
+ * the current device's SM count; 0 for sizes that need none or that it refuses). */
+size_t rowops_add_rmsnorm_bwd_workspace(int64_t rows, int64_t cols);
+
+/*
+ * Backward of rowops_add_rmsnorm_fwd (of y itself, whatever it was quantised to).
+ *   n = h / rms,  g = dy * gamma,  t = dh + (g - n * mean_j(g_j n_j)) / rms
+ *   dresidual = t,  dx = drop(t),  dgamma_j = sum_i dy_ij n_ij   (overwritten)
+ * dy, dx: rows x cols of x_type; h, dh, dresidual: rows x cols of h_type; gamma,
+ * dgamma: cols; row_rms: rows.  dh is the gradient that arrives at h from elsewhere
+ * (the residual stream; NULL: none).  dresidual and dx may be NULL where they are not
+ * wanted; without dropout and with one type they are the same values.  dresidual may
+ * be exactly dh, and dx exactly dy; any other overlap of an output is
+ * ROWOPS_ERR_ALIAS.  dgamma is summed in a fixed order, through `workspace`: at least
+ * rowops_add_rmsnorm_bwd_workspace(rows, cols) bytes, 16-byte aligned, with
+ * concurrent calls in separate ones.  cols == 0 is ROWOPS_ERR_SHAPE; rows == 0 writes
+ * zeros to dgamma.
+ */
+int rowops_add_rmsnorm_bwd(const void *dy, const float *gamma, const void *h, const float *row_rms,
+                           const void *dh, const uint64_t *rng, void *dresidual, void *dx,
+                           float *dgamma, int64_t rows, int64_t cols, float p, int x_type,
+                           int h_type, void *workspace, size_t workspace_bytes,
+                           rowops_stream stream);
 
 #ifdef __cplusplus
 }

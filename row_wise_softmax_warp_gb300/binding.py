@@ -67,6 +67,15 @@ SIGNATURES = {
     "rowops_quantize_blocks": ([_P, _P, _P, _I64, _I64, _I64, _I64, _I, _P], ctypes.c_int),
     "rowops_expert_matmul_fp8": ([_P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I, _P, ctypes.c_size_t, _P],
                                  ctypes.c_int),
+    "rowops_quantize_mx4": ([_P, _P, _P, _I64, _I64, _I, _P], ctypes.c_int),
+    "rowops_expert_matmul_mx4_workspace": ([_I64, _I64, _I64, _I64], ctypes.c_size_t),
+    "rowops_expert_matmul_mx4": ([_P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I, _P, ctypes.c_size_t, _P],
+                                 ctypes.c_int),
+    "rowops_dropout": ([_P, _P, _P, _P, _I64, _I64, _F, _I, _I, _P], ctypes.c_int),
+    "rowops_add_rmsnorm_fwd": ([_P, _P, _P, _P, _P, _P, _P, _P, _I64, _I64, _F, _F, _I, _I, _I, _P], ctypes.c_int),
+    "rowops_add_rmsnorm_bwd_workspace": ([_I64, _I64], ctypes.c_size_t),
+    "rowops_add_rmsnorm_bwd": ([_P, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _I64, _F, _I, _I, _P, ctypes.c_size_t, _P],
+                               ctypes.c_int),
 }
 
 
@@ -406,6 +415,8 @@ _HALVES = (torch.float16, torch.bfloat16)
 _F32 = (torch.float32,)
 _INT = (torch.int32,)
 _E4M3 = (torch.float8_e4m3fn,)
+_BYTE = (torch.uint8,)
+_INT64 = (torch.int64,)
 _ONE_LAUNCH_PAIRS = 2048  # plans of so many pairs need no workspace, as the header says
 
 
@@ -715,3 +726,175 @@ def rowops_expert_matmul_fp8(xq, xs, wq, ws, offsets=None, y=None, dtype=torch.b
                                         y.data_ptr(), slots, in_cols, out_cols, experts, _DTYPES.get(y.dtype, -1),
                                         _ptr(workspace), size, _raw_stream(device)))
     return y
+
+
+def rowops_quantize_mx4(x, q=None, scale=None, stream=None):
+    """Returns (q, scale), torch.uint8: microscaled 4-bit values of x (..., cols), two e2m1 codes a byte with the lower
+    column in the lower bits, (..., ceil(cols / 2)), and a power of two for each 32 columns, (..., ceil(cols / 32))."""
+    _typed(x, "x", _FLOATS)
+    if _elsewhere(x, stream):
+        with _Placed(x, stream):
+            return rowops_quantize_mx4(x, q, scale)
+    shape = x.shape
+    if not shape:
+        raise ValueError("x must have columns")
+    cols = shape[-1]
+    device = x.get_device()
+    q = _given(q, "q", torch.uint8, (*shape[:-1], (cols + 1) // 2), x, device)
+    scale = _given(scale, "scale", torch.uint8, (*shape[:-1], (cols + 31) // 32), x, device)
+    _check(library().rowops_quantize_mx4(x.data_ptr(), q.data_ptr(), scale.data_ptr(), math.prod(shape[:-1]), cols,
+                                         _DTYPES[x.dtype], _raw_stream(device)))
+    return q, scale
+
+
+def rowops_expert_matmul_mx4_workspace(slots: int, in_cols: int, out_cols: int, experts: int) -> int:
+    return int(library().rowops_expert_matmul_mx4_workspace(slots, in_cols, out_cols, experts))
+
+
+def rowops_expert_matmul_mx4(xq, xs, wq, ws, offsets=None, y=None, dtype=torch.bfloat16, workspace=None, stream=None):
+    """rowops_expert_matmul on microscaled 4-bit operands, as rowops_quantize_mx4 gives them: xq (slots, in / 2) with
+    xs, wq (experts, out, in / 2) with ws; y of `dtype`."""
+    _typed(xq, "xq", _BYTE)
+    if _elsewhere(xq, stream):
+        with _Placed(xq, stream):
+            return rowops_expert_matmul_mx4(xq, xs, wq, ws, offsets, y, dtype, workspace)
+    slots, width = _dims(xq, "xq", 2)
+    device = xq.get_device()
+    experts, out_cols, k = _dims(_typed(wq, "wq", _BYTE, None, device), "wq", 3)
+    if k != width:
+        raise ValueError(f"wq must have rows of {width} bytes, got {tuple(wq.shape)}")
+    blocks = -(-width // 16)
+    _typed(xs, "xs", _BYTE, (slots, blocks), device)
+    _typed(ws, "ws", _BYTE, (experts, out_cols, blocks), device)
+    _offsets(offsets, experts, device)
+    if y is None:
+        y = torch.empty((slots, out_cols), dtype=dtype, device=xq.device)
+    else:
+        _typed(y, "y", _FLOATS, (slots, out_cols), device)
+    lib = library()
+    need = 0 if width % 16 == 0 else lib.rowops_expert_matmul_mx4_workspace(slots, 2 * width, out_cols, experts)
+    if (xq.data_ptr() | wq.data_ptr()) % 16 and workspace is None:
+        need += _shifted_room((xq, slots, width), (wq, experts * out_cols, width))
+    workspace, size = _scratch(workspace, need, xq)
+    _check(lib.rowops_expert_matmul_mx4(xq.data_ptr(), xs.data_ptr(), wq.data_ptr(), ws.data_ptr(), _ptr(offsets),
+                                        y.data_ptr(), slots, 2 * width, out_cols, experts, _DTYPES.get(y.dtype, -1),
+                                        _ptr(workspace), size, _raw_stream(device)))
+    return y
+
+
+# ------------------------------------------------ between two sublayers' products
+
+def _rng(rng, p: float, device):
+    """Seed and offset of the generator; may be None without dropout."""
+    if rng is not None:
+        return _typed(rng, "rng", _INT64, (2,), device)
+    if p != 0 and p != 1:
+        raise ValueError("rng is needed where values drop")
+    return None
+
+
+def rowops_dropout(x, rng, p, residual=None, y=None, dtype=None, stream=None):
+    """y = residual + x with values dropped with probability p and the others multiplied by 1 / (1 - p); y of `dtype`
+    (default the residual's, or x's).  rng: two int64 on the device, seed and offset; the same rng, p and shape drop the
+    same values, so the gradient with respect to x is this call on y's gradient without the residual."""
+    _typed(x, "x", _FLOATS)
+    if _elsewhere(x, stream):
+        with _Placed(x, stream):
+            return rowops_dropout(x, rng, p, residual, y, dtype)
+    device = x.get_device()
+    _rng(rng, p, device)
+    shape = x.shape
+    if dtype is None:
+        dtype = y.dtype if y is not None else x.dtype if residual is None else residual.dtype
+    if residual is not None:
+        _typed(residual, "residual", (dtype,), shape, device)
+    y = _given(y, "y", dtype, shape, x, device)
+    rows, cols = _shape(x)
+    _check(library().rowops_dropout(x.data_ptr(), _ptr(residual), _ptr(rng), y.data_ptr(), rows, cols, p,
+                                    _DTYPES[x.dtype], _DTYPES.get(dtype, -1), _raw_stream(device)))
+    return y
+
+
+_QUANTISED = {"e4m3": 3, "mx4": 4}  # rowops_dtype
+
+
+def rowops_add_rmsnorm_fwd(x, gamma, residual=None, rng=None, p=0.0, eps=1e-5, quantize=None, out=None, scale=None,
+                           h=None, row_rms=None, stream=None):
+    """Returns (out, scale, h, row_rms): h = residual + x with dropout, out = gamma * h / rms(h).
+
+    h is of the residual's type, which is x's or torch.float32 (without a residual of h's, or x's where that is None;
+    and without dropout either h is x itself).  quantize None: out of x's type, scale None; "e4m3": out and scale as
+    rowops_quantize_blocks gives them; "mx4": as rowops_quantize_mx4 does.  h may be the residual."""
+    _typed(x, "x", _FLOATS)
+    if _elsewhere(x, stream):
+        with _Placed(x, stream):
+            return rowops_add_rmsnorm_fwd(x, gamma, residual, rng, p, eps, quantize, out, scale, h, row_rms)
+    device, shape = x.get_device(), x.shape
+    rows, cols = _shape(x)
+    _typed(gamma, "gamma", _F32, (cols,), device)
+    _rng(rng, p, device)
+    if residual is not None:
+        _typed(residual, "residual", _FLOATS, shape, device)
+    like = x if residual is None and h is None else h if residual is None else residual
+    if h is None and like is x and p == 0:
+        h, h_ptr = x, None  # the sum is x
+    else:
+        h = _given(h, "h", like.dtype, shape, x, device)
+        h_ptr = h.data_ptr()
+    if quantize is None:
+        if scale is not None:
+            raise ValueError("scale is of quantised answers only")
+        out = _given(out, "out", x.dtype, shape, x, device)
+        out_type = _DTYPES[x.dtype]
+    elif quantize == "e4m3":
+        out = _given(out, "out", torch.float8_e4m3fn, shape, x, device)
+        scale = _given(scale, "scale", torch.float32, (*shape[:-1], -(-cols // 128)), x, device)
+    elif quantize == "mx4":
+        out = _given(out, "out", torch.uint8, (*shape[:-1], -(-cols // 2)), x, device)
+        scale = _given(scale, "scale", torch.uint8, (*shape[:-1], -(-cols // 32)), x, device)
+    else:
+        raise ValueError('quantize must be None, "e4m3" or "mx4"')
+    row_rms = _given(row_rms, "row_rms", torch.float32, shape[:-1], x, device)
+    _check(library().rowops_add_rmsnorm_fwd(
+        x.data_ptr(), _ptr(residual), gamma.data_ptr(), _ptr(rng), h_ptr, out.data_ptr(), _ptr(scale),
+        row_rms.data_ptr(), rows, cols, eps, p, _DTYPES[x.dtype], _DTYPES[h.dtype],
+        out_type if quantize is None else _QUANTISED[quantize], _raw_stream(device)))
+    return out, scale, h, row_rms
+
+
+def rowops_add_rmsnorm_bwd_workspace(rows: int, cols: int) -> int:
+    return int(library().rowops_add_rmsnorm_bwd_workspace(rows, cols))
+
+
+def rowops_add_rmsnorm_bwd(dy, gamma, h, row_rms, dh=None, rng=None, p=0.0, dx=None, dresidual=None, dgamma=None,
+                           workspace=None, stream=None):
+    """Returns (dx, dresidual, dgamma) of rowops_add_rmsnorm_fwd.  dh: the gradient that arrives at h from elsewhere.
+
+    dx is of dy's type, dresidual of h's.  Without dropout and with one type they are the same values, and the same
+    tensor where dx is None.  dx may be dy, and dresidual may be dh."""
+    _typed(dy, "dy", _FLOATS)
+    if _elsewhere(dy, stream):
+        with _Placed(dy, stream):
+            return rowops_add_rmsnorm_bwd(dy, gamma, h, row_rms, dh, rng, p, dx, dresidual, dgamma, workspace)
+    device, shape = dy.get_device(), dy.shape
+    rows, cols = _shape(dy)
+    _typed(gamma, "gamma", _F32, (cols,), device)
+    _typed(h, "h", _FLOATS, shape, device)
+    _typed(row_rms, "row_rms", _F32, shape[:-1], device)
+    _rng(rng, p, device)
+    if dh is not None:
+        _typed(dh, "dh", (h.dtype,), shape, device)
+    dresidual = _given(dresidual, "dresidual", h.dtype, shape, dy, device)
+    if dx is None and p == 0 and dy.dtype == h.dtype:
+        dx, dx_ptr = dresidual, None
+    else:
+        dx = _given(dx, "dx", dy.dtype, shape, dy, device)
+        dx_ptr = dx.data_ptr()
+    dgamma = _given(dgamma, "dgamma", torch.float32, (cols,), dy, device)
+    lib = library()
+    need = lib.rowops_add_rmsnorm_bwd_workspace(rows, cols) if workspace is None else 0
+    workspace, size = _scratch(workspace, need, dy)
+    _check(lib.rowops_add_rmsnorm_bwd(dy.data_ptr(), gamma.data_ptr(), h.data_ptr(), row_rms.data_ptr(), _ptr(dh),
+                                      _ptr(rng), dresidual.data_ptr(), dx_ptr, dgamma.data_ptr(), rows, cols, p,
+                                      _DTYPES[dy.dtype], _DTYPES[h.dtype], _ptr(workspace), size, _raw_stream(device)))
+    return dx, dresidual, dgamma

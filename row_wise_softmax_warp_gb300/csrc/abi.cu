@@ -534,6 +534,21 @@ size_t copy_bytes(int64_t rows, int64_t row_bytes) {
 }
 size_t with_slack(size_t bytes) { return bytes ? bytes + 256 : 0; }
 
+// Rows whose columns, rounded up to 256, have numbers in 32 bits.
+int check_width(int64_t rows, int64_t cols) {
+    if (cols > INT32_MAX - 256) return ROWOPS_ERR_SHAPE;
+    return check_dims(rows, cols);
+}
+
+// Whether some values drop and others stay: the rounded probability is neither 0 nor 1.
+bool needs_rng(float p) {
+    const int t = rowops::dropout_threshold(p);
+    return t > 0 && t < 65536;
+}
+
+// A branch's type and its residual stream's: the same, or fp32.
+bool branch_types(int x_type, int h_type) { return any_type(x_type) && (h_type == x_type || h_type == ROWOPS_F32); }
+
 }  // namespace
 
 extern "C" {
@@ -691,6 +706,117 @@ int rowops_expert_matmul_fp8(const uint8_t* xq, const float* xs, const uint8_t* 
     if (int e = check_workspace(workspace, workspace_bytes, {bx, bxs, bw, bws, bo, by})) return e;
     return to_status(rowops::launch_expert_matmul_fp8(xq, xs, wq, ws, offsets, y, slots, in_cols, out_cols, experts,
                                                       y_type, scratch_of(workspace, workspace_bytes), st(stream)));
+}
+
+int rowops_quantize_mx4(const void* x, uint8_t* q, uint8_t* scale, int64_t rows, int64_t cols, int x_type,
+                        rowops_stream stream) {
+    if (!any_type(x_type)) return ROWOPS_ERR_SHAPE;
+    if (int e = check_width(rows, cols)) return e;
+    if (rows == 0 || cols == 0) return ROWOPS_OK;
+    if (!x || !q || !scale) return ROWOPS_ERR_NULL;
+    const int64_t xb = type_bytes(x_type);
+    if (!elems_aligned({{x, xb}})) return ROWOPS_ERR_ALIGN;
+    if (int e = check_overlap({{x, rows * cols * xb}}, {{q, rows * ((cols + 1) / 2)}, {scale, rows * ((cols + 31) / 32)}}))
+        return e;
+    return to_status(rowops::launch_quantize_mx4(x, q, scale, rows, cols, x_type, st(stream)));
+}
+
+size_t rowops_expert_matmul_mx4_workspace(int64_t slots, int64_t in_cols, int64_t out_cols, int64_t experts) {
+    if (slots <= 0 || in_cols % 2 != 0 || check_sizes(slots, in_cols, out_cols, experts)) return 0;
+    return with_slack(copy_bytes(slots, in_cols / 2) + copy_bytes(experts * out_cols, in_cols / 2));
+}
+
+int rowops_expert_matmul_mx4(const uint8_t* xq, const uint8_t* xs, const uint8_t* wq, const uint8_t* ws,
+                             const int32_t* offsets, void* y, int64_t slots, int64_t in_cols, int64_t out_cols,
+                             int64_t experts, int y_type, void* workspace, size_t workspace_bytes,
+                             rowops_stream stream) {
+    if (!any_type(y_type) || in_cols % 2 != 0) return ROWOPS_ERR_SHAPE;
+    if (int e = check_product(offsets, slots, in_cols, out_cols, experts)) return e;
+    if (slots == 0) return ROWOPS_OK;
+    if (!xq || !xs || !wq || !ws || !y) return ROWOPS_ERR_NULL;
+    const int64_t yb = type_bytes(y_type);
+    if (!elems_aligned({{offsets, 4}, {y, yb}})) return ROWOPS_ERR_ALIGN;
+    const int64_t bytes = in_cols / 2, kb = (in_cols + 31) / 32;
+    const Buf bx{xq, slots * bytes}, bxs{xs, slots * kb}, bw{wq, experts * out_cols * bytes},
+        bws{ws, experts * out_cols * kb}, bo{offsets, (experts + 1) * 4}, by{y, slots * out_cols * yb};
+    if (int e = check_overlap({bx, bxs, bw, bws, bo}, {by})) return e;
+    if (int e = check_workspace(workspace, workspace_bytes, {bx, bxs, bw, bws, bo, by})) return e;
+    return to_status(
+        rowops::launch_matmul_mx4_any(xq, xs, wq, ws, offsets, y, slots, in_cols, out_cols, experts, y_type, st(stream)));
+}
+
+// ------------------------------------------- between two sublayers' products
+
+int rowops_dropout(const void* x, const void* residual, const uint64_t* rng, void* y, int64_t rows, int64_t cols,
+                   float p, int x_type, int y_type, rowops_stream stream) {
+    if (!any_type(x_type) || !any_type(y_type)) return ROWOPS_ERR_SHAPE;
+    if (int e = check_width(rows, cols)) return e;
+    if (!(p >= 0.f && p <= 1.f)) return ROWOPS_ERR_SHAPE;
+    if (rows == 0 || cols == 0) return ROWOPS_OK;
+    if (!x || !y || (needs_rng(p) && !rng)) return ROWOPS_ERR_NULL;
+    const int64_t xb = type_bytes(x_type), yb = type_bytes(y_type), n = rows * cols;
+    if (!elems_aligned({{x, xb}, {residual, yb}, {rng, 8}, {y, yb}})) return ROWOPS_ERR_ALIGN;
+    const Buf out{y, n * yb};
+    if (!(x == y && x_type == y_type) && overlap(out, {x, n * xb})) return ROWOPS_ERR_ALIAS;
+    if (residual != y && overlap(out, {residual, n * yb})) return ROWOPS_ERR_ALIAS;
+    if (overlap(out, {rng, 16})) return ROWOPS_ERR_ALIAS;
+    return to_status(rowops::launch_dropout(x, residual, rng, y, rows, cols, p, x_type, y_type, st(stream)));
+}
+
+int rowops_add_rmsnorm_fwd(const void* x, const void* residual, const float* gamma, const uint64_t* rng, void* h,
+                           void* out, void* scale, float* row_rms, int64_t rows, int64_t cols, float eps, float p,
+                           int x_type, int h_type, int out_type, rowops_stream stream) {
+    const bool quantised = out_type == ROWOPS_E4M3 || out_type == ROWOPS_E2M1;
+    if (!branch_types(x_type, h_type) || (out_type != x_type && !quantised)) return ROWOPS_ERR_SHAPE;
+    if (int e = check_width(rows, cols)) return e;
+    if (cols == 0 || !std::isfinite(eps) || eps < 0.f || !(p >= 0.f && p <= 1.f)) return ROWOPS_ERR_SHAPE;
+    if (rows == 0) return ROWOPS_OK;
+    if (!x || !gamma || !out || (quantised && !scale) || (needs_rng(p) && !rng)) return ROWOPS_ERR_NULL;
+    const int64_t xb = type_bytes(x_type), hb = type_bytes(h_type), n = rows * cols;
+    const int64_t ob = quantised ? 1 : xb, sb = out_type == ROWOPS_E4M3 ? 4 : 1;
+    if (!quantised) scale = nullptr;
+    if (!elems_aligned({{x, xb}, {residual, hb}, {gamma, 4}, {rng, 8}, {h, hb}, {out, ob}, {scale, sb}, {row_rms, 4}}))
+        return ROWOPS_ERR_ALIGN;
+    const int64_t out_bytes = out_type == ROWOPS_E2M1 ? rows * ((cols + 1) / 2) : n * ob;
+    const int64_t scale_bytes = out_type == ROWOPS_E4M3 ? rows * ((cols + 127) / 128) * 4 : rows * ((cols + 31) / 32);
+    const Buf in_place{h == residual ? nullptr : residual, n * hb};
+    if (int e = check_overlap({{x, n * xb}, in_place, {gamma, cols * 4}, {rng, 16}},
+                              {{h, n * hb}, {out, out_bytes}, {scale, scale_bytes}, {row_rms, rows * 4}}))
+        return e;
+    return to_status(rowops::launch_add_rmsnorm_fwd(x, residual, gamma, rng, h, out, scale, row_rms, rows, cols, eps, p,
+                                                    x_type, h_type, out_type, st(stream)));
+}
+
+size_t rowops_add_rmsnorm_bwd_workspace(int64_t rows, int64_t cols) {
+    if (check_width(rows, cols) != ROWOPS_OK || cols == 0) return 0;
+    return rowops::add_rmsnorm_bwd_workspace(rows, cols);
+}
+
+int rowops_add_rmsnorm_bwd(const void* dy, const float* gamma, const void* h, const float* row_rms, const void* dh,
+                           const uint64_t* rng, void* dresidual, void* dx, float* dgamma, int64_t rows, int64_t cols,
+                           float p, int x_type, int h_type, void* workspace, size_t workspace_bytes,
+                           rowops_stream stream) {
+    if (!branch_types(x_type, h_type)) return ROWOPS_ERR_SHAPE;
+    if (int e = check_width(rows, cols)) return e;
+    if (cols == 0 || !(p >= 0.f && p <= 1.f)) return ROWOPS_ERR_SHAPE;
+    if (!dgamma || (rows && (!dy || !gamma || !h || !row_rms || (dx && needs_rng(p) && !rng)))) return ROWOPS_ERR_NULL;
+    const int64_t xb = type_bytes(x_type), hb = type_bytes(h_type), n = rows * cols;
+    if (!elems_aligned({{dy, xb}, {gamma, 4}, {h, hb}, {row_rms, 4}, {dh, hb}, {rng, 8}, {dresidual, hb}, {dx, xb}, {dgamma, 4}}))
+        return ROWOPS_ERR_ALIGN;
+    if (rows == 0) return to_status(cudaMemsetAsync(dgamma, 0, size_t(cols) * 4, st(stream)));
+    const Buf bdy{dy, n * xb}, bdh{dh, n * hb}, bh{h, n * hb}, bg{gamma, cols * 4}, br{row_rms, rows * 4}, bn{rng, 16};
+    const Buf bdr{dresidual, n * hb}, bdx{dx, n * xb}, bdg{dgamma, cols * 4};
+    if (int e = check_overlap({bh, bg, br, bn}, {bdr, bdx, bdg})) return e;
+    for (const Buf& o : {bdr, bdx, bdg}) {
+        if (!(o.p == dx && dx == dy) && overlap(o, bdy)) return ROWOPS_ERR_ALIAS;
+        if (!(o.p == dresidual && dresidual == dh) && overlap(o, bdh)) return ROWOPS_ERR_ALIAS;
+    }
+    const size_t need = rowops::add_rmsnorm_bwd_workspace(rows, cols);
+    if (!workspace || workspace_bytes < need || !aligned(workspace, 16)) return ROWOPS_ERR_WORKSPACE;
+    for (const Buf& b : {bdy, bdh, bh, bg, br, bn, bdr, bdx, bdg})
+        if (overlap({workspace, int64_t(need)}, b)) return ROWOPS_ERR_ALIAS;
+    return to_status(rowops::launch_add_rmsnorm_bwd(dy, gamma, h, row_rms, dh, rng, dresidual, dx, dgamma, rows, cols, p,
+                                                    x_type, h_type, static_cast<float*>(workspace), st(stream)));
 }
 
 }  // extern "C"

@@ -1,0 +1,193 @@
+// add_rmsnorm.cu - a branch's dropout, the residual's addition and the
+// root-mean-square norm of the sum, in one pass.
+//
+//   h = residual + drop(x),  rms = sqrt(mean_j h_j^2 + eps),  y = gamma * h / rms
+//
+// y goes out in x's type, in e4m3 with a scale for each 128 columns (quantize.cu), or
+// in e2m1 with a power of two for each 32 (quant.cuh).  The sum stays in fp32 registers
+// between its statistic and its norm, so y is not of the rounded h.
+//
+// Bound by HBM: x and residual are read once, h and y written once.  A row lies in the
+// registers of a group of lanes, of a warp, or of up to 32 warps that meet once, at a
+// barrier of their own.
+#include "eight.cuh"
+#include "quant.cuh"
+
+namespace rowops {
+namespace {
+
+enum Answer { kPlain, kE4m3, kE2m1 };
+
+struct AddNormArgs {
+    const void* x;
+    const void* residual;  // may be NULL
+    const float* gamma;
+    void* h;    // may be NULL
+    void* out;
+    void* scale;
+    float* row_rms;  // may be NULL
+    Dropout drop;
+    int64_t rows;
+    int cols;
+    float eps;
+    Answer answer;
+    RowSplit split;
+};
+
+// h of eight columns in fp32, written in the stream's type.
+template <typename T, typename R, int LANES, bool VEC>
+struct Sum {
+    Held<T, LANES, VEC> x;
+    Held<R, LANES, VEC> residual;
+    __device__ __forceinline__ void load(const AddNormArgs& a, int64_t row, int base, int g, int cols) {
+        x.load(static_cast<const T*>(a.x) + row * a.cols, base, g, cols);
+        if (a.residual) residual.load(static_cast<const R*>(a.residual) + row * a.cols, base, g, cols);
+    }
+    __device__ __forceinline__ void get(const AddNormArgs& a, const Masker& m, int64_t row, int base, int g,
+                                        float (&v)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = x.get(i);
+        drop_eight<LANES, VEC>(v, a.drop, m, row, (a.cols + 7) / 8, base, g);
+        if (a.residual)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] += residual.get(i);
+    }
+};
+
+// Eight columns of the answer.
+template <typename T, int LANES, bool VEC>
+__device__ __forceinline__ void answer_eight(const AddNormArgs& a, int64_t row, int base, int g, int cols,
+                                             const float (&y)[8]) {
+    if (a.answer == kPlain) {
+        store_eight<LANES, VEC>(static_cast<T*>(a.out) + row * a.cols, base, g, cols, y);
+        return;
+    }
+    if (a.answer == kE4m3) {
+        store_e4m3<LANES, VEC>(static_cast<uint8_t*>(a.out) + row * a.cols,
+                               static_cast<float*>(a.scale) + row * ((a.cols + 127) / 128), base, g, cols, y);
+    } else {
+        store_mx4<LANES, VEC>(static_cast<uint8_t*>(a.out) + row * ((a.cols + 1) / 2),
+                              static_cast<uint8_t*>(a.scale) + row * ((a.cols + 31) / 32), base, g, cols, y);
+    }
+}
+
+template <typename T, typename R, int LANES, int NV, bool VEC, int MOST>
+__global__ void __launch_bounds__(MOST) add_rmsnorm_rows(const AddNormArgs a) {
+    __shared__ float scratch[2][32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int slot = warp / a.split.warps, w = warp % a.split.warps, g = lane % LANES;
+    constexpr int kGroups = 32 / LANES;
+    const float inv_cols = 1.0f / float(a.cols);
+    const Masker masker(a.drop);
+    int turn = 0;
+    for (int64_t first = (int64_t(blockIdx.x) * a.split.slots + slot) * kGroups; first < a.rows;
+         first += int64_t(gridDim.x) * a.split.slots * kGroups, turn ^= 1) {
+        const int64_t row = first + lane / LANES;
+        const int cols = row < a.rows ? a.cols : 0;
+        Sum<T, R, LANES, VEC> in[NV];
+#pragma unroll
+        for (int k = 0; k < NV; ++k) in[k].load(a, row < a.rows ? row : 0, (k * a.split.warps + w) * 256, g, cols);
+        float h[NV][8], squares = 0.f;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int base = (k * a.split.warps + w) * 256;
+            in[k].get(a, masker, row, base, g, h[k]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) squares = fmaf(h[k][i], h[k][i], squares);  // 0 past the row's end
+            if (a.h) store_eight<LANES, VEC>(static_cast<R*>(a.h) + row * a.cols, base, g, cols, h[k]);
+        }
+        const float rms = sqrtf(sum_of_row<LANES>(squares, scratch[turn], a.split.warps, slot, w) * inv_cols + a.eps);
+        if (a.row_rms && w == 0 && g == 0 && row < a.rows) a.row_rms[row] = rms;
+        const float inv = 1.0f / rms;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int base = (k * a.split.warps + w) * 256;
+            float gamma[8], y[8];
+            load_weights<LANES, VEC>(a.gamma, base, g, cols, gamma);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] = h[k][i] * inv * gamma[i];
+            answer_eight<T, LANES, VEC>(a, row, base, g, cols, y);
+        }
+    }
+}
+
+// Rows of more than 16384 values: one block a row, which reads x and the residual a
+// second time, from the L2, for the answer.  h is written only then: it may lie where
+// the residual does.
+template <typename T, typename R, bool VEC>
+__global__ void __launch_bounds__(1024) add_rmsnorm_long(const AddNormArgs a) {
+    __shared__ float scratch[2][32];
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const float inv_cols = 1.0f / float(a.cols);
+    const Masker masker(a.drop);
+    const int64_t units = (int64_t(a.cols) + 255) / 256;
+    int turn = 0;
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
+        float squares = 0.f;
+        for (int64_t u = w; u < units; u += 32) {
+            Sum<T, R, 32, VEC> in;
+            float h[8];
+            in.load(a, row, int(u * 256), lane, a.cols);
+            in.get(a, masker, row, int(u * 256), lane, h);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) squares = fmaf(h[i], h[i], squares);
+        }
+        const float rms = sqrtf(sum_of_row<32>(squares, scratch[turn], 32, 0, w) * inv_cols + a.eps);
+        if (a.row_rms && threadIdx.x == 0) a.row_rms[row] = rms;
+        const float inv = 1.0f / rms;
+        for (int64_t u = w; u < units; u += 32) {
+            const int base = int(u * 256);
+            Sum<T, R, 32, VEC> in;
+            float h[8], gamma[8];
+            in.load(a, row, base, lane, a.cols);
+            load_weights<32, VEC>(a.gamma, base, lane, a.cols, gamma);
+            in.get(a, masker, row, base, lane, h);
+            if (a.h) store_eight<32, VEC>(static_cast<R*>(a.h) + row * a.cols, base, lane, a.cols, h);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) h[i] = h[i] * inv * gamma[i];
+            answer_eight<T, 32, VEC>(a, row, base, lane, a.cols, h);
+        }
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_add_rmsnorm_fwd(const void* x, const void* residual, const float* gamma, const uint64_t* rng,
+                                   void* h, void* out, void* scale, float* row_rms, int64_t rows, int64_t cols,
+                                   float eps, float p, int x_type, int h_type, int out_type, cudaStream_t stream) {
+    AddNormArgs a{x, residual, gamma, h, out, scale, row_rms, dropout_of(rng, p), rows, int(cols), eps, kPlain, {1, 1}};
+    if (out_type == ROWOPS_E4M3) a.answer = kE4m3;
+    if (out_type == ROWOPS_E2M1) a.answer = kE2m1;
+    const bool vec = cols % 8 == 0 && ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(residual) |
+                                        reinterpret_cast<uintptr_t>(gamma) | reinterpret_cast<uintptr_t>(h) |
+                                        reinterpret_cast<uintptr_t>(out)) & 15) == 0;
+    const int units = int((cols + 255) / 256);
+    auto go = [&](auto kernel, int groups, int warps, int slots) {
+        a.split = {warps, slots};
+        const int64_t per = int64_t(slots) * groups, blocks = (rows + per - 1) / per, most = int64_t(1) << 20;
+        kernel<<<unsigned(blocks < most ? blocks : most), unsigned(warps * slots * 32), 0, stream>>>(a);
+    };
+    with_branch_types(x_type, h_type, [&](auto t, auto r) {
+        using T = decltype(t);
+        using R = decltype(r);
+        auto pick = [&](auto v) {
+            constexpr bool VEC = decltype(v)::value;
+            if (VEC && cols <= 64) go(add_rmsnorm_rows<T, R, VEC ? 8 : 32, 1, VEC, 128>, 4, 1, 4);
+            else if (VEC && cols <= 128) go(add_rmsnorm_rows<T, R, VEC ? 16 : 32, 1, VEC, 128>, 2, 1, 4);
+            else if (units == 1) go(add_rmsnorm_rows<T, R, 32, 1, VEC, 128>, 1, 1, 4);
+            else if (units <= 32 && rows <= 4 * int64_t(sm_count()))
+                go(add_rmsnorm_rows<T, R, 32, 1, VEC, 1024>, 1, units, units <= 4 ? 2 : 1);
+            else if (units <= 64) {
+                const int warps = (units + 1) / 2;
+                go(add_rmsnorm_rows<T, R, 32, 2, VEC, 1024>, 1, warps, warps <= 4 ? 8 / warps : 1);
+            } else
+                go(add_rmsnorm_long<T, R, VEC>, 1, 32, 1);
+        };
+        if (vec) pick(std::true_type{});
+        else pick(std::false_type{});
+    });
+    note_launches(1);
+    return cudaGetLastError();
+}
+
+}  // namespace rowops

@@ -9,6 +9,7 @@
 
 #include <cuda_runtime.h>
 
+#include <cmath>
 #include <cstddef>
 #include <cstdint>
 
@@ -229,6 +230,24 @@ cudaError_t launch_expert_combine_bwd(const void* dout, const void* y, const int
                                       int64_t slots, int out_type, int y_type, cudaStream_t stream);
 cudaError_t launch_quantize_blocks(const void* x, uint8_t* q, float* scale, int64_t batches, int64_t rows,
                                    int64_t cols, int64_t block_rows, int x_type, cudaStream_t stream);
+cudaError_t launch_quantize_mx4(const void* x, uint8_t* q, uint8_t* scale, int64_t rows, int64_t cols, int x_type,
+                                cudaStream_t stream);
+// What lies between two sublayers' products.
+// The rounded probability, as the number of the 65536 halves that drop.
+inline int dropout_threshold(float p) { return int(lrint(double(p) * 65536.0)); }
+inline float dropout_scale(int threshold) {
+    return threshold < 65536 ? float(65536.0 / double(65536 - threshold)) : 0.f;
+}
+cudaError_t launch_dropout(const void* x, const void* residual, const uint64_t* rng, void* y, int64_t rows,
+                           int64_t cols, float p, int x_type, int y_type, cudaStream_t stream);
+cudaError_t launch_add_rmsnorm_fwd(const void* x, const void* residual, const float* gamma, const uint64_t* rng,
+                                   void* h, void* out, void* scale, float* row_rms, int64_t rows, int64_t cols,
+                                   float eps, float p, int x_type, int h_type, int out_type, cudaStream_t stream);
+size_t add_rmsnorm_bwd_workspace(int64_t rows, int64_t cols);
+cudaError_t launch_add_rmsnorm_bwd(const void* dy, const float* gamma, const void* h, const float* row_rms,
+                                   const void* dh, const uint64_t* rng, void* dresidual, void* dx, float* dgamma,
+                                   int64_t rows, int64_t cols, float p, int x_type, int h_type, float* parts,
+                                   cudaStream_t stream);
 // Scratch memory of one call: `take` gives 256-byte aligned parts of it in turn.
 struct Scratch {
     void* p;
@@ -271,6 +290,9 @@ cudaError_t launch_matmul_wgrad_any(const void* dy, const void* x, const int32_t
                                     int64_t in, int64_t out, int64_t experts, int dtype, int dw_type,
                                     cudaStream_t stream);
 cudaError_t launch_matmul_fp8_any(const uint8_t* x, const float* x_scale, const uint8_t* w, const float* w_scale,
+                                  const int32_t* offsets, void* y, int64_t slots, int64_t in, int64_t out,
+                                  int64_t experts, int y_type, cudaStream_t stream);
+cudaError_t launch_matmul_mx4_any(const uint8_t* x, const uint8_t* xs, const uint8_t* w, const uint8_t* ws,
                                   const int32_t* offsets, void* y, int64_t slots, int64_t in, int64_t out,
                                   int64_t experts, int y_type, cudaStream_t stream);
 

@@ -1,0 +1,180 @@
+// quant.cuh - e4m3 values with a scale for a block, and e2m1 values with a power of two.
+#pragma once
+
+#include <cuda_fp4.h>
+#include <cuda_fp8.h>
+
+#include "common.cuh"
+
+namespace rowops {
+
+constexpr float kLargest = 448.0f;        // of e4m3
+constexpr float kSmallestMax = 0x1p-100f;
+
+// Largest magnitude; NaN values do not count, infinite ones do.
+__device__ __forceinline__ float largest(const float (&v)[8]) {
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[i]));
+    return m;
+}
+// Largest finite magnitude.
+__device__ __forceinline__ float largest_finite(const float (&v)[8]) {
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (fabsf(v[i]) < INFINITY) m = fmaxf(m, fabsf(v[i]));
+    return m;
+}
+
+// a / 448, correctly rounded: the same step with the rounded reciprocal of 448.
+__device__ __forceinline__ float scale_of(float a) {
+    constexpr float kInv = 1.0f / kLargest;
+    const float q0 = a * kInv;
+    return fmaf(fmaf(-q0, kLargest, a), kInv, q0);
+}
+
+// 448 x / a by the reciprocal and one residual step (Markstein 1990): q0 is off by
+// at most three units, r is its exact residual, and a quotient that fp32 holds (as
+// every border between e4m3 values does) comes out exact.  An infinite or NaN x
+// makes r NaN.  x and a are divided by 2^32 where 448 x could overflow.
+struct Divisor {
+    float scale, d, inv;
+    __device__ __forceinline__ explicit Divisor(float a) {
+        const float s = a > 0x1p100f ? 0x1p-32f : 1.0f;
+        scale = kLargest * s;
+        d = a * s;
+        asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(inv) : "f"(d));  // off by a unit at most
+    }
+    __device__ __forceinline__ float operator()(float x) const {
+        const float t = x * scale, q0 = t * inv, r = fmaf(-q0, d, t);
+        return fmaf(r, inv, q0);
+    }
+};
+
+__device__ __forceinline__ uint2 quantize8(const float (&v)[8], const Divisor& over) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        w[i] = __nv_cvt_float2_to_fp8x2(make_float2(over(v[2 * i]), over(v[2 * i + 1])), __NV_SATFINITE, __NV_E4M3);
+    return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+}
+
+// ------------------------------------------------- microscaled 4 bits (e2m1, e8m0)
+//
+// A block of 32 shares 2^(code - 127) with code - 127 = floor(log2 a) - 2 (2: the
+// exponent of 6, the largest e2m1), at least -127: OCP Microscaling Formats 1.0, 6.3.
+// Values past 6 after the division become 6.  A block with an infinite or NaN value has
+// code 255, which stands for NaN, and zeros.
+
+// The largest magnitude as its bits, in which NaN lies above infinity.
+__device__ __forceinline__ uint32_t largest_bits(const float (&v)[8]) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
+    return m;
+}
+template <int LANES>
+__device__ __forceinline__ uint32_t group_max_bits(uint32_t v) {
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(kFullMask, v, o));
+    return v;
+}
+// The block's code from its largest magnitude.  A subnormal's exponent field is 0, and
+// floor(log2 a) - 2 lies below -127 for it.
+__device__ __forceinline__ uint32_t mx4_code(uint32_t bits) {
+    const uint32_t e = bits >> 23;
+    return e == 255 ? 255 : max(int(e) - 2, 0);
+}
+// 2^(127 - code), by which a block's values are multiplied: exact but where the result is
+// far below the least e2m1.  0 for code 255.
+__device__ __forceinline__ float mx4_inverse(uint32_t code) {
+    return code == 255 ? 0.f : __uint_as_float((254 - code) << 23);
+}
+// Two codes in a byte, the first value in the lower half; 0 times an infinite or NaN value
+// would be NaN, so blocks of code 255 are told.
+__device__ __forceinline__ uint32_t mx4_pair(float x, float y, float inverse) {
+    return __nv_cvt_float2_to_fp4x2(make_float2(x * inverse, y * inverse), __NV_E2M1, cudaRoundNearest);
+}
+__device__ __forceinline__ uint32_t mx4_eight(const float (&v)[8], uint32_t code) {
+    if (code == 255) return 0;
+    const float inverse = mx4_inverse(code);
+    uint32_t w = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w |= mx4_pair(v[2 * i], v[2 * i + 1], inverse) << (8 * i);
+    return w;
+}
+
+// ----------------------------------------------------- quantised columns of a row
+//
+// Eight values of each lane of a group, placed as in eight.cuh, to their row of bytes and
+// of scales.  The whole warp calls them.  Blocks of 128 columns are 16 lanes' (VEC), or
+// four values of each of 32 lanes, or the whole of a shorter group.
+
+template <int LANES, bool VEC>
+__device__ __forceinline__ void store_e4m3(uint8_t* q, float* scale, int base, int g, int cols, const float (&y)[8]) {
+    scale += base / 128;
+    if constexpr (VEC) {
+        constexpr int kBlock = LANES < 16 ? LANES : 16;
+        float most = group_max<kBlock>(largest(y));
+        if (__any_sync(kFullMask, most == INFINITY)) most = group_max<kBlock>(largest_finite(y));
+        most = fmaxf(most, kSmallestMax);
+        if (base + 8 * g < cols) {
+            *reinterpret_cast<uint2*>(q + base + 8 * g) = quantize8(y, Divisor(most));
+            if (g % kBlock == 0) scale[g / kBlock] = scale_of(most);
+        }
+    } else {
+        constexpr int kEach = 128 / LANES < 8 ? 128 / LANES : 8;  // a lane's values of a block
+#pragma unroll
+        for (int b = 0; b < 8 / kEach; ++b) {
+            float most = 0.f, fine = 0.f;
+#pragma unroll
+            for (int i = 0; i < kEach; ++i) {
+                const float v = fabsf(y[b * kEach + i]);
+                most = fmaxf(most, v);
+                if (v < INFINITY) fine = fmaxf(fine, v);
+            }
+            most = group_max<LANES>(most);
+            if (__any_sync(kFullMask, most == INFINITY)) most = group_max<LANES>(fine);
+            most = fmaxf(most, kSmallestMax);
+            const Divisor over(most);
+#pragma unroll
+            for (int i = 0; i < kEach; ++i) {
+                const int c = base + (b * kEach + i) * LANES + g;
+                if (c < cols) q[c] = __nv_cvt_float_to_fp8(over(y[b * kEach + i]), __NV_SATFINITE, __NV_E4M3);
+            }
+            if (g == 0 && base + b * 128 < cols) scale[b] = scale_of(most);
+        }
+    }
+}
+
+template <int LANES, bool VEC>
+__device__ __forceinline__ void store_mx4(uint8_t* q, uint8_t* scale, int base, int g, int cols, const float (&y)[8]) {
+    scale += base / 32;
+    if constexpr (VEC) {
+        const uint32_t code = mx4_code(group_max_bits<4>(largest_bits(y)));
+        if (base + 8 * g < cols) {
+            *reinterpret_cast<uint32_t*>(q + base / 2 + 4 * g) = mx4_eight(y, code);
+            if (g % 4 == 0) scale[g / 4] = uint8_t(code);
+        }
+    } else {
+        constexpr int kEach = 32 / LANES;  // a lane's values of a block
+#pragma unroll
+        for (int b = 0; b < 8 / kEach; ++b) {
+            uint32_t bits = 0;
+#pragma unroll
+            for (int i = 0; i < kEach; ++i) bits = max(bits, __float_as_uint(y[b * kEach + i]) & 0x7fffffffu);
+            const uint32_t code = mx4_code(group_max_bits<LANES>(bits));
+            const float inverse = mx4_inverse(code);
+#pragma unroll
+            for (int i = 0; i < kEach; ++i) {  // columns are even and odd as g is
+                const float v = y[b * kEach + i], next = __shfl_down_sync(kFullMask, v, 1);
+                const int c = base + (b * kEach + i) * LANES + g;
+                if (c < cols && (g & 1) == 0) q[c / 2] = code == 255 ? 0 : uint8_t(mx4_pair(v, next, inverse));
+            }
+            if (g == 0 && base + b * 32 < cols) scale[b] = uint8_t(code);
+        }
+    }
+}
+
+}  // namespace rowops

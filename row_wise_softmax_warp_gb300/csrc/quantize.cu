@@ -16,8 +16,7 @@
 // reciprocal a block.  16384 x 4096 bf16: 35 us by rows; 4096 x 4096 by tiles: 14.2 us,
 // whose loads, maximum and stores follow one another in each block of threads.  Rows
 // that are no multiple of 8 values are read value by value (8192 x 1001: 10.5 us, x 1000: 6.4).
-#include <cuda_fp8.h>
-
+#include "quant.cuh"
 #include "types.cuh"
 
 namespace rowops {
@@ -25,8 +24,6 @@ namespace {
 
 constexpr int kQuantThreads = 256;
 constexpr int kQuantGroups = kQuantThreads / 16;
-constexpr float kLargest = 448.0f;        // of e4m3
-constexpr float kSmallestMax = 0x1p-100f;
 
 // 8 consecutive values, of which `n` are there (the others are 0), as loaded:
 // widened to fp32 only when they are used, so loads on their way take few registers.
@@ -58,55 +55,6 @@ struct Eight<T, false> {
         for (int i = 0; i < 8; ++i) v[i] = f[i];
     }
 };
-
-// Largest magnitude; NaN values do not count, infinite ones do.
-__device__ __forceinline__ float largest(const float (&v)[8]) {
-    float m = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[i]));
-    return m;
-}
-// Largest finite magnitude.
-__device__ __forceinline__ float largest_finite(const float (&v)[8]) {
-    float m = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (fabsf(v[i]) < INFINITY) m = fmaxf(m, fabsf(v[i]));
-    return m;
-}
-
-// a / 448, correctly rounded: the same step with the rounded reciprocal of 448.
-__device__ __forceinline__ float scale_of(float a) {
-    constexpr float kInv = 1.0f / kLargest;
-    const float q0 = a * kInv;
-    return fmaf(fmaf(-q0, kLargest, a), kInv, q0);
-}
-
-// 448 x / a by the reciprocal and one residual step (Markstein 1990): q0 is off by
-// at most three units, r is its exact residual, and a quotient that fp32 holds (as
-// every border between e4m3 values does) comes out exact.  An infinite or NaN x
-// makes r NaN.  x and a are divided by 2^32 where 448 x could overflow.
-struct Divisor {
-    float scale, d, inv;
-    __device__ __forceinline__ explicit Divisor(float a) {
-        const float s = a > 0x1p100f ? 0x1p-32f : 1.0f;
-        scale = kLargest * s;
-        d = a * s;
-        asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(inv) : "f"(d));  // off by a unit at most
-    }
-    __device__ __forceinline__ float operator()(float x) const {
-        const float t = x * scale, q0 = t * inv, r = fmaf(-q0, d, t);
-        return fmaf(r, inv, q0);
-    }
-};
-
-__device__ __forceinline__ uint2 quantize8(const float (&v)[8], const Divisor& over) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        w[i] = __nv_cvt_float2_to_fp8x2(make_float2(over(v[2 * i]), over(v[2 * i + 1])), __NV_SATFINITE, __NV_E4M3);
-    return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
-}
 
 template <bool VEC>
 __device__ __forceinline__ void store8(uint8_t* p, int n, uint2 w) {
