@@ -741,8 +741,8 @@ int rowops_expert_matmul_mx4(const uint8_t* xq, const uint8_t* xs, const uint8_t
         bws{ws, experts * out_cols * kb}, bo{offsets, (experts + 1) * 4}, by{y, slots * out_cols * yb};
     if (int e = check_overlap({bx, bxs, bw, bws, bo}, {by})) return e;
     if (int e = check_workspace(workspace, workspace_bytes, {bx, bxs, bw, bws, bo, by})) return e;
-    return to_status(
-        rowops::launch_matmul_mx4_any(xq, xs, wq, ws, offsets, y, slots, in_cols, out_cols, experts, y_type, st(stream)));
+    return to_status(rowops::launch_expert_matmul_mx4(xq, xs, wq, ws, offsets, y, slots, in_cols, out_cols, experts,
+                                                      y_type, scratch_of(workspace, workspace_bytes), st(stream)));
 }
 
 // ------------------------------------------- between two sublayers' products

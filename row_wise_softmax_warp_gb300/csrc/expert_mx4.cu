@@ -1,0 +1,403 @@
+// expert_mx4.cu - the experts' product on microscaled 4-bit operands (tcgen05
+// kind::mxf4, clusters of two CTAs).
+//
+//   y[s][n] = sum_k 2^(ws - 127) wq[e][n][k] * 2^(xs - 127) xq[s][k]     rows s of expert e
+//
+// Laid out as expert_matmul.cu: weights on the M side, 256 output columns of a pair of
+// CTAs; tokens on the N side, up to 224 of a group; a stage of 128 bytes along the sum,
+// which is 256 values in eight blocks.  The tensor cores multiply by the scales: they
+// read them from tensor memory, where the 128 rows of an operand lie as 32 lanes of four
+// columns, four blocks a column, the same in all four quarters.  Each CTA needs the
+// scales of its own 128 output columns and those of all tokens.  Three warps a CTA read
+// them as they lie in memory, write them to the stage in that order, and
+// tcgen05.cp moves them, in order with the products that follow.
+//
+// Two accumulators of 224 columns and two stages' scales (24 columns each) fill 496 of
+// the 512 columns of tensor memory; with 256 tokens a tile there would be no room for
+// the scales, or for the second accumulator that hides the write-out.
+#include "groups.cuh"
+#include "tensor_core.cuh"
+#include "types.cuh"
+
+namespace rowops {
+namespace {
+
+constexpr int kTileRows = 224;                // most tokens of a tile
+constexpr int kStepBytes = 128, kStepBlocks = 8;  // of the sum per stage
+constexpr int kStages = 6;
+constexpr uint32_t kWBytes = 128 * 128, kXBytes = kTileRows / 2 * 128;  // a CTA's share of a stage
+constexpr uint32_t kAtom = 512;               // scales of 128 rows and four blocks
+constexpr uint32_t kScaleBytes = 6 * kAtom;   // weights' two, tokens' four
+constexpr uint32_t kStageBytes = kWBytes + kXBytes + kScaleBytes;
+static_assert(kStageBytes % 1024 == 0 && kXBytes % 1024 == 0, "operands start on whole swizzle atoms");
+constexpr int kCopyWarpW = 4, kCopyWarpX = 5, kProductWarp = 6, kScaleWarp = 7;  // and the two behind it
+constexpr int kScaleWarps = 3;
+constexpr int kThreads = (kScaleWarp + kScaleWarps) * 32;
+constexpr uint32_t kTmemColumns = 512;
+constexpr uint32_t kScaleColumn = 2 * kTileRows, kScaleColumns = 24;
+
+struct Mx4ProductArgs {
+    CUtensorMap w;        // boxes of 128 output columns
+    CUtensorMap x;        // boxes of 64 rows
+    CUtensorMap x_small;  // boxes of 16 rows
+    const uint8_t* xs;
+    const uint8_t* ws;
+    const int32_t* offsets;
+    void* y;
+    int slots, experts;
+    int out, bytes;  // bytes of a row of an operand
+    int blocks;      // scales of a row
+    int scale_vec;   // bytes that a load of scales may take: 16, 8 or 1
+};
+
+struct Mx4Shared {
+    uint64_t full[kStages], empty[kStages];
+    uint64_t acc_full[2], acc_empty[2];
+    int warp_tiles[kThreads / 32];
+    uint32_t tmem;
+    uint32_t progress;  // stages whose copies are under way, for waits that span many
+    int abort;
+};
+
+struct Mx4Tile {
+    int expert = 0;
+    int m0;     // first output column of the pair's 256
+    int n0, n;  // rows
+    int width;  // rows the products compute
+};
+
+__device__ __forceinline__ bool tile_at(const Mx4ProductArgs& g, const int* table, int t, int tiles, Mx4Tile& w) {
+    if (t >= tiles) return false;
+    const int tiles_m = (g.out + 255) / 256;
+    const RowTile r = row_tile<kTileRows>(g.offsets, g.experts, g.slots, table, t / tiles_m, w.expert);
+    w.expert = uniform(r.expert);
+    w.m0 = t % tiles_m * 256;
+    w.n0 = uniform(r.first);
+    w.n = uniform(r.count);
+    w.width = (w.n + 31) & ~31;
+    return true;
+}
+
+// Descriptor of an atom of scales: rows of 16 bytes, 8 of them in 128, no swizzle.
+__device__ __forceinline__ uint64_t scale_desc(uint32_t addr) {
+    return uint64_t((addr >> 4) & 0x3fff) | (uint64_t(1) << 16) | (uint64_t(128 >> 4) << 32) | (uint64_t(1) << 46);
+}
+// An atom to four columns of tensor memory of each CTA, from its own shared memory.
+__device__ __forceinline__ void copy_scales(uint32_t to, uint64_t desc) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n}\n" ::"r"(to),
+        "l"(desc)
+        : "memory");
+}
+
+// Block-scaled instruction descriptor: e2m1 (code 1) both, power-of-two scales, M = 256,
+// 64 values of the sum; `id`: the first of the two blocks' bytes within a column.
+constexpr uint32_t mx4_desc(uint32_t id) {
+    return (id << 4) | (1u << 7) | (1u << 10) | (1u << 23) | ((256u >> 4) << 24) | (id << 29);
+}
+// A stage: four products of 64 values.  ws, xs: the stage's scales in tensor memory, four
+// blocks in 4 and in 8 columns.
+__device__ __forceinline__ void mma_pair_mx4_4(uint32_t d, uint64_t a, uint64_t b, uint32_t n_bits, uint32_t ws, uint32_t xs,
+                                               bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t.reg .b64 a, b;\n\t.reg .b32 i, j, u, v;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "or.b32 i, %3, %7;\n\tor.b32 j, %3, %8;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, i, [%4], [%5], p;\n\t"
+        "setp.eq.b32 p, 0, 0;\n\t"
+        "add.s64 a, %1, 2;\n\tadd.s64 b, %2, 2;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], a, b, j, [%4], [%5], p;\n\t"
+        "add.s64 a, a, 2;\n\tadd.s64 b, b, 2;\n\tadd.u32 u, %4, 4;\n\tadd.u32 v, %5, 8;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], a, b, i, [u], [v], p;\n\t"
+        "add.s64 a, a, 2;\n\tadd.s64 b, b, 2;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], a, b, j, [u], [v], p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(n_bits), "r"(ws), "r"(xs), "r"(uint32_t(add)), "n"(mx4_desc(0)), "n"(mx4_desc(2))
+        : "memory");
+}
+
+// What a scale warp reads next: 16 scales (two stages) of each of four rows a lane, which
+// lie 32 apart.
+struct ScaleRows {
+    const uint8_t* p[4];  // their rows of scales; NULL: none
+    __device__ __forceinline__ void load(int block, int blocks, int vec, uint32_t (&r)[4][4]) const {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) r[j][i] = 0;
+            if (p[j] == nullptr) continue;
+            const uint8_t* at = p[j] + block;
+            const int left = blocks - block;  // at least 1
+            if (vec == 16) {                  // rows of a multiple of 16
+                const uint4 v = __ldg(reinterpret_cast<const uint4*>(at));
+                r[j][0] = v.x, r[j][1] = v.y, r[j][2] = v.z, r[j][3] = v.w;
+            } else if (vec == 8) {
+                const uint2 v = __ldg(reinterpret_cast<const uint2*>(at));
+                r[j][0] = v.x, r[j][1] = v.y;
+                if (left > 8) {
+                    const uint2 u = __ldg(reinterpret_cast<const uint2*>(at + 8));
+                    r[j][2] = u.x, r[j][3] = u.y;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (i < left) r[j][i / 4] |= uint32_t(__ldg(at + i)) << (8 * (i % 4));
+            }
+        }
+    }
+};
+
+// One warp's 32 output columns of a tile: a lane holds one, a register a row of y.
+template <typename O>
+__device__ __forceinline__ void write_rows(const Mx4ProductArgs& g, const Mx4Tile& w, uint32_t tmem, uint32_t free_bar, int m) {
+    for (int c = 0; c < w.n; c += 32) {
+        uint32_t r[32];
+        tmem_load32(tmem + uint32_t(c), r);
+        tmem_wait_load(r);
+        if (c + 32 >= w.n) {
+            tcgen05_fence_before();
+            __syncwarp();
+            elect_arrive_pair(free_bar);
+        }
+        if (m < g.out) {
+            O* p = static_cast<O*>(g.y) + int64_t(w.n0 + c) * g.out + m;
+            const int rows = w.n - c;
+            if (rows >= 32) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i, p += g.out) *p = from_float<O>(__uint_as_float(r[i]));
+            } else {
+#pragma unroll
+                for (int i = 0; i < 32; ++i, p += g.out)
+                    if (i < rows) *p = from_float<O>(__uint_as_float(r[i]));
+            }
+        }
+        __syncwarp();
+    }
+}
+
+template <typename O>
+__global__ void __launch_bounds__(kThreads, 1) expert_product_mx4(const __grid_constant__ Mx4ProductArgs g) {
+    extern __shared__ unsigned char raw[];
+    unsigned char* stages = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
+    int* table = reinterpret_cast<int*>(stages + kStages * kStageBytes);
+    __shared__ Mx4Shared sh;
+    volatile int* abort_flag = &sh.abort;
+    volatile uint32_t* progress = &sh.progress;
+
+    const int warp = uniform(int(threadIdx.x >> 5)), lane = threadIdx.x & 31;
+    const uint32_t rank = uniform(cluster_rank());
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&sh.full[i], 2 + 2 * kScaleWarps);  // a copying lane per operand, both CTAs' scale warps
+            mbar_init(&sh.empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh.acc_full[i], 1);
+            mbar_init(&sh.acc_empty[i], 8);  // the write-out warps of both CTAs
+        }
+        sh.progress = 0;
+        sh.abort = 0;
+        fence_barrier_init();
+    }
+    if (warp == kCopyWarpW && lane == 0) {
+        prefetch_map(&g.w);
+        prefetch_map(&g.x);
+        prefetch_map(&g.x_small);
+    }
+    if (warp == kProductWarp) tmem_alloc_pair(&sh.tmem, kTmemColumns);
+    build_tile_table<kTileRows, kThreads>(g.offsets, g.experts, g.slots, table, sh.warp_tiles);
+    tcgen05_fence_before();
+    __syncthreads();
+    cluster_sync_all();
+    tcgen05_fence_after();
+    const uint32_t tmem = uniform(sh.tmem), stage0 = uniform(smem_addr(stages));
+
+    const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
+    const int tiles = uniform(all_tiles(table[g.experts], (g.out + 255) / 256));
+    const int steps = (g.bytes + kStepBytes - 1) / kStepBytes;  // stages of a sum
+    bool ok = true;
+    if (warp == kCopyWarpW || warp == kCopyWarpX) {
+        const bool is_w = warp == kCopyWarpW;
+        const uint32_t to = stage0 + (is_w ? 0 : kWBytes);
+        const uint32_t full0 = map_to_rank(sh.full, 0);
+        uint32_t s = 0, phase = 1;  // the stage, and the parity of its release
+        uint32_t stages_begun = 0;
+        Mx4Tile w;
+        for (int t = first; ok && tile_at(g, table, t, tiles, w); t += step) {
+            const int half = w.width / 2;
+            const int m0 = w.m0 + int(rank) * 128, n0 = w.n0 + int(rank) * half;
+            const uint32_t mine = is_w ? kWBytes : uint32_t(half) * 128;
+            for (int kb = 0; kb < steps; ++kb) {
+                ok = warp_wait(&sh.empty[s], phase, abort_flag);
+                if (!ok) break;
+                const uint32_t bar = full0 + s * 8, dst = to + s * kStageBytes;
+                if (rank == 0) elect_arrive_expect_tx(&sh.full[s], 2 * mine);
+                if (is_w) {
+                    *progress = ++stages_begun;
+                    tma_load_3d(dst, &g.w, kb * kStepBytes, m0, w.expert, bar);
+                } else {
+                    load_rows(dst, &g.x, &g.x_small, kb * kStepBytes, n0, half, bar);
+                }
+                next_stage<kStages>(s, phase);
+            }
+        }
+        // every stage is released in this CTA too before it may leave
+        for (int i = 0; ok && i < kStages; ++i) {
+            ok = warp_wait(&sh.empty[s], phase, abort_flag);
+            next_stage<kStages>(s, phase);
+        }
+    } else if (warp == kProductWarp) {
+        if (rank == 0) {
+            uint32_t s = 0, phase = 0, acc = 0, turn = 0;  // turn: which of the two stages' scales
+            const uint64_t a0 = operand_desc(stage0, 16, 1024), b0 = operand_desc(stage0 + kWBytes, 16, 1024);
+            const uint64_t s0 = scale_desc(stage0 + kWBytes + kXBytes);
+            Mx4Tile w;
+            for (int t = first; ok && tile_at(g, table, t, tiles, w); t += step) {
+                const uint32_t d = tmem + (acc & 1) * kTileRows, n_bits = uint32_t(w.width >> 3) << 17;
+                const bool two = w.width > 128;
+                ok = warp_wait(&sh.acc_empty[acc & 1], ((acc >> 1) & 1) ^ 1, abort_flag);
+                bool ready = false;  // the stage was seen full
+                for (int kb = 0; ok && kb < steps; ++kb) {
+                    ok = ready || warp_wait<true>(&sh.full[s], phase, abort_flag);
+                    if (!ok) break;
+                    tcgen05_fence_after();
+                    const uint32_t here = s, at = s * (kStageBytes >> 4);
+                    next_stage<kStages>(s, phase);
+                    const uint32_t looks = kb + 1 < steps ? look<true>(&sh.full[s], phase) : 0;
+                    const uint32_t ws = tmem + kScaleColumn + turn * kScaleColumns, xs = ws + 8;
+                    turn ^= 1;
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        copy_scales(ws + q * 4, s0 + at + q * (kAtom >> 4));
+                        copy_scales(xs + q * 8, s0 + at + (2 + q) * (kAtom >> 4));
+                        if (two) copy_scales(xs + q * 8 + 4, s0 + at + (4 + q) * (kAtom >> 4));
+                    }
+                    mma_pair_mx4_4(d, a0 + at, b0 + at, n_bits, ws, xs, kb > 0);
+                    mma_commit_pair(&sh.empty[here]);
+                    ready = saw(looks);
+                }
+                if (ok) mma_commit_pair(&sh.acc_full[acc & 1]);
+                ++acc;
+            }
+        }
+    } else if (warp >= kScaleWarp) {
+        // Warp 0 of the three has the weights' scales, 1 and 2 the tokens'.  16 scales a row are
+        // on their way while the 16 before them are written, across tiles too.
+        const int which = warp - kScaleWarp;
+        const uint32_t full0 = map_to_rank(sh.full, 0);
+        const auto rows_of = [&](const Mx4Tile& w, ScaleRows& r) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int row = (which == 2 ? 128 : 0) + 32 * j + lane;
+                if (which == 0) {
+                    const int m = w.m0 + int(rank) * 128 + row;
+                    r.p[j] = m < g.out ? g.ws + (int64_t(w.expert) * g.out + m) * g.blocks : nullptr;
+                } else {
+                    r.p[j] = row < w.n ? g.xs + int64_t(w.n0 + row) * g.blocks : nullptr;
+                }
+            }
+        };
+        uint32_t s = 0, phase = 1;
+        Mx4Tile w;
+        ScaleRows rows;
+        uint32_t now[4][4];
+        int t = first, kb = 0;
+        bool more = tile_at(g, table, t, tiles, w);
+        if (more) {
+            rows_of(w, rows);
+            rows.load(0, g.blocks, g.scale_vec, now);
+        }
+        while (ok && more) {
+            const int stages_here = min(2, steps - kb);
+            kb += 2;
+            if (kb >= steps) {
+                kb = 0;
+                t += step;
+                more = tile_at(g, table, t, tiles, w);
+                if (more) rows_of(w, rows);
+            }
+            uint32_t next[4][4];
+            if (more) rows.load(kb * kStepBlocks, g.blocks, g.scale_vec, next);
+            __syncwarp();
+            for (int h = 0; h < stages_here; ++h) {
+                ok = warp_wait(&sh.empty[s], phase, abort_flag);
+                if (!ok) break;
+                unsigned char* to = stages + s * kStageBytes + kWBytes + kXBytes + which * 2 * kAtom + lane * 16;
+#pragma unroll
+                for (int q = 0; q < 2; ++q)
+                    *reinterpret_cast<uint4*>(to + q * kAtom) =
+                        h == 0 ? make_uint4(now[0][q], now[1][q], now[2][q], now[3][q])
+                               : make_uint4(now[0][2 + q], now[1][2 + q], now[2][2 + q], now[3][2 + q]);
+                fence_async_shared();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(full0 + s * 8);
+                next_stage<kStages>(s, phase);
+            }
+            if (more)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) now[j][i] = next[j][i];
+        }
+    } else {
+        uint32_t acc = 0;
+        Mx4Tile w;
+        for (int t = first; tile_at(g, table, t, tiles, w); t += step) {
+            if (!warp_wait_stages(&sh.acc_full[acc & 1], (acc >> 1) & 1, abort_flag, progress)) break;
+            tcgen05_fence_after();
+            write_rows<O>(g, w, tmem + (uint32_t(warp * 32) << 16) + (acc & 1) * kTileRows,
+                          map_to_rank(&sh.acc_empty[acc & 1], 0), w.m0 + int(rank) * 128 + warp * 32 + lane);
+            ++acc;
+        }
+    }
+    __syncwarp();
+    if (*abort_flag) let_copies_land();
+    tcgen05_fence_before();
+    __syncthreads();
+    cluster_sync_all();  // no CTA leaves, or frees tensor memory, while the other still uses it
+    tcgen05_fence_after();
+    if (warp == kProductWarp) tmem_dealloc_pair(tmem, kTmemColumns);
+}
+
+constexpr size_t kMostSmem = 1024 + kStages * size_t(kStageBytes) + (kMaxExperts + 1) * 4;
+
+}  // namespace
+
+uint32_t pipeline_timeouts_mx4() { return read_pipeline_timeouts(); }
+
+cudaError_t launch_expert_matmul_mx4(const uint8_t* x, const uint8_t* xs, const uint8_t* w, const uint8_t* ws,
+                                     const int32_t* offsets, void* y, int64_t slots, int64_t in, int64_t out,
+                                     int64_t experts, int y_type, Scratch scratch, cudaStream_t stream) {
+    Matrix mx = matrix_of(x, in / 2, slots, 1, 1), mw = matrix_of(w, in / 2, out, experts, 1);
+    Matrix* ms[2] = {&mx, &mw};
+    cudaError_t err;
+    if (!make_readable(ms, {false, true}, offsets, slots, scratch, stream, &err))
+        return launch_matmul_mx4_any(x, xs, w, ws, offsets, y, slots, in, out, experts, y_type, stream);
+    if (err != cudaSuccess) return err;
+    const CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+    Mx4ProductArgs g;
+    if (!make_map(&g.w, type, mw, kStepBytes, 128, true) || !make_map(&g.x_small, type, mx, kStepBytes, 16, false))
+        return cudaErrorInvalidValue;
+    g.x = g.x_small;  // half a tile is 64 rows or more only where a tile has more than 96
+    if (slots > 96 && !make_map(&g.x, type, mx, kStepBytes, 64, false)) return cudaErrorInvalidValue;
+    g.xs = xs;
+    g.ws = ws;
+    g.offsets = offsets;
+    g.y = y;
+    g.slots = int(slots);
+    g.experts = int(experts);
+    g.out = int(out);
+    g.bytes = int(in / 2);
+    g.blocks = int((in + 31) / 32);
+    const uintptr_t at = reinterpret_cast<uintptr_t>(xs) | reinterpret_cast<uintptr_t>(ws) | uintptr_t(g.blocks);
+    g.scale_vec = at % 16 == 0 ? 16 : at % 8 == 0 ? 8 : 1;
+    const int64_t tiles = most_row_tiles(slots, experts, kTileRows) * ((out + 255) / 256);
+    cudaError_t e = cudaErrorInvalidValue;
+    if (tiles >= kMostTiles) return e;  // more than a device's memory holds
+    with_type(y_type, [&](auto o) {
+        e = launch_pairs<expert_product_mx4<decltype(o)>>(tiles, kThreads, kMostSmem, stream, g);
+    });
+    return e;
+}
+
+}  // namespace rowops

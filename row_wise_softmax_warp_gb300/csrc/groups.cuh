@@ -14,7 +14,7 @@ constexpr int kMaxExperts = 1024;
 
 // Groups that overlap (offsets that fall and rise again: bad ones, but stay in
 // bounds) can name every row up to 512 times, so counts of tiles are added up
-// unsigned, which holds 512 * 2^30 rows in tiles of 256, and cut at kMostTiles.
+// unsigned, which holds 512 * 2^30 rows in tiles of more than 128, and cut at kMostTiles.
 // Groups that do not overlap have fewer: the host refuses more than kMostTiles.
 constexpr int kMostTiles = 1 << 30;
 
@@ -76,7 +76,7 @@ __device__ __forceinline__ bool find_row_tile(const int32_t* offsets, int expert
 template <int TILE, int NT>
 __device__ __forceinline__ void build_tile_table(const int32_t* offsets, int experts, int slots, int* table,
                                                  int* scratch) {
-    static_assert(TILE >= 256, "512 groups of 2^30 rows have to fit the sum");
+    static_assert(TILE > 128, "512 groups of 2^30 rows have to fit the sum");
     constexpr int kPer = (kMaxExperts + NT - 1) / NT;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int per = (experts + NT - 1) / NT, first = threadIdx.x * per;  // a run of experts each
@@ -119,21 +119,23 @@ __device__ __forceinline__ int tile_expert(const int* table, int experts, int ti
 }
 
 // Groups cut into even tiles for the tcgen05 products: a group of n rows into
-// ceil(n / kMostRows) tiles of a multiple of 32 rows (the last may be shorter).
+// ceil(n / MOST) tiles of a multiple of 32 rows (the last may be shorter).
 constexpr int kMostRows = 256;
 
 struct RowTile {
     int expert, first, count;
 };
 
-// table: build_tile_table<kMostRows>; 0 <= tile < table[experts], and from as for tile_expert.
+// table: build_tile_table<MOST>; 0 <= tile < table[experts], and from as for tile_expert.
+template <int MOST = kMostRows>
 __device__ __forceinline__ RowTile row_tile(const int32_t* offsets, int experts, int slots, const int* table,
                                             int tile, int from) {
     RowTile t;
     t.expert = tile_expert(table, experts, tile, from);
     const RowRange r = group_rows(offsets, t.expert, slots);
-    const int tiles = (r.count + kMostRows - 1) / kMostRows;
-    const int each = ((r.count + tiles - 1) / tiles + 31) & ~31;  // at most kMostRows, and every tile gets a row
+    static_assert(MOST % 32 == 0 && MOST > 128, "even tiles of a multiple of 32 rows are no more than MOST");
+    const int tiles = (r.count + MOST - 1) / MOST;
+    const int each = ((r.count + tiles - 1) / tiles + 31) & ~31;  // at most MOST, and every tile gets a row
     const int at = (tile - table[t.expert]) * each;
     t.first = r.first + at;
     t.count = min(each, r.count - at);
@@ -141,8 +143,8 @@ __device__ __forceinline__ RowTile row_tile(const int32_t* offsets, int experts,
 }
 
 // Host: the most row tiles that groups of `slots` rows in all can have.
-inline int64_t most_row_tiles(int64_t slots, int64_t experts) {
-    return slots / kMostRows + (experts < slots ? experts : slots);
+inline int64_t most_row_tiles(int64_t slots, int64_t experts, int most = kMostRows) {
+    return slots / most + (experts < slots ? experts : slots);
 }
 
 }  // namespace rowops

@@ -148,6 +148,7 @@ uint32_t pipeline_timeouts_pairs();
 uint32_t pipeline_timeouts_ln();
 uint32_t pipeline_timeouts_matmul();
 uint32_t pipeline_timeouts_fp8();
+uint32_t pipeline_timeouts_mx4();
 // LayerNorm backward stage 1 on rows of 384..1024 floats on 16-byte
 // boundaries through the bulk-copy ring (one CTA per SM, at most 2^17 / cols
 // and at most max_ctas, 0: no further limit); writes
@@ -280,6 +281,9 @@ cudaError_t launch_expert_matmul_wgrad(const void* dy, const void* x, const int3
                                        int64_t slots, int64_t in, int64_t out, int64_t experts, int dtype,
                                        int dw_type, Scratch scratch, cudaStream_t stream);
 cudaError_t launch_expert_matmul_fp8(const uint8_t* x, const float* x_scale, const uint8_t* w, const float* w_scale,
+                                     const int32_t* offsets, void* y, int64_t slots, int64_t in, int64_t out,
+                                     int64_t experts, int y_type, Scratch scratch, cudaStream_t stream);
+cudaError_t launch_expert_matmul_mx4(const uint8_t* x, const uint8_t* xs, const uint8_t* w, const uint8_t* ws,
                                      const int32_t* offsets, void* y, int64_t slots, int64_t in, int64_t out,
                                      int64_t experts, int y_type, Scratch scratch, cudaStream_t stream);
 // The same products for matrices of any alignment, without scratch memory.

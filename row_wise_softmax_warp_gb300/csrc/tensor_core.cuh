@@ -222,17 +222,29 @@ __device__ __forceinline__ void let_copies_land() {
 // before the cluster's first synchronisation; the parity is 0 or 1; and the instructions
 // take their documented operands alone.  A form with the suspend hint as a fourth operand
 // under the elected lane's predicate ended in an illegal instruction and is not used.
+// CLUSTER: the acquire is the cluster's, for barriers on which the other CTA's threads
+// arrive after writes of their own.
 enum class Polled { kDone, kAborted, kRanOut };
+template <bool CLUSTER = false>
 __device__ __forceinline__ Polled warp_poll(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint32_t polls) {
     for (uint32_t i = 0; i < polls; ++i) {
         uint32_t done;
-        asm volatile(
-            "{\n\t.reg .pred p, e;\n\tsetp.ne.u32 p, 0, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
-            "@e mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-            "selp.u32 %0, 1, 0, p;\n}\n"
-            : "=r"(done)
-            : "r"(smem_addr(bar)), "r"(parity)
-            : "memory");
+        if constexpr (CLUSTER)
+            asm volatile(
+                "{\n\t.reg .pred p, e;\n\tsetp.ne.u32 p, 0, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+                "@e mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+                "selp.u32 %0, 1, 0, p;\n}\n"
+                : "=r"(done)
+                : "r"(smem_addr(bar)), "r"(parity)
+                : "memory");
+        else
+            asm volatile(
+                "{\n\t.reg .pred p, e;\n\tsetp.ne.u32 p, 0, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+                "@e mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+                "selp.u32 %0, 1, 0, p;\n}\n"
+                : "=r"(done)
+                : "r"(smem_addr(bar)), "r"(parity)
+                : "memory");
         if (__any_sync(kFullMask, done)) {
             __syncwarp();
             return Polled::kDone;
@@ -243,8 +255,9 @@ __device__ __forceinline__ Polled warp_poll(uint64_t* bar, uint32_t parity, vola
 }
 // Bounded wait of a whole warp; false (after raising the abort) on timeout or abort.
 // For what comes after a stage's or a tile's writing at the latest.
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
-    const Polled p = warp_poll(bar, parity, abort_flag, kQuickPolls);
+    const Polled p = warp_poll<CLUSTER>(bar, parity, abort_flag, kQuickPolls);
     if (p == Polled::kRanOut && (threadIdx.x & 31) == 0) raise_abort(abort_flag);
     return p == Polled::kDone;
 }
@@ -266,15 +279,25 @@ __device__ __forceinline__ bool warp_wait_stages(uint64_t* bar, uint32_t parity,
 // A look at barriers without waiting: under the tensor cores' traffic one takes some
 // 280 clocks (55 on an idle SM), so a loop looks at the next stage's before it
 // works on this one's and asks for the answer, saw(), afterwards.  The whole warp.
+template <bool CLUSTER = false>
 __device__ __forceinline__ uint32_t look(uint64_t* bar, uint32_t parity) {
     uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p, e;\n\tsetp.ne.u32 p, 0, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
-        "@e mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(done)
-        : "r"(smem_addr(bar)), "r"(parity)
-        : "memory");
+    if constexpr (CLUSTER)
+        asm volatile(
+            "{\n\t.reg .pred p, e;\n\tsetp.ne.u32 p, 0, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+            "@e mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n}\n"
+            : "=r"(done)
+            : "r"(smem_addr(bar)), "r"(parity)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p, e;\n\tsetp.ne.u32 p, 0, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+            "@e mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n}\n"
+            : "=r"(done)
+            : "r"(smem_addr(bar)), "r"(parity)
+            : "memory");
     return done;
 }
 __device__ __forceinline__ bool saw(uint32_t looks) {
