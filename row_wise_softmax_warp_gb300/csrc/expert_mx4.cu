@@ -23,16 +23,20 @@ namespace rowops {
 namespace {
 
 constexpr int kTileRows = 224;                // most tokens of a tile
-constexpr int kStepBytes = 128, kStepBlocks = 8;  // of the sum per stage
+constexpr int kStepBytes = 128;               // of the sum per stage: eight blocks
 constexpr int kStages = 6;
 constexpr uint32_t kWBytes = 128 * 128, kXBytes = kTileRows / 2 * 128;  // a CTA's share of a stage
-constexpr uint32_t kAtom = 512;               // scales of 128 rows and four blocks
-constexpr uint32_t kScaleBytes = 6 * kAtom;   // weights' two, tokens' four
-constexpr uint32_t kStageBytes = kWBytes + kXBytes + kScaleBytes;
+constexpr uint32_t kStageBytes = kWBytes + kXBytes;
 static_assert(kStageBytes % 1024 == 0 && kXBytes % 1024 == 0, "operands start on whole swizzle atoms");
-constexpr int kCopyWarpW = 4, kCopyWarpX = 5, kProductWarp = 6, kScaleWarp = 7;  // and the two behind it
-constexpr int kScaleWarps = 3;
-constexpr int kThreads = (kScaleWarp + kScaleWarps) * 32;
+constexpr int kAhead = 4;                     // stages whose scales are written together
+constexpr int kScaleSlots = 3;                // of such scales
+constexpr uint32_t kAtom = 512;               // scales of 128 rows and four blocks
+constexpr uint32_t kRoleBytes = kAhead * 2 * kAtom;  // of 128 rows in a slot
+constexpr int kRoles = 3;                     // weights, tokens 0 .. 127, tokens 128 ..
+constexpr uint32_t kSlotBytes = kRoles * kRoleBytes;
+constexpr int kScaleSets = 2;                 // of warps, which take turns
+constexpr int kCopyWarpW = 4, kCopyWarpX = 5, kProductWarp = 6, kScaleWarp = 7;
+constexpr int kThreads = (kScaleWarp + kRoles * kScaleSets) * 32;
 constexpr uint32_t kTmemColumns = 512;
 constexpr uint32_t kScaleColumn = 2 * kTileRows, kScaleColumns = 24;
 
@@ -52,6 +56,7 @@ struct Mx4ProductArgs {
 
 struct Mx4Shared {
     uint64_t full[kStages], empty[kStages];
+    uint64_t scale_full[kScaleSlots], scale_empty[kScaleSlots];
     uint64_t acc_full[2], acc_empty[2];
     int warp_tiles[kThreads / 32];
     uint32_t tmem;
@@ -116,31 +121,35 @@ __device__ __forceinline__ void mma_pair_mx4_4(uint32_t d, uint64_t a, uint64_t 
         : "memory");
 }
 
-// What a scale warp reads next: 16 scales (two stages) of each of four rows a lane, which
+// What a scale warp reads: the scales of four stages of each of four rows a lane, which
 // lie 32 apart.
 struct ScaleRows {
     const uint8_t* p[4];  // their rows of scales; NULL: none
-    __device__ __forceinline__ void load(int block, int blocks, int vec, uint32_t (&r)[4][4]) const {
+    __device__ __forceinline__ void load(int block, int blocks, int vec, uint32_t (&r)[4][2 * kAhead]) const {
+        const int left = blocks - block;  // at least 1
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) r[j][i] = 0;
+            for (int i = 0; i < 2 * kAhead; ++i) r[j][i] = 0;
             if (p[j] == nullptr) continue;
             const uint8_t* at = p[j] + block;
-            const int left = blocks - block;  // at least 1
-            if (vec == 16) {                  // rows of a multiple of 16
-                const uint4 v = __ldg(reinterpret_cast<const uint4*>(at));
-                r[j][0] = v.x, r[j][1] = v.y, r[j][2] = v.z, r[j][3] = v.w;
+            if (vec == 16) {  // blocks is a multiple of 16
+#pragma unroll
+                for (int i = 0; i < kAhead / 2; ++i)
+                    if (left > 16 * i) {
+                        const uint4 v = __ldg(reinterpret_cast<const uint4*>(at + 16 * i));
+                        r[j][4 * i] = v.x, r[j][4 * i + 1] = v.y, r[j][4 * i + 2] = v.z, r[j][4 * i + 3] = v.w;
+                    }
             } else if (vec == 8) {
-                const uint2 v = __ldg(reinterpret_cast<const uint2*>(at));
-                r[j][0] = v.x, r[j][1] = v.y;
-                if (left > 8) {
-                    const uint2 u = __ldg(reinterpret_cast<const uint2*>(at + 8));
-                    r[j][2] = u.x, r[j][3] = u.y;
-                }
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i)
+                    if (left > 8 * i) {
+                        const uint2 v = __ldg(reinterpret_cast<const uint2*>(at + 8 * i));
+                        r[j][2 * i] = v.x, r[j][2 * i + 1] = v.y;
+                    }
             } else {
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
+                for (int i = 0; i < 8 * kAhead; ++i)
                     if (i < left) r[j][i / 4] |= uint32_t(__ldg(at + i)) << (8 * (i % 4));
             }
         }
@@ -179,7 +188,8 @@ template <typename O>
 __global__ void __launch_bounds__(kThreads, 1) expert_product_mx4(const __grid_constant__ Mx4ProductArgs g) {
     extern __shared__ unsigned char raw[];
     unsigned char* stages = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
-    int* table = reinterpret_cast<int*>(stages + kStages * kStageBytes);
+    unsigned char* slots = stages + kStages * kStageBytes;
+    int* table = reinterpret_cast<int*>(slots + kScaleSlots * kSlotBytes);
     __shared__ Mx4Shared sh;
     volatile int* abort_flag = &sh.abort;
     volatile uint32_t* progress = &sh.progress;
@@ -188,8 +198,12 @@ __global__ void __launch_bounds__(kThreads, 1) expert_product_mx4(const __grid_c
     const uint32_t rank = uniform(cluster_rank());
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(&sh.full[i], 2 + 2 * kScaleWarps);  // a copying lane per operand, both CTAs' scale warps
+            mbar_init(&sh.full[i], 2);  // a copying lane per operand
             mbar_init(&sh.empty[i], 1);
+        }
+        for (int i = 0; i < kScaleSlots; ++i) {
+            mbar_init(&sh.scale_full[i], 2 * kRoles);  // both CTAs' scale warps
+            mbar_init(&sh.scale_empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.acc_full[i], 1);
@@ -220,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_product_mx4(const __grid_c
         const bool is_w = warp == kCopyWarpW;
         const uint32_t to = stage0 + (is_w ? 0 : kWBytes);
         const uint32_t full0 = map_to_rank(sh.full, 0);
-        uint32_t s = 0, phase = 1;  // the stage, and the parity of its release
+        uint32_t s = 0, phase = 1, slot = 0, slot_phase = 1;  // the stage and the scales' slot, and their releases' parities
         uint32_t stages_begun = 0;
         Mx4Tile w;
         for (int t = first; ok && tile_at(g, table, t, tiles, w); t += step) {
@@ -239,18 +253,23 @@ __global__ void __launch_bounds__(kThreads, 1) expert_product_mx4(const __grid_c
                     load_rows(dst, &g.x, &g.x_small, kb * kStepBytes, n0, half, bar);
                 }
                 next_stage<kStages>(s, phase);
+                if (kb % kAhead == 0) next_stage<kScaleSlots>(slot, slot_phase);
             }
         }
-        // every stage is released in this CTA too before it may leave
+        // every stage and slot is released in this CTA too before it may leave
         for (int i = 0; ok && i < kStages; ++i) {
             ok = warp_wait(&sh.empty[s], phase, abort_flag);
             next_stage<kStages>(s, phase);
         }
+        for (int i = 0; ok && i < kScaleSlots; ++i) {
+            ok = warp_wait(&sh.scale_empty[slot], slot_phase, abort_flag);
+            next_stage<kScaleSlots>(slot, slot_phase);
+        }
     } else if (warp == kProductWarp) {
         if (rank == 0) {
-            uint32_t s = 0, phase = 0, acc = 0, turn = 0;  // turn: which of the two stages' scales
+            uint32_t s = 0, phase = 0, slot = 0, slot_phase = 0, acc = 0, turn = 0;  // turn: of the two places in tensor memory
             const uint64_t a0 = operand_desc(stage0, 16, 1024), b0 = operand_desc(stage0 + kWBytes, 16, 1024);
-            const uint64_t s0 = scale_desc(stage0 + kWBytes + kXBytes);
+            const uint64_t s0 = scale_desc(uniform(smem_addr(slots)));
             Mx4Tile w;
             for (int t = first; ok && tile_at(g, table, t, tiles, w); t += step) {
                 const uint32_t d = tmem + (acc & 1) * kTileRows, n_bits = uint32_t(w.width >> 3) << 17;
@@ -258,22 +277,28 @@ __global__ void __launch_bounds__(kThreads, 1) expert_product_mx4(const __grid_c
                 ok = warp_wait(&sh.acc_empty[acc & 1], ((acc >> 1) & 1) ^ 1, abort_flag);
                 bool ready = false;  // the stage was seen full
                 for (int kb = 0; ok && kb < steps; ++kb) {
-                    ok = ready || warp_wait<true>(&sh.full[s], phase, abort_flag);
+                    if (kb % kAhead == 0) ok = warp_wait<true>(&sh.scale_full[slot], slot_phase, abort_flag);
+                    ok = ok && (ready || warp_wait(&sh.full[s], phase, abort_flag));
                     if (!ok) break;
                     tcgen05_fence_after();
                     const uint32_t here = s, at = s * (kStageBytes >> 4);
                     next_stage<kStages>(s, phase);
-                    const uint32_t looks = kb + 1 < steps ? look<true>(&sh.full[s], phase) : 0;
+                    const uint32_t looks = kb + 1 < steps ? look(&sh.full[s], phase) : 0;
                     const uint32_t ws = tmem + kScaleColumn + turn * kScaleColumns, xs = ws + 8;
+                    const uint64_t from = s0 + slot * (kSlotBytes >> 4) + (kb % kAhead) * 2 * (kAtom >> 4);
                     turn ^= 1;
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
-                        copy_scales(ws + q * 4, s0 + at + q * (kAtom >> 4));
-                        copy_scales(xs + q * 8, s0 + at + (2 + q) * (kAtom >> 4));
-                        if (two) copy_scales(xs + q * 8 + 4, s0 + at + (4 + q) * (kAtom >> 4));
+                        copy_scales(ws + q * 4, from + q * (kAtom >> 4));
+                        copy_scales(xs + q * 8, from + (kRoleBytes + q * kAtom) / 16);
+                        if (two) copy_scales(xs + q * 8 + 4, from + (2 * kRoleBytes + q * kAtom) / 16);
                     }
                     mma_pair_mx4_4(d, a0 + at, b0 + at, n_bits, ws, xs, kb > 0);
                     mma_commit_pair(&sh.empty[here]);
+                    if (kb % kAhead == kAhead - 1 || kb == steps - 1) {
+                        mma_commit_pair(&sh.scale_empty[slot]);
+                        next_stage<kScaleSlots>(slot, slot_phase);
+                    }
                     ready = saw(looks);
                 }
                 if (ok) mma_commit_pair(&sh.acc_full[acc & 1]);
@@ -281,63 +306,61 @@ __global__ void __launch_bounds__(kThreads, 1) expert_product_mx4(const __grid_c
             }
         }
     } else if (warp >= kScaleWarp) {
-        // Warp 0 of the three has the weights' scales, 1 and 2 the tokens'.  16 scales a row are
-        // on their way while the 16 before them are written, across tiles too.
-        const int which = warp - kScaleWarp;
-        const uint32_t full0 = map_to_rank(sh.full, 0);
-        const auto rows_of = [&](const Mx4Tile& w, ScaleRows& r) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int row = (which == 2 ? 128 : 0) + 32 * j + lane;
-                if (which == 0) {
-                    const int m = w.m0 + int(rank) * 128 + row;
-                    r.p[j] = m < g.out ? g.ws + (int64_t(w.expert) * g.out + m) * g.blocks : nullptr;
-                } else {
-                    r.p[j] = row < w.n ? g.xs + int64_t(w.n0 + row) * g.blocks : nullptr;
-                }
-            }
-        };
-        uint32_t s = 0, phase = 1;
-        Mx4Tile w;
+        // Two sets of a warp a role take turns at the slots.  What a warp writes next is on its
+        // way while it writes, across tiles too.
+        const int role = (warp - kScaleWarp) % kRoles, set = (warp - kScaleWarp) / kRoles;
+        const uint32_t full0 = map_to_rank(sh.scale_full, 0);
+        const int parts = (steps + kAhead - 1) / kAhead;  // slots of a sum
         ScaleRows rows;
-        uint32_t now[4][4];
-        int t = first, kb = 0;
-        bool more = tile_at(g, table, t, tiles, w);
-        if (more) {
-            rows_of(w, rows);
-            rows.load(0, g.blocks, g.scale_vec, now);
-        }
-        while (ok && more) {
-            const int stages_here = min(2, steps - kb);
-            kb += 2;
-            if (kb >= steps) {
-                kb = 0;
+        Mx4Tile w;
+        int t = first, part = 0;
+        bool more = tile_at(g, table, t, tiles, w), moved = true;
+        const auto skip = [&](int n) {  // n slots on
+            for (part += n; more && part >= parts; part -= parts) {
                 t += step;
                 more = tile_at(g, table, t, tiles, w);
-                if (more) rows_of(w, rows);
+                moved = true;
             }
-            uint32_t next[4][4];
-            if (more) rows.load(kb * kStepBlocks, g.blocks, g.scale_vec, next);
+        };
+        const auto fetch = [&](uint32_t (&r)[4][2 * kAhead]) {
+            if (moved) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int row = (role == 2 ? 128 : 0) + 32 * j + lane;
+                    if (role == 0) {
+                        const int m = w.m0 + int(rank) * 128 + row;
+                        rows.p[j] = m < g.out ? g.ws + (int64_t(w.expert) * g.out + m) * g.blocks : nullptr;
+                    } else {
+                        rows.p[j] = row < w.n ? g.xs + int64_t(w.n0 + row) * g.blocks : nullptr;
+                    }
+                }
+                moved = false;
+            }
+            rows.load(part * 8 * kAhead, g.blocks, g.scale_vec, r);
+        };
+        uint32_t slot = 0, phase = 1;
+        for (int i = 0; i < set; ++i) next_stage<kScaleSlots>(slot, phase);
+        skip(set);
+        uint32_t now[4][2 * kAhead], next[4][2 * kAhead];
+        if (more) fetch(now);
+        while (ok && more) {
+            skip(kScaleSets);
+            if (more) fetch(next);
             __syncwarp();
-            for (int h = 0; h < stages_here; ++h) {
-                ok = warp_wait(&sh.empty[s], phase, abort_flag);
-                if (!ok) break;
-                unsigned char* to = stages + s * kStageBytes + kWBytes + kXBytes + which * 2 * kAtom + lane * 16;
+            ok = warp_wait(&sh.scale_empty[slot], phase, abort_flag);
+            if (!ok) break;
+            unsigned char* to = slots + slot * kSlotBytes + role * kRoleBytes + lane * 16;
 #pragma unroll
-                for (int q = 0; q < 2; ++q)
-                    *reinterpret_cast<uint4*>(to + q * kAtom) =
-                        h == 0 ? make_uint4(now[0][q], now[1][q], now[2][q], now[3][q])
-                               : make_uint4(now[0][2 + q], now[1][2 + q], now[2][2 + q], now[3][2 + q]);
-                fence_async_shared();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(full0 + s * 8);
-                next_stage<kStages>(s, phase);
-            }
-            if (more)
+            for (int q = 0; q < 2 * kAhead; ++q)
+                *reinterpret_cast<uint4*>(to + q * kAtom) = make_uint4(now[0][q], now[1][q], now[2][q], now[3][q]);
+            fence_async_shared();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(full0 + slot * 8);
+            for (int i = 0; i < kScaleSets; ++i) next_stage<kScaleSlots>(slot, phase);
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
+            for (int j = 0; j < 4; ++j)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) now[j][i] = next[j][i];
+                for (int i = 0; i < 2 * kAhead; ++i) now[j][i] = next[j][i];
         }
     } else {
         uint32_t acc = 0;
@@ -359,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_product_mx4(const __grid_c
     if (warp == kProductWarp) tmem_dealloc_pair(tmem, kTmemColumns);
 }
 
-constexpr size_t kMostSmem = 1024 + kStages * size_t(kStageBytes) + (kMaxExperts + 1) * 4;
+constexpr size_t kMostSmem = 1024 + kStages * size_t(kStageBytes) + kScaleSlots * kSlotBytes + (kMaxExperts + 1) * 4;
 
 }  // namespace
 
