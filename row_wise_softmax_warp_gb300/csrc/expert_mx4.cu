@@ -24,19 +24,19 @@ namespace {
 
 constexpr int kTileRows = 224;                // most tokens of a tile
 constexpr int kStepBytes = 128;               // of the sum per stage: eight blocks
-constexpr int kStages = 6;
+constexpr int kStages = 5;
 constexpr uint32_t kWBytes = 128 * 128, kXBytes = kTileRows / 2 * 128;  // a CTA's share of a stage
 constexpr uint32_t kStageBytes = kWBytes + kXBytes;
 static_assert(kStageBytes % 1024 == 0 && kXBytes % 1024 == 0, "operands start on whole swizzle atoms");
 constexpr int kAhead = 4;                     // stages whose scales are written together
-constexpr int kScaleSlots = 3;                // of such scales
+constexpr int kScaleSlots = 3;                // of such scales, each with a set of warps that writes it
 constexpr uint32_t kAtom = 512;               // scales of 128 rows and four blocks
 constexpr uint32_t kRoleBytes = kAhead * 2 * kAtom;  // of 128 rows in a slot
 constexpr int kRoles = 3;                     // weights, tokens 0 .. 127, tokens 128 ..
 constexpr uint32_t kSlotBytes = kRoles * kRoleBytes;
-constexpr int kScaleSets = 2;                 // of warps, which take turns
-constexpr int kCopyWarpW = 4, kCopyWarpX = 5, kProductWarp = 6, kScaleWarp = 7;
-constexpr int kThreads = (kScaleWarp + kRoles * kScaleSets) * 32;
+constexpr int kWriteWarps = 8;                // two for each 32 lanes of tensor memory, a block of 32 rows each in turn
+constexpr int kCopyWarpW = kWriteWarps, kCopyWarpX = kCopyWarpW + 1, kProductWarp = kCopyWarpX + 1, kScaleWarp = kProductWarp + 1;
+constexpr int kThreads = (kScaleWarp + kRoles * kScaleSlots) * 32;
 constexpr uint32_t kTmemColumns = 512;
 constexpr uint32_t kScaleColumn = 2 * kTileRows, kScaleColumns = 24;
 
@@ -52,6 +52,7 @@ struct Mx4ProductArgs {
     int out, bytes;  // bytes of a row of an operand
     int blocks;      // scales of a row
     int scale_vec;   // bytes that a load of scales may take: 16, 8 or 1
+    bool vec;        // rows of y allow 16-byte stores
 };
 
 struct Mx4Shared {
@@ -156,32 +157,52 @@ struct ScaleRows {
     }
 };
 
-// One warp's 32 output columns of a tile: a lane holds one, a register a row of y.
+// A block of 32 rows by a warp's 32 output columns: a lane holds a column, a register a
+// row.  16-bit results are turned in shared memory, pairs of rows in a word, and written
+// 16 bytes a lane: eight rows of 64 bytes a store, in place of one.
+constexpr int kTurnPitch = 128 + 16;          // of a pair of rows; the step keeps a read's lanes in banks of their own
+constexpr int kTurnBytes = 8 * kTurnPitch;
 template <typename O>
-__device__ __forceinline__ void write_rows(const Mx4ProductArgs& g, const Mx4Tile& w, uint32_t tmem, uint32_t free_bar, int m) {
-    for (int c = 0; c < w.n; c += 32) {
-        uint32_t r[32];
-        tmem_load32(tmem + uint32_t(c), r);
-        tmem_wait_load(r);
-        if (c + 32 >= w.n) {
-            tcgen05_fence_before();
-            __syncwarp();
-            elect_arrive_pair(free_bar);
-        }
-        if (m < g.out) {
-            O* p = static_cast<O*>(g.y) + int64_t(w.n0 + c) * g.out + m;
-            const int rows = w.n - c;
-            if (rows >= 32) {
+__device__ __forceinline__ void write_block(unsigned char* turn, O* p, int64_t pitch, int rows, int cols, bool vec,
+                                            const uint32_t (&r)[32]) {
+    const int lane = threadIdx.x & 31;
+    if constexpr (sizeof(O) == 2) {
+        if (vec) {
+            const int pair = lane / 4, col = lane % 4 * 8;  // a lane's two rows and eight columns
 #pragma unroll
-                for (int i = 0; i < 32; ++i, p += g.out) *p = from_float<O>(__uint_as_float(r[i]));
-            } else {
+            for (int half = 0; half < 2; ++half) {  // of the rows
 #pragma unroll
-                for (int i = 0; i < 32; ++i, p += g.out)
-                    if (i < rows) *p = from_float<O>(__uint_as_float(r[i]));
+                for (int i = 0; i < 8; ++i) {
+                    Chunk<O, 2> c;
+                    c.set(0, __uint_as_float(r[16 * half + 2 * i]));
+                    c.set(1, __uint_as_float(r[16 * half + 2 * i + 1]));
+                    *reinterpret_cast<uint32_t*>(turn + i * kTurnPitch + lane * 4) = c.raw;
+                }
+                __syncwarp();
+                const uint4* from = reinterpret_cast<const uint4*>(turn + pair * kTurnPitch + col * 4);
+                const uint4 a = from[0], b = from[1];
+                __syncwarp();
+                const uint4 low = make_uint4(__byte_perm(a.x, a.y, 0x5410), __byte_perm(a.z, a.w, 0x5410),
+                                             __byte_perm(b.x, b.y, 0x5410), __byte_perm(b.z, b.w, 0x5410));
+                const uint4 high = make_uint4(__byte_perm(a.x, a.y, 0x7632), __byte_perm(a.z, a.w, 0x7632),
+                                              __byte_perm(b.x, b.y, 0x7632), __byte_perm(b.z, b.w, 0x7632));
+                const int row = 16 * half + 2 * pair;
+                O* at = p + row * pitch + col;
+                if (col < cols) {  // cols is a multiple of 8
+                    if (row < rows) *reinterpret_cast<uint4*>(at) = low;
+                    if (row + 1 < rows) *reinterpret_cast<uint4*>(at + pitch) = high;
+                }
             }
+            return;
         }
-        __syncwarp();
     }
+    if (lane < cols) {
+        p += lane;
+#pragma unroll
+        for (int i = 0; i < 32; ++i, p += pitch)
+            if (i < rows) *p = from_float<O>(__uint_as_float(r[i]));
+    }
+    __syncwarp();
 }
 
 template <typename O>
@@ -189,7 +210,8 @@ __global__ void __launch_bounds__(kThreads, 1) expert_product_mx4(const __grid_c
     extern __shared__ unsigned char raw[];
     unsigned char* stages = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
     unsigned char* slots = stages + kStages * kStageBytes;
-    int* table = reinterpret_cast<int*>(slots + kScaleSlots * kSlotBytes);
+    unsigned char* turn = slots + kScaleSlots * kSlotBytes;
+    int* table = reinterpret_cast<int*>(turn + kWriteWarps * kTurnBytes);
     __shared__ Mx4Shared sh;
     volatile int* abort_flag = &sh.abort;
     volatile uint32_t* progress = &sh.progress;
@@ -207,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_product_mx4(const __grid_c
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.acc_full[i], 1);
-            mbar_init(&sh.acc_empty[i], 8);  // the write-out warps of both CTAs
+            mbar_init(&sh.acc_empty[i], 2 * kWriteWarps);  // of both CTAs
         }
         sh.progress = 0;
         sh.abort = 0;
@@ -275,17 +297,22 @@ __global__ void __launch_bounds__(kThreads, 1) expert_product_mx4(const __grid_c
                 const uint32_t d = tmem + (acc & 1) * kTileRows, n_bits = uint32_t(w.width >> 3) << 17;
                 const bool two = w.width > 128;
                 ok = warp_wait(&sh.acc_empty[acc & 1], ((acc >> 1) & 1) ^ 1, abort_flag);
-                bool ready = false;  // the stage was seen full
+                bool ready = false;  // the stage was seen full, and its scales
                 for (int kb = 0; ok && kb < steps; ++kb) {
-                    if (kb % kAhead == 0) ok = warp_wait<true>(&sh.scale_full[slot], slot_phase, abort_flag);
-                    ok = ok && (ready || warp_wait(&sh.full[s], phase, abort_flag));
-                    if (!ok) break;
+                    if (!ready) {
+                        if (kb % kAhead == 0) ok = warp_wait<true>(&sh.scale_full[slot], slot_phase, abort_flag);
+                        ok = ok && warp_wait(&sh.full[s], phase, abort_flag);
+                        if (!ok) break;
+                    }
                     tcgen05_fence_after();
-                    const uint32_t here = s, at = s * (kStageBytes >> 4);
+                    const uint32_t here = s, at = s * (kStageBytes >> 4), scales = slot;
+                    const bool last_of_slot = kb % kAhead == kAhead - 1 || kb == steps - 1;
                     next_stage<kStages>(s, phase);
-                    const uint32_t looks = kb + 1 < steps ? look(&sh.full[s], phase) : 0;
+                    if (last_of_slot) next_stage<kScaleSlots>(slot, slot_phase);
+                    uint32_t looks = kb + 1 < steps ? look(&sh.full[s], phase) : 0;
+                    if (last_of_slot && kb + 1 < steps) looks &= look<true>(&sh.scale_full[slot], slot_phase);
                     const uint32_t ws = tmem + kScaleColumn + turn * kScaleColumns, xs = ws + 8;
-                    const uint64_t from = s0 + slot * (kSlotBytes >> 4) + (kb % kAhead) * 2 * (kAtom >> 4);
+                    const uint64_t from = s0 + scales * (kSlotBytes >> 4) + (kb % kAhead) * 2 * (kAtom >> 4);
                     turn ^= 1;
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
@@ -295,10 +322,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_product_mx4(const __grid_c
                     }
                     mma_pair_mx4_4(d, a0 + at, b0 + at, n_bits, ws, xs, kb > 0);
                     mma_commit_pair(&sh.empty[here]);
-                    if (kb % kAhead == kAhead - 1 || kb == steps - 1) {
-                        mma_commit_pair(&sh.scale_empty[slot]);
-                        next_stage<kScaleSlots>(slot, slot_phase);
-                    }
+                    if (last_of_slot) mma_commit_pair(&sh.scale_empty[scales]);
                     ready = saw(looks);
                 }
                 if (ok) mma_commit_pair(&sh.acc_full[acc & 1]);
@@ -306,61 +330,43 @@ __global__ void __launch_bounds__(kThreads, 1) expert_product_mx4(const __grid_c
             }
         }
     } else if (warp >= kScaleWarp) {
-        // Two sets of a warp a role take turns at the slots.  What a warp writes next is on its
-        // way while it writes, across tiles too.
-        const int role = (warp - kScaleWarp) % kRoles, set = (warp - kScaleWarp) / kRoles;
-        const uint32_t full0 = map_to_rank(sh.scale_full, 0);
+        // A set of a warp a role for each slot.  A fence waits for a thread's loads too, so a warp
+        // asks for its next scales behind the hand-over of these: they come while it waits for
+        // its slot.
+        const int role = (warp - kScaleWarp) % kRoles, slot = (warp - kScaleWarp) / kRoles;
+        const uint32_t full = map_to_rank(&sh.scale_full[slot], 0);
+        unsigned char* to = slots + slot * kSlotBytes + role * kRoleBytes + lane * 16;
         const int parts = (steps + kAhead - 1) / kAhead;  // slots of a sum
-        ScaleRows rows;
+        uint32_t phase = 1;
+        int part = slot;
         Mx4Tile w;
-        int t = first, part = 0;
-        bool more = tile_at(g, table, t, tiles, w), moved = true;
-        const auto skip = [&](int n) {  // n slots on
-            for (part += n; more && part >= parts; part -= parts) {
-                t += step;
-                more = tile_at(g, table, t, tiles, w);
-                moved = true;
-            }
-        };
-        const auto fetch = [&](uint32_t (&r)[4][2 * kAhead]) {
-            if (moved) {
+        for (int t = first; ok && tile_at(g, table, t, tiles, w); t += step, part -= parts) {
+            if (part >= parts) continue;
+            ScaleRows rows;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int row = (role == 2 ? 128 : 0) + 32 * j + lane;
-                    if (role == 0) {
-                        const int m = w.m0 + int(rank) * 128 + row;
-                        rows.p[j] = m < g.out ? g.ws + (int64_t(w.expert) * g.out + m) * g.blocks : nullptr;
-                    } else {
-                        rows.p[j] = row < w.n ? g.xs + int64_t(w.n0 + row) * g.blocks : nullptr;
-                    }
+            for (int j = 0; j < 4; ++j) {
+                const int row = (role == 2 ? 128 : 0) + 32 * j + lane;
+                if (role == 0) {
+                    const int m = w.m0 + int(rank) * 128 + row;
+                    rows.p[j] = m < g.out ? g.ws + (int64_t(w.expert) * g.out + m) * g.blocks : nullptr;
+                } else {
+                    rows.p[j] = row < w.n ? g.xs + int64_t(w.n0 + row) * g.blocks : nullptr;
                 }
-                moved = false;
             }
-            rows.load(part * 8 * kAhead, g.blocks, g.scale_vec, r);
-        };
-        uint32_t slot = 0, phase = 1;
-        for (int i = 0; i < set; ++i) next_stage<kScaleSlots>(slot, phase);
-        skip(set);
-        uint32_t now[4][2 * kAhead], next[4][2 * kAhead];
-        if (more) fetch(now);
-        while (ok && more) {
-            skip(kScaleSets);
-            if (more) fetch(next);
-            __syncwarp();
-            ok = warp_wait(&sh.scale_empty[slot], phase, abort_flag);
-            if (!ok) break;
-            unsigned char* to = slots + slot * kSlotBytes + role * kRoleBytes + lane * 16;
+            for (; part < parts; part += kScaleSlots) {
+                uint32_t r[4][2 * kAhead];
+                rows.load(part * 8 * kAhead, g.blocks, g.scale_vec, r);
+                __syncwarp();
+                ok = warp_wait(&sh.scale_empty[slot], phase, abort_flag);
+                if (!ok) break;
+                phase ^= 1;
 #pragma unroll
-            for (int q = 0; q < 2 * kAhead; ++q)
-                *reinterpret_cast<uint4*>(to + q * kAtom) = make_uint4(now[0][q], now[1][q], now[2][q], now[3][q]);
-            fence_async_shared();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(full0 + slot * 8);
-            for (int i = 0; i < kScaleSets; ++i) next_stage<kScaleSlots>(slot, phase);
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-                for (int i = 0; i < 2 * kAhead; ++i) now[j][i] = next[j][i];
+                for (int q = 0; q < 2 * kAhead; ++q)
+                    *reinterpret_cast<uint4*>(to + q * kAtom) = make_uint4(r[0][q], r[1][q], r[2][q], r[3][q]);
+                fence_async_shared();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(full);
+            }
         }
     } else {
         uint32_t acc = 0;
@@ -368,8 +374,26 @@ __global__ void __launch_bounds__(kThreads, 1) expert_product_mx4(const __grid_c
         for (int t = first; tile_at(g, table, t, tiles, w); t += step) {
             if (!warp_wait_stages(&sh.acc_full[acc & 1], (acc >> 1) & 1, abort_flag, progress)) break;
             tcgen05_fence_after();
-            write_rows<O>(g, w, tmem + (uint32_t(warp * 32) << 16) + (acc & 1) * kTileRows,
-                          map_to_rank(&sh.acc_empty[acc & 1], 0), w.m0 + int(rank) * 128 + warp * 32 + lane);
+            const uint32_t from = tmem + (uint32_t(warp & 3) << 21) + (acc & 1) * kTileRows;  // lane 32 * (warp % 4)
+            const int m = w.m0 + int(rank) * 128 + (warp & 3) * 32;
+            O* p = static_cast<O*>(g.y) + int64_t(w.n0) * g.out + m;
+            constexpr int kStep = kWriteWarps / 4 * 32;
+            int c = warp / 4 * 32;
+            for (; c < w.n; c += kStep) {
+                uint32_t r[32];
+                tmem_load32(from + uint32_t(c), r);
+                tmem_wait_load(r);
+                if (c + kStep >= w.n) {
+                    tcgen05_fence_before();
+                    __syncwarp();
+                    elect_arrive_pair(map_to_rank(&sh.acc_empty[acc & 1], 0));
+                }
+                write_block(turn + warp * kTurnBytes, p + int64_t(c) * g.out, g.out, w.n - c, g.out - m, g.vec, r);
+            }
+            if (warp / 4 * 32 >= w.n) {  // nothing here for the second warp
+                __syncwarp();
+                elect_arrive_pair(map_to_rank(&sh.acc_empty[acc & 1], 0));
+            }
             ++acc;
         }
     }
@@ -382,7 +406,9 @@ __global__ void __launch_bounds__(kThreads, 1) expert_product_mx4(const __grid_c
     if (warp == kProductWarp) tmem_dealloc_pair(tmem, kTmemColumns);
 }
 
-constexpr size_t kMostSmem = 1024 + kStages * size_t(kStageBytes) + kScaleSlots * kSlotBytes + (kMaxExperts + 1) * 4;
+constexpr size_t kMostSmem = 1024 + kStages * size_t(kStageBytes) + kScaleSlots * kSlotBytes + kWriteWarps * kTurnBytes +
+                             (kMaxExperts + 1) * 4;
+static_assert(kMostSmem <= kMaxDynSmem, "one CTA on an SM");
 
 }  // namespace
 
@@ -414,6 +440,8 @@ cudaError_t launch_expert_matmul_mx4(const uint8_t* x, const uint8_t* xs, const 
     g.blocks = int((in + 31) / 32);
     const uintptr_t at = reinterpret_cast<uintptr_t>(xs) | reinterpret_cast<uintptr_t>(ws) | uintptr_t(g.blocks);
     g.scale_vec = at % 16 == 0 ? 16 : at % 8 == 0 ? 8 : 1;
+    const int y_size = y_type == ROWOPS_F32 ? 4 : 2;
+    g.vec = out * y_size % 16 == 0 && reinterpret_cast<uintptr_t>(y) % 16 == 0;
     const int64_t tiles = most_row_tiles(slots, experts, kTileRows) * ((out + 255) / 256);
     cudaError_t e = cudaErrorInvalidValue;
     if (tiles >= kMostTiles) return e;  // more than a device's memory holds

@@ -76,6 +76,7 @@ __device__ __forceinline__ uint32_t largest_bits(const float (&v)[8]) {
 }
 template <int LANES>
 __device__ __forceinline__ uint32_t group_max_bits(uint32_t v) {
+    if constexpr (LANES == 32) return __reduce_max_sync(kFullMask, v);
 #pragma unroll
     for (int o = LANES / 2; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(kFullMask, v, o));
     return v;
@@ -108,8 +109,8 @@ __device__ __forceinline__ uint32_t mx4_eight(const float (&v)[8], uint32_t code
 // ----------------------------------------------------- quantised columns of a row
 //
 // Eight values of each lane of a group, placed as in eight.cuh, to their row of bytes and
-// of scales.  The whole warp calls them.  Blocks of 128 columns are 16 lanes' (VEC), or
-// four values of each of 32 lanes, or the whole of a shorter group.
+// of scales.  The whole warp calls them.  Blocks of 128 columns are 16 lanes' (VEC; or the
+// whole of a shorter group), or four values of each of 32 lanes.
 
 template <int LANES, bool VEC>
 __device__ __forceinline__ void store_e4m3(uint8_t* q, float* scale, int base, int g, int cols, const float (&y)[8]) {
@@ -124,26 +125,26 @@ __device__ __forceinline__ void store_e4m3(uint8_t* q, float* scale, int base, i
             if (g % kBlock == 0) scale[g / kBlock] = scale_of(most);
         }
     } else {
-        constexpr int kEach = 128 / LANES < 8 ? 128 / LANES : 8;  // a lane's values of a block
+        static_assert(LANES == 32, "a value of each lane is 32 columns");
 #pragma unroll
-        for (int b = 0; b < 8 / kEach; ++b) {
-            float most = 0.f, fine = 0.f;
+        for (int b = 0; b < 2; ++b) {
+            uint32_t most = 0, fine = 0;  // as bits; NaN does not count
 #pragma unroll
-            for (int i = 0; i < kEach; ++i) {
-                const float v = fabsf(y[b * kEach + i]);
-                most = fmaxf(most, v);
-                if (v < INFINITY) fine = fmaxf(fine, v);
+            for (int i = 0; i < 4; ++i) {
+                const float v = fmaxf(fabsf(y[b * 4 + i]), 0.f);
+                most = max(most, __float_as_uint(v));
+                if (v < INFINITY) fine = max(fine, __float_as_uint(v));
             }
-            most = group_max<LANES>(most);
-            if (__any_sync(kFullMask, most == INFINITY)) most = group_max<LANES>(fine);
-            most = fmaxf(most, kSmallestMax);
-            const Divisor over(most);
+            float a = __uint_as_float(group_max_bits<32>(most));
+            if (a == INFINITY) a = __uint_as_float(group_max_bits<32>(fine));  // the same in all lanes
+            a = fmaxf(a, kSmallestMax);
+            const Divisor over(a);
 #pragma unroll
-            for (int i = 0; i < kEach; ++i) {
-                const int c = base + (b * kEach + i) * LANES + g;
-                if (c < cols) q[c] = __nv_cvt_float_to_fp8(over(y[b * kEach + i]), __NV_SATFINITE, __NV_E4M3);
+            for (int i = 0; i < 4; ++i) {
+                const int c = base + (b * 4 + i) * 32 + g;
+                if (c < cols) q[c] = __nv_cvt_float_to_fp8(over(y[b * 4 + i]), __NV_SATFINITE, __NV_E4M3);
             }
-            if (g == 0 && base + b * 128 < cols) scale[b] = scale_of(most);
+            if (g == 0 && base + b * 128 < cols) scale[b] = scale_of(a);
         }
     }
 }
@@ -158,21 +159,22 @@ __device__ __forceinline__ void store_mx4(uint8_t* q, uint8_t* scale, int base, 
             if (g % 4 == 0) scale[g / 4] = uint8_t(code);
         }
     } else {
-        constexpr int kEach = 32 / LANES;  // a lane's values of a block
+        static_assert(LANES == 32, "a value of each lane is a block");
+        uint32_t code[8];
 #pragma unroll
-        for (int b = 0; b < 8 / kEach; ++b) {
-            uint32_t bits = 0;
+        for (int i = 0; i < 8; ++i) {
+            code[i] = mx4_code(group_max_bits<32>(__float_as_uint(y[i]) & 0x7fffffffu));
+            if (g == 0 && base + i * 32 < cols) scale[i] = uint8_t(code[i]);
+        }
+        // Of two blocks, even lanes write the first's bytes, odd lanes the second's.
+        const bool odd = g & 1;
 #pragma unroll
-            for (int i = 0; i < kEach; ++i) bits = max(bits, __float_as_uint(y[b * kEach + i]) & 0x7fffffffu);
-            const uint32_t code = mx4_code(group_max_bits<LANES>(bits));
-            const float inverse = mx4_inverse(code);
-#pragma unroll
-            for (int i = 0; i < kEach; ++i) {  // columns are even and odd as g is
-                const float v = y[b * kEach + i], next = __shfl_down_sync(kFullMask, v, 1);
-                const int c = base + (b * kEach + i) * LANES + g;
-                if (c < cols && (g & 1) == 0) q[c / 2] = code == 255 ? 0 : uint8_t(mx4_pair(v, next, inverse));
-            }
-            if (g == 0 && base + b * 32 < cols) scale[b] = uint8_t(code);
+        for (int i = 0; i < 8; i += 2) {
+            const float other = __shfl_xor_sync(kFullMask, odd ? y[i] : y[i + 1], 1);
+            const uint32_t mine = odd ? code[i + 1] : code[i];
+            const int c = base + (i + odd) * 32 + g - odd;
+            if (c < cols)
+                q[c / 2] = mine == 255 ? 0 : uint8_t(mx4_pair(odd ? other : y[i], odd ? y[i + 1] : other, mx4_inverse(mine)));
         }
     }
 }

@@ -10,6 +10,51 @@
 namespace rowops {
 namespace {
 
+// The largest magnitude of eight values as fp32 bits; 16-bit values are compared as they
+// are, two at a time.
+template <typename T>
+__device__ __forceinline__ uint32_t most_of(const Held<T, 32, true>& x) {
+    if constexpr (sizeof(T) == 4) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(x.get(i)) & 0x7fffffffu);
+        return group_max_bits<4>(m);
+    } else {
+        const uint4 w = x.c[0].raw;
+        uint32_t m = __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu),
+                              __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu));
+#pragma unroll
+        for (int o = 2; o > 0; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(kFullMask, m, o));
+        Chunk<T, 2> c;
+        c.raw = max(m & 0xffffu, m >> 16);
+        return __float_as_uint(c.get(0));
+    }
+}
+
+// Rows that are whole blocks: the matrix as one run of chunks of eight values, ITEMS of
+// them a thread.
+template <typename T, int ITEMS, int THREADS>
+__global__ void __launch_bounds__(THREADS)
+    quantize_mx4_run(const T* x, uint32_t* __restrict__ q, uint8_t* __restrict__ scale, int64_t chunks) {
+    const int64_t first = int64_t(blockIdx.x) * (THREADS * ITEMS) + threadIdx.x;
+    Held<T, 32, true> in[ITEMS];
+#pragma unroll
+    for (int n = 0; n < ITEMS; ++n)
+        if (first + n * THREADS < chunks) in[n].load(x + (first + n * THREADS) * 8, 0, 0, 8);
+#pragma unroll
+    for (int n = 0; n < ITEMS; ++n) {
+        const int64_t at = first + n * THREADS;
+        const uint32_t code = mx4_code(most_of<T>(in[n]));
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = in[n].get(i);
+        if (at < chunks) {
+            q[at] = mx4_eight(v, code);
+            if ((threadIdx.x & 3) == 0) scale[at / 4] = uint8_t(code);
+        }
+    }
+}
+
 constexpr int kMxThreads = 256;
 
 struct Mx4Args {
@@ -18,45 +63,23 @@ struct Mx4Args {
     uint8_t* scale;
     int64_t rows;
     int cols, units;
-    int64_t items;  // of 256 values: of the matrix (FLAT), or units of its rows
+    int64_t items;  // units of all rows
 };
 
-template <typename T, bool VEC, bool FLAT, int ITEMS>
+// Other rows, a warp 256 columns.
+template <typename T, bool VEC>
 __global__ void __launch_bounds__(kMxThreads) quantize_mx4_rows(const Mx4Args a) {
     const int lane = threadIdx.x & 31;
-    const int64_t first = (int64_t(blockIdx.x) * (kMxThreads / 32) + (threadIdx.x >> 5)) * ITEMS;
-    const int64_t step = int64_t(gridDim.x) * (kMxThreads / 32) * ITEMS;
-    for (int64_t item0 = first; item0 < a.items; item0 += step) {
-        Held<T, 32, VEC> x[ITEMS];
-        int64_t row[ITEMS];
-        int base[ITEMS], cols[ITEMS];
+    const int64_t step = int64_t(gridDim.x) * (kMxThreads / 32);
+    for (int64_t item = int64_t(blockIdx.x) * (kMxThreads / 32) + (threadIdx.x >> 5); item < a.items; item += step) {
+        const int64_t row = item / a.units;
+        const int base = int(item - row * a.units) * 256;
+        Held<T, 32, VEC> x;
+        x.load(static_cast<const T*>(a.x) + row * a.cols, base, lane, a.cols);
+        float v[8];
 #pragma unroll
-        for (int n = 0; n < ITEMS; ++n) {
-            const int64_t item = item0 + n;
-            if constexpr (FLAT) {  // the matrix as rows of 256
-                row[n] = item;
-                base[n] = 0;
-                const int64_t left = a.rows * int64_t(a.cols) - item * 256;
-                cols[n] = left < 256 ? int(max(left, int64_t(0))) : 256;
-            } else {
-                row[n] = item / a.units;
-                base[n] = int(item - row[n] * a.units) * 256;
-                cols[n] = item < a.items ? a.cols : 0;
-            }
-            x[n].load(static_cast<const T*>(a.x) + row[n] * (FLAT ? 256 : a.cols), base[n], lane, cols[n]);
-        }
-#pragma unroll
-        for (int n = 0; n < ITEMS; ++n) {
-            float v[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = x[n].get(i);
-            if constexpr (FLAT) {
-                store_mx4<32, VEC>(a.q + row[n] * 128, a.scale + row[n] * 8, 0, lane, cols[n], v);
-            } else {
-                store_mx4<32, VEC>(a.q + row[n] * ((a.cols + 1) / 2), a.scale + row[n] * ((a.cols + 31) / 32), base[n],
-                                   lane, cols[n], v);
-            }
-        }
+        for (int i = 0; i < 8; ++i) v[i] = x.get(i);
+        store_mx4<32, VEC>(a.q + row * ((a.cols + 1) / 2), a.scale + row * ((a.cols + 31) / 32), base, lane, a.cols, v);
     }
 }
 
@@ -64,20 +87,26 @@ __global__ void __launch_bounds__(kMxThreads) quantize_mx4_rows(const Mx4Args a)
 
 cudaError_t launch_quantize_mx4(const void* x, uint8_t* q, uint8_t* scale, int64_t rows, int64_t cols, int x_type,
                                 cudaStream_t stream) {
-    Mx4Args a{x, q, scale, rows, int(cols), int((cols + 255) / 256), 0};
     const bool vec = cols % 8 == 0 && reinterpret_cast<uintptr_t>(x) % 16 == 0 && reinterpret_cast<uintptr_t>(q) % 4 == 0;
-    const bool flat = vec && cols % 32 == 0;
-    a.items = flat ? (rows * cols + 255) / 256 : rows * a.units;
-    auto go = [&](auto kernel, int each) {
-        const int64_t per = int64_t(kMxThreads / 32) * each;
-        const int64_t blocks = (a.items + per - 1) / per, most = int64_t(1) << 20;
-        kernel<<<unsigned(blocks < most ? blocks : most), kMxThreads, 0, stream>>>(a);
-    };
     with_type(x_type, [&](auto t) {
         using T = decltype(t);
-        if (flat) go(quantize_mx4_rows<T, true, true, 1>, 1);
-        else if (vec) go(quantize_mx4_rows<T, true, false, 1>, 1);
-        else go(quantize_mx4_rows<T, false, false, 1>, 1);
+        if (vec && cols % 32 == 0) {
+            const int64_t chunks = rows * cols / 8;
+            auto go = [&](auto kernel, int per, int threads) {
+                kernel<<<unsigned((chunks + per - 1) / per), threads, 0, stream>>>(
+                    static_cast<const T*>(x), reinterpret_cast<uint32_t*>(q), scale, chunks);
+            };
+            const bool few = chunks < 2048 * int64_t(sm_count());
+            if (few) go(quantize_mx4_run<T, 1, 128>, 128, 128);
+            else go(quantize_mx4_run<T, 4, 256>, 4 * 256, 256);
+        } else {
+            Mx4Args a{x, q, scale, rows, int(cols), int((cols + 255) / 256), 0};
+            a.items = rows * a.units;
+            const int64_t blocks = (a.items + kMxThreads / 32 - 1) / (kMxThreads / 32), most = int64_t(1) << 20;
+            const unsigned grid = unsigned(blocks < most ? blocks : most);
+            if (vec) quantize_mx4_rows<T, true><<<grid, kMxThreads, 0, stream>>>(a);
+            else quantize_mx4_rows<T, false><<<grid, kMxThreads, 0, stream>>>(a);
+        }
     });
     note_launches(1);
     return cudaGetLastError();
