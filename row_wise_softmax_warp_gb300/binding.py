@@ -728,22 +728,42 @@ def rowops_expert_matmul_fp8(xq, xs, wq, ws, offsets=None, y=None, dtype=torch.b
     return y
 
 
+# What a new output costs is a good part of a small call's time on the host (1.6 us by
+# torch.empty on a Grace core, 0.9 by this), so they come from the allocator directly
+# where torch offers it.
+_empty_cuda = getattr(getattr(getattr(torch._C, "_dynamo", None), "guards", None), "_empty_strided_cuda", None)
+
+
+def _new(shape, dtype, like):
+    """An uninitialised contiguous tensor on the current device, which is that of `like`."""
+    if _empty_cuda is not None:
+        if len(shape) == 2:
+            return _empty_cuda(shape, (shape[1] or 1, 1), dtype)
+        if len(shape) == 1:
+            return _empty_cuda(shape, (1,), dtype)
+    return torch.empty(shape, dtype=dtype, device=like.device)
+
+
 def rowops_quantize_mx4(x, q=None, scale=None, stream=None):
     """Returns (q, scale), torch.uint8: microscaled 4-bit values of x (..., cols), two e2m1 codes a byte with the lower
     column in the lower bits, (..., ceil(cols / 2)), and a power of two for each 32 columns, (..., ceil(cols / 32))."""
     _typed(x, "x", _FLOATS)
-    if _elsewhere(x, stream):
+    device = x.get_device()
+    if stream is not None or device != _current_device():
         with _Placed(x, stream):
             return rowops_quantize_mx4(x, q, scale)
     shape = x.shape
     if not shape:
         raise ValueError("x must have columns")
-    cols = shape[-1]
-    device = x.get_device()
-    q = _given(q, "q", torch.uint8, (*shape[:-1], (cols + 1) // 2), x, device)
-    scale = _given(scale, "scale", torch.uint8, (*shape[:-1], (cols + 31) // 32), x, device)
-    _check(library().rowops_quantize_mx4(x.data_ptr(), q.data_ptr(), scale.data_ptr(), math.prod(shape[:-1]), cols,
-                                         _DTYPES[x.dtype], _raw_stream(device)))
+    *lead, cols = shape
+    wide, blocks = (*lead, (cols + 1) // 2), (*lead, (cols + 31) // 32)
+    q = _new(wide, torch.uint8, x) if q is None else _typed(q, "q", _BYTE, wide, device)
+    scale = _new(blocks, torch.uint8, x) if scale is None else _typed(scale, "scale", _BYTE, blocks, device)
+    rows = lead[0] if len(lead) == 1 else math.prod(lead)
+    status = library().rowops_quantize_mx4(x.data_ptr(), q.data_ptr(), scale.data_ptr(), rows, cols, _DTYPES[x.dtype],
+                                           _raw_stream(device))
+    if status:
+        _check(status)
     return q, scale
 
 
@@ -755,11 +775,11 @@ def rowops_expert_matmul_mx4(xq, xs, wq, ws, offsets=None, y=None, dtype=torch.b
     """rowops_expert_matmul on microscaled 4-bit operands, as rowops_quantize_mx4 gives them: xq (slots, in / 2) with
     xs, wq (experts, out, in / 2) with ws; y of `dtype`."""
     _typed(xq, "xq", _BYTE)
-    if _elsewhere(xq, stream):
+    device = xq.get_device()
+    if stream is not None or device != _current_device():
         with _Placed(xq, stream):
             return rowops_expert_matmul_mx4(xq, xs, wq, ws, offsets, y, dtype, workspace)
     slots, width = _dims(xq, "xq", 2)
-    device = xq.get_device()
     experts, out_cols, k = _dims(_typed(wq, "wq", _BYTE, None, device), "wq", 3)
     if k != width:
         raise ValueError(f"wq must have rows of {width} bytes, got {tuple(wq.shape)}")
@@ -767,27 +787,30 @@ def rowops_expert_matmul_mx4(xq, xs, wq, ws, offsets=None, y=None, dtype=torch.b
     _typed(xs, "xs", _BYTE, (slots, blocks), device)
     _typed(ws, "ws", _BYTE, (experts, out_cols, blocks), device)
     _offsets(offsets, experts, device)
-    if y is None:
-        y = torch.empty((slots, out_cols), dtype=dtype, device=xq.device)
-    else:
-        _typed(y, "y", _FLOATS, (slots, out_cols), device)
+    y = _new((slots, out_cols), dtype, xq) if y is None else _typed(y, "y", _FLOATS, (slots, out_cols), device)
     lib = library()
-    need = 0 if width % 16 == 0 else lib.rowops_expert_matmul_mx4_workspace(slots, 2 * width, out_cols, experts)
-    if (xq.data_ptr() | wq.data_ptr()) % 16 and workspace is None:
+    need, x_at, w_at = 0, xq.data_ptr(), wq.data_ptr()
+    if workspace is None and (width | x_at | w_at) % 16:
+        need = lib.rowops_expert_matmul_mx4_workspace(slots, 2 * width, out_cols, experts)
         need += _shifted_room((xq, slots, width), (wq, experts * out_cols, width))
-    workspace, size = _scratch(workspace, need, xq)
-    _check(lib.rowops_expert_matmul_mx4(xq.data_ptr(), xs.data_ptr(), wq.data_ptr(), ws.data_ptr(), _ptr(offsets),
-                                        y.data_ptr(), slots, 2 * width, out_cols, experts, _DTYPES.get(y.dtype, -1),
-                                        _ptr(workspace), size, _raw_stream(device)))
+    at, size = None, 0
+    if need or workspace is not None:
+        workspace, size = _scratch(workspace, need, xq)
+        at = _ptr(workspace)
+    status = lib.rowops_expert_matmul_mx4(x_at, xs.data_ptr(), w_at, ws.data_ptr(), _ptr(offsets), y.data_ptr(), slots,
+                                          2 * width, out_cols, experts, _DTYPES.get(y.dtype, -1), at, size,
+                                          _raw_stream(device))
+    if status:
+        _check(status)
     return y
 
 
 # ------------------------------------------------ between two sublayers' products
 
 def _rng(rng, p: float, device):
-    """Seed and offset of the generator; may be None without dropout."""
+    """The address of seed and offset of the generator; None without dropout."""
     if rng is not None:
-        return _typed(rng, "rng", _INT64, (2,), device)
+        return _typed(rng, "rng", _INT64, (2,), device).data_ptr()
     if p != 0 and p != 1:
         raise ValueError("rng is needed where values drop")
     return None
@@ -798,20 +821,22 @@ def rowops_dropout(x, rng, p, residual=None, y=None, dtype=None, stream=None):
     (default the residual's, or x's).  rng: two int64 on the device, seed and offset; the same rng, p and shape drop the
     same values, so the gradient with respect to x is this call on y's gradient without the residual."""
     _typed(x, "x", _FLOATS)
-    if _elsewhere(x, stream):
+    device = x.get_device()
+    if stream is not None or device != _current_device():
         with _Placed(x, stream):
             return rowops_dropout(x, rng, p, residual, y, dtype)
-    device = x.get_device()
-    _rng(rng, p, device)
-    shape = x.shape
+    at = _rng(rng, p, device)
+    shape = tuple(x.shape)
     if dtype is None:
         dtype = y.dtype if y is not None else x.dtype if residual is None else residual.dtype
     if residual is not None:
-        _typed(residual, "residual", (dtype,), shape, device)
-    y = _given(y, "y", dtype, shape, x, device)
-    rows, cols = _shape(x)
-    _check(library().rowops_dropout(x.data_ptr(), _ptr(residual), _ptr(rng), y.data_ptr(), rows, cols, p,
-                                    _DTYPES[x.dtype], _DTYPES.get(dtype, -1), _raw_stream(device)))
+        residual = _typed(residual, "residual", (dtype,), shape, device).data_ptr()
+    y = _new(shape, dtype, x) if y is None else _typed(y, "y", (dtype,), shape, device)
+    rows, cols = shape if len(shape) == 2 else _shape(x)
+    status = library().rowops_dropout(x.data_ptr(), residual, at, y.data_ptr(), rows, cols, p, _DTYPES[x.dtype],
+                                      _DTYPES.get(dtype, -1), _raw_stream(device))
+    if status:
+        _check(status)
     return y
 
 
@@ -826,39 +851,48 @@ def rowops_add_rmsnorm_fwd(x, gamma, residual=None, rng=None, p=0.0, eps=1e-5, q
     and without dropout either h is x itself).  quantize None: out of x's type, scale None; "e4m3": out and scale as
     rowops_quantize_blocks gives them; "mx4": as rowops_quantize_mx4 does.  h may be the residual."""
     _typed(x, "x", _FLOATS)
-    if _elsewhere(x, stream):
+    device = x.get_device()
+    if stream is not None or device != _current_device():
         with _Placed(x, stream):
             return rowops_add_rmsnorm_fwd(x, gamma, residual, rng, p, eps, quantize, out, scale, h, row_rms)
-    device, shape = x.get_device(), x.shape
-    rows, cols = _shape(x)
+    shape, dtype = tuple(x.shape), x.dtype
+    rows, cols = shape if len(shape) == 2 else _shape(x)
+    lead = shape[:-1]
     _typed(gamma, "gamma", _F32, (cols,), device)
-    _rng(rng, p, device)
-    if residual is not None:
-        _typed(residual, "residual", _FLOATS, shape, device)
-    like = x if residual is None and h is None else h if residual is None else residual
-    if h is None and like is x and p == 0:
-        h, h_ptr = x, None  # the sum is x
+    at = _rng(rng, p, device)
+    if residual is None:
+        h_type, residual_at = dtype if h is None else h.dtype, None
     else:
-        h = _given(h, "h", like.dtype, shape, x, device)
-        h_ptr = h.data_ptr()
+        h_type, residual_at = residual.dtype, _typed(residual, "residual", _FLOATS, shape, device).data_ptr()
+    if h is not None:
+        h_at = _typed(h, "h", (h_type,), shape, device).data_ptr()
+    elif residual is None and p == 0:
+        h, h_at = x, None  # the sum is x
+    else:
+        h = _new(shape, h_type, x)
+        h_at = h.data_ptr()
     if quantize is None:
         if scale is not None:
             raise ValueError("scale is of quantised answers only")
-        out = _given(out, "out", x.dtype, shape, x, device)
-        out_type = _DTYPES[x.dtype]
-    elif quantize == "e4m3":
-        out = _given(out, "out", torch.float8_e4m3fn, shape, x, device)
-        scale = _given(scale, "scale", torch.float32, (*shape[:-1], -(-cols // 128)), x, device)
-    elif quantize == "mx4":
-        out = _given(out, "out", torch.uint8, (*shape[:-1], -(-cols // 2)), x, device)
-        scale = _given(scale, "scale", torch.uint8, (*shape[:-1], -(-cols // 32)), x, device)
+        out_type, scale_at = _DTYPES[dtype], None
+        out = _new(shape, dtype, x) if out is None else _typed(out, "out", (dtype,), shape, device)
     else:
-        raise ValueError('quantize must be None, "e4m3" or "mx4"')
-    row_rms = _given(row_rms, "row_rms", torch.float32, shape[:-1], x, device)
-    _check(library().rowops_add_rmsnorm_fwd(
-        x.data_ptr(), _ptr(residual), gamma.data_ptr(), _ptr(rng), h_ptr, out.data_ptr(), _ptr(scale),
-        row_rms.data_ptr(), rows, cols, eps, p, _DTYPES[x.dtype], _DTYPES[h.dtype],
-        out_type if quantize is None else _QUANTISED[quantize], _raw_stream(device)))
+        out_type = _QUANTISED.get(quantize)
+        if out_type is None:
+            raise ValueError('quantize must be None, "e4m3" or "mx4"')
+        if out_type == 3:
+            types, wide, blocks = (torch.float8_e4m3fn, torch.float32), shape, (*lead, (cols + 127) // 128)
+        else:
+            types, wide, blocks = (torch.uint8, torch.uint8), (*lead, (cols + 1) // 2), (*lead, (cols + 31) // 32)
+        out = _new(wide, types[0], x) if out is None else _typed(out, "out", types[:1], wide, device)
+        scale = _new(blocks, types[1], x) if scale is None else _typed(scale, "scale", types[1:], blocks, device)
+        scale_at = scale.data_ptr()
+    row_rms = _new(lead, torch.float32, x) if row_rms is None else _typed(row_rms, "row_rms", _F32, lead, device)
+    status = library().rowops_add_rmsnorm_fwd(
+        x.data_ptr(), residual_at, gamma.data_ptr(), at, h_at, out.data_ptr(), scale_at, row_rms.data_ptr(), rows, cols,
+        eps, p, _DTYPES[dtype], _DTYPES.get(h_type, -1), out_type, _raw_stream(device))
+    if status:
+        _check(status)
     return out, scale, h, row_rms
 
 
@@ -873,28 +907,36 @@ def rowops_add_rmsnorm_bwd(dy, gamma, h, row_rms, dh=None, rng=None, p=0.0, dx=N
     dx is of dy's type, dresidual of h's.  Without dropout and with one type they are the same values, and the same
     tensor where dx is None.  dx may be dy, and dresidual may be dh."""
     _typed(dy, "dy", _FLOATS)
-    if _elsewhere(dy, stream):
+    device = dy.get_device()
+    if stream is not None or device != _current_device():
         with _Placed(dy, stream):
             return rowops_add_rmsnorm_bwd(dy, gamma, h, row_rms, dh, rng, p, dx, dresidual, dgamma, workspace)
-    device, shape = dy.get_device(), dy.shape
-    rows, cols = _shape(dy)
+    shape, dtype = tuple(dy.shape), dy.dtype
+    rows, cols = shape if len(shape) == 2 else _shape(dy)
     _typed(gamma, "gamma", _F32, (cols,), device)
-    _typed(h, "h", _FLOATS, shape, device)
+    h_type = _typed(h, "h", _FLOATS, shape, device).dtype
     _typed(row_rms, "row_rms", _F32, shape[:-1], device)
-    _rng(rng, p, device)
-    if dh is not None:
-        _typed(dh, "dh", (h.dtype,), shape, device)
-    dresidual = _given(dresidual, "dresidual", h.dtype, shape, dy, device)
-    if dx is None and p == 0 and dy.dtype == h.dtype:
-        dx, dx_ptr = dresidual, None
+    at = _rng(rng, p, device)
+    dh_at = None if dh is None else _typed(dh, "dh", (h_type,), shape, device).data_ptr()
+    dresidual = (_new(shape, h_type, dy) if dresidual is None
+                 else _typed(dresidual, "dresidual", (h_type,), shape, device))
+    if dx is not None:
+        dx_at = _typed(dx, "dx", (dtype,), shape, device).data_ptr()
+    elif p == 0 and dtype == h_type:
+        dx, dx_at = dresidual, None
     else:
-        dx = _given(dx, "dx", dy.dtype, shape, dy, device)
-        dx_ptr = dx.data_ptr()
-    dgamma = _given(dgamma, "dgamma", torch.float32, (cols,), dy, device)
+        dx = _new(shape, dtype, dy)
+        dx_at = dx.data_ptr()
+    dgamma = _new((cols,), torch.float32, dy) if dgamma is None else _typed(dgamma, "dgamma", _F32, (cols,), device)
     lib = library()
-    need = lib.rowops_add_rmsnorm_bwd_workspace(rows, cols) if workspace is None else 0
-    workspace, size = _scratch(workspace, need, dy)
-    _check(lib.rowops_add_rmsnorm_bwd(dy.data_ptr(), gamma.data_ptr(), h.data_ptr(), row_rms.data_ptr(), _ptr(dh),
-                                      _ptr(rng), dresidual.data_ptr(), dx_ptr, dgamma.data_ptr(), rows, cols, p,
-                                      _DTYPES[dy.dtype], _DTYPES[h.dtype], _ptr(workspace), size, _raw_stream(device)))
+    if workspace is None:
+        size = lib.rowops_add_rmsnorm_bwd_workspace(rows, cols)
+        workspace = _new((size,), torch.uint8, dy)
+    else:
+        workspace, size = _scratch(workspace, 0, dy)
+    status = lib.rowops_add_rmsnorm_bwd(dy.data_ptr(), gamma.data_ptr(), h.data_ptr(), row_rms.data_ptr(), dh_at, at,
+                                        dresidual.data_ptr(), dx_at, dgamma.data_ptr(), rows, cols, p, _DTYPES[dtype],
+                                        _DTYPES[h_type], workspace.data_ptr(), size, _raw_stream(device))
+    if status:
+        _check(status)
     return dx, dresidual, dgamma
