@@ -6,7 +6,8 @@ outputs the caller leaves as ``None`` with torch, passes raw device pointers
 and the current torch stream to the C ABI and raises ``RowopsError`` on a
 nonzero status.  All arithmetic happens in the library's CUDA kernels; there
 is no other code path.  The library is loaded on first use and a missing build
-is an error, never a fallback.
+is an error, never a fallback.  The last operators' calls are marshalled by a
+compiled module, to the same entry points.
 """
 from __future__ import annotations
 
@@ -415,8 +416,6 @@ _HALVES = (torch.float16, torch.bfloat16)
 _F32 = (torch.float32,)
 _INT = (torch.int32,)
 _E4M3 = (torch.float8_e4m3fn,)
-_BYTE = (torch.uint8,)
-_INT64 = (torch.int64,)
 _ONE_LAUNCH_PAIRS = 2048  # plans of so many pairs need no workspace, as the header says
 
 
@@ -728,43 +727,51 @@ def rowops_expert_matmul_fp8(xq, xs, wq, ws, offsets=None, y=None, dtype=torch.b
     return y
 
 
-# What a new output costs is a good part of a small call's time on the host (1.6 us by
-# torch.empty on a Grace core, 0.9 by this), so they come from the allocator directly
-# where torch offers it.
-_empty_cuda = getattr(getattr(getattr(torch._C, "_dynamo", None), "guards", None), "_empty_strided_cuda", None)
+# ---------------------------------- microscaled 4 bits, and between two sublayers
+# Checks, outputs and the C call of these are compiled (csrc/host_binding.cpp): a call of
+# rowops_add_rmsnorm_fwd on 32 x 4096 that takes the device 3 us took the host 16 us by
+# ctypes.
+
+_host = None
 
 
-def _new(shape, dtype, like):
-    """An uninitialised contiguous tensor on the current device, which is that of `like`."""
-    if _empty_cuda is not None:
-        if len(shape) == 2:
-            return _empty_cuda(shape, (shape[1] or 1, 1), dtype)
-        if len(shape) == 1:
-            return _empty_cuda(shape, (1,), dtype)
-    return torch.empty(shape, dtype=dtype, device=like.device)
+def _native():
+    """The compiled part of the binding, which calls the same library."""
+    global _host
+    if _host is None:
+        library()
+        try:
+            from . import _host as module
+        except ImportError as e:
+            raise RuntimeError(
+                "the compiled part of the binding (_host.so) is missing: build it with "
+                "row_wise_softmax_warp_gb300.build.build() (or __graft_entry__.build())") from e
+        module.load(LIB_PATH)
+        _host = module
+    return _host
+
+
+def _done(answer):
+    """The answer of a compiled call, which is an int where the library refused."""
+    if answer.__class__ is int:
+        _check(answer)
+    return answer
+
+
+def _on_stream(fn, first, stream, *args):
+    """fn on its arguments with `stream` (and its device) current."""
+    if not isinstance(first, torch.Tensor) or not first.is_cuda:
+        return fn(first, *args)  # which refuses it
+    with _Placed(first, stream):
+        return fn(first, *args)
 
 
 def rowops_quantize_mx4(x, q=None, scale=None, stream=None):
     """Returns (q, scale), torch.uint8: microscaled 4-bit values of x (..., cols), two e2m1 codes a byte with the lower
     column in the lower bits, (..., ceil(cols / 2)), and a power of two for each 32 columns, (..., ceil(cols / 32))."""
-    _typed(x, "x", _FLOATS)
-    device = x.get_device()
-    if stream is not None or device != _current_device():
-        with _Placed(x, stream):
-            return rowops_quantize_mx4(x, q, scale)
-    shape = x.shape
-    if not shape:
-        raise ValueError("x must have columns")
-    *lead, cols = shape
-    wide, blocks = (*lead, (cols + 1) // 2), (*lead, (cols + 31) // 32)
-    q = _new(wide, torch.uint8, x) if q is None else _typed(q, "q", _BYTE, wide, device)
-    scale = _new(blocks, torch.uint8, x) if scale is None else _typed(scale, "scale", _BYTE, blocks, device)
-    rows = lead[0] if len(lead) == 1 else math.prod(lead)
-    status = library().rowops_quantize_mx4(x.data_ptr(), q.data_ptr(), scale.data_ptr(), rows, cols, _DTYPES[x.dtype],
-                                           _raw_stream(device))
-    if status:
-        _check(status)
-    return q, scale
+    if stream is not None:
+        return _on_stream(rowops_quantize_mx4, x, stream, q, scale)
+    return _done((_host or _native()).quantize_mx4(x, q, scale))
 
 
 def rowops_expert_matmul_mx4_workspace(slots: int, in_cols: int, out_cols: int, experts: int) -> int:
@@ -774,73 +781,18 @@ def rowops_expert_matmul_mx4_workspace(slots: int, in_cols: int, out_cols: int, 
 def rowops_expert_matmul_mx4(xq, xs, wq, ws, offsets=None, y=None, dtype=torch.bfloat16, workspace=None, stream=None):
     """rowops_expert_matmul on microscaled 4-bit operands, as rowops_quantize_mx4 gives them: xq (slots, in / 2) with
     xs, wq (experts, out, in / 2) with ws; y of `dtype`."""
-    _typed(xq, "xq", _BYTE)
-    device = xq.get_device()
-    if stream is not None or device != _current_device():
-        with _Placed(xq, stream):
-            return rowops_expert_matmul_mx4(xq, xs, wq, ws, offsets, y, dtype, workspace)
-    slots, width = _dims(xq, "xq", 2)
-    experts, out_cols, k = _dims(_typed(wq, "wq", _BYTE, None, device), "wq", 3)
-    if k != width:
-        raise ValueError(f"wq must have rows of {width} bytes, got {tuple(wq.shape)}")
-    blocks = -(-width // 16)
-    _typed(xs, "xs", _BYTE, (slots, blocks), device)
-    _typed(ws, "ws", _BYTE, (experts, out_cols, blocks), device)
-    _offsets(offsets, experts, device)
-    y = _new((slots, out_cols), dtype, xq) if y is None else _typed(y, "y", _FLOATS, (slots, out_cols), device)
-    lib = library()
-    need, x_at, w_at = 0, xq.data_ptr(), wq.data_ptr()
-    if workspace is None and (width | x_at | w_at) % 16:
-        need = lib.rowops_expert_matmul_mx4_workspace(slots, 2 * width, out_cols, experts)
-        need += _shifted_room((xq, slots, width), (wq, experts * out_cols, width))
-    at, size = None, 0
-    if need or workspace is not None:
-        workspace, size = _scratch(workspace, need, xq)
-        at = _ptr(workspace)
-    status = lib.rowops_expert_matmul_mx4(x_at, xs.data_ptr(), w_at, ws.data_ptr(), _ptr(offsets), y.data_ptr(), slots,
-                                          2 * width, out_cols, experts, _DTYPES.get(y.dtype, -1), at, size,
-                                          _raw_stream(device))
-    if status:
-        _check(status)
-    return y
-
-
-# ------------------------------------------------ between two sublayers' products
-
-def _rng(rng, p: float, device):
-    """The address of seed and offset of the generator; None without dropout."""
-    if rng is not None:
-        return _typed(rng, "rng", _INT64, (2,), device).data_ptr()
-    if p != 0 and p != 1:
-        raise ValueError("rng is needed where values drop")
-    return None
+    if stream is not None:
+        return _on_stream(rowops_expert_matmul_mx4, xq, stream, xs, wq, ws, offsets, y, dtype, workspace)
+    return _done((_host or _native()).expert_matmul_mx4(xq, xs, wq, ws, offsets, y, dtype, workspace))
 
 
 def rowops_dropout(x, rng, p, residual=None, y=None, dtype=None, stream=None):
     """y = residual + x with values dropped with probability p and the others multiplied by 1 / (1 - p); y of `dtype`
     (default the residual's, or x's).  rng: two int64 on the device, seed and offset; the same rng, p and shape drop the
     same values, so the gradient with respect to x is this call on y's gradient without the residual."""
-    _typed(x, "x", _FLOATS)
-    device = x.get_device()
-    if stream is not None or device != _current_device():
-        with _Placed(x, stream):
-            return rowops_dropout(x, rng, p, residual, y, dtype)
-    at = _rng(rng, p, device)
-    shape = tuple(x.shape)
-    if dtype is None:
-        dtype = y.dtype if y is not None else x.dtype if residual is None else residual.dtype
-    if residual is not None:
-        residual = _typed(residual, "residual", (dtype,), shape, device).data_ptr()
-    y = _new(shape, dtype, x) if y is None else _typed(y, "y", (dtype,), shape, device)
-    rows, cols = shape if len(shape) == 2 else _shape(x)
-    status = library().rowops_dropout(x.data_ptr(), residual, at, y.data_ptr(), rows, cols, p, _DTYPES[x.dtype],
-                                      _DTYPES.get(dtype, -1), _raw_stream(device))
-    if status:
-        _check(status)
-    return y
-
-
-_QUANTISED = {"e4m3": 3, "mx4": 4}  # rowops_dtype
+    if stream is not None:
+        return _on_stream(rowops_dropout, x, stream, rng, p, residual, y, dtype)
+    return _done((_host or _native()).dropout(x, rng, p, residual, y, dtype))
 
 
 def rowops_add_rmsnorm_fwd(x, gamma, residual=None, rng=None, p=0.0, eps=1e-5, quantize=None, out=None, scale=None,
@@ -850,50 +802,9 @@ def rowops_add_rmsnorm_fwd(x, gamma, residual=None, rng=None, p=0.0, eps=1e-5, q
     h is of the residual's type, which is x's or torch.float32 (without a residual of h's, or x's where that is None;
     and without dropout either h is x itself).  quantize None: out of x's type, scale None; "e4m3": out and scale as
     rowops_quantize_blocks gives them; "mx4": as rowops_quantize_mx4 does.  h may be the residual."""
-    _typed(x, "x", _FLOATS)
-    device = x.get_device()
-    if stream is not None or device != _current_device():
-        with _Placed(x, stream):
-            return rowops_add_rmsnorm_fwd(x, gamma, residual, rng, p, eps, quantize, out, scale, h, row_rms)
-    shape, dtype = tuple(x.shape), x.dtype
-    rows, cols = shape if len(shape) == 2 else _shape(x)
-    lead = shape[:-1]
-    _typed(gamma, "gamma", _F32, (cols,), device)
-    at = _rng(rng, p, device)
-    if residual is None:
-        h_type, residual_at = dtype if h is None else h.dtype, None
-    else:
-        h_type, residual_at = residual.dtype, _typed(residual, "residual", _FLOATS, shape, device).data_ptr()
-    if h is not None:
-        h_at = _typed(h, "h", (h_type,), shape, device).data_ptr()
-    elif residual is None and p == 0:
-        h, h_at = x, None  # the sum is x
-    else:
-        h = _new(shape, h_type, x)
-        h_at = h.data_ptr()
-    if quantize is None:
-        if scale is not None:
-            raise ValueError("scale is of quantised answers only")
-        out_type, scale_at = _DTYPES[dtype], None
-        out = _new(shape, dtype, x) if out is None else _typed(out, "out", (dtype,), shape, device)
-    else:
-        out_type = _QUANTISED.get(quantize)
-        if out_type is None:
-            raise ValueError('quantize must be None, "e4m3" or "mx4"')
-        if out_type == 3:
-            types, wide, blocks = (torch.float8_e4m3fn, torch.float32), shape, (*lead, (cols + 127) // 128)
-        else:
-            types, wide, blocks = (torch.uint8, torch.uint8), (*lead, (cols + 1) // 2), (*lead, (cols + 31) // 32)
-        out = _new(wide, types[0], x) if out is None else _typed(out, "out", types[:1], wide, device)
-        scale = _new(blocks, types[1], x) if scale is None else _typed(scale, "scale", types[1:], blocks, device)
-        scale_at = scale.data_ptr()
-    row_rms = _new(lead, torch.float32, x) if row_rms is None else _typed(row_rms, "row_rms", _F32, lead, device)
-    status = library().rowops_add_rmsnorm_fwd(
-        x.data_ptr(), residual_at, gamma.data_ptr(), at, h_at, out.data_ptr(), scale_at, row_rms.data_ptr(), rows, cols,
-        eps, p, _DTYPES[dtype], _DTYPES.get(h_type, -1), out_type, _raw_stream(device))
-    if status:
-        _check(status)
-    return out, scale, h, row_rms
+    if stream is not None:
+        return _on_stream(rowops_add_rmsnorm_fwd, x, stream, gamma, residual, rng, p, eps, quantize, out, scale, h, row_rms)
+    return _done((_host or _native()).add_rmsnorm_fwd(x, gamma, residual, rng, p, eps, quantize, out, scale, h, row_rms))
 
 
 def rowops_add_rmsnorm_bwd_workspace(rows: int, cols: int) -> int:
@@ -906,37 +817,6 @@ def rowops_add_rmsnorm_bwd(dy, gamma, h, row_rms, dh=None, rng=None, p=0.0, dx=N
 
     dx is of dy's type, dresidual of h's.  Without dropout and with one type they are the same values, and the same
     tensor where dx is None.  dx may be dy, and dresidual may be dh."""
-    _typed(dy, "dy", _FLOATS)
-    device = dy.get_device()
-    if stream is not None or device != _current_device():
-        with _Placed(dy, stream):
-            return rowops_add_rmsnorm_bwd(dy, gamma, h, row_rms, dh, rng, p, dx, dresidual, dgamma, workspace)
-    shape, dtype = tuple(dy.shape), dy.dtype
-    rows, cols = shape if len(shape) == 2 else _shape(dy)
-    _typed(gamma, "gamma", _F32, (cols,), device)
-    h_type = _typed(h, "h", _FLOATS, shape, device).dtype
-    _typed(row_rms, "row_rms", _F32, shape[:-1], device)
-    at = _rng(rng, p, device)
-    dh_at = None if dh is None else _typed(dh, "dh", (h_type,), shape, device).data_ptr()
-    dresidual = (_new(shape, h_type, dy) if dresidual is None
-                 else _typed(dresidual, "dresidual", (h_type,), shape, device))
-    if dx is not None:
-        dx_at = _typed(dx, "dx", (dtype,), shape, device).data_ptr()
-    elif p == 0 and dtype == h_type:
-        dx, dx_at = dresidual, None
-    else:
-        dx = _new(shape, dtype, dy)
-        dx_at = dx.data_ptr()
-    dgamma = _new((cols,), torch.float32, dy) if dgamma is None else _typed(dgamma, "dgamma", _F32, (cols,), device)
-    lib = library()
-    if workspace is None:
-        size = lib.rowops_add_rmsnorm_bwd_workspace(rows, cols)
-        workspace = _new((size,), torch.uint8, dy)
-    else:
-        workspace, size = _scratch(workspace, 0, dy)
-    status = lib.rowops_add_rmsnorm_bwd(dy.data_ptr(), gamma.data_ptr(), h.data_ptr(), row_rms.data_ptr(), dh_at, at,
-                                        dresidual.data_ptr(), dx_at, dgamma.data_ptr(), rows, cols, p, _DTYPES[dtype],
-                                        _DTYPES[h_type], workspace.data_ptr(), size, _raw_stream(device))
-    if status:
-        _check(status)
-    return dx, dresidual, dgamma
+    if stream is not None:
+        return _on_stream(rowops_add_rmsnorm_bwd, dy, stream, gamma, h, row_rms, dh, rng, p, dx, dresidual, dgamma, workspace)
+    return _done((_host or _native()).add_rmsnorm_bwd(dy, gamma, h, row_rms, dh, rng, p, dx, dresidual, dgamma, workspace))

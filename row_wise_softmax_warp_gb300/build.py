@@ -3,16 +3,20 @@
 Each .cu file is compiled in its own nvcc process (in parallel) and the
 objects are linked into ``row_wise_softmax_warp_gb300/librowops.so`` with the
 CUDA runtime linked statically.  Only one architecture is generated:
-``-gencode arch=compute_103a,code=sm_103a``.
+``-gencode arch=compute_103a,code=sm_103a``.  Beside them the C++ compiler makes
+``_host.so``, the compiled part of the Python binding, against the installed torch.
 """
 from __future__ import annotations
 
 import glob
 import hashlib
+import importlib.metadata
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -20,6 +24,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "librowops.so")
+HOST_SOURCE = os.path.join(CSRC, "host_binding.cpp")
+HOST = os.path.join(PKG, "_host.so")
 INCLUDE = os.path.join(ROOT, "include")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -44,7 +50,18 @@ def _fingerprint(extra=()) -> str:
         with open(p, "rb") as f:
             h.update(p.encode() + b"\0" + f.read())
     h.update(" ".join(ARCH + NVCC_FLAGS + list(extra)).encode())
+    h.update(f"{importlib.metadata.version('torch')} {sys.version}".encode())
     return h.hexdigest()
+
+
+def _host_command(out: str):
+    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    nvcc = os.path.realpath(_nvcc())
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc)), "include")
+    return [os.environ.get("CXX") or "g++", "-std=c++17", "-O2", "-fPIC", "-shared", "-fvisibility=hidden", f"-I{INCLUDE}",
+            f"-I{torch}/include", f"-I{torch}/include/torch/csrc/api/include",
+            f"-I{sysconfig.get_paths()['include']}", f"-I{cuda}", HOST_SOURCE, "-o", out, f"-L{torch}/lib",
+            "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10_cuda", "-lc10", "-ldl"]
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
@@ -52,11 +69,17 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     os.makedirs(BUILD, exist_ok=True)
     stamp = os.path.join(BUILD, "fingerprint")
     fp = _fingerprint(extra_flags)
-    if not force and os.path.exists(LIB) and os.path.exists(stamp) and open(stamp).read() == fp:
+    built = os.path.exists(LIB) and os.path.exists(HOST) and os.path.exists(stamp)
+    if not force and built and open(stamp).read() == fp:
         return LIB
     nvcc = _nvcc()
 
     def compile_one(src):
+        if src == HOST_SOURCE:
+            r = subprocess.run(_host_command(host), capture_output=True, text=True)
+            if r.returncode != 0:
+                raise RuntimeError(f"the C++ compiler failed on {os.path.basename(src)}:\n{r.stdout}{r.stderr}")
+            return None
         obj = os.path.join(BUILD, os.path.basename(src)[:-3] + ".o")
         cmd = [nvcc, *ARCH, *NVCC_FLAGS, *extra_flags, "-c", src, "-o", obj]
         if verbose:
@@ -68,15 +91,17 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             print(r.stdout + r.stderr, file=sys.stderr)
         return obj
 
-    srcs = _sources()
+    host = HOST + f".tmp{os.getpid()}"
+    srcs = [HOST_SOURCE, *_sources()]
     with ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 1))) as ex:
-        objs = list(ex.map(compile_one, srcs))
+        objs = [o for o in ex.map(compile_one, srcs) if o]
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}{r.stderr}")
     os.replace(tmp, LIB)
+    os.replace(host, HOST)
     with open(stamp, "w") as f:
         f.write(fp)
     return LIB
