@@ -34,32 +34,44 @@ struct AddNormArgs {
     RowSplit split;
 };
 
-// h of eight columns in fp32, written in the stream's type.
+// h of eight columns in fp32.
 template <typename T, typename R, int LANES, bool VEC>
 struct Sum {
     Held<T, LANES, VEC> x;
     Held<R, LANES, VEC> residual;
-    __device__ __forceinline__ void load(const AddNormArgs& a, int64_t row, int base, int g, int cols) {
-        x.load(static_cast<const T*>(a.x) + row * a.cols, base, g, cols);
-        if (a.residual) residual.load(static_cast<const R*>(a.residual) + row * a.cols, base, g, cols);
+    __device__ __forceinline__ void load(const AddNormArgs& a, const Place<LANES, VEC>& o) {
+        x.load(static_cast<const T*>(a.x), o);
+        if (a.residual) residual.load(static_cast<const R*>(a.residual), o);
     }
     __device__ __forceinline__ void get(const AddNormArgs& a, const Masker& m, int64_t row, int base, int g,
-                                        float (&v)[8]) const {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = x.get(i);
+                                        float2 (&v)[4]) const {
+        x.get(v);
         drop_eight<LANES, VEC>(v, a.drop, m, row, (a.cols + 7) / 8, base, g);
-        if (a.residual)
+        if (a.residual) {
+            float2 r[4];
+            residual.get(r);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] += residual.get(i);
+            for (int i = 0; i < 4; ++i) v[i] = add2(v[i], r[i]);
+        }
     }
 };
+
+// y of eight columns.
+template <int LANES, bool VEC>
+__device__ __forceinline__ void normed(const AddNormArgs& a, int base, int g, int cols, float inv, const float2 (&h)[4],
+                                       float2 (&y)[4]) {
+    float2 gamma[4];
+    load_weights<LANES, VEC>(a.gamma, Place<LANES, VEC>(0, 0, base, g, cols), gamma);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = mul2(mul2(h[i], both(inv)), gamma[i]);
+}
 
 // Eight columns of the answer.
 template <typename T, int LANES, bool VEC>
 __device__ __forceinline__ void answer_eight(const AddNormArgs& a, int64_t row, int base, int g, int cols,
-                                             const float (&y)[8]) {
+                                             const float2 (&y)[4]) {
     if (a.answer == kPlain) {
-        store_eight<LANES, VEC>(static_cast<T*>(a.out) + row * a.cols, base, g, cols, y);
+        store_eight<LANES, VEC>(static_cast<T*>(a.out), Place<LANES, VEC>(row, a.cols, base, g, cols), y);
         return;
     }
     if (a.answer == kE4m3) {
@@ -86,26 +98,26 @@ __global__ void __launch_bounds__(MOST) add_rmsnorm_rows(const AddNormArgs a) {
         const int cols = row < a.rows ? a.cols : 0;
         Sum<T, R, LANES, VEC> in[NV];
 #pragma unroll
-        for (int k = 0; k < NV; ++k) in[k].load(a, row < a.rows ? row : 0, (k * a.split.warps + w) * 256, g, cols);
-        float h[NV][8], squares = 0.f;
+        for (int k = 0; k < NV; ++k)
+            in[k].load(a, Place<LANES, VEC>(row, a.cols, (k * a.split.warps + w) * 256, g, cols));
+        float2 h[NV][4], squares = both(0.f);
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int base = (k * a.split.warps + w) * 256;
             in[k].get(a, masker, row, base, g, h[k]);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) squares = fmaf(h[k][i], h[k][i], squares);  // 0 past the row's end
-            if (a.h) store_eight<LANES, VEC>(static_cast<R*>(a.h) + row * a.cols, base, g, cols, h[k]);
+            for (int i = 0; i < 4; ++i) squares = fma2(h[k][i], h[k][i], squares);  // 0 past the row's end
+            if (a.h) store_eight<LANES, VEC>(static_cast<R*>(a.h), Place<LANES, VEC>(row, a.cols, base, g, cols), h[k]);
         }
-        const float rms = sqrtf(sum_of_row<LANES>(squares, scratch[turn], a.split.warps, slot, w) * inv_cols + a.eps);
+        const float sum = sum_of_row<LANES>(squares.x + squares.y, scratch[turn], a.split.warps, slot, w);
+        const float rms = sqrtf(sum * inv_cols + a.eps);
         if (a.row_rms && w == 0 && g == 0 && row < a.rows) a.row_rms[row] = rms;
         const float inv = 1.0f / rms;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int base = (k * a.split.warps + w) * 256;
-            float gamma[8], y[8];
-            load_weights<LANES, VEC>(a.gamma, base, g, cols, gamma);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = h[k][i] * inv * gamma[i];
+            float2 y[4];
+            normed<LANES, VEC>(a, base, g, cols, inv, h[k], y);
             answer_eight<T, LANES, VEC>(a, row, base, g, cols, y);
         }
     }
@@ -123,29 +135,28 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_long(const AddNormArgs a) {
     const int64_t units = (int64_t(a.cols) + 255) / 256;
     int turn = 0;
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
-        float squares = 0.f;
+        float2 squares = both(0.f);
         for (int64_t u = w; u < units; u += 32) {
             Sum<T, R, 32, VEC> in;
-            float h[8];
-            in.load(a, row, int(u * 256), lane, a.cols);
+            float2 h[4];
+            in.load(a, Place<32, VEC>(row, a.cols, int(u * 256), lane, a.cols));
             in.get(a, masker, row, int(u * 256), lane, h);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) squares = fmaf(h[i], h[i], squares);
+            for (int i = 0; i < 4; ++i) squares = fma2(h[i], h[i], squares);
         }
-        const float rms = sqrtf(sum_of_row<32>(squares, scratch[turn], 32, 0, w) * inv_cols + a.eps);
+        const float rms = sqrtf(sum_of_row<32>(squares.x + squares.y, scratch[turn], 32, 0, w) * inv_cols + a.eps);
         if (a.row_rms && threadIdx.x == 0) a.row_rms[row] = rms;
         const float inv = 1.0f / rms;
         for (int64_t u = w; u < units; u += 32) {
             const int base = int(u * 256);
+            const Place<32, VEC> o(row, a.cols, base, lane, a.cols);
             Sum<T, R, 32, VEC> in;
-            float h[8], gamma[8];
-            in.load(a, row, base, lane, a.cols);
-            load_weights<32, VEC>(a.gamma, base, lane, a.cols, gamma);
+            float2 h[4], y[4];
+            in.load(a, o);
             in.get(a, masker, row, base, lane, h);
-            if (a.h) store_eight<32, VEC>(static_cast<R*>(a.h) + row * a.cols, base, lane, a.cols, h);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) h[i] = h[i] * inv * gamma[i];
-            answer_eight<T, 32, VEC>(a, row, base, lane, a.cols, h);
+            if (a.h) store_eight<32, VEC>(static_cast<R*>(a.h), o, h);
+            normed<32, VEC>(a, base, lane, a.cols, inv, h, y);
+            answer_eight<T, 32, VEC>(a, row, base, lane, a.cols, y);
         }
     }
 }

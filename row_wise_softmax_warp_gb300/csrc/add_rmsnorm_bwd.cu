@@ -9,8 +9,8 @@
 //
 // A row lies in the registers of a group of lanes or of up to 32 warps, which walk over
 // rows and keep their columns' part of dgamma in registers; a block adds its sets of
-// warps up in order and writes one row of partial sums, and column sums (rmsnorm.cu)
-// add those, all in an order that only the sizes and the device decide.
+// warps up in order and writes one row of partial sums, and a second launch adds those,
+// all in an order that only the sizes, the alignment and the device decide.
 #include "eight.cuh"
 
 namespace rowops {
@@ -32,75 +32,148 @@ struct AddNormBwdArgs {
     bool wide;  // long rows: the sums fit in shared memory
 };
 
+// g and n of eight columns; adds to their products and to dgamma.
 template <typename T, typename R, int LANES, bool VEC>
-__device__ __forceinline__ void gradients(const AddNormBwdArgs& a, const Masker& m, int64_t row, int base, int g,
-                                          int cols, const Held<R, LANES, VEC>& dh, const float (&gy)[8],
-                                          const float (&n)[8], float inv, float mean) {
-    float t[8];
+__device__ __forceinline__ void factors(const Held<T, LANES, VEC>& dy, const Held<R, LANES, VEC>& h, const float2 (&gamma)[4],
+                                        float inv, float2 (&gy)[4], float2 (&n)[4], float2& dot, float2 (&dgamma)[4]) {
+    dy.get(gy);
+    h.get(n);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        t[i] = (gy[i] - n[i] * mean) * inv;
-        if (a.dh) t[i] += dh.get(i);
-    }
-    if (a.dresidual) store_eight<LANES, VEC>(static_cast<R*>(a.dresidual) + row * a.cols, base, g, cols, t);
-    if (a.dx) {
-        drop_eight<LANES, VEC>(t, a.drop, m, row, (a.cols + 7) / 8, base, g);
-        store_eight<LANES, VEC>(static_cast<T*>(a.dx) + row * a.cols, base, g, cols, t);
+    for (int i = 0; i < 4; ++i) {
+        n[i] = mul2(n[i], both(inv));
+        dgamma[i] = fma2(gy[i], n[i], dgamma[i]);
+        gy[i] = mul2(gy[i], gamma[i]);
+        dot = fma2(gy[i], n[i], dot);
     }
 }
 
 template <typename T, typename R, int LANES, bool VEC>
+__device__ __forceinline__ void gradients(const AddNormBwdArgs& a, const Masker& m, const Place<LANES, VEC>& o, int64_t row,
+                                          int base, int g, const Held<R, LANES, VEC>& dh, const float2 (&gy)[4],
+                                          const float2 (&n)[4], float inv, float mean) {
+    float2 t[4], r[4];
+    if (a.dh) dh.get(r);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        t[i] = mul2(fma2(n[i], both(-mean), gy[i]), both(inv));
+        if (a.dh) t[i] = add2(t[i], r[i]);
+    }
+    if (a.dresidual) store_eight<LANES, VEC>(static_cast<R*>(a.dresidual), o, t);
+    if (a.dx) {
+        drop_eight<LANES, VEC>(t, a.drop, m, row, (a.cols + 7) / 8, base, g);
+        store_eight<LANES, VEC>(static_cast<T*>(a.dx), o, t);
+    }
+}
+
+// VEC: rows come through shared memory, where each thread keeps places for kStages rows of
+// its own columns, so that the next rows are on their way while it works on one.
+constexpr int kStages = 2;
+template <typename T, typename R>
+constexpr int kPlaces = Held<T, 32, true>::kChunks + 2 * Held<R, 32, true>::kChunks;  // of 16 bytes, a row
+
+template <typename T, typename R, int LANES, bool VEC>
 __global__ void __launch_bounds__(1024) add_rmsnorm_bwd_rows(const AddNormBwdArgs a) {
-    extern __shared__ float sums[];  // a.split.warps * 256
+    extern __shared__ __align__(16) float shared[];  // the places; afterwards sums of a.split.warps * 256 columns
     __shared__ float scratch[2][32];
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int slot = warp / a.split.warps, w = warp % a.split.warps, g = lane % LANES;
     constexpr int kGroups = 32 / LANES;
     const float inv_cols = 1.0f / float(a.cols);
     const Masker masker(a.drop);
     const int base = w * 256;
-    float gamma[8], dgamma[8];
-    load_weights<LANES, VEC>(a.gamma, base, g, a.cols, gamma);
+    float2 gamma[4], dgamma[4];
+    load_weights<LANES, VEC>(a.gamma, Place<LANES, VEC>(0, 0, base, g, a.cols), gamma);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) dgamma[i] = 0.f;
-    int turn = 0;
-    for (int64_t first = (int64_t(blockIdx.x) * a.split.slots + slot) * kGroups; first < a.rows;
-         first += int64_t(gridDim.x) * a.split.slots * kGroups, turn ^= 1) {
-        const bool live = first + lane / LANES < a.rows;
-        const int64_t row = live ? first + lane / LANES : 0;
-        const int cols = live ? a.cols : 0;
-        Held<T, LANES, VEC> dy;
-        Held<R, LANES, VEC> h, dh;
-        dy.load(static_cast<const T*>(a.dy) + row * a.cols, base, g, cols);
-        h.load(static_cast<const R*>(a.h) + row * a.cols, base, g, cols);
-        if (a.dh) dh.load(static_cast<const R*>(a.dh) + row * a.cols, base, g, cols);
-        const float inv = live ? 1.0f / __ldg(a.row_rms + row) : 0.f;
-        float gy[8], n[8], dot = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float d = dy.get(i);
-            n[i] = h.get(i) * inv;
-            dgamma[i] = fmaf(d, n[i], dgamma[i]);
-            gy[i] = d * gamma[i];
-            dot = fmaf(gy[i], n[i], dot);
+    for (int i = 0; i < 4; ++i) dgamma[i] = both(0.f);
+
+    using HeldT = Held<T, LANES, VEC>;
+    using HeldR = Held<R, LANES, VEC>;
+    const uint32_t step = blockDim.x * 16;  // from place to place
+    const uint32_t places = uint32_t(__cvta_generic_to_shared(shared)) + threadIdx.x * 16;
+    const int64_t first = (int64_t(blockIdx.x) * a.split.slots + slot) * kGroups;
+    const int64_t stride = int64_t(gridDim.x) * a.split.slots * kGroups;
+    const auto begin = [&](int64_t from, uint32_t at) {  // copies of the rows at `from`
+        if constexpr (VEC) {
+            const int64_t row = from + lane / LANES;
+            const Place<LANES, VEC> o(row, a.cols, base, g, row < a.rows ? a.cols : 0);
+            HeldT::copy(at, step, static_cast<const T*>(a.dy), o);
+            at += HeldT::kChunks * step;
+            HeldR::copy(at, step, static_cast<const R*>(a.h), o);
+            at += HeldR::kChunks * step;
+            if (a.dh) HeldR::copy(at, step, static_cast<const R*>(a.dh), o);
+            copies_end();
         }
-        dot = sum_of_row<LANES>(dot, scratch[turn], a.split.warps, slot, w);
-        gradients<T, R, LANES, VEC>(a, masker, row, base, g, cols, dh, gy, n, inv, dot * inv_cols);
+    };
+#pragma unroll
+    for (int s = 0; s < kStages; ++s) begin(first + s * stride, places + s * kPlaces<T, R> * step);
+    int turn = 0;
+    for (int64_t from = first; from < a.rows; from += stride, turn ^= 1) {
+        const bool live = from + lane / LANES < a.rows;
+        const int64_t row = live ? from + lane / LANES : 0;
+        const Place<LANES, VEC> o(row, a.cols, base, g, live ? a.cols : 0);
+        const float inv = live ? 1.0f / __ldg(a.row_rms + row) : 0.f;
+        HeldT dy;
+        HeldR h, dh;
+        const uint32_t at = places + turn * kPlaces<T, R> * step;  // kStages is 2
+        if constexpr (VEC) {
+            copies_wait<kStages - 1>();
+            dy.take(at, step, o);
+            h.take(at + HeldT::kChunks * step, step, o);
+        } else {
+            dy.load(static_cast<const T*>(a.dy), o);
+            h.load(static_cast<const R*>(a.h), o);
+            if (a.dh) dh.load(static_cast<const R*>(a.dh), o);
+        }
+        float2 gy[4], n[4], dots = both(0.f);
+        factors<T, R, LANES, VEC>(dy, h, gamma, inv, gy, n, dots, dgamma);
+        const float dot = sum_of_row<LANES>(dots.x + dots.y, scratch[turn], a.split.warps, slot, w);
+        if constexpr (VEC) {
+            if (a.dh) dh.take(at + (HeldT::kChunks + HeldR::kChunks) * step, step, o);
+        }
+        gradients<T, R, LANES, VEC>(a, masker, o, row, base, g, dh, gy, n, inv, dot * inv_cols);
+        begin(from + kStages * stride, at);  // where all has been read
     }
+    if constexpr (VEC) copies_wait<0>();
+    __syncthreads();
     // the groups of a warp, then the sets of warps in order
 #pragma unroll
-    for (int i = 0; i < 8; ++i) dgamma[i] = across_groups_sum<LANES>(dgamma[i]);
+    for (int i = 0; i < 4; ++i)
+        dgamma[i] = make_float2(across_groups_sum<LANES>(dgamma[i].x), across_groups_sum<LANES>(dgamma[i].y));
     for (int s = 0; s < a.split.slots; ++s) {
         if (slot == s && lane < LANES) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                float* to = sums + base + (VEC ? 8 * g + i : i * LANES + g);
-                *to = s == 0 ? dgamma[i] : *to + dgamma[i];
+                float* to = shared + base + (VEC ? 8 * g + i : i * LANES + g);
+                const float d = i & 1 ? dgamma[i / 2].y : dgamma[i / 2].x;
+                *to = s == 0 ? d : *to + d;
             }
         }
         __syncthreads();
     }
-    for (int c = threadIdx.x; c < a.cols; c += blockDim.x) a.parts[int64_t(blockIdx.x) * a.cols + c] = sums[c];
+    for (int c = threadIdx.x; c < a.cols; c += blockDim.x) a.parts[int64_t(blockIdx.x) * a.cols + c] = shared[c];
+}
+
+// dgamma = the blocks' parts, added in order within each warp and then over the warps: a
+// warp 32 columns of every 16th part.  A programmatic dependent of what writes them.
+constexpr int kSumWarps = 16;
+__global__ void __launch_bounds__(kSumWarps * 32) sum_parts(const float* parts, float* dgamma, int blocks, int cols) {
+    __shared__ float sums[kSumWarps][32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t c = int64_t(blockIdx.x) * 32 + lane;
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    float sum = 0.f;
+    if (c < cols) {
+#pragma unroll 8
+        for (int b = warp; b < blocks; b += kSumWarps) sum += parts[int64_t(b) * cols + c];
+    }
+    sums[warp][lane] = sum;
+    __syncthreads();
+    if (warp == 0 && c < cols) {
+#pragma unroll
+        for (int q = 1; q < kSumWarps; ++q) sum += sums[q][lane];
+        dgamma[c] = sum;
+    }
 }
 
 // Rows of more than 8192 values: one block a row.  dy and h are read a second time,
@@ -110,6 +183,7 @@ template <typename T, typename R, bool VEC>
 __global__ void __launch_bounds__(1024) add_rmsnorm_bwd_long(const AddNormBwdArgs a) {
     extern __shared__ float sums[];
     __shared__ float scratch[2][32];
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const float inv_cols = 1.0f / float(a.cols);
     const Masker masker(a.drop);
@@ -126,37 +200,33 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_bwd_long(const AddNormBwdArg
     for (int64_t u = w; u < units; u += 32) each(int(u * 256), [&](int c, int) { mine[c] = 0.f; });
     int turn = 0;
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
-        const T* dy_row = static_cast<const T*>(a.dy) + row * a.cols;
-        const R* h_row = static_cast<const R*>(a.h) + row * a.cols;
         const float inv = 1.0f / __ldg(a.row_rms + row);
-        float dot = 0.f;
+        const auto read = [&](int base, Held<T, 32, VEC>& dy, Held<R, 32, VEC>& h, float2 (&gamma)[4]) {
+            const Place<32, VEC> o(row, a.cols, base, lane, a.cols);
+            dy.load(static_cast<const T*>(a.dy), o);
+            h.load(static_cast<const R*>(a.h), o);
+            load_weights<32, VEC>(a.gamma, Place<32, VEC>(0, 0, base, lane, a.cols), gamma);
+            return o;
+        };
+        float2 dots = both(0.f);
         for (int64_t u = w; u < units; u += 32) {
             Held<T, 32, VEC> dy;
             Held<R, 32, VEC> h;
-            float gamma[8];
-            dy.load(dy_row, int(u * 256), lane, a.cols);
-            h.load(h_row, int(u * 256), lane, a.cols);
-            load_weights<32, VEC>(a.gamma, int(u * 256), lane, a.cols, gamma);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) dot = fmaf(dy.get(i) * gamma[i], h.get(i) * inv, dot);
+            float2 gamma[4], gy[4], n[4], none[4] = {};
+            read(int(u * 256), dy, h, gamma);
+            factors<T, R, 32, VEC>(dy, h, gamma, inv, gy, n, dots, none);
         }
-        dot = sum_of_row<32>(dot, scratch[turn], 32, 0, w);
+        const float mean = sum_of_row<32>(dots.x + dots.y, scratch[turn], 32, 0, w) * inv_cols;
         for (int64_t u = w; u < units; u += 32) {
             const int base = int(u * 256);
             Held<T, 32, VEC> dy;
             Held<R, 32, VEC> h, dh;
-            float gy[8], n[8];
-            dy.load(dy_row, base, lane, a.cols);
-            h.load(h_row, base, lane, a.cols);
-            if (a.dh) dh.load(static_cast<const R*>(a.dh) + row * a.cols, base, lane, a.cols);
-            load_weights<32, VEC>(a.gamma, base, lane, a.cols, gy);
-            each(base, [&](int col, int i) { mine[col] = fmaf(dy.get(i), h.get(i) * inv, mine[col]); });
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                n[i] = h.get(i) * inv;
-                gy[i] *= dy.get(i);
-            }
-            gradients<T, R, 32, VEC>(a, masker, row, base, lane, a.cols, dh, gy, n, inv, dot * inv_cols);
+            float2 gamma[4], gy[4], n[4], none = both(0.f), dgamma[4] = {};
+            const Place<32, VEC> o = read(base, dy, h, gamma);
+            if (a.dh) dh.load(static_cast<const R*>(a.dh), o);
+            factors<T, R, 32, VEC>(dy, h, gamma, inv, gy, n, none, dgamma);
+            each(base, [&](int col, int i) { mine[col] += i & 1 ? dgamma[i / 2].y : dgamma[i / 2].x; });
+            gradients<T, R, 32, VEC>(a, masker, o, row, base, lane, dh, gy, n, inv, mean);
         }
     }
     if (!a.wide) return;
@@ -201,17 +271,16 @@ cudaError_t launch_add_rmsnorm_bwd(const void* dy, const float* gamma, const voi
                                         reinterpret_cast<uintptr_t>(h) | reinterpret_cast<uintptr_t>(dh) |
                                         reinterpret_cast<uintptr_t>(dresidual) | reinterpret_cast<uintptr_t>(dx)) & 15) == 0;
     cudaError_t e = cudaSuccess;
-    auto go = [&](auto kernel, size_t smem) {
-        if (smem > 32 * 1024) e = allow_smem(kernel, smem);  // 48 KB with the static part need no leave
-        if (e != cudaSuccess) return;
-        kernel<<<unsigned(plan.blocks), unsigned(plan.warps * plan.slots * 32), smem, stream>>>(a);
-        note_launches(1);
-        e = cudaGetLastError();
-    };
     with_branch_types(x_type, h_type, [&](auto t, auto r) {
         using T = decltype(t);
         using R = decltype(r);
-        const size_t smem = size_t(plan.warps) * 256 * 4;
+        auto go = [&](auto kernel, size_t smem) {
+            if (smem > 32 * 1024) e = allow_smem(kernel, smem);  // 48 KB with the static part need no leave
+            if (e == cudaSuccess) kernel<<<unsigned(plan.blocks), unsigned(plan.warps * plan.slots * 32), smem, stream>>>(a);
+        };
+        const size_t sums = size_t(plan.warps) * 256 * 4;
+        const size_t staged = size_t(kStages) * kPlaces<T, R> * 16 * plan.warps * plan.slots * 32;
+        const size_t smem = vec && staged > sums ? staged : sums;
         if (cols > kRegisterCols) {
             const size_t wide = a.wide ? size_t(cols) * 4 : 0;
             if (vec) go(add_rmsnorm_bwd_long<T, R, true>, wide);
@@ -222,7 +291,19 @@ cudaError_t launch_add_rmsnorm_bwd(const void* dy, const float* gamma, const voi
         else go(add_rmsnorm_bwd_rows<T, R, 32, true>, smem);
     });
     if (e != cudaSuccess) return e;
-    return launch_column_sums(parts, dgamma, plan.blocks, cols, 0.f, stream);
+    note_launches(2);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(unsigned((cols + 31) / 32));
+    cfg.blockDim = dim3(kSumWarps * 32);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, sum_parts, static_cast<const float*>(parts), dgamma, int(plan.blocks), int(cols));
 }
 
 }  // namespace rowops

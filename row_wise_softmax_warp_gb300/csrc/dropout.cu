@@ -33,7 +33,7 @@ __global__ void __launch_bounds__(kDropThreads) dropout_rows(const DropoutArgs g
     for (int64_t item0 = first; item0 < g.items; item0 += step) {
         Held<T, 32, VEC> x[ITEMS];
         Held<R, 32, VEC> residual[ITEMS];
-        int64_t row[ITEMS], at[ITEMS];
+        int64_t row[ITEMS];
         int base[ITEMS], cols[ITEMS];
 #pragma unroll
         for (int n = 0; n < ITEMS; ++n) {
@@ -41,28 +41,29 @@ __global__ void __launch_bounds__(kDropThreads) dropout_rows(const DropoutArgs g
             if constexpr (VEC) {  // the matrix as rows of 256
                 row[n] = item;
                 base[n] = 0;
-                at[n] = item * 256;
-                const int64_t left = g.rows * int64_t(g.cols) - at[n];
-                cols[n] = left < 256 ? int(max(left, int64_t(0))) : 256;
+                cols[n] = int(max(int64_t(0), min(int64_t(256), g.rows * int64_t(g.cols) - item * 256)));
             } else {
                 row[n] = item / g.units;
                 base[n] = int(item - row[n] * g.units) * 256;
-                at[n] = row[n] * g.cols;
                 cols[n] = item < g.items ? g.cols : 0;
             }
-            x[n].load(static_cast<const T*>(g.x) + at[n], base[n], lane, cols[n]);
-            if (g.residual) residual[n].load(static_cast<const R*>(g.residual) + at[n], base[n], lane, cols[n]);
+            const Place<32, VEC> o(row[n], VEC ? 256 : g.cols, base[n], lane, cols[n]);
+            x[n].load(static_cast<const T*>(g.x), o);
+            if (g.residual) residual[n].load(static_cast<const R*>(g.residual), o);
         }
 #pragma unroll
         for (int n = 0; n < ITEMS; ++n) {
-            float v[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = x[n].get(i);
+            const Place<32, VEC> o(row[n], VEC ? 256 : g.cols, base[n], lane, cols[n]);
+            float2 v[4];
+            x[n].get(v);
             drop_eight<32, VEC>(v, g.drop, masker, row[n], VEC ? 32 : (g.cols + 7) / 8, base[n], lane);
-            if (g.residual)
+            if (g.residual) {
+                float2 r[4];
+                residual[n].get(r);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] += residual[n].get(i);
-            store_eight<32, VEC>(static_cast<R*>(g.y) + at[n], base[n], lane, cols[n], v);
+                for (int i = 0; i < 4; ++i) v[i] = add2(v[i], r[i]);
+            }
+            store_eight<32, VEC>(static_cast<R*>(g.y), o, v);
         }
     }
 }

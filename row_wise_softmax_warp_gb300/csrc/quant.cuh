@@ -68,18 +68,22 @@ __device__ __forceinline__ uint2 quantize8(const float (&v)[8], const Divisor& o
 // code 255, which stands for NaN, and zeros.
 
 // The largest magnitude as its bits, in which NaN lies above infinity.
-__device__ __forceinline__ uint32_t largest_bits(const float (&v)[8]) {
+__device__ __forceinline__ uint32_t largest_bits(const float2 (&v)[4]) {
     uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
+    for (int i = 0; i < 4; ++i)
+        m = max(m, max(__float_as_uint(v[i].x) & 0x7fffffffu, __float_as_uint(v[i].y) & 0x7fffffffu));
     return m;
 }
 template <int LANES>
 __device__ __forceinline__ uint32_t group_max_bits(uint32_t v) {
-    if constexpr (LANES == 32) return __reduce_max_sync(kFullMask, v);
+    if constexpr (LANES == 32) {
+        return __reduce_max_sync(kFullMask, v);
+    } else {
 #pragma unroll
-    for (int o = LANES / 2; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(kFullMask, v, o));
-    return v;
+        for (int o = LANES / 2; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(kFullMask, v, o));
+        return v;
+    }
 }
 // The block's code from its largest magnitude.  A subnormal's exponent field is 0, and
 // floor(log2 a) - 2 lies below -127 for it.
@@ -94,15 +98,15 @@ __device__ __forceinline__ float mx4_inverse(uint32_t code) {
 }
 // Two codes in a byte, the first value in the lower half; 0 times an infinite or NaN value
 // would be NaN, so blocks of code 255 are told.
-__device__ __forceinline__ uint32_t mx4_pair(float x, float y, float inverse) {
-    return __nv_cvt_float2_to_fp4x2(make_float2(x * inverse, y * inverse), __NV_E2M1, cudaRoundNearest);
+__device__ __forceinline__ uint32_t mx4_pair(float2 v, float inverse) {
+    return __nv_cvt_float2_to_fp4x2(make_float2(v.x * inverse, v.y * inverse), __NV_E2M1, cudaRoundNearest);
 }
-__device__ __forceinline__ uint32_t mx4_eight(const float (&v)[8], uint32_t code) {
+__device__ __forceinline__ uint32_t mx4_eight(const float2 (&v)[4], uint32_t code) {
     if (code == 255) return 0;
     const float inverse = mx4_inverse(code);
     uint32_t w = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w |= mx4_pair(v[2 * i], v[2 * i + 1], inverse) << (8 * i);
+    for (int i = 0; i < 4; ++i) w |= mx4_pair(v[i], inverse) << (8 * i);
     return w;
 }
 
@@ -113,7 +117,10 @@ __device__ __forceinline__ uint32_t mx4_eight(const float (&v)[8], uint32_t code
 // whole of a shorter group), or four values of each of 32 lanes.
 
 template <int LANES, bool VEC>
-__device__ __forceinline__ void store_e4m3(uint8_t* q, float* scale, int base, int g, int cols, const float (&y)[8]) {
+__device__ __forceinline__ void store_e4m3(uint8_t* q, float* scale, int base, int g, int cols, const float2 (&pairs)[4]) {
+    float y[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[2 * i] = pairs[i].x, y[2 * i + 1] = pairs[i].y;
     scale += base / 128;
     if constexpr (VEC) {
         constexpr int kBlock = LANES < 16 ? LANES : 16;
@@ -150,17 +157,20 @@ __device__ __forceinline__ void store_e4m3(uint8_t* q, float* scale, int base, i
 }
 
 template <int LANES, bool VEC>
-__device__ __forceinline__ void store_mx4(uint8_t* q, uint8_t* scale, int base, int g, int cols, const float (&y)[8]) {
+__device__ __forceinline__ void store_mx4(uint8_t* q, uint8_t* scale, int base, int g, int cols, const float2 (&pairs)[4]) {
     scale += base / 32;
     if constexpr (VEC) {
-        const uint32_t code = mx4_code(group_max_bits<4>(largest_bits(y)));
+        const uint32_t code = mx4_code(group_max_bits<4>(largest_bits(pairs)));
         if (base + 8 * g < cols) {
-            *reinterpret_cast<uint32_t*>(q + base / 2 + 4 * g) = mx4_eight(y, code);
+            *reinterpret_cast<uint32_t*>(q + base / 2 + 4 * g) = mx4_eight(pairs, code);
             if (g % 4 == 0) scale[g / 4] = uint8_t(code);
         }
     } else {
         static_assert(LANES == 32, "a value of each lane is a block");
         uint32_t code[8];
+        float y[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[2 * i] = pairs[i].x, y[2 * i + 1] = pairs[i].y;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             code[i] = mx4_code(group_max_bits<32>(__float_as_uint(y[i]) & 0x7fffffffu));
@@ -174,7 +184,7 @@ __device__ __forceinline__ void store_mx4(uint8_t* q, uint8_t* scale, int base, 
             const uint32_t mine = odd ? code[i + 1] : code[i];
             const int c = base + (i + odd) * 32 + g - odd;
             if (c < cols)
-                q[c / 2] = mine == 255 ? 0 : uint8_t(mx4_pair(odd ? other : y[i], odd ? y[i + 1] : other, mx4_inverse(mine)));
+                q[c / 2] = mine == 255 ? 0 : uint8_t(mx4_pair(make_float2(odd ? other : y[i], odd ? y[i + 1] : other), mx4_inverse(mine)));
         }
     }
 }

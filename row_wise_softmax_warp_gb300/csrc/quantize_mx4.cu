@@ -17,17 +17,17 @@ __device__ __forceinline__ uint32_t most_of(const Held<T, 32, true>& x) {
     if constexpr (sizeof(T) == 4) {
         uint32_t m = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(x.get(i)) & 0x7fffffffu);
+        for (int h = 0; h < 2; ++h)
+            m = max(max(m, max(x.c[h].x & 0x7fffffffu, x.c[h].y & 0x7fffffffu)),
+                    max(x.c[h].z & 0x7fffffffu, x.c[h].w & 0x7fffffffu));
         return group_max_bits<4>(m);
     } else {
-        const uint4 w = x.c[0].raw;
+        const uint4 w = x.c[0];
         uint32_t m = __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu),
                               __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu));
 #pragma unroll
         for (int o = 2; o > 0; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(kFullMask, m, o));
-        Chunk<T, 2> c;
-        c.raw = max(m & 0xffffu, m >> 16);
-        return __float_as_uint(c.get(0));
+        return __float_as_uint(unpack2<T>(max(m & 0xffffu, m >> 16)).x);
     }
 }
 
@@ -40,14 +40,13 @@ __global__ void __launch_bounds__(THREADS)
     Held<T, 32, true> in[ITEMS];
 #pragma unroll
     for (int n = 0; n < ITEMS; ++n)
-        if (first + n * THREADS < chunks) in[n].load(x + (first + n * THREADS) * 8, 0, 0, 8);
+        in[n].load(x, Place<32, true>(first + n * THREADS, 8, 0, 0, first + n * THREADS < chunks ? 8 : 0));
 #pragma unroll
     for (int n = 0; n < ITEMS; ++n) {
         const int64_t at = first + n * THREADS;
         const uint32_t code = mx4_code(most_of<T>(in[n]));
-        float v[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = in[n].get(i);
+        float2 v[4];
+        in[n].get(v);
         if (at < chunks) {
             q[at] = mx4_eight(v, code);
             if ((threadIdx.x & 3) == 0) scale[at / 4] = uint8_t(code);
@@ -75,10 +74,9 @@ __global__ void __launch_bounds__(kMxThreads) quantize_mx4_rows(const Mx4Args a)
         const int64_t row = item / a.units;
         const int base = int(item - row * a.units) * 256;
         Held<T, 32, VEC> x;
-        x.load(static_cast<const T*>(a.x) + row * a.cols, base, lane, a.cols);
-        float v[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = x.get(i);
+        x.load(static_cast<const T*>(a.x), Place<32, VEC>(row, a.cols, base, lane, a.cols));
+        float2 v[4];
+        x.get(v);
         store_mx4<32, VEC>(a.q + row * ((a.cols + 1) / 2), a.scale + row * ((a.cols + 31) / 32), base, lane, a.cols, v);
     }
 }
