@@ -66,14 +66,18 @@ __device__ __forceinline__ void gradients(const AddNormBwdArgs& a, const Masker&
 }
 
 // VEC: rows come through shared memory, where each thread keeps places for kStages rows of
-// its own columns, so that the next rows are on their way while it works on one.
+// its own columns, so that the next rows are on their way while it works on one.  A block of
+// 512 threads an SM then does (16384 x 4096, bf16 and fp32 stream with dropout: 170 us; two
+// blocks, whose threads have half the registers, 177; without the places 181; three and
+// four stages are no faster).  Rows that are read directly hide more behind two blocks
+// (16384 x 1023: 68 us, one: 77).
 constexpr int kStages = 2;
 template <typename T, typename R>
 constexpr int kPlaces = Held<T, 32, true>::kChunks + 2 * Held<R, 32, true>::kChunks;  // of 16 bytes, a row
 
-template <typename T, typename R, int LANES, bool VEC>
-__global__ void __launch_bounds__(1024) add_rmsnorm_bwd_rows(const AddNormBwdArgs a) {
-    extern __shared__ __align__(16) float shared[];  // the places; afterwards sums of a.split.warps * 256 columns
+template <typename T, typename R, int LANES, int NV, bool VEC>
+__global__ void __launch_bounds__(512, VEC ? 1 : 2) add_rmsnorm_bwd_rows(const AddNormBwdArgs a) {
+    extern __shared__ __align__(16) float shared[];  // the places; afterwards sums of a.split.warps * NV * 256 columns
     __shared__ float scratch[2][32];
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -81,11 +85,14 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_bwd_rows(const AddNormBwdArg
     constexpr int kGroups = 32 / LANES;
     const float inv_cols = 1.0f / float(a.cols);
     const Masker masker(a.drop);
-    const int base = w * 256;
-    float2 gamma[4], dgamma[4];
-    load_weights<LANES, VEC>(a.gamma, Place<LANES, VEC>(0, 0, base, g, a.cols), gamma);
+    const auto base_of = [&](int k) { return (k * a.split.warps + w) * 256; };
+    float2 gamma[NV][4], dgamma[NV][4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) dgamma[i] = both(0.f);
+    for (int k = 0; k < NV; ++k) {
+        load_weights<LANES, VEC>(a.gamma, Place<LANES, VEC>(0, 0, base_of(k), g, a.cols), gamma[k]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) dgamma[k][i] = both(0.f);
+    }
 
     using HeldT = Held<T, LANES, VEC>;
     using HeldR = Held<R, LANES, VEC>;
@@ -96,58 +103,78 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_bwd_rows(const AddNormBwdArg
     const auto begin = [&](int64_t from, uint32_t at) {  // copies of the rows at `from`
         if constexpr (VEC) {
             const int64_t row = from + lane / LANES;
-            const Place<LANES, VEC> o(row, a.cols, base, g, row < a.rows ? a.cols : 0);
-            HeldT::copy(at, step, static_cast<const T*>(a.dy), o);
-            at += HeldT::kChunks * step;
-            HeldR::copy(at, step, static_cast<const R*>(a.h), o);
-            at += HeldR::kChunks * step;
-            if (a.dh) HeldR::copy(at, step, static_cast<const R*>(a.dh), o);
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                const Place<LANES, VEC> o(row, a.cols, base_of(k), g, row < a.rows ? a.cols : 0);
+                HeldT::copy(at, step, static_cast<const T*>(a.dy), o);
+                at += HeldT::kChunks * step;
+                HeldR::copy(at, step, static_cast<const R*>(a.h), o);
+                at += HeldR::kChunks * step;
+                if (a.dh) HeldR::copy(at, step, static_cast<const R*>(a.dh), o);
+                at += HeldR::kChunks * step;
+            }
             copies_end();
         }
     };
 #pragma unroll
-    for (int s = 0; s < kStages; ++s) begin(first + s * stride, places + s * kPlaces<T, R> * step);
+    for (int s = 0; s < kStages; ++s) begin(first + s * stride, places + s * NV * kPlaces<T, R> * step);
+    const auto rms_at = [&](int64_t from) { return from + lane / LANES < a.rows ? __ldg(a.row_rms + from + lane / LANES) : 1.f; };
+    float next_rms = VEC ? rms_at(first) : 0.f;  // asked for a row ahead
     int turn = 0;
     for (int64_t from = first; from < a.rows; from += stride, turn ^= 1) {
-        const bool live = from + lane / LANES < a.rows;
-        const int64_t row = live ? from + lane / LANES : 0;
-        const Place<LANES, VEC> o(row, a.cols, base, g, live ? a.cols : 0);
-        const float inv = live ? 1.0f / __ldg(a.row_rms + row) : 0.f;
-        HeldT dy;
-        HeldR h, dh;
-        const uint32_t at = places + turn * kPlaces<T, R> * step;  // kStages is 2
-        if constexpr (VEC) {
-            copies_wait<kStages - 1>();
-            dy.take(at, step, o);
-            h.take(at + HeldT::kChunks * step, step, o);
-        } else {
-            dy.load(static_cast<const T*>(a.dy), o);
-            h.load(static_cast<const R*>(a.h), o);
-            if (a.dh) dh.load(static_cast<const R*>(a.dh), o);
+        const int64_t row = from + lane / LANES;
+        const int there = row < a.rows ? a.cols : 0;
+        const float inv = 1.0f / (VEC ? next_rms : rms_at(from));
+        if (VEC) next_rms = rms_at(from + stride);
+        HeldR dh[NV];
+        float2 gy[NV][4], n[NV][4], dots = both(0.f);
+        const uint32_t stage = places + turn * NV * kPlaces<T, R> * step;  // kStages is 2
+        if constexpr (VEC) copies_wait<kStages - 1>();
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const Place<LANES, VEC> o(row, a.cols, base_of(k), g, there);
+            const uint32_t at = stage + k * kPlaces<T, R> * step;
+            HeldT dy;
+            HeldR h;
+            if constexpr (VEC) {
+                dy.take(at, step, o);
+                h.take(at + HeldT::kChunks * step, step, o);
+            } else {
+                dy.load(static_cast<const T*>(a.dy), o);
+                h.load(static_cast<const R*>(a.h), o);
+                if (a.dh) dh[k].load(static_cast<const R*>(a.dh), o);
+            }
+            factors<T, R, LANES, VEC>(dy, h, gamma[k], inv, gy[k], n[k], dots, dgamma[k]);
         }
-        float2 gy[4], n[4], dots = both(0.f);
-        factors<T, R, LANES, VEC>(dy, h, gamma, inv, gy, n, dots, dgamma);
         const float dot = sum_of_row<LANES>(dots.x + dots.y, scratch[turn], a.split.warps, slot, w);
-        if constexpr (VEC) {
-            if (a.dh) dh.take(at + (HeldT::kChunks + HeldR::kChunks) * step, step, o);
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const Place<LANES, VEC> o(row, a.cols, base_of(k), g, there);
+            if constexpr (VEC) {
+                if (a.dh) dh[k].take(stage + (k * kPlaces<T, R> + HeldT::kChunks + HeldR::kChunks) * step, step, o);
+            }
+            gradients<T, R, LANES, VEC>(a, masker, o, row, base_of(k), g, dh[k], gy[k], n[k], inv, dot * inv_cols);
         }
-        gradients<T, R, LANES, VEC>(a, masker, o, row, base, g, dh, gy, n, inv, dot * inv_cols);
-        begin(from + kStages * stride, at);  // where all has been read
+        begin(from + kStages * stride, stage);  // where all has been read
     }
     if constexpr (VEC) copies_wait<0>();
     __syncthreads();
     // the groups of a warp, then the sets of warps in order
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        dgamma[i] = make_float2(across_groups_sum<LANES>(dgamma[i].x), across_groups_sum<LANES>(dgamma[i].y));
+    for (int k = 0; k < NV; ++k)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            dgamma[k][i] = make_float2(across_groups_sum<LANES>(dgamma[k][i].x), across_groups_sum<LANES>(dgamma[k][i].y));
     for (int s = 0; s < a.split.slots; ++s) {
         if (slot == s && lane < LANES) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                float* to = shared + base + (VEC ? 8 * g + i : i * LANES + g);
-                const float d = i & 1 ? dgamma[i / 2].y : dgamma[i / 2].x;
-                *to = s == 0 ? d : *to + d;
-            }
+            for (int k = 0; k < NV; ++k)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    float* to = shared + base_of(k) + (VEC ? 8 * g + i : i * LANES + g);
+                    const float d = i & 1 ? dgamma[k][i / 2].y : dgamma[k][i / 2].x;
+                    *to = s == 0 ? d : *to + d;
+                }
         }
         __syncthreads();
     }
@@ -233,43 +260,46 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_bwd_long(const AddNormBwdArg
     for (int64_t u = w; u < units; u += 32) each(int(u * 256), [&](int c, int) { parts[c] = sums[c]; });
 }
 
-constexpr int64_t kRegisterCols = 8192;  // one group of 256 columns for each of 32 warps
+constexpr int64_t kRegisterCols = 8192;  // 256 or 512 columns for each of the most warps of a row
 constexpr int64_t kWideCols = 48 * 1024;  // sums in shared memory
 
-// Lanes, warps and sets of warps by the row's length, and blocks by the rows.
+// Lanes, columns of a lane, warps and sets of warps by the row's length, and blocks by the
+// rows.
 struct BwdPlan {
-    int lanes, warps, slots;
+    int lanes, nv, warps, slots;
     int64_t blocks;
 };
-BwdPlan plan_of(int64_t rows, int64_t cols) {
+BwdPlan plan_of(int64_t rows, int64_t cols, bool vec) {
     const int64_t sms = sm_count() > 0 ? sm_count() : 132;
-    if (cols > kRegisterCols) return {32, 32, 1, rows < sms ? rows : sms};
+    if (cols > kRegisterCols) return {32, 1, 32, 1, rows < sms ? rows : sms};
     BwdPlan p;
     const int units = int((cols + 255) / 256);
     p.lanes = cols <= 64 ? 8 : cols <= 128 ? 16 : 32;
-    p.warps = units;
-    p.slots = units >= 16 ? 1 : units >= 2 ? 16 / units : 8;
+    p.nv = units > 16 ? 2 : 1;
+    p.warps = (units + p.nv - 1) / p.nv;
+    p.slots = 16 / p.warps;
     const int64_t sets = (rows + p.slots - 1) / p.slots;
-    p.blocks = sets < 2 * sms ? sets : 2 * sms;
+    const int64_t most = vec ? sms : 2 * sms;
+    p.blocks = sets < most ? sets : most;
     return p;
 }
 
 }  // namespace
 
 size_t add_rmsnorm_bwd_workspace(int64_t rows, int64_t cols) {
-    return rows > 0 ? size_t(plan_of(rows, cols).blocks) * size_t(cols) * 4 : 0;
+    return rows > 0 ? size_t(plan_of(rows, cols, false).blocks) * size_t(cols) * 4 : 0;  // the more of the two
 }
 
 cudaError_t launch_add_rmsnorm_bwd(const void* dy, const float* gamma, const void* h, const float* row_rms,
                                    const void* dh, const uint64_t* rng, void* dresidual, void* dx, float* dgamma,
                                    int64_t rows, int64_t cols, float p, int x_type, int h_type, float* parts,
                                    cudaStream_t stream) {
-    const BwdPlan plan = plan_of(rows, cols);
-    AddNormBwdArgs a{dy,   gamma,     h,           row_rms, dh, dresidual, dx, parts, dropout_of(rng, p),
-                     rows, int(cols), {plan.warps, plan.slots}, cols <= kWideCols};
     const bool vec = cols % 8 == 0 && ((reinterpret_cast<uintptr_t>(dy) | reinterpret_cast<uintptr_t>(gamma) |
                                         reinterpret_cast<uintptr_t>(h) | reinterpret_cast<uintptr_t>(dh) |
                                         reinterpret_cast<uintptr_t>(dresidual) | reinterpret_cast<uintptr_t>(dx)) & 15) == 0;
+    const BwdPlan plan = plan_of(rows, cols, vec);
+    AddNormBwdArgs a{dy,   gamma,     h,           row_rms, dh, dresidual, dx, parts, dropout_of(rng, p),
+                     rows, int(cols), {plan.warps, plan.slots}, cols <= kWideCols};
     cudaError_t e = cudaSuccess;
     with_branch_types(x_type, h_type, [&](auto t, auto r) {
         using T = decltype(t);
@@ -278,17 +308,20 @@ cudaError_t launch_add_rmsnorm_bwd(const void* dy, const float* gamma, const voi
             if (smem > 32 * 1024) e = allow_smem(kernel, smem);  // 48 KB with the static part need no leave
             if (e == cudaSuccess) kernel<<<unsigned(plan.blocks), unsigned(plan.warps * plan.slots * 32), smem, stream>>>(a);
         };
-        const size_t sums = size_t(plan.warps) * 256 * 4;
-        const size_t staged = size_t(kStages) * kPlaces<T, R> * 16 * plan.warps * plan.slots * 32;
+        const size_t sums = size_t(plan.warps) * plan.nv * 256 * 4;
+        const size_t staged = size_t(kStages) * plan.nv * kPlaces<T, R> * 16 * plan.warps * plan.slots * 32;
         const size_t smem = vec && staged > sums ? staged : sums;
         if (cols > kRegisterCols) {
             const size_t wide = a.wide ? size_t(cols) * 4 : 0;
             if (vec) go(add_rmsnorm_bwd_long<T, R, true>, wide);
             else go(add_rmsnorm_bwd_long<T, R, false>, wide);
-        } else if (!vec) go(add_rmsnorm_bwd_rows<T, R, 32, false>, smem);
-        else if (plan.lanes == 8) go(add_rmsnorm_bwd_rows<T, R, 8, true>, smem);
-        else if (plan.lanes == 16) go(add_rmsnorm_bwd_rows<T, R, 16, true>, smem);
-        else go(add_rmsnorm_bwd_rows<T, R, 32, true>, smem);
+        } else if (!vec) {
+            if (plan.nv == 1) go(add_rmsnorm_bwd_rows<T, R, 32, 1, false>, smem);
+            else go(add_rmsnorm_bwd_rows<T, R, 32, 2, false>, smem);
+        } else if (plan.lanes == 8) go(add_rmsnorm_bwd_rows<T, R, 8, 1, true>, smem);
+        else if (plan.lanes == 16) go(add_rmsnorm_bwd_rows<T, R, 16, 1, true>, smem);
+        else if (plan.nv == 1) go(add_rmsnorm_bwd_rows<T, R, 32, 1, true>, smem);
+        else go(add_rmsnorm_bwd_rows<T, R, 32, 2, true>, smem);
     });
     if (e != cudaSuccess) return e;
     note_launches(2);
