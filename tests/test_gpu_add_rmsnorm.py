@@ -21,7 +21,7 @@ EPS = 1e-5
 PAIRS = [("f32", "f32"), ("f16", "f16"), ("f16", "f32"), ("bf16", "bf16"), ("bf16", "f32")]
 SHAPES = [(1, 1), (5, 8), (3, 33), (9, 64), (7, 72), (6, 128), (5, 136), (4, 255), (3, 256), (700, 264), (2, 768),
           (3, 1023), (5, 1024), (2, 2056), (2, 4096), (700, 2048), (1, 8192), (3, 8200), (2, 16384), (2, 16392), (1, 20001),
-          (1, 50000)]
+          (1, 50000), (1300, 40), (1300, 120), (1300, 200), (700, 1023), (650, 4104)]
 
 
 def inputs(seed, shape, types, shift=0, residual=True):
