@@ -86,6 +86,7 @@ __device__ __forceinline__ void answer_eight(const AddNormArgs& a, int64_t row, 
 template <typename T, typename R, int LANES, int NV, bool VEC, int MOST>
 __global__ void __launch_bounds__(MOST) add_rmsnorm_rows(const AddNormArgs a) {
     __shared__ float scratch[2][32];
+    let_next_start();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int slot = warp / a.split.warps, w = warp % a.split.warps, g = lane % LANES;
     constexpr int kGroups = 32 / LANES;
@@ -137,6 +138,7 @@ template <typename T, typename R, int LANES, int NV>
 __global__ void __launch_bounds__(512, kBlocks<NV>) add_rmsnorm_stream(const AddNormArgs a) {
     extern __shared__ __align__(16) unsigned char shared[];
     __shared__ float scratch[2][32];
+    let_next_start();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int slot = warp / a.split.warps, w = warp % a.split.warps, g = lane % LANES;
     constexpr int kGroups = 32 / LANES;
@@ -206,6 +208,7 @@ __global__ void __launch_bounds__(512, kBlocks<NV>) add_rmsnorm_stream(const Add
 template <typename T, typename R, bool VEC>
 __global__ void __launch_bounds__(1024) add_rmsnorm_long(const AddNormArgs a) {
     __shared__ float scratch[2][32];
+    let_next_start();
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const float inv_cols = 1.0f / float(a.cols);
     const Masker masker(a.drop);

@@ -79,7 +79,7 @@ template <typename T, typename R, int LANES, int NV, bool VEC>
 __global__ void __launch_bounds__(512, VEC ? 1 : 2) add_rmsnorm_bwd_rows(const AddNormBwdArgs a) {
     extern __shared__ __align__(16) float shared[];  // the places; afterwards sums of a.split.warps * NV * 256 columns
     __shared__ float scratch[2][32];
-    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+    let_next_start();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int slot = warp / a.split.warps, w = warp % a.split.warps, g = lane % LANES;
     constexpr int kGroups = 32 / LANES;
@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(kSumWarps * 32) sum_parts(const float* parts, 
     __shared__ float sums[kSumWarps][32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t c = int64_t(blockIdx.x) * 32 + lane;
-    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    wait_for_earlier();
     float sum = 0.f;
     if (c < cols) {
 #pragma unroll 8
@@ -210,7 +210,7 @@ template <typename T, typename R, bool VEC>
 __global__ void __launch_bounds__(1024) add_rmsnorm_bwd_long(const AddNormBwdArgs a) {
     extern __shared__ float sums[];
     __shared__ float scratch[2][32];
-    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+    let_next_start();
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const float inv_cols = 1.0f / float(a.cols);
     const Masker masker(a.drop);

@@ -36,6 +36,12 @@ __device__ __forceinline__ float exp_shifted(float x, float m) {
     return ex2_approx((x - m) * kLog2e);
 }
 
+// Programmatic dependents.  A kernel that lets the next one start early says so at its
+// beginning; one that is launched so waits, before it touches what others wrote, for
+// everything before it in the stream to end.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
+__device__ __forceinline__ void wait_for_earlier() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
+
 // ----------------------------------------------------------------- memory
 
 template <int VEC>

@@ -15,6 +15,7 @@
 // Two accumulators of 224 columns and two stages' scales (24 columns each) fill 496 of
 // the 512 columns of tensor memory; with 256 tokens a tile there would be no room for
 // the scales, or for the second accumulator that hides the write-out.
+#include "bytes.cuh"
 #include "groups.cuh"
 #include "tensor_core.cuh"
 #include "types.cuh"
@@ -51,7 +52,7 @@ struct Mx4ProductArgs {
     int slots, experts;
     int out, bytes;  // bytes of a row of an operand
     int blocks;      // scales of a row
-    int scale_vec;   // bytes that a load of scales may take: 16, 8 or 1
+    int scale_vec;   // bytes that a load of scales may take: 32, 16, 8 or 1
     bool vec;        // rows of y allow 16-byte stores
 };
 
@@ -126,6 +127,8 @@ __device__ __forceinline__ void mma_pair_mx4_4(uint32_t d, uint64_t a, uint64_t 
 // lie 32 apart.
 struct ScaleRows {
     const uint8_t* p[4];  // their rows of scales; NULL: none
+    const uint8_t* begin;
+    const uint8_t* end;   // of all rows
     __device__ __forceinline__ void load(int block, int blocks, int vec, uint32_t (&r)[4][2 * kAhead]) const {
         const int left = blocks - block;  // at least 1
 #pragma unroll
@@ -134,7 +137,12 @@ struct ScaleRows {
             for (int i = 0; i < 2 * kAhead; ++i) r[j][i] = 0;
             if (p[j] == nullptr) continue;
             const uint8_t* at = p[j] + block;
-            if (vec == 16) {  // blocks is a multiple of 16
+            if (vec == 32) {  // blocks is a multiple of 32
+                asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n"
+                             : "=r"(r[j][0]), "=r"(r[j][1]), "=r"(r[j][2]), "=r"(r[j][3]), "=r"(r[j][4]), "=r"(r[j][5]),
+                               "=r"(r[j][6]), "=r"(r[j][7])
+                             : "l"(at));
+            } else if (vec == 16) {  // blocks is a multiple of 16
 #pragma unroll
                 for (int i = 0; i < kAhead / 2; ++i)
                     if (left > 16 * i) {
@@ -149,9 +157,16 @@ struct ScaleRows {
                         r[j][2 * i] = v.x, r[j][2 * i + 1] = v.y;
                     }
             } else {
+                const int off = int(reinterpret_cast<uintptr_t>(at) & 3);
+                uint32_t word[2 * kAhead + 1];
 #pragma unroll
-                for (int i = 0; i < 8 * kAhead; ++i)
-                    if (i < left) r[j][i / 4] |= uint32_t(__ldg(at + i)) << (8 * (i % 4));
+                for (int i = 0; i <= 2 * kAhead; ++i) word[i] = 4 * i < left + off ? word_at(at - off + 4 * i, begin, end) : 0;
+#pragma unroll
+                for (int i = 0; i < 2 * kAhead; ++i) {
+                    const int there = left - 4 * i;  // the next row's scales are not this one's: 0 times NaN is NaN
+                    const uint32_t v = __funnelshift_r(word[i], word[i + 1], 8 * off);
+                    r[j][i] = there >= 4 ? v : there > 0 ? v & ((1u << (8 * there)) - 1) : 0;
+                }
             }
         }
     }
@@ -241,6 +256,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_product_mx4(const __grid_c
         prefetch_map(&g.x_small);
     }
     if (warp == kProductWarp) tmem_alloc_pair(&sh.tmem, kTmemColumns);
+    wait_for_earlier();  // what quantised the rows lets this kernel come this far
     build_tile_table<kTileRows, kThreads>(g.offsets, g.experts, g.slots, table, sh.warp_tiles);
     tcgen05_fence_before();
     __syncthreads();
@@ -343,6 +359,8 @@ __global__ void __launch_bounds__(kThreads, 1) expert_product_mx4(const __grid_c
         for (int t = first; ok && tile_at(g, table, t, tiles, w); t += step, part -= parts) {
             if (part >= parts) continue;
             ScaleRows rows;
+            rows.begin = role == 0 ? g.ws : g.xs;
+            rows.end = rows.begin + (role == 0 ? int64_t(g.experts) * g.out : int64_t(g.slots)) * g.blocks;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int row = (role == 2 ? 128 : 0) + 32 * j + lane;
@@ -420,7 +438,7 @@ cudaError_t launch_expert_matmul_mx4(const uint8_t* x, const uint8_t* xs, const 
     Matrix mx = matrix_of(x, in / 2, slots, 1, 1), mw = matrix_of(w, in / 2, out, experts, 1);
     Matrix* ms[2] = {&mx, &mw};
     cudaError_t err;
-    if (!make_readable(ms, {false, true}, offsets, slots, scratch, stream, &err))
+    if (!make_readable(ms, {false, true}, offsets, slots, scratch, stream, &err, true))
         return launch_matmul_mx4_any(x, xs, w, ws, offsets, y, slots, in, out, experts, y_type, stream);
     if (err != cudaSuccess) return err;
     const CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_UINT8;
@@ -439,14 +457,14 @@ cudaError_t launch_expert_matmul_mx4(const uint8_t* x, const uint8_t* xs, const 
     g.bytes = int(in / 2);
     g.blocks = int((in + 31) / 32);
     const uintptr_t at = reinterpret_cast<uintptr_t>(xs) | reinterpret_cast<uintptr_t>(ws) | uintptr_t(g.blocks);
-    g.scale_vec = at % 16 == 0 ? 16 : at % 8 == 0 ? 8 : 1;
+    g.scale_vec = at % 32 == 0 ? 32 : at % 16 == 0 ? 16 : at % 8 == 0 ? 8 : 1;
     const int y_size = y_type == ROWOPS_F32 ? 4 : 2;
     g.vec = out * y_size % 16 == 0 && reinterpret_cast<uintptr_t>(y) % 16 == 0;
     const int64_t tiles = most_row_tiles(slots, experts, kTileRows) * ((out + 255) / 256);
     cudaError_t e = cudaErrorInvalidValue;
     if (tiles >= kMostTiles) return e;  // more than a device's memory holds
     with_type(y_type, [&](auto o) {
-        e = launch_pairs<expert_product_mx4<decltype(o)>>(tiles, kThreads, kMostSmem, stream, g);
+        e = launch_pairs<expert_product_mx4<decltype(o)>>(tiles, kThreads, kMostSmem, stream, g, true);
     });
     return e;
 }

@@ -272,7 +272,9 @@ struct RepackJob {
 };
 __host__ __device__ inline int64_t repack_pitch(int64_t row_bytes) { return (row_bytes + 15) & ~int64_t(15); }
 inline size_t repack_bytes(int64_t rows, int64_t row_bytes) { return size_t(rows * repack_pitch(row_bytes) + 255) & ~size_t(255); }
-cudaError_t launch_repack(const RepackJob* jobs, int n, const int32_t* offsets, int64_t slots, cudaStream_t stream);
+// early: as a programmatic dependent of what runs before.
+cudaError_t launch_repack(const RepackJob* jobs, int n, const int32_t* offsets, int64_t slots, cudaStream_t stream,
+                          bool early = false);
 
 cudaError_t launch_expert_matmul(const void* x, const void* w, const int32_t* offsets, void* y, int64_t slots,
                                  int64_t in, int64_t out, int64_t experts, bool transposed, int dtype,

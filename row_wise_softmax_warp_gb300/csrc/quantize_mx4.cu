@@ -36,6 +36,7 @@ __device__ __forceinline__ uint32_t most_of(const Held<T, 32, true>& x) {
 template <typename T, int ITEMS, int THREADS>
 __global__ void __launch_bounds__(THREADS)
     quantize_mx4_run(const T* x, uint32_t* __restrict__ q, uint8_t* __restrict__ scale, int64_t chunks) {
+    let_next_start();
     const int64_t first = int64_t(blockIdx.x) * (THREADS * ITEMS) + threadIdx.x;
     Held<T, 32, true> in[ITEMS];
 #pragma unroll
@@ -68,6 +69,7 @@ struct Mx4Args {
 // Other rows, a warp 256 columns.
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kMxThreads) quantize_mx4_rows(const Mx4Args a) {
+    let_next_start();
     const int lane = threadIdx.x & 31;
     const int64_t step = int64_t(gridDim.x) * (kMxThreads / 32);
     for (int64_t item = int64_t(blockIdx.x) * (kMxThreads / 32) + (threadIdx.x >> 5); item < a.items; item += step) {

@@ -6,6 +6,7 @@
 // 1001 fp16 and 8192 rows of 1001: 97 MB in about 23 us with its launch).  What lies between a
 // row's end and the next boundary is whatever the source holds there; the tensor
 // map over the copy ends at the row's true width.
+#include "bytes.cuh"
 #include "groups.cuh"
 #include "launch.h"
 
@@ -28,16 +29,9 @@ struct RepackArgs {
     int each;  // rows of a warp
 };
 
-// The aligned word at `at`, of whose bytes those in [begin, end) are there.
-__device__ __forceinline__ uint32_t word_at(const uint8_t* at, const uint8_t* begin, const uint8_t* end) {
-    if (at >= begin && at + 4 <= end) return __ldg(reinterpret_cast<const uint32_t*>(at));
-    uint32_t w = 0;
-    for (int i = 0; i < 4; ++i)
-        if (at + i >= begin && at + i < end) w |= uint32_t(at[i]) << (8 * i);
-    return w;
-}
-
 __global__ void __launch_bounds__(kRepackThreads) repack(const RepackArgs g) {
+    let_next_start();
+    wait_for_earlier();
     const int lane = threadIdx.x & 31;
     const int64_t first = (int64_t(blockIdx.x) * (kRepackThreads / 32) + (threadIdx.x >> 5)) * g.each;
     for (int64_t r = first; r < first + g.each; ++r) {
@@ -76,7 +70,8 @@ __global__ void __launch_bounds__(kRepackThreads) repack(const RepackArgs g) {
 
 }  // namespace
 
-cudaError_t launch_repack(const RepackJob* jobs, int n, const int32_t* offsets, int64_t slots, cudaStream_t stream) {
+cudaError_t launch_repack(const RepackJob* jobs, int n, const int32_t* offsets, int64_t slots, cudaStream_t stream,
+                          bool early) {
     RepackArgs g = {};
     int64_t rows = 0;
     for (int i = 0; i < n; ++i) {
@@ -87,9 +82,18 @@ cudaError_t launch_repack(const RepackJob* jobs, int n, const int32_t* offsets, 
     g.slots = int(slots);
     g.each = rows >= kManyRows ? kRepackRows : 1;
     const int64_t per = kRepackThreads / 32 * g.each;
-    repack<<<unsigned((rows + per - 1) / per), kRepackThreads, 0, stream>>>(g);
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(unsigned((rows + per - 1) / per));
+    cfg.blockDim = dim3(kRepackThreads);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = early ? 1 : 0;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, repack, g);
     note_launches(1);
-    return cudaGetLastError();
+    return e;
 }
 
 }  // namespace rowops

@@ -345,7 +345,7 @@ inline bool tma_reads(const Matrix& m) { return m.pitch % 16 == 0 && reinterpret
 // there; false where there is too little of it.  by_expert: the operand holds a
 // matrix an expert.
 inline bool make_readable(Matrix* (&ms)[2], const bool (&by_expert)[2], const int32_t* offsets, int64_t slots,
-                          Scratch scratch, cudaStream_t stream, cudaError_t* err) {
+                          Scratch scratch, cudaStream_t stream, cudaError_t* err, bool early = false) {
     RepackJob jobs[2];
     int n = 0;
     *err = cudaSuccess;
@@ -359,7 +359,7 @@ inline bool make_readable(Matrix* (&ms)[2], const bool (&by_expert)[2], const in
         m.base = dst;
         m.pitch = repack_pitch(bytes);
     }
-    if (n > 0) *err = launch_repack(jobs, n, offsets, slots, stream);
+    if (n > 0) *err = launch_repack(jobs, n, offsets, slots, stream, early);
     return true;
 }
 
@@ -402,23 +402,26 @@ int resident_pairs(int threads, size_t smem) {
     return n;
 }
 
+// early: as a programmatic dependent of what runs before; the kernel calls wait_for_earlier().
 template <auto kernel, typename A>
-cudaError_t launch_pairs(int64_t pairs, int threads, size_t smem, cudaStream_t stream, const A& args) {
+cudaError_t launch_pairs(int64_t pairs, int threads, size_t smem, cudaStream_t stream, const A& args, bool early = false) {
     const int resident = resident_pairs<kernel>(threads, smem);
     if (resident <= 0) {
         const cudaError_t e = cudaGetLastError();
         return e == cudaSuccess ? cudaErrorInvalidConfiguration : e;
     }
     cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim = {2, 1, 1};
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.gridDim = dim3(2 * unsigned(pairs < resident ? pairs : resident));
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = early ? 2 : 1;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args);
     note_launches(1);
     return e;
