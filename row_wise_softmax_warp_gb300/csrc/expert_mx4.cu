@@ -15,6 +15,17 @@
 // Two accumulators of 224 columns and two stages' scales (24 columns each) fill 496 of
 // the 512 columns of tensor memory; with 256 tokens a tile there would be no room for
 // the scales, or for the second accumulator that hides the write-out.
+//
+// What bounds it: 16384 x 4096 -> 4096 takes 107 to 111 us (4950 to 5140 TFLOP/s; the bf16
+// product 299).  Variants that leave work out: products alone 66 us, copies alone 73 (16
+// TB/s from the L2, near what the SMs take), both without scales 90, with scales that are
+// written but not loaded 96.  So it is the L2's bandwidth that the operands share with the
+// scales (9% of their bytes: a tile's 256 columns and, in both CTAs, its rows) and the
+// results.  A single tile takes 6.8 us with its launch (5.5 where nothing is loaded or
+// written), 64 experts of 768 x 2048 with 8192 rows 24 us against 14 of HBM traffic.
+// Scales written stage by stage took 256 us: every hand-over to the other CTA has a fence
+// that a thread's loads, stores and a cluster-wide release wait for, so one hand-over
+// serves four stages, three sets of warps take turns, and loads follow it.
 #include "bytes.cuh"
 #include "groups.cuh"
 #include "tensor_core.cuh"
@@ -308,25 +319,32 @@ __global__ void __launch_bounds__(kThreads, 1) expert_product_mx4(const __grid_c
             uint32_t s = 0, phase = 0, slot = 0, slot_phase = 0, acc = 0, turn = 0;  // turn: of the two places in tensor memory
             const uint64_t a0 = operand_desc(stage0, 16, 1024), b0 = operand_desc(stage0 + kWBytes, 16, 1024);
             const uint64_t s0 = scale_desc(uniform(smem_addr(slots)));
-            Mx4Tile w;
-            for (int t = first; ok && tile_at(g, table, t, tiles, w); t += step) {
+            Mx4Tile w, next;
+            bool ready = false;  // the next stage was seen full, with its scales and its accumulator
+            bool more = tile_at(g, table, first, tiles, w);
+            for (int t = first; ok && more; t += step, w = next) {
+                next = w;
+                more = tile_at(g, table, t + step, tiles, next);
                 const uint32_t d = tmem + (acc & 1) * kTileRows, n_bits = uint32_t(w.width >> 3) << 17;
                 const bool two = w.width > 128;
-                ok = warp_wait(&sh.acc_empty[acc & 1], ((acc >> 1) & 1) ^ 1, abort_flag);
-                bool ready = false;  // the stage was seen full, and its scales
-                for (int kb = 0; ok && kb < steps; ++kb) {
+                for (int kb = 0; kb < steps; ++kb) {
                     if (!ready) {
-                        if (kb % kAhead == 0) ok = warp_wait<true>(&sh.scale_full[slot], slot_phase, abort_flag);
+                        if (kb == 0) ok = warp_wait(&sh.acc_empty[acc & 1], ((acc >> 1) & 1) ^ 1, abort_flag);
+                        if (kb % kAhead == 0) ok = ok && warp_wait<true>(&sh.scale_full[slot], slot_phase, abort_flag);
                         ok = ok && warp_wait(&sh.full[s], phase, abort_flag);
                         if (!ok) break;
                     }
                     tcgen05_fence_after();
                     const uint32_t here = s, at = s * (kStageBytes >> 4), scales = slot;
-                    const bool last_of_slot = kb % kAhead == kAhead - 1 || kb == steps - 1;
+                    const bool last = kb == steps - 1, last_of_slot = kb % kAhead == kAhead - 1 || last;
                     next_stage<kStages>(s, phase);
                     if (last_of_slot) next_stage<kScaleSlots>(slot, slot_phase);
-                    uint32_t looks = kb + 1 < steps ? look(&sh.full[s], phase) : 0;
-                    if (last_of_slot && kb + 1 < steps) looks &= look<true>(&sh.scale_full[slot], slot_phase);
+                    uint32_t looks = 0;
+                    if (!last || more) {
+                        looks = look(&sh.full[s], phase);
+                        if (last_of_slot) looks &= look<true>(&sh.scale_full[slot], slot_phase);
+                        if (last) looks &= look(&sh.acc_empty[(acc + 1) & 1], (((acc + 1) >> 1) & 1) ^ 1);
+                    }
                     const uint32_t ws = tmem + kScaleColumn + turn * kScaleColumns, xs = ws + 8;
                     const uint64_t from = s0 + scales * (kSlotBytes >> 4) + (kb % kAhead) * 2 * (kAtom >> 4);
                     turn ^= 1;
@@ -339,9 +357,9 @@ __global__ void __launch_bounds__(kThreads, 1) expert_product_mx4(const __grid_c
                     mma_pair_mx4_4(d, a0 + at, b0 + at, n_bits, ws, xs, kb > 0);
                     mma_commit_pair(&sh.empty[here]);
                     if (last_of_slot) mma_commit_pair(&sh.scale_empty[scales]);
+                    if (last) mma_commit_pair(&sh.acc_full[acc & 1]);
                     ready = saw(looks);
                 }
-                if (ok) mma_commit_pair(&sh.acc_full[acc & 1]);
                 ++acc;
             }
         }

@@ -2,8 +2,11 @@
 // block of 32 columns of a row (quant.cuh).
 //
 // Bound by HBM: reads the input once, writes 17 bytes for 32 values.  Four lanes hold
-// a block, a warp 256 columns.  Where rows are whole blocks the matrix is one run of
-// them, and a warp's eight scales go out as one store.
+// a block.  Where rows are whole blocks the matrix is one run of chunks of eight values,
+// of which a thread has four on their way (16384 x 4096 bf16: 27 us, 6.2 TB/s; one at a
+// time 49, eight 36), and the maximum of 16-bit values is taken on their bits, two at a
+// time.  Rows of other lengths are read value by value where they are no multiple of 8
+// (16384 x 1001: 24 us, x 1000: 15).
 #include "eight.cuh"
 #include "quant.cuh"
 

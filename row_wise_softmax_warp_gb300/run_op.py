@@ -4,7 +4,10 @@
 
 Ops: softmax_fwd, softmax_bwd, attn_fwd, attn_bwd (cols = seq_len), logsumexp,
 softmax_ce, layernorm_fwd, layernorm_bwd, rmsnorm_fwd, rmsnorm_bwd, masked_softmax, topk_kept,
-router_masked_topk, top_k_rows, argmax_onehot, soft_ce, teacher_ce.  For rows of
+router_masked_topk, top_k_rows, argmax_onehot, soft_ce, teacher_ce; dropout,
+add_rmsnorm_fwd, add_rmsnorm_bwd (bf16 branch, fp32 stream, p = 0.1; ROWOPS_STREAM=bf16
+and ROWOPS_P change that, ROWOPS_QUANTIZE=e4m3 or mx4 the forward's answer), quantize_mx4
+and expert_matmul_mx4 (bf16, one dense product to as many columns).  For rows of
 more than 1024 floats, top_k_rows and argmax_onehot take logits-like rows
 (top_k_rows with k from ROWOPS_TOPK, default 50); topk_kept,
 router_masked_topk and top_k_rows on shorter rows take k from ROWOPS_K
@@ -113,6 +116,33 @@ def make(op: str, rows: int, cols: int, dev):
             return lambda: ro.rowops_top_k_rows(x, k, True, vals, idx)
         oh = torch.empty_like(x)
         return lambda: ro.rowops_argmax_onehot(x, oh)
+    if op in ("dropout", "add_rmsnorm_fwd", "add_rmsnorm_bwd"):
+        p = float(os.environ.get("ROWOPS_P", "0.1"))
+        stream = torch.bfloat16 if os.environ.get("ROWOPS_STREAM") == "bf16" else torch.float32
+        n = inputs.layernorm(0, rows=rows, cols=cols)
+        x, h, gm = t(n["dy"]).bfloat16(), t(n["x"]).to(stream), t(n["gamma"])
+        rng = torch.tensor([1, 2], device=dev)
+        if op == "dropout":
+            y = torch.empty_like(h)
+            return lambda: ro.rowops_dropout(x, rng, p, residual=h, y=y)
+        if op == "add_rmsnorm_fwd":
+            q = os.environ.get("ROWOPS_QUANTIZE")
+            out, scale, s, rr = ro.rowops_add_rmsnorm_fwd(x, gm, residual=h, rng=rng, p=p, quantize=q)
+            return lambda: ro.rowops_add_rmsnorm_fwd(x, gm, residual=h, rng=rng, p=p, quantize=q, out=out, scale=scale,
+                                                     h=s, row_rms=rr)
+        _, _, s, rr = ro.rowops_add_rmsnorm_fwd(x, gm, residual=h, rng=rng, p=p)
+        dx, dr, dg = torch.empty_like(x), torch.empty_like(h), torch.empty_like(gm)
+        ws = torch.empty(ro.rowops_add_rmsnorm_bwd_workspace(rows, cols), dtype=torch.uint8, device=dev)
+        return lambda: ro.rowops_add_rmsnorm_bwd(x, gm, s, rr, dh=h, rng=rng, p=p, dx=dx, dresidual=dr, dgamma=dg,
+                                                 workspace=ws)
+    if op in ("quantize_mx4", "expert_matmul_mx4"):
+        x = t(inputs.layernorm(0, rows=rows, cols=cols)["dy"]).bfloat16()
+        q, scale = ro.rowops_quantize_mx4(x)
+        if op == "quantize_mx4":
+            return lambda: ro.rowops_quantize_mx4(x, q, scale)
+        wq, ws = ro.rowops_quantize_mx4(t(inputs.layernorm(1, rows=cols, cols=cols)["dy"]).bfloat16()[None])
+        y = torch.empty((rows, cols), dtype=torch.bfloat16, device=dev)
+        return lambda: ro.rowops_expert_matmul_mx4(q, scale, wq, ws, y=y)
     raise SystemExit(f"unknown op {op}")
 
 

@@ -12,7 +12,7 @@ from test_gpu_expert_matmul import TINY, TYPES, UNIT, f64
 
 pytestmark = pytest.mark.gpu
 
-SHAPES = [(1, 1), (1, 8), (3, 7), (5, 16), (2, 255), (7, 256), (4, 257), (9, 768), (3, 1023), (2, 4104), (33, 64), (1, 20000)]
+SHAPES = [(1, 1), (1, 8), (3, 7), (5, 16), (2, 255), (7, 256), (4, 257), (9, 768), (3, 1023), (2, 4104), (33, 64), (1, 20000), (70, 33), (19, 100), (5, 129)]
 
 
 def rng_of(key, offset):
