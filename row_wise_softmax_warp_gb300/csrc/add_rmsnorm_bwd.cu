@@ -67,17 +67,17 @@ __device__ __forceinline__ void gradients(const AddNormBwdArgs& a, const Masker&
 }
 
 // VEC: rows come through shared memory, where each thread keeps places for kStages rows of
-// its own columns, so that the next rows are on their way while it works on one.  A block of
-// 512 threads an SM then does (16384 x 4096, bf16 and fp32 stream with dropout: 170 us; two
-// blocks, whose threads have half the registers, 177; without the places 181; three and
-// four stages are no faster).  Rows that are read directly hide more behind two blocks
-// (16384 x 1023: 68 us, one: 77).
+// its own columns, so that the next rows are on their way while it works on one.  512 threads
+// an SM then do (16384 x 4096, bf16 and fp32 stream with dropout: 170 us; 1024, which have
+// half the registers, 177; without the places 181; three and four stages are no faster),
+// in two blocks where a row takes 8 warps at most (4096 x 768 fp32: 13.6 us, in one 14.3).
+// Rows that are read directly hide more behind 1024 threads (16384 x 1023: 67 us, 512: 77).
 constexpr int kStages = 2;
 template <typename T, typename R>
 constexpr int kPlaces = Held<T, 32, true>::kChunks + 2 * Held<R, 32, true>::kChunks;  // of 16 bytes, a row
 
-template <typename T, typename R, int LANES, int NV, bool VEC>
-__global__ void __launch_bounds__(512, VEC ? 1 : 2) add_rmsnorm_bwd_rows(const AddNormBwdArgs a) {
+template <typename T, typename R, int LANES, int NV, bool VEC, int THREADS>
+__global__ void __launch_bounds__(THREADS, VEC ? 512 / THREADS : 2) add_rmsnorm_bwd_rows(const AddNormBwdArgs a) {
     extern __shared__ __align__(16) float shared[];  // the places; afterwards sums of a.split.warps * NV * 256 columns
     __shared__ float scratch[2][32];
     let_next_start();
@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(kSumWarps * 32) sum_parts(const float* parts, 
 // the block's row of parts.  A thread reads and writes its own columns only.
 template <typename T, typename R, bool VEC>
 __global__ void __launch_bounds__(1024) add_rmsnorm_bwd_long(const AddNormBwdArgs a) {
-    extern __shared__ float sums[];
+    extern __shared__ __align__(16) float sums[];
     __shared__ float scratch[2][32];
     let_next_start();
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -253,7 +253,19 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_bwd_long(const AddNormBwdArg
             const Place<32, VEC> o = read(base, dy, h, gamma);
             if (a.dh) dh.load(static_cast<const R*>(a.dh), o);
             factors<T, R, 32, VEC>(dy, h, gamma, inv, gy, n, none, dgamma);
-            each(base, [&](int col, int i) { mine[col] += i & 1 ? dgamma[i / 2].y : dgamma[i / 2].x; });
+            if constexpr (VEC) {
+                if (o.left > 0) {
+                    float4* sum = reinterpret_cast<float4*>(mine + base + 8 * lane);
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        float4 v = sum[q];
+                        v.x += dgamma[2 * q].x, v.y += dgamma[2 * q].y, v.z += dgamma[2 * q + 1].x, v.w += dgamma[2 * q + 1].y;
+                        sum[q] = v;
+                    }
+                }
+            } else {
+                each(base, [&](int col, int i) { mine[col] += i & 1 ? dgamma[i / 2].y : dgamma[i / 2].x; });
+            }
             gradients<T, R, 32, VEC>(a, masker, o, row, base, lane, dh, gy, n, inv, mean);
         }
     }
@@ -268,19 +280,22 @@ constexpr int64_t kWideCols = 48 * 1024;  // sums in shared memory
 // rows.
 struct BwdPlan {
     int lanes, nv, warps, slots;
+    int threads;  // at most
     int64_t blocks;
 };
 BwdPlan plan_of(int64_t rows, int64_t cols, bool vec) {
     const int64_t sms = sm_count() > 0 ? sm_count() : 132;
-    if (cols > kRegisterCols) return {32, 1, 32, 1, rows < sms ? rows : sms};
+    if (cols > kRegisterCols) return {32, 1, 32, 1, 1024, rows < sms ? rows : sms};
     BwdPlan p;
     const int units = int((cols + 255) / 256);
     p.lanes = cols <= 64 ? 8 : cols <= 128 ? 16 : 32;
     p.nv = units > 16 ? 2 : 1;
     p.warps = (units + p.nv - 1) / p.nv;
-    p.slots = 16 / p.warps;
+    const bool half = vec && p.warps <= 8;  // of the block, twice
+    p.threads = half ? 256 : 512;
+    p.slots = p.threads / 32 / p.warps;
     const int64_t sets = (rows + p.slots - 1) / p.slots;
-    const int64_t most = vec ? sms : 2 * sms;
+    const int64_t most = half || !vec ? 2 * sms : sms;
     p.blocks = sets < most ? sets : most;
     return p;
 }
@@ -288,7 +303,9 @@ BwdPlan plan_of(int64_t rows, int64_t cols, bool vec) {
 }  // namespace
 
 size_t add_rmsnorm_bwd_workspace(int64_t rows, int64_t cols) {
-    return rows > 0 ? size_t(plan_of(rows, cols, false).blocks) * size_t(cols) * 4 : 0;  // the more of the two
+    if (rows <= 0) return 0;  // of rows on 16-byte boundaries and others, whichever take more
+    const int64_t a = plan_of(rows, cols, true).blocks, b = plan_of(rows, cols, false).blocks;
+    return size_t(a > b ? a : b) * size_t(cols) * 4;
 }
 
 cudaError_t launch_add_rmsnorm_bwd(const void* dy, const float* gamma, const void* h, const float* row_rms,
@@ -317,12 +334,13 @@ cudaError_t launch_add_rmsnorm_bwd(const void* dy, const float* gamma, const voi
             if (vec) go(add_rmsnorm_bwd_long<T, R, true>, wide);
             else go(add_rmsnorm_bwd_long<T, R, false>, wide);
         } else if (!vec) {
-            if (plan.nv == 1) go(add_rmsnorm_bwd_rows<T, R, 32, 1, false>, smem);
-            else go(add_rmsnorm_bwd_rows<T, R, 32, 2, false>, smem);
-        } else if (plan.lanes == 8) go(add_rmsnorm_bwd_rows<T, R, 8, 1, true>, smem);
-        else if (plan.lanes == 16) go(add_rmsnorm_bwd_rows<T, R, 16, 1, true>, smem);
-        else if (plan.nv == 1) go(add_rmsnorm_bwd_rows<T, R, 32, 1, true>, smem);
-        else go(add_rmsnorm_bwd_rows<T, R, 32, 2, true>, smem);
+            if (plan.nv == 1) go(add_rmsnorm_bwd_rows<T, R, 32, 1, false, 512>, smem);
+            else go(add_rmsnorm_bwd_rows<T, R, 32, 2, false, 512>, smem);
+        } else if (plan.lanes == 8) go(add_rmsnorm_bwd_rows<T, R, 8, 1, true, 256>, smem);
+        else if (plan.lanes == 16) go(add_rmsnorm_bwd_rows<T, R, 16, 1, true, 256>, smem);
+        else if (plan.threads == 256) go(add_rmsnorm_bwd_rows<T, R, 32, 1, true, 256>, smem);
+        else if (plan.nv == 1) go(add_rmsnorm_bwd_rows<T, R, 32, 1, true, 512>, smem);
+        else go(add_rmsnorm_bwd_rows<T, R, 32, 2, true, 512>, smem);
     });
     if (e != cudaSuccess) return e;
     note_launches(2);
