@@ -135,7 +135,8 @@ __device__ __forceinline__ void mma_pair_mx4_4(uint32_t d, uint64_t a, uint64_t 
 }
 
 // What a scale warp reads: the scales of four stages of each of four rows a lane, which
-// lie 32 apart.
+// lie 32 apart.  The loads are not of the read-only kind: what wrote the scales may have
+// ended after this kernel began.
 struct ScaleRows {
     const uint8_t* p[4];  // their rows of scales; NULL: none
     const uint8_t* begin;
@@ -149,22 +150,23 @@ struct ScaleRows {
             if (p[j] == nullptr) continue;
             const uint8_t* at = p[j] + block;
             if (vec == 32) {  // blocks is a multiple of 32
-                asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n"
+                asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n"
                              : "=r"(r[j][0]), "=r"(r[j][1]), "=r"(r[j][2]), "=r"(r[j][3]), "=r"(r[j][4]), "=r"(r[j][5]),
                                "=r"(r[j][6]), "=r"(r[j][7])
-                             : "l"(at));
+                             : "l"(at)
+                             : "memory");
             } else if (vec == 16) {  // blocks is a multiple of 16
 #pragma unroll
                 for (int i = 0; i < kAhead / 2; ++i)
                     if (left > 16 * i) {
-                        const uint4 v = __ldg(reinterpret_cast<const uint4*>(at + 16 * i));
+                        const uint4 v = *reinterpret_cast<const uint4*>(at + 16 * i);
                         r[j][4 * i] = v.x, r[j][4 * i + 1] = v.y, r[j][4 * i + 2] = v.z, r[j][4 * i + 3] = v.w;
                     }
             } else if (vec == 8) {
 #pragma unroll
                 for (int i = 0; i < kAhead; ++i)
                     if (left > 8 * i) {
-                        const uint2 v = __ldg(reinterpret_cast<const uint2*>(at + 8 * i));
+                        const uint2 v = *reinterpret_cast<const uint2*>(at + 8 * i);
                         r[j][2 * i] = v.x, r[j][2 * i + 1] = v.y;
                     }
             } else {

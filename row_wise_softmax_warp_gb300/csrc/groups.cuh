@@ -32,8 +32,8 @@ struct RowRange {
 
 __device__ __forceinline__ RowRange group_rows(const int32_t* offsets, int e, int slots) {
     if (offsets == nullptr) return {0, slots};  // one dense group
-    const int lo = min(max(__ldg(offsets + e), 0), slots);
-    const int hi = min(max(__ldg(offsets + e + 1), lo), slots);
+    const int lo = min(max(offsets[e], 0), slots);  // plain loads: a programmatic dependent reads them too
+    const int hi = min(max(offsets[e + 1], lo), slots);
     return {lo, hi - lo};
 }
 
