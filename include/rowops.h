@@ -653,7 +653,8 @@ size_t rowops_add_rmsnorm_bwd_workspace(int64_t rows, int64_t cols);
  * dy, dx: rows x cols of x_type; h, dh, dresidual: rows x cols of h_type; gamma,
  * dgamma: cols; row_rms: rows.  dh is the gradient that arrives at h from elsewhere
  * (the residual stream; NULL: none).  dresidual and dx may be NULL where they are not
- * wanted; without dropout and with one type they are the same values.  dresidual may
+ * wanted, and rng without dx; without dropout and with one type they are the same
+ * values.  dresidual may
  * be exactly dh, and dx exactly dy; any other overlap of an output is
  * ROWOPS_ERR_ALIAS.  dgamma is summed in a fixed order, through `workspace`: at least
  * rowops_add_rmsnorm_bwd_workspace(rows, cols) bytes, 16-byte aligned, with

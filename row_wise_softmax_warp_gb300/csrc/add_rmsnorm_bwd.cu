@@ -318,7 +318,8 @@ cudaError_t launch_add_rmsnorm_bwd(const void* dy, const float* gamma, const voi
                                         reinterpret_cast<uintptr_t>(h) | reinterpret_cast<uintptr_t>(dh) |
                                         reinterpret_cast<uintptr_t>(dresidual) | reinterpret_cast<uintptr_t>(dx)) & 15) == 0;
     const BwdPlan plan = plan_of(rows, cols, vec);
-    AddNormBwdArgs a{dy,   gamma,     h,           row_rms, dh, dresidual, dx, parts, dropout_of(rng, p),
+    // Without dx there is no mask to make, and rng may be NULL.
+    AddNormBwdArgs a{dy,   gamma,     h,           row_rms, dh, dresidual, dx, parts, dropout_of(rng, dx ? p : 0.f),
                      rows, int(cols), {plan.warps, plan.slots}, cols <= kWideCols};
     cudaError_t e = cudaSuccess;
     with_branch_types(x_type, h_type, [&](auto t, auto r) {

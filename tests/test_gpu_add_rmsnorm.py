@@ -222,6 +222,30 @@ def test_guard_bands(ro):
             assert (buf[:4096] == 0x5A).all() and (buf[-4096:] == 0x5A).all(), (name, rows, cols)
 
 
+@pytest.mark.parametrize("cols", [33, 768, 9000])
+def test_answers_that_are_not_wanted(ro, cols):
+    """C calls with NULL for an answer: the others are what they are with all.  Without dx no mask is made, and rng is NULL."""
+    lib, stream = ro.library(), torch.cuda.current_stream().cuda_stream
+    x, r, gamma, key = inputs(cols, (40, cols), ("bf16", "f32"))
+    rng = rng_of(*key)
+    y, _, h, rms = ro.rowops_add_rmsnorm_fwd(x, gamma, residual=r, rng=rng, p=0.2)
+    want = ro.rowops_add_rmsnorm_bwd(x, gamma, h, rms, dh=r, rng=rng, p=0.2)
+    out = torch.empty_like(y)
+    status = lib.rowops_add_rmsnorm_fwd(x.data_ptr(), r.data_ptr(), gamma.data_ptr(), rng.data_ptr(), None, out.data_ptr(), None,
+                                        None, 40, cols, EPS, 0.2, 2, 0, 2, stream)
+    assert status == 0 and torch.equal(out, ro.rowops_add_rmsnorm_fwd(x, gamma, residual=r, rng=rng, p=0.2, eps=EPS)[0])
+    ws = torch.empty(ro.rowops_add_rmsnorm_bwd_workspace(40, cols), dtype=torch.uint8, device="cuda")
+    for with_dx, with_res in ((False, True), (True, False), (False, False)):
+        dx, dres, dgamma = torch.empty_like(x), torch.empty_like(r), torch.empty_like(gamma)
+        status = lib.rowops_add_rmsnorm_bwd(x.data_ptr(), gamma.data_ptr(), h.data_ptr(), rms.data_ptr(), r.data_ptr(),
+                                            rng.data_ptr() if with_dx else None, dres.data_ptr() if with_res else None,
+                                            dx.data_ptr() if with_dx else None, dgamma.data_ptr(), 40, cols, 0.2, 2, 0,
+                                            ws.data_ptr(), ws.numel(), stream)
+        assert status == 0 and torch.equal(dgamma, want[2])
+        assert not with_dx or torch.equal(dx, want[0])
+        assert not with_res or torch.equal(dres, want[1])
+
+
 def test_refusals(ro):
     x, gamma = torch.zeros(4, 16, device="cuda"), torch.ones(16, device="cuda")
     rms, rng = torch.ones(4, device="cuda"), rng_of(0, 0)
