@@ -62,6 +62,7 @@ struct Mx4ProductArgs {
     void* y;
     int slots, experts;
     int out, bytes;  // bytes of a row of an operand
+    Divisor32 across;  // tiles of 256 output columns
     int blocks;      // scales of a row
     int scale_vec;   // bytes that a load of scales may take: 32, 16, 8 or 1
     bool vec;        // rows of y allow 16-byte stores
@@ -84,12 +85,13 @@ struct Mx4Tile {
     int width;  // rows the products compute
 };
 
-__device__ __forceinline__ bool tile_at(const Mx4ProductArgs& g, const int* table, int t, int tiles, Mx4Tile& w) {
+__device__ __forceinline__ bool tile_at(const Mx4ProductArgs& g, const int* table, const Group* groups, int t, int tiles,
+                                        Mx4Tile& w) {
     if (t >= tiles) return false;
-    const int tiles_m = (g.out + 255) / 256;
-    const RowTile r = row_tile<kTileRows>(g.offsets, g.experts, g.slots, table, t / tiles_m, w.expert);
+    const int row_tile = int(g.across.quotient(uint32_t(t)));
+    const RowTile r = kept_row_tile(groups, g.experts, table, row_tile, w.expert);
     w.expert = uniform(r.expert);
-    w.m0 = t % tiles_m * 256;
+    w.m0 = (t - row_tile * int(g.across.d)) * 256;
     w.n0 = uniform(r.first);
     w.n = uniform(r.count);
     w.width = (w.n + 31) & ~31;
@@ -239,7 +241,8 @@ __global__ void __launch_bounds__(kThreads, 1) expert_product_mx4(const __grid_c
     unsigned char* stages = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
     unsigned char* slots = stages + kStages * kStageBytes;
     unsigned char* turn = slots + kScaleSlots * kSlotBytes;
-    int* table = reinterpret_cast<int*>(turn + kWriteWarps * kTurnBytes);
+    Group* groups = reinterpret_cast<Group*>(turn + kWriteWarps * kTurnBytes);
+    int* table = reinterpret_cast<int*>(groups + kMaxExperts);
     __shared__ Mx4Shared sh;
     volatile int* abort_flag = &sh.abort;
     volatile uint32_t* progress = &sh.progress;
@@ -269,16 +272,19 @@ __global__ void __launch_bounds__(kThreads, 1) expert_product_mx4(const __grid_c
         prefetch_map(&g.x_small);
     }
     if (warp == kProductWarp) tmem_alloc_pair(&sh.tmem, kTmemColumns);
-    wait_for_earlier();  // what quantised the rows lets this kernel come this far
-    build_tile_table<kTileRows, kThreads>(g.offsets, g.experts, g.slots, table, sh.warp_tiles);
+    // Each CTA's barriers and tensor memory are there; the other hears of it while the table is
+    // built.  (An arrival with a release behind the table took 1500 clocks.)
     tcgen05_fence_before();
+    cluster_arrive_relaxed();
+    wait_for_earlier();  // what quantised the rows lets this kernel come this far
+    build_tile_table<kTileRows, kThreads>(g.offsets, g.experts, g.slots, table, sh.warp_tiles, KeepGroups<kTileRows>{groups});
     __syncthreads();
-    cluster_sync_all();
+    cluster_wait();
     tcgen05_fence_after();
     const uint32_t tmem = uniform(sh.tmem), stage0 = uniform(smem_addr(stages));
 
     const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
-    const int tiles = uniform(all_tiles(table[g.experts], (g.out + 255) / 256));
+    const int tiles = uniform(all_tiles(table[g.experts], int(g.across.d)));
     const int steps = (g.bytes + kStepBytes - 1) / kStepBytes;  // stages of a sum
     bool ok = true;
     if (warp == kCopyWarpW || warp == kCopyWarpX) {
@@ -288,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_product_mx4(const __grid_c
         uint32_t s = 0, phase = 1, slot = 0, slot_phase = 1;  // the stage and the scales' slot, and their releases' parities
         uint32_t stages_begun = 0;
         Mx4Tile w;
-        for (int t = first; ok && tile_at(g, table, t, tiles, w); t += step) {
+        for (int t = first; ok && tile_at(g, table, groups, t, tiles, w); t += step) {
             const int half = w.width / 2;
             const int m0 = w.m0 + int(rank) * 128, n0 = w.n0 + int(rank) * half;
             const uint32_t mine = is_w ? kWBytes : uint32_t(half) * 128;
@@ -323,10 +329,10 @@ __global__ void __launch_bounds__(kThreads, 1) expert_product_mx4(const __grid_c
             const uint64_t s0 = scale_desc(uniform(smem_addr(slots)));
             Mx4Tile w, next;
             bool ready = false;  // the next stage was seen full, with its scales and its accumulator
-            bool more = tile_at(g, table, first, tiles, w);
+            bool more = tile_at(g, table, groups, first, tiles, w);
             for (int t = first; ok && more; t += step, w = next) {
                 next = w;
-                more = tile_at(g, table, t + step, tiles, next);
+                more = tile_at(g, table, groups, t + step, tiles, next);
                 const uint32_t d = tmem + (acc & 1) * kTileRows, n_bits = uint32_t(w.width >> 3) << 17;
                 const bool two = w.width > 128;
                 for (int kb = 0; kb < steps; ++kb) {
@@ -376,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_product_mx4(const __grid_c
         uint32_t phase = 1;
         int part = slot;
         Mx4Tile w;
-        for (int t = first; ok && tile_at(g, table, t, tiles, w); t += step, part -= parts) {
+        for (int t = first; ok && tile_at(g, table, groups, t, tiles, w); t += step, part -= parts) {
             if (part >= parts) continue;
             ScaleRows rows;
             rows.begin = role == 0 ? g.ws : g.xs;
@@ -409,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_product_mx4(const __grid_c
     } else {
         uint32_t acc = 0;
         Mx4Tile w;
-        for (int t = first; tile_at(g, table, t, tiles, w); t += step) {
+        for (int t = first; tile_at(g, table, groups, t, tiles, w); t += step) {
             if (!warp_wait_stages(&sh.acc_full[acc & 1], (acc >> 1) & 1, abort_flag, progress)) break;
             tcgen05_fence_after();
             const uint32_t from = tmem + (uint32_t(warp & 3) << 21) + (acc & 1) * kTileRows;  // lane 32 * (warp % 4)
@@ -445,7 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_product_mx4(const __grid_c
 }
 
 constexpr size_t kMostSmem = 1024 + kStages * size_t(kStageBytes) + kScaleSlots * kSlotBytes + kWriteWarps * kTurnBytes +
-                             (kMaxExperts + 1) * 4;
+                             kMaxExperts * sizeof(Group) + (kMaxExperts + 1) * 4;
 static_assert(kMostSmem <= kMaxDynSmem, "one CTA on an SM");
 
 }  // namespace
@@ -474,6 +480,7 @@ cudaError_t launch_expert_matmul_mx4(const uint8_t* x, const uint8_t* xs, const 
     g.slots = int(slots);
     g.experts = int(experts);
     g.out = int(out);
+    g.across = Divisor32(uint32_t((out + 255) / 256));
     g.bytes = int(in / 2);
     g.blocks = int((in + 31) / 32);
     const uintptr_t at = reinterpret_cast<uintptr_t>(xs) | reinterpret_cast<uintptr_t>(ws) | uintptr_t(g.blocks);

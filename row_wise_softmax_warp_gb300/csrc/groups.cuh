@@ -73,9 +73,13 @@ __device__ __forceinline__ bool find_row_tile(const int32_t* offsets, int expert
 
 // table[e] = row tiles of the experts before e (table[experts]: all), cut at kMostTiles.
 // Called by the whole block, which synchronises before the table is read; scratch: an int a warp.
-template <int TILE, int NT>
+// keep(expert, rows, tiles) is called by the thread that looked the expert's rows up.
+struct KeepNothing {
+    __device__ __forceinline__ void operator()(int, const RowRange&, unsigned) const {}
+};
+template <int TILE, int NT, typename Keep = KeepNothing>
 __device__ __forceinline__ void build_tile_table(const int32_t* offsets, int experts, int slots, int* table,
-                                                 int* scratch) {
+                                                 int* scratch, Keep keep = Keep()) {
     static_assert(TILE > 128, "512 groups of 2^30 rows have to fit the sum");
     constexpr int kPer = (kMaxExperts + NT - 1) / NT;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -84,7 +88,11 @@ __device__ __forceinline__ void build_tile_table(const int32_t* offsets, int exp
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         n[i] = 0;
-        if (i < per && first + i < experts) n[i] = tiles_of(group_rows(offsets, first + i, slots).count, TILE);
+        if (i < per && first + i < experts) {
+            const RowRange r = group_rows(offsets, first + i, slots);
+            n[i] = tiles_of(r.count, TILE);
+            keep(first + i, r, n[i]);
+        }
         sum += n[i];
     }
     unsigned upto = sum;
@@ -119,28 +127,64 @@ __device__ __forceinline__ int tile_expert(const int* table, int experts, int ti
 }
 
 // Groups cut into even tiles for the tcgen05 products: a group of n rows into
-// ceil(n / MOST) tiles of a multiple of 32 rows (the last may be shorter).
+// ceil(n / kMostRows) tiles of a multiple of 32 rows (the last may be shorter).
 constexpr int kMostRows = 256;
 
 struct RowTile {
     int expert, first, count;
 };
 
-// table: build_tile_table<MOST>; 0 <= tile < table[experts], and from as for tile_expert.
-template <int MOST = kMostRows>
+// table: build_tile_table<kMostRows>; 0 <= tile < table[experts], and from as for tile_expert.
 __device__ __forceinline__ RowTile row_tile(const int32_t* offsets, int experts, int slots, const int* table,
                                             int tile, int from) {
     RowTile t;
     t.expert = tile_expert(table, experts, tile, from);
     const RowRange r = group_rows(offsets, t.expert, slots);
-    static_assert(MOST % 32 == 0 && MOST > 128, "even tiles of a multiple of 32 rows are no more than MOST");
-    const int tiles = (r.count + MOST - 1) / MOST;
-    const int each = ((r.count + tiles - 1) / tiles + 31) & ~31;  // at most MOST, and every tile gets a row
+    const int tiles = (r.count + kMostRows - 1) / kMostRows;
+    const int each = ((r.count + tiles - 1) / tiles + 31) & ~31;  // at most kMostRows, and every tile gets a row
     const int at = (tile - table[t.expert]) * each;
     t.first = r.first + at;
     t.count = min(each, r.count - at);
     return t;
 }
+
+// The same from shared memory: what a tile needs of its group is worked out once, by the
+// thread that builds the table, so that a tile is found without a look at memory or a
+// division (a warp alone took 1300 clocks for its first tile, so some 250).
+struct Group {
+    int first, count, each;  // rows, and those of a tile
+};
+template <int MOST>
+struct KeepGroups {
+    static_assert(MOST % 32 == 0 && MOST > 128, "even tiles of a multiple of 32 rows are no more than MOST");
+    Group* groups;
+    __device__ __forceinline__ void operator()(int e, const RowRange& r, unsigned tiles) const {
+        const int n = tiles > 1 ? int((unsigned(r.count) + tiles - 1) / tiles) : r.count;
+        groups[e] = {r.first, r.count, (n + 31) & ~31};
+    }
+};
+// table: build_tile_table<MOST> with KeepGroups<MOST>
+__device__ __forceinline__ RowTile kept_row_tile(const Group* groups, int experts, const int* table, int tile, int from) {
+    RowTile t;
+    t.expert = tile_expert(table, experts, tile, from);
+    const Group r = groups[t.expert];
+    const int at = (tile - table[t.expert]) * r.each;
+    t.first = r.first + at;
+    t.count = min(r.each, r.count - at);
+    return t;
+}
+
+// n / d for 0 <= n < 2^31 by a product (Granlund, Montgomery: Division by invariant integers
+// using multiplication, PLDI 1994).
+struct Divisor32 {
+    uint32_t d, m;
+    int shift;
+    __host__ __device__ explicit Divisor32(uint32_t by = 1) : d(by), m(0), shift(0) {
+        while ((uint64_t(1) << shift) < d) ++shift;
+        m = uint32_t((((uint64_t(1) << shift) - d) << 32) / d + 1);
+    }
+    __device__ __forceinline__ uint32_t quotient(uint32_t n) const { return (__umulhi(m, n) + n) >> shift; }
+};
 
 // Host: the most row tiles that groups of `slots` rows in all can have.
 inline int64_t most_row_tiles(int64_t slots, int64_t experts, int most = kMostRows) {
