@@ -16,13 +16,14 @@
 // the 512 columns of tensor memory; with 256 tokens a tile there would be no room for
 // the scales, or for the second accumulator that hides the write-out.
 //
-// What bounds it: 16384 x 4096 -> 4096 takes 107 to 111 us (4950 to 5140 TFLOP/s; the bf16
+// What bounds it: 16384 x 4096 -> 4096 takes 103 to 106 us (5200 to 5350 TFLOP/s; the bf16
 // product 299).  Variants that leave work out: products alone 66 us, copies alone 73 (16
 // TB/s from the L2, near what the SMs take), both without scales 90, with scales that are
 // written but not loaded 96.  So it is the L2's bandwidth that the operands share with the
 // scales (9% of their bytes: a tile's 256 columns and, in both CTAs, its rows) and the
-// results.  A single tile takes 6.8 us with its launch (5.5 where nothing is loaded or
-// written), 64 experts of 768 x 2048 with 8192 rows 24 us against 14 of HBM traffic.
+// results.  A single tile takes 5.5 us with its launch, 64 experts of 768 x 2048 with 8192
+// rows 21 us against 14 of HBM traffic, with 32 rows 8.9 against 3.2.  Four sets of scale
+// warps, or fewer rows a tile and more stages, are no faster; two sets take 7% longer.
 // Scales written stage by stage took 256 us: every hand-over to the other CTA has a fence
 // that a thread's loads, stores and a cluster-wide release wait for, so one hand-over
 // serves four stages, three sets of warps take turns, and loads follow it.
@@ -422,19 +423,21 @@ __global__ void __launch_bounds__(kThreads, 1) expert_product_mx4(const __grid_c
             const int m = w.m0 + int(rank) * 128 + (warp & 3) * 32;
             O* p = static_cast<O*>(g.y) + int64_t(w.n0) * g.out + m;
             constexpr int kStep = kWriteWarps / 4 * 32;
+            // An arrival that nothing waits for could reach a CTA that has left.
+            const bool again = t < tiles - 2 * step;
             int c = warp / 4 * 32;
             for (; c < w.n; c += kStep) {
                 uint32_t r[32];
                 tmem_load32(from + uint32_t(c), r);
                 tmem_wait_load(r);
-                if (c + kStep >= w.n) {
+                if (c + kStep >= w.n && again) {
                     tcgen05_fence_before();
                     __syncwarp();
                     elect_arrive_pair(map_to_rank(&sh.acc_empty[acc & 1], 0));
                 }
                 write_block(turn + warp * kTurnBytes, p + int64_t(c) * g.out, g.out, w.n - c, g.out - m, g.vec, r);
             }
-            if (warp / 4 * 32 >= w.n) {  // nothing here for the second warp
+            if (warp / 4 * 32 >= w.n && again) {  // nothing here for the second warp
                 __syncwarp();
                 elect_arrive_pair(map_to_rank(&sh.acc_empty[acc & 1], 0));
             }
@@ -445,7 +448,11 @@ __global__ void __launch_bounds__(kThreads, 1) expert_product_mx4(const __grid_c
     if (*abort_flag) let_copies_land();
     tcgen05_fence_before();
     __syncthreads();
-    cluster_sync_all();  // no CTA leaves, or frees tensor memory, while the other still uses it
+    if (*abort_flag) cluster_sync_all();
+    else {
+        cluster_arrive_relaxed();
+        cluster_wait();
+    }
     tcgen05_fence_after();
     if (warp == kProductWarp) tmem_dealloc_pair(tmem, kTmemColumns);
 }
