@@ -175,8 +175,7 @@ struct ScaleRows {
             } else {
                 const int off = int(reinterpret_cast<uintptr_t>(at) & 3);
                 uint32_t word[2 * kAhead + 1];
-#pragma unroll
-                for (int i = 0; i <= 2 * kAhead; ++i) word[i] = 4 * i < left + off ? word_at(at - off + 4 * i, begin, end) : 0;
+                words_at(at - off, begin, end, word);
 #pragma unroll
                 for (int i = 0; i < 2 * kAhead; ++i) {
                     const int there = left - 4 * i;  // the next row's scales are not this one's: 0 times NaN is NaN

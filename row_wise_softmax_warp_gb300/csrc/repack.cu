@@ -54,9 +54,7 @@ __global__ void __launch_bounds__(kRepackThreads) repack(const RepackArgs g) {
             uint32_t w[U][5];
 #pragma unroll
             for (int u = 0; u < U; ++u)
-                if (c0 + u * 512 < j.row_bytes)
-#pragma unroll
-                    for (int i = 0; i < 5; ++i) w[u][i] = word_at(from + c0 + u * 512 + 4 * i, begin, end);
+                if (c0 + u * 512 < j.row_bytes) words_at(from + c0 + u * 512, begin, end, w[u]);
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 if (c0 + u * 512 >= j.row_bytes) break;
