@@ -2,9 +2,9 @@
 // boundaries, so that TMA can read them (an in-width of 773 values of 2 bytes, say).
 //
 // A warp takes a row; a lane makes 16 bytes of the copy from five aligned 4-byte
-// words, shifted together.  Bound by HBM: every byte is read and written once (8 experts of 2003 x
-// 1001 fp16 and 8192 rows of 1001: 97 MB in about 23 us with its launch).  What lies between a
-// row's end and the next boundary is whatever the source holds there; the tensor
+// words, shifted together.  Bound by HBM: every byte is read and written once (8 experts of
+// 2003 x 1001 fp16 and 8192 rows of 1001, 97 MB: some 18 us of the product's 52).  What lies
+// between a row's end and the next boundary is whatever the source holds there; the tensor
 // map over the copy ends at the row's true width.
 #include "bytes.cuh"
 #include "groups.cuh"
@@ -19,6 +19,8 @@ constexpr int kRepackThreads = 256;
 // no expert needs costs little then), one where each is a wait of its own.  The product
 // with its copies, four against one row a warp: 3606 rows 17.8 and 15.8 us, 24216 56.5 and
 // 55.8, 41280 53.3 and 54.1; 2 rows of x and 64 experts, 33090 16.5 and 20.6, 128194 27.1 and 56.0.
+// Of rows of one piece of 512 bytes two are on their way together (4-bit products of 65536 x
+// 514, with two 60.7, one or four 65 us; 64 experts of 770 -> 2048 with 8192 rows 56 and 67).
 constexpr int kRepackRows = 4;
 constexpr int64_t kManyRows = 32768;
 
@@ -29,39 +31,53 @@ struct RepackArgs {
     int each;  // rows of a warp
 };
 
+// Rows R at a time, of which U pieces of 512 bytes are on their way together.
+template <int R, int U>
 __global__ void __launch_bounds__(kRepackThreads) repack(const RepackArgs g) {
+    static_assert(R == 1 || U == 1, "rows of several pieces are taken one at a time");
     let_next_start();
     wait_for_earlier();
     const int lane = threadIdx.x & 31;
     const int64_t first = (int64_t(blockIdx.x) * (kRepackThreads / 32) + (threadIdx.x >> 5)) * g.each;
-    for (int64_t r = first; r < first + g.each; ++r) {
-        const bool second = r >= g.job[0].rows;
-        const RepackJob& j = g.job[second];
-        const int64_t row = second ? r - g.job[0].rows : r;
-        if (row >= j.rows) return;
-        // a matrix of weights whose expert has no rows is not read later either
-        if (j.rows_per_expert > 0 && g.offsets != nullptr &&
-            group_rows(g.offsets, int(row / j.rows_per_expert), g.slots).count == 0)
-            continue;
-        const uint8_t* begin = static_cast<const uint8_t*>(j.src);
-        const uint8_t* end = begin + j.rows * j.row_bytes;
-        const uint8_t* from = begin + row * j.row_bytes;
-        const int off = int(reinterpret_cast<uintptr_t>(from) & 3);
-        from -= off;
-        uint8_t* to = static_cast<uint8_t*>(j.dst) + row * repack_pitch(j.row_bytes);
-        constexpr int U = 4;
-        for (int64_t c0 = lane * 16; c0 < j.row_bytes; c0 += U * 512) {
-            uint32_t w[U][5];
+    for (int64_t r = first; r < first + g.each; r += R) {
+        const uint8_t *from[R], *begin[R], *end[R];
+        uint8_t* to[R];
+        int off[R];
+        int64_t bytes[R];  // 0: no such row, or not wanted
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (c0 + u * 512 < j.row_bytes) words_at(from + c0 + u * 512, begin, end, w[u]);
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                if (c0 + u * 512 >= j.row_bytes) break;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) w[u][i] = __funnelshift_r(w[u][i], w[u][i + 1], 8 * off);
-                *reinterpret_cast<uint4*>(to + c0 + u * 512) = make_uint4(w[u][0], w[u][1], w[u][2], w[u][3]);
+        for (int n = 0; n < R; ++n) {
+            const bool second = r + n >= g.job[0].rows;
+            const RepackJob j = second ? g.job[1] : g.job[0];
+            const int64_t row = second ? r + n - g.job[0].rows : r + n;
+            bytes[n] = row < j.rows ? j.row_bytes : 0;
+            // a matrix of weights whose expert has no rows is not read later either
+            if (bytes[n] != 0 && j.rows_per_expert > 0 && g.offsets != nullptr) {
+                const int e = row <= UINT32_MAX ? int(uint32_t(row) / uint32_t(j.rows_per_expert)) : int(row / j.rows_per_expert);
+                if (group_rows(g.offsets, e, g.slots).count == 0) bytes[n] = 0;
             }
+            begin[n] = static_cast<const uint8_t*>(j.src);
+            end[n] = begin[n] + j.rows * j.row_bytes;
+            from[n] = begin[n] + row * j.row_bytes;
+            off[n] = int(reinterpret_cast<uintptr_t>(from[n]) & 3);
+            to[n] = static_cast<uint8_t*>(j.dst) + row * repack_pitch(j.row_bytes);
+        }
+        for (int64_t c0 = lane * 16; c0 < (R == 1 ? bytes[0] : 512); c0 += U * 512) {
+            uint32_t w[R][U][5];
+#pragma unroll
+            for (int n = 0; n < R; ++n)
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (c0 + u * 512 < bytes[n]) words_at(from[n] - off[n] + c0 + u * 512, begin[n], end[n], w[n][u]);
+#pragma unroll
+            for (int n = 0; n < R; ++n)
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    if (c0 + u * 512 >= bytes[n]) break;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) w[n][u][i] = __funnelshift_r(w[n][u][i], w[n][u][i + 1], 8 * off[n]);
+                    *reinterpret_cast<uint4*>(to[n] + c0 + u * 512) =
+                        make_uint4(w[n][u][0], w[n][u][1], w[n][u][2], w[n][u][3]);
+                }
         }
     }
 }
@@ -89,7 +105,10 @@ cudaError_t launch_repack(const RepackJob* jobs, int n, const int32_t* offsets, 
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = early ? 1 : 0;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, repack, g);
+    const bool narrow = jobs[0].row_bytes <= 512 && jobs[n - 1].row_bytes <= 512;
+    const cudaError_t e = !narrow            ? cudaLaunchKernelEx(&cfg, repack<1, 4>, g)
+                          : g.each == 1      ? cudaLaunchKernelEx(&cfg, repack<1, 1>, g)
+                                             : cudaLaunchKernelEx(&cfg, repack<2, 1>, g);
     note_launches(1);
     return e;
 }
