@@ -119,6 +119,29 @@ def test_product_off_a_boundary(ro, widths, shift):
     check(y, x64, w64, offsets, "f32")
 
 
+@pytest.mark.parametrize("shift", [0, 3])
+def test_many_short_odd_rows(ro, shift):
+    """More than 2^15 rows of 35 and of 66 bytes, which are copied to 16-byte boundaries; an expert between has none."""
+    sizes, cout = [9, 0, 31], 12501
+    args, x64, w64 = operands(ro, np.random.default_rng(11), sizes, 70, cout, 0)
+    at = torch.from_numpy(offsets_of(sizes)).cuda()
+
+    def moved(t):
+        buf = torch.zeros(t.numel() + 16, dtype=t.dtype, device="cuda")
+        buf[shift:shift + t.numel()] = t.reshape(-1)
+        return buf[shift:shift + t.numel()].view(t.shape)
+
+    y = ro.rowops_expert_matmul_mx4(*(moved(t) for t in args), at, dtype=torch.float32)
+    check(y, x64, w64, offsets_of(sizes), "f32")
+    g = torch.Generator(device="cuda").manual_seed(12)
+    x = moved(torch.randint(-2, 3, (40, 33), generator=g, device="cuda").half())
+    w = moved(torch.randint(-2, 3, (3, cout, 33), generator=g, device="cuda").half())
+    y = ro.rowops_expert_matmul(x, w, at)  # of whole numbers below 2^11: exact
+    for e, rows in ((0, slice(0, 9)), (2, slice(9, 40))):
+        assert torch.equal(y[rows].double(), x[rows].double() @ w[e].double().T)
+    assert ro.library().rowops_pipeline_timeouts() == 0
+
+
 @pytest.mark.parametrize("widths", [(1056, 384), (4096, 256), (2050, 131)])
 def test_product_long(ro, widths):
     cin, cout = widths
