@@ -19,24 +19,17 @@ __device__ __forceinline__ uint32_t part_of_word(const uint8_t* at, const uint8_
 }
 template <int N>
 __device__ __forceinline__ void words_at(const uint8_t* at, const uint8_t* begin, const uint8_t* end, uint32_t (&w)[N]) {
+    const int64_t there = end - at;
+    const int whole = there >= 4 * N ? N : there > 0 ? int(there) >> 2 : 0;
+    const bool front = at >= begin;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const uint8_t* p = at + 4 * i;
-        w[i] = p >= begin && p + 4 <= end ? *reinterpret_cast<const uint32_t*>(p) : 0;
-    }
-    if (at < begin) {
-        const uint8_t* first = begin - (reinterpret_cast<uintptr_t>(begin) & 3);
-        const uint32_t part = part_of_word(first, begin, end);
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-            if (at + 4 * i == first) w[i] = part;
-    }
-    const uint8_t* last = end - (reinterpret_cast<uintptr_t>(end) & 3);
-    if (last < end && at + 4 * N > last) {
-        const uint32_t part = part_of_word(last, begin, end);
+    for (int i = 0; i < N; ++i) w[i] = i < whole && (i > 0 || front) ? reinterpret_cast<const uint32_t*>(at)[i] : 0;
+    if (!front || whole < N) {
+        const uint32_t last = part_of_word(at + 4 * whole, begin, end);
 #pragma unroll
         for (int i = 0; i < N; ++i)
-            if (at + 4 * i == last) w[i] = part;
+            if (i == whole) w[i] = last;
+        if (!front) w[0] = part_of_word(at, begin, end);
     }
 }
 

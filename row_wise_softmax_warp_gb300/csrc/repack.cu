@@ -3,7 +3,7 @@
 //
 // A warp takes a row; a lane makes 16 bytes of the copy from five aligned 4-byte
 // words, shifted together.  Bound by HBM: every byte is read and written once (8 experts of
-// 2003 x 1001 fp16 and 8192 rows of 1001, 97 MB: some 18 us of the product's 52).  What lies
+// 2003 x 1001 fp16 and 8192 rows of 1001, 97 MB: some 16 us of the product's 50).  What lies
 // between a row's end and the next boundary is whatever the source holds there; the tensor
 // map over the copy ends at the row's true width.
 #include "bytes.cuh"
@@ -20,7 +20,7 @@ constexpr int kRepackThreads = 256;
 // with its copies, four against one row a warp: 3606 rows 17.8 and 15.8 us, 24216 56.5 and
 // 55.8, 41280 53.3 and 54.1; 2 rows of x and 64 experts, 33090 16.5 and 20.6, 128194 27.1 and 56.0.
 // Of rows of one piece of 512 bytes two are on their way together (4-bit products of 65536 x
-// 514, with two 60.7, one or four 65 us; 64 experts of 770 -> 2048 with 8192 rows 56 and 67).
+// 514, with two 61, one or four 65 us; 64 experts of 770 -> 2048 with 8192 rows 56 and 67).
 constexpr int kRepackRows = 4;
 constexpr int64_t kManyRows = 32768;
 
