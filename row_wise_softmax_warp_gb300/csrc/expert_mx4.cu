@@ -17,11 +17,11 @@
 // the scales, or for the second accumulator that hides the write-out.
 //
 // What bounds it: 16384 x 4096 -> 4096 takes 103 to 106 us (5200 to 5350 TFLOP/s; the bf16
-// product 299).  Variants that leave work out: products alone 66 us, copies alone 73 (16
-// TB/s from the L2, near what the SMs take), both without scales 90, with scales that are
-// written but not loaded 96.  So it is the L2's bandwidth that the operands share with the
-// scales (9% of their bytes: a tile's 256 columns and, in both CTAs, its rows) and the
-// results.  A single tile takes 5.5 us with its launch, 64 experts of 768 x 2048 with 8192
+// product 299).  Variants that leave work out, when all of it took 107: products alone 66 us,
+// copies alone 73 (16 TB/s from the L2, 52 bytes a clock into an SM), both without scales 90,
+// with scales that are written but not loaded 96.  So it is what an SM takes in: operands,
+// scales (9% of their bytes: a tile's 256 columns and, in both CTAs, its rows), and the hand-
+// over of the latter.  A single tile takes 5.5 us with its launch, 64 experts of 768 x 2048 with 8192
 // rows 21 us against 14 of HBM traffic, with 32 rows 8.9 against 3.2.  Four sets of scale
 // warps, or fewer rows a tile and more stages, are no faster; two sets take 7% longer.
 // Scales written stage by stage took 256 us: every hand-over to the other CTA has a fence
