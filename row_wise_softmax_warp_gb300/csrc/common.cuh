@@ -36,6 +36,18 @@ __device__ __forceinline__ float exp_shifted(float x, float m) {
     return ex2_approx((x - m) * kLog2e);
 }
 
+// n / d for 0 <= n < 2^31 by a product (Granlund, Montgomery: Division by invariant integers
+// using multiplication, PLDI 1994).
+struct Divisor32 {
+    uint32_t d, m;
+    int shift;
+    __host__ __device__ explicit Divisor32(uint32_t by = 1) : d(by), m(0), shift(0) {
+        while ((uint64_t(1) << shift) < d) ++shift;
+        m = uint32_t((((uint64_t(1) << shift) - d) << 32) / d + 1);
+    }
+    __device__ __forceinline__ uint32_t quotient(uint32_t n) const { return (__umulhi(m, n) + n) >> shift; }
+};
+
 // Programmatic dependents.  A kernel that lets the next one start early says so at its
 // beginning; one that is launched so waits, before it touches what others wrote, for
 // everything before it in the stream to end.

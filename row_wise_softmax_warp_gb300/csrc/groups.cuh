@@ -174,18 +174,6 @@ __device__ __forceinline__ RowTile kept_row_tile(const Group* groups, int expert
     return t;
 }
 
-// n / d for 0 <= n < 2^31 by a product (Granlund, Montgomery: Division by invariant integers
-// using multiplication, PLDI 1994).
-struct Divisor32 {
-    uint32_t d, m;
-    int shift;
-    __host__ __device__ explicit Divisor32(uint32_t by = 1) : d(by), m(0), shift(0) {
-        while ((uint64_t(1) << shift) < d) ++shift;
-        m = uint32_t((((uint64_t(1) << shift) - d) << 32) / d + 1);
-    }
-    __device__ __forceinline__ uint32_t quotient(uint32_t n) const { return (__umulhi(m, n) + n) >> shift; }
-};
-
 // Host: the most row tiles that groups of `slots` rows in all can have.
 inline int64_t most_row_tiles(int64_t slots, int64_t experts, int most = kMostRows) {
     return slots / most + (experts < slots ? experts : slots);

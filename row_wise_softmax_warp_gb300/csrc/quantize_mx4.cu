@@ -5,8 +5,10 @@
 // a block.  Where rows are whole blocks the matrix is one run of chunks of eight values,
 // of which a thread has four on their way (16384 x 4096 bf16: 27 us, 6.2 TB/s; one at a
 // time 49, eight 36), and the maximum of 16-bit values is taken on their bits, two at a
-// time.  Rows of other lengths are read value by value where they are no multiple of 8
-// (16384 x 1001: 24 us, x 1000: 15).
+// time.  Other rows are a run of chunks too, with the last block's filled up to four
+// (16384 x 1000: 10.3 us with four on their way, 12.8 with one); chunks that start anywhere
+// come by words and go by bytes (x 1001: 16.9 us with two, 17.9 with one, 18.4 with four).
+#include "bytes.cuh"
 #include "eight.cuh"
 #include "quant.cuh"
 
@@ -58,31 +60,88 @@ __global__ void __launch_bounds__(THREADS)
     }
 }
 
-constexpr int kMxThreads = 256;
-
 struct Mx4Args {
     const void* x;
     uint8_t* q;
     uint8_t* scale;
     int64_t rows;
-    int cols, units;
-    int64_t items;  // units of all rows
+    int cols;
+    Divisor32 across;  // chunks of a row, filled up to whole blocks of four
 };
 
-// Other rows, a warp 256 columns.
-template <typename T, bool VEC>
-__global__ void __launch_bounds__(kMxThreads) quantize_mx4_rows(const Mx4Args a) {
+// Eight values that start anywhere, of which the first `left` are there.
+template <typename T>
+__device__ __forceinline__ void load_anywhere(Held<T, 32, true>& x, const T* from, int left, const T* begin, const T* end) {
+    if constexpr (sizeof(T) == 4) {
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = i < left ? __float_as_uint(__ldcs(reinterpret_cast<const float*>(from) + i)) : 0;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) x.c[h] = make_uint4(w[4 * h], w[4 * h + 1], w[4 * h + 2], w[4 * h + 3]);
+    } else {
+        const uint8_t* at = reinterpret_cast<const uint8_t*>(from);
+        const int off = int(reinterpret_cast<uintptr_t>(at) & 2);
+        uint32_t w[5];
+        words_at(at - off, reinterpret_cast<const uint8_t*>(begin), reinterpret_cast<const uint8_t*>(end), w);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            w[i] = __funnelshift_r(w[i], w[i + 1], 8 * off);
+            if (2 * i + 1 >= left) w[i] &= 2 * i < left ? 0xffffu : 0u;  // the next row's
+        }
+        x.c[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
+// Other rows: chunks of eight columns, filled up to whole blocks in every row, ITEMS a
+// thread.  VEC: rows are whole chunks on 16-byte boundaries; others start anywhere.
+template <typename T, bool VEC, int ITEMS, int THREADS>
+__global__ void __launch_bounds__(THREADS) quantize_mx4_rows(const Mx4Args a) {
     let_next_start();
-    const int lane = threadIdx.x & 31;
-    const int64_t step = int64_t(gridDim.x) * (kMxThreads / 32);
-    for (int64_t item = int64_t(blockIdx.x) * (kMxThreads / 32) + (threadIdx.x >> 5); item < a.items; item += step) {
-        const int64_t row = item / a.units;
-        const int base = int(item - row * a.units) * 256;
-        Held<T, 32, VEC> x;
-        x.load(static_cast<const T*>(a.x), Place<32, VEC>(row, a.cols, base, lane, a.cols));
+    const T* x = static_cast<const T*>(a.x);
+    const int64_t block = int64_t(blockIdx.x) * (THREADS * ITEMS);
+    const int64_t row0 = block <= UINT32_MAX ? int64_t(uint32_t(block) / a.across.d) : block / a.across.d;
+    const uint32_t in_row = uint32_t(block - row0 * a.across.d) + threadIdx.x;
+    // the n-th chunk's row, its place there and how many of its values there are
+    const auto place = [&](int n, int64_t& row, int& chunk) {
+        const uint32_t at = in_row + n * THREADS, down = a.across.quotient(at);
+        row = row0 + down;
+        chunk = int(at - down * a.across.d);
+        return row < a.rows ? min(a.cols - 8 * chunk, 8) : 0;
+    };
+    Held<T, 32, true> in[ITEMS];
+#pragma unroll
+    for (int n = 0; n < ITEMS; ++n) {
+        int64_t row;
+        int chunk;
+        const int left = place(n, row, chunk);
+        if constexpr (VEC) {
+            in[n].load(x, Place<32, true>(row, a.cols, 8 * chunk, 0, left > 0 ? a.cols : 0));
+        } else {
+#pragma unroll
+            for (auto& c : in[n].c) c = make_uint4(0, 0, 0, 0);
+            if (left > 0) load_anywhere(in[n], x + row * a.cols + 8 * chunk, left, x, x + a.rows * a.cols);
+        }
+    }
+#pragma unroll
+    for (int n = 0; n < ITEMS; ++n) {
+        const uint32_t code = mx4_code(most_of<T>(in[n]));
         float2 v[4];
-        x.get(v);
-        store_mx4<32, VEC>(a.q + row * ((a.cols + 1) / 2), a.scale + row * ((a.cols + 31) / 32), base, lane, a.cols, v);
+        in[n].get(v);
+        const uint32_t q = mx4_eight(v, code);
+        int64_t row;
+        int chunk;
+        const int left = place(n, row, chunk);
+        if (left > 0) {
+            uint8_t* to = a.q + row * ((a.cols + 1) / 2) + 4 * chunk;
+            if constexpr (VEC) {
+                *reinterpret_cast<uint32_t*>(to) = q;
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (2 * i < left) to[i] = uint8_t(q >> (8 * i));
+            }
+            if (chunk % 4 == 0) a.scale[row * ((a.cols + 31) / 32) + chunk / 4] = uint8_t(code);
+        }
     }
 }
 
@@ -91,25 +150,21 @@ __global__ void __launch_bounds__(kMxThreads) quantize_mx4_rows(const Mx4Args a)
 cudaError_t launch_quantize_mx4(const void* x, uint8_t* q, uint8_t* scale, int64_t rows, int64_t cols, int x_type,
                                 cudaStream_t stream) {
     const bool vec = cols % 8 == 0 && reinterpret_cast<uintptr_t>(x) % 16 == 0 && reinterpret_cast<uintptr_t>(q) % 4 == 0;
+    const bool run = vec && cols % 32 == 0;
+    const int64_t across = run ? cols / 8 : (cols + 31) / 32 * 4, chunks = rows * across;
+    const Mx4Args a{x, q, scale, rows, int(cols), Divisor32(uint32_t(across))};
+    const bool few = chunks < 2048 * int64_t(sm_count());
+    auto grid = [&](int per) { return unsigned((chunks + per - 1) / per); };
     with_type(x_type, [&](auto t) {
         using T = decltype(t);
-        if (vec && cols % 32 == 0) {
-            const int64_t chunks = rows * cols / 8;
-            auto go = [&](auto kernel, int per, int threads) {
-                kernel<<<unsigned((chunks + per - 1) / per), threads, 0, stream>>>(
-                    static_cast<const T*>(x), reinterpret_cast<uint32_t*>(q), scale, chunks);
-            };
-            const bool few = chunks < 2048 * int64_t(sm_count());
-            if (few) go(quantize_mx4_run<T, 1, 128>, 128, 128);
-            else go(quantize_mx4_run<T, 4, 256>, 4 * 256, 256);
-        } else {
-            Mx4Args a{x, q, scale, rows, int(cols), int((cols + 255) / 256), 0};
-            a.items = rows * a.units;
-            const int64_t blocks = (a.items + kMxThreads / 32 - 1) / (kMxThreads / 32), most = int64_t(1) << 20;
-            const unsigned grid = unsigned(blocks < most ? blocks : most);
-            if (vec) quantize_mx4_rows<T, true><<<grid, kMxThreads, 0, stream>>>(a);
-            else quantize_mx4_rows<T, false><<<grid, kMxThreads, 0, stream>>>(a);
-        }
+        const T* from = static_cast<const T*>(x);
+        uint32_t* words = reinterpret_cast<uint32_t*>(q);
+        if (run && few) quantize_mx4_run<T, 1, 128><<<grid(128), 128, 0, stream>>>(from, words, scale, chunks);
+        else if (run) quantize_mx4_run<T, 4, 256><<<grid(4 * 256), 256, 0, stream>>>(from, words, scale, chunks);
+        else if (vec && few) quantize_mx4_rows<T, true, 1, 128><<<grid(128), 128, 0, stream>>>(a);
+        else if (vec) quantize_mx4_rows<T, true, 4, 256><<<grid(4 * 256), 256, 0, stream>>>(a);
+        else if (few) quantize_mx4_rows<T, false, 1, 128><<<grid(128), 128, 0, stream>>>(a);
+        else quantize_mx4_rows<T, false, 2, 256><<<grid(2 * 256), 256, 0, stream>>>(a);
     });
     note_launches(1);
     return cudaGetLastError();

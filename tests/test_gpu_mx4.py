@@ -53,6 +53,22 @@ def test_quantize_odd_values(ro, cols):
     assert q.shape == (0, (cols + 1) // 2)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("rows,cols", [(4001, 777), (3999, 1000), (70001, 40), (90001, 33), (1200001, 3), (3, 3000001)])
+def test_quantize_many_odd_rows(ro, rows, cols, dtype):
+    """Long runs of rows that are no whole blocks give what the same rows filled up with zeros give."""
+    g = torch.Generator(device="cuda").manual_seed(cols)
+    full = torch.zeros(rows, (cols + 31) // 32 * 32, dtype=TYPES[dtype], device="cuda")
+    full[:, :cols] = torch.randn(rows, cols, generator=g, device="cuda")
+    want, code = ro.rowops_quantize_mx4(full)
+    for shift in (0, 1):
+        buf = torch.full((rows * cols + 16,), float("nan"), dtype=TYPES[dtype], device="cuda")
+        x = buf[shift:shift + rows * cols].view(rows, cols)
+        x.copy_(full[:, :cols])
+        q, scale = ro.rowops_quantize_mx4(x)
+        assert torch.equal(q, want[:, :(cols + 1) // 2]) and torch.equal(scale, code)
+
+
 def operands(ro, g, sizes, cin, cout, extra):
     rows = sum(sizes)
     x = np.concatenate([g.normal(size=(rows, cin)), np.full((extra, cin), np.nan)])
