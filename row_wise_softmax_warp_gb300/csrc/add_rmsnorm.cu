@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_long(const AddNormArgs a) {
     int turn = 0;
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
         float2 squares = both(0.f);
-#pragma unroll 2
+#pragma unroll VEC ? 2 : 1
         for (int64_t u = w; u < units; u += 32) {
             Sum<T, R, 32, VEC> in;
             float2 h[4];
@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_long(const AddNormArgs a) {
         const float rms = sqrtf(sum_of_row<32>(squares.x + squares.y, scratch[turn], 32, 0, w) * inv_cols + a.eps);
         if (a.row_rms && threadIdx.x == 0) a.row_rms[row] = rms;
         const float inv = 1.0f / rms;
-#pragma unroll 2
+#pragma unroll VEC ? 2 : 1
         for (int64_t u = w; u < units; u += 32) {
             const int base = int(u * 256);
             const Place<32, VEC> o(row, a.cols, base, lane, a.cols);

@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_bwd_long(const AddNormBwdArg
             return o;
         };
         float2 dots = both(0.f);
-#pragma unroll 2
+#pragma unroll VEC ? 2 : 1
         for (int64_t u = w; u < units; u += 32) {
             Held<T, 32, VEC> dy;
             Held<R, 32, VEC> h;
@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_bwd_long(const AddNormBwdArg
             factors<T, R, 32, VEC>(dy, h, gamma, inv, gy, n, dots, none);
         }
         const float mean = sum_of_row<32>(dots.x + dots.y, scratch[turn], 32, 0, w) * inv_cols;
-#pragma unroll 2
+#pragma unroll VEC ? 2 : 1
         for (int64_t u = w; u < units; u += 32) {
             const int base = int(u * 256);
             Held<T, 32, VEC> dy;
