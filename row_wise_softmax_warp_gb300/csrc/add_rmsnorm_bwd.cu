@@ -8,11 +8,15 @@
 // written once (16384 x 4096, bf16 and an fp32 stream, with dropout: 170 us, 6.3 TB/s; all
 // bf16: 103 us, 5.2 TB/s); a warp takes 271 instructions for a row's 256 columns with dropout.
 //
-// A row lies in the registers of a group of lanes or of up to 32 warps, which walk over
-// rows and keep their columns' part of dgamma in registers; a block adds its sets of
+// A row lies in the registers of a group of lanes, of up to 16 warps, or of a cluster's CTAs
+// (SPREAD below), which walk over rows and keep their columns' part of dgamma in registers;
+// a block adds its sets of
 // warps up in order and writes one row of partial sums, and a second launch adds those,
 // all in an order that only the sizes, the alignment and the device decide.
+#include <atomic>
+
 #include "eight.cuh"
+#include "pipeline.cuh"
 
 namespace rowops {
 namespace {
@@ -31,6 +35,7 @@ struct AddNormBwdArgs {
     int cols;
     RowSplit split;
     bool wide;  // long rows: the sums fit in shared memory
+    int spread, span;  // CTAs of a cluster that share a row, and columns of each
 };
 
 // g and n of eight columns; adds to their products and to dgamma.
@@ -76,21 +81,60 @@ constexpr int kStages = 2;
 template <typename T, typename R>
 constexpr int kPlaces = Held<T, 32, true>::kChunks + 2 * Held<R, 32, true>::kChunks;  // of 16 bytes, a row
 
-template <typename T, typename R, int LANES, int NV, bool VEC, int THREADS>
+// SPREAD: the CTAs of a cluster share a row.  Each warp writes its part of the row's sum to
+// every CTA, whose barrier counts the bytes (arrivals with a release would wait for the
+// results' stores, row after row), and every warp adds all parts in the same order.  A CTA
+// is at most a row ahead of another: what it writes two rows later was read by then.
+// Against one block a row, which reads dy and h twice: 4096 x 16384 bf16 121 and 184 us, 2048 x
+// 32768 with an fp32 stream 173 and 273, 4096 x 10000 110 and 194, 3 x 12064 fp32 6.1 and 15.7.
+constexpr int kMostSpread = 8;
+template <bool SPREAD>
+struct SpreadSums {
+    float sums[2][kMostSpread * 16];
+    uint64_t bar[2];
+    int abort;
+};
+template <>
+struct SpreadSums<false> {};
+
+__device__ __forceinline__ void spread_part(float v, float* at, uint64_t* bar, uint32_t rank) {
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.f32 [%0], %1, [%2];\n" ::"r"(map_to_rank(at, rank)),
+                 "f"(v), "r"(map_to_rank(bar, rank))
+                 : "memory");
+}
+
+template <typename T, typename R, int LANES, int NV, bool VEC, int THREADS, bool SPREAD = false>
 __global__ void __launch_bounds__(THREADS, VEC ? 512 / THREADS : 2) add_rmsnorm_bwd_rows(const AddNormBwdArgs a) {
     extern __shared__ __align__(16) float shared[];  // the places; afterwards sums of a.split.warps * NV * 256 columns
     __shared__ float scratch[2][32];
+    __shared__ SpreadSums<SPREAD> all;
     let_next_start();
+    // this CTA's columns, and its row among the clusters'
+    int begin_col = 0, end_col = a.cols, group = blockIdx.x, groups = gridDim.x;
+    if constexpr (SPREAD) {
+        begin_col = int(cluster_rank()) * a.span;
+        end_col = min(a.cols, begin_col + a.span);
+        group = blockIdx.x / a.spread;
+        groups = gridDim.x / a.spread;
+        if (threadIdx.x == 0) {
+            mbar_init(&all.bar[0], 1);
+            mbar_init(&all.bar[1], 1);
+            all.abort = 0;
+            asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+        }
+        cluster_arrive_relaxed();
+        cluster_wait();
+    }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int slot = warp / a.split.warps, w = warp % a.split.warps, g = lane % LANES;
     constexpr int kGroups = 32 / LANES;
     const float inv_cols = 1.0f / float(a.cols);
     const Masker masker(a.drop);
-    const auto base_of = [&](int k) { return (k * a.split.warps + w) * 256; };
+    const auto base_of = [&](int k) { return begin_col + (k * a.split.warps + w) * 256; };
     float2 gamma[NV][4], dgamma[NV][4];
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-        load_weights<LANES, VEC>(a.gamma, Place<LANES, VEC>(0, 0, base_of(k), g, a.cols), gamma[k]);
+        load_weights<LANES, VEC>(a.gamma, Place<LANES, VEC>(0, 0, base_of(k), g, end_col), gamma[k]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) dgamma[k][i] = both(0.f);
     }
@@ -99,14 +143,14 @@ __global__ void __launch_bounds__(THREADS, VEC ? 512 / THREADS : 2) add_rmsnorm_
     using HeldR = Held<R, LANES, VEC>;
     const uint32_t step = blockDim.x * 16;  // from place to place
     const uint32_t places = uint32_t(__cvta_generic_to_shared(shared)) + threadIdx.x * 16;
-    const int64_t first = (int64_t(blockIdx.x) * a.split.slots + slot) * kGroups;
-    const int64_t stride = int64_t(gridDim.x) * a.split.slots * kGroups;
+    const int64_t first = (int64_t(group) * a.split.slots + slot) * kGroups;
+    const int64_t stride = int64_t(groups) * a.split.slots * kGroups;
     const auto begin = [&](int64_t from, uint32_t at) {  // copies of the rows at `from`
         if constexpr (VEC) {
             const int64_t row = from + lane / LANES;
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
-                const Place<LANES, VEC> o(row, a.cols, base_of(k), g, row < a.rows ? a.cols : 0);
+                const Place<LANES, VEC> o(row, a.cols, base_of(k), g, row < a.rows ? end_col : 0);
                 HeldT::copy(at, step, static_cast<const T*>(a.dy), o);
                 at += HeldT::kChunks * step;
                 HeldR::copy(at, step, static_cast<const R*>(a.h), o);
@@ -122,9 +166,10 @@ __global__ void __launch_bounds__(THREADS, VEC ? 512 / THREADS : 2) add_rmsnorm_
     const auto rms_at = [&](int64_t from) { return from + lane / LANES < a.rows ? __ldg(a.row_rms + from + lane / LANES) : 1.f; };
     float next_rms = VEC ? rms_at(first) : 0.f;  // asked for a row ahead
     int turn = 0;
+    uint32_t phase = 0;
     for (int64_t from = first; from < a.rows; from += stride, turn ^= 1) {
         const int64_t row = from + lane / LANES;
-        const int there = row < a.rows ? a.cols : 0;
+        const int there = row < a.rows ? end_col : 0;
         const float inv = 1.0f / (VEC ? next_rms : rms_at(from));
         if (VEC) next_rms = rms_at(from + stride);
         HeldR dh[NV];
@@ -147,7 +192,23 @@ __global__ void __launch_bounds__(THREADS, VEC ? 512 / THREADS : 2) add_rmsnorm_
             }
             factors<T, R, LANES, VEC>(dy, h, gamma[k], inv, gy[k], n[k], dots, dgamma[k]);
         }
-        const float dot = sum_of_row<LANES>(dots.x + dots.y, scratch[turn], a.split.warps, slot, w);
+        float dot;
+        if constexpr (SPREAD) {
+            const int parts = a.spread * a.split.warps;
+            if (threadIdx.x == 0) mbar_arrive_expect_tx(&all.bar[turn], parts * 4);
+            const float part = group_sum<32>(dots.x + dots.y);
+            if (lane < a.spread) spread_part(part, &all.sums[turn][cluster_rank() * a.split.warps + w], &all.bar[turn], lane);
+            if (!__all_sync(kFullMask, mbar_wait(&all.bar[turn], phase, &all.abort))) {
+                if (lane == 0) raise_abort(&all.abort);
+                break;
+            }
+            phase ^= turn;
+            dot = 0.f;
+            for (int i = lane; i < parts; i += 32) dot += all.sums[turn][i];
+            dot = group_sum<32>(dot);
+        } else {
+            dot = sum_of_row<LANES>(dots.x + dots.y, scratch[turn], a.split.warps, slot, w);
+        }
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const Place<LANES, VEC> o(row, a.cols, base_of(k), g, there);
@@ -172,14 +233,18 @@ __global__ void __launch_bounds__(THREADS, VEC ? 512 / THREADS : 2) add_rmsnorm_
             for (int k = 0; k < NV; ++k)
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    float* to = shared + base_of(k) + (VEC ? 8 * g + i : i * LANES + g);
+                    float* to = shared + base_of(k) - begin_col + (VEC ? 8 * g + i : i * LANES + g);
                     const float d = i & 1 ? dgamma[k][i / 2].y : dgamma[k][i / 2].x;
                     *to = s == 0 ? d : *to + d;
                 }
         }
         __syncthreads();
     }
-    for (int c = threadIdx.x; c < a.cols; c += blockDim.x) a.parts[int64_t(blockIdx.x) * a.cols + c] = shared[c];
+    for (int c = begin_col + threadIdx.x; c < end_col; c += blockDim.x) a.parts[int64_t(group) * a.cols + c] = shared[c - begin_col];
+    if constexpr (SPREAD) {  // after a wait that was given up the others may still write here
+        cluster_arrive_relaxed();
+        cluster_wait();
+    }
 }
 
 // dgamma = the blocks' parts, added in order within each warp and then over the warps: a
@@ -204,7 +269,7 @@ __global__ void __launch_bounds__(kSumWarps * 32) sum_parts(const float* parts, 
     }
 }
 
-// Rows of more than 8192 values: one block a row.  dy and h are read a second time,
+// Rows of more than 65536 values, or of more than 8192 off 16-byte boundaries: one block a row.  dy and h are read a second time,
 // from the L2, and the sums over rows lie in shared memory, or where that is too small in
 // the block's row of parts.  A thread reads and writes its own columns only.
 template <typename T, typename R, bool VEC>
@@ -283,10 +348,20 @@ constexpr int64_t kWideCols = 48 * 1024;  // sums in shared memory
 struct BwdPlan {
     int lanes, nv, warps, slots;
     int threads;  // at most
-    int64_t blocks;
+    int64_t blocks;  // that write a row of parts: blocks, or clusters of `spread`
+    int spread = 1, span = 0;
 };
 BwdPlan plan_of(int64_t rows, int64_t cols, bool vec) {
     const int64_t sms = sm_count() > 0 ? sm_count() : 132;
+    if (vec && cols > kRegisterCols && cols <= kMostSpread * kRegisterCols) {
+        BwdPlan p{32, 2, 0, 1, 512, 0, 2, 0};
+        // more CTAs a row where there are rows for few (3 x 12064 fp32: by two 8.2 us, by eight 6.1)
+        while (p.spread * kRegisterCols < cols || (p.spread < kMostSpread && rows * p.spread * 2 <= sms)) p.spread *= 2;
+        p.span = int((cols + 256 * p.spread - 1) / (256 * p.spread)) * 256;
+        p.warps = (p.span / 256 + 1) / 2;
+        p.blocks = rows < sms / p.spread ? rows : sms / p.spread;
+        return p;
+    }
     if (cols > kRegisterCols) return {32, 1, 32, 1, 1024, rows < sms ? rows : sms};
     BwdPlan p;
     const int units = int((cols + 255) / 256);
@@ -302,7 +377,24 @@ BwdPlan plan_of(int64_t rows, int64_t cols, bool vec) {
     return p;
 }
 
+// Clusters of a.spread CTAs that the device runs at once (0 if unknown): one more than
+// those would run behind them, as a second round.
+template <auto kernel>
+int64_t resident_clusters(cudaLaunchConfig_t cfg, int spread) {
+    static std::atomic<int> cached[64][kMostSpread + 1];
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return 0;
+    if (dev < 64)
+        if (const int c = cached[dev][spread].load(std::memory_order_relaxed)) return c;
+    cfg.blockDim = dim3(512);  // the most that any call takes
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) return 0;
+    if (dev < 64) cached[dev][spread].store(n, std::memory_order_relaxed);
+    return n;
+}
+
 }  // namespace
+
+uint32_t pipeline_timeouts_norm() { return read_pipeline_timeouts(); }
 
 size_t add_rmsnorm_bwd_workspace(int64_t rows, int64_t cols) {
     if (rows <= 0) return 0;  // of rows on 16-byte boundaries and others, whichever take more
@@ -317,10 +409,10 @@ cudaError_t launch_add_rmsnorm_bwd(const void* dy, const float* gamma, const voi
     const bool vec = cols % 8 == 0 && ((reinterpret_cast<uintptr_t>(dy) | reinterpret_cast<uintptr_t>(gamma) |
                                         reinterpret_cast<uintptr_t>(h) | reinterpret_cast<uintptr_t>(dh) |
                                         reinterpret_cast<uintptr_t>(dresidual) | reinterpret_cast<uintptr_t>(dx)) & 15) == 0;
-    const BwdPlan plan = plan_of(rows, cols, vec);
+    BwdPlan plan = plan_of(rows, cols, vec);
     // Without dx there is no mask to make, and rng may be NULL.
     AddNormBwdArgs a{dy,   gamma,     h,           row_rms, dh, dresidual, dx, parts, dropout_of(rng, dx ? p : 0.f),
-                     rows, int(cols), {plan.warps, plan.slots}, cols <= kWideCols};
+                     rows, int(cols), {plan.warps, plan.slots}, cols <= kWideCols, plan.spread, plan.span};
     cudaError_t e = cudaSuccess;
     with_branch_types(x_type, h_type, [&](auto t, auto r) {
         using T = decltype(t);
@@ -332,7 +424,26 @@ cudaError_t launch_add_rmsnorm_bwd(const void* dy, const float* gamma, const voi
         const size_t sums = size_t(plan.warps) * plan.nv * 256 * 4;
         const size_t staged = size_t(kStages) * plan.nv * kPlaces<T, R> * 16 * plan.warps * plan.slots * 32;
         const size_t smem = vec && staged > sums ? staged : sums;
-        if (cols > kRegisterCols) {
+        if (plan.spread > 1) {
+            cudaLaunchConfig_t cfg = {};
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim = {unsigned(plan.spread), 1, 1};
+            cfg.gridDim = dim3(unsigned(plan.spread));
+            cfg.dynamicSmemBytes = size_t(kStages) * plan.nv * kPlaces<T, R> * 16 * 512;
+            cfg.stream = stream;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            constexpr auto kernel = add_rmsnorm_bwd_rows<T, R, 32, 2, true, 512, true>;
+            e = allow_smem(kernel, cfg.dynamicSmemBytes);
+            if (e != cudaSuccess) return;
+            const int64_t most = resident_clusters<kernel>(cfg, plan.spread);
+            if (most > 0 && most < plan.blocks) plan.blocks = most;
+            cfg.gridDim = dim3(unsigned(plan.blocks * plan.spread));
+            cfg.blockDim = dim3(unsigned(plan.warps * 32));
+            cfg.dynamicSmemBytes = smem;
+            e = cudaLaunchKernelEx(&cfg, kernel, a);
+        } else if (cols > kRegisterCols) {
             const size_t wide = a.wide ? size_t(cols) * 4 : 0;
             if (vec) go(add_rmsnorm_bwd_long<T, R, true>, wide);
             else go(add_rmsnorm_bwd_long<T, R, false>, wide);

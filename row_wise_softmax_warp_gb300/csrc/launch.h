@@ -149,6 +149,7 @@ uint32_t pipeline_timeouts_ln();
 uint32_t pipeline_timeouts_matmul();
 uint32_t pipeline_timeouts_fp8();
 uint32_t pipeline_timeouts_mx4();
+uint32_t pipeline_timeouts_norm();
 // LayerNorm backward stage 1 on rows of 384..1024 floats on 16-byte
 // boundaries through the bulk-copy ring (one CTA per SM, at most 2^17 / cols
 // and at most max_ctas, 0: no further limit); writes

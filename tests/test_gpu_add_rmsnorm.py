@@ -132,7 +132,7 @@ def test_bad_values_stay_in_their_rows(ro, cols, quantize):
 
 
 @pytest.mark.parametrize("types", PAIRS)
-@pytest.mark.parametrize("shape", SHAPES + [(1500, 64), (1000, 33), (400, 8192), (300, 9000)])
+@pytest.mark.parametrize("shape", SHAPES + [(1500, 64), (1000, 33), (400, 8192), (300, 9000), (170, 16384), (90, 24584), (50, 65536), (3, 65544)])
 def test_backward(ro, shape, types):
     a, b = types
     rows, cols = shape
