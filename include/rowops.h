@@ -656,7 +656,8 @@ size_t rowops_add_rmsnorm_bwd_workspace(int64_t rows, int64_t cols);
  * wanted, and rng without dx; without dropout and with one type they are the same
  * values.  dresidual may
  * be exactly dh, and dx exactly dy; any other overlap of an output is
- * ROWOPS_ERR_ALIAS.  dgamma is summed in a fixed order, through `workspace`: at least
+ * ROWOPS_ERR_ALIAS.  Rows of 8193 to 65536 values share a cluster, whose waits are
+ * bounded as rowops_pipeline_timeouts says.  dgamma is summed in a fixed order, through `workspace`: at least
  * rowops_add_rmsnorm_bwd_workspace(rows, cols) bytes, 16-byte aligned, with
  * concurrent calls in separate ones.  cols == 0 is ROWOPS_ERR_SHAPE; rows == 0 writes
  * zeros to dgamma.

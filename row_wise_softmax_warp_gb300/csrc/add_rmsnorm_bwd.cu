@@ -10,9 +10,9 @@
 //
 // A row lies in the registers of a group of lanes, of up to 16 warps, or of a cluster's CTAs
 // (SPREAD below), which walk over rows and keep their columns' part of dgamma in registers;
-// a block adds its sets of
-// warps up in order and writes one row of partial sums, and a second launch adds those,
-// all in an order that only the sizes, the alignment and the device decide.
+// a block adds its sets of warps up in order and writes one row of partial sums, and a
+// second launch adds those, all in an order that only the sizes, the alignment and the
+// device decide.
 #include <atomic>
 
 #include "eight.cuh"

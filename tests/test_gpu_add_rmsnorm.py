@@ -185,6 +185,30 @@ def test_repeats_bit_for_bit_and_empty(ro):
     assert (dgamma == 0).all()
 
 
+@pytest.mark.parametrize("rows,cols", [(2, 8200), (37, 12064), (500, 16384), (60, 40000), (41, 65536)])
+def test_long_rows_on_three_streams(ro, rows, cols):
+    """Rows that a cluster shares: calls at once, and replayed from a graph, give what one call gives, bit for bit."""
+    x, r, gamma, key = inputs(cols, (rows, cols), ("bf16", "f32"))
+    rng = rng_of(*key)
+    _, _, h, rms = ro.rowops_add_rmsnorm_fwd(x, gamma, residual=r, rng=rng, p=0.1)
+    want = ro.rowops_add_rmsnorm_bwd(x, gamma, h, rms, dh=r, rng=rng, p=0.1)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = ro.rowops_add_rmsnorm_bwd(x, gamma, h, rms, dh=r, rng=rng, p=0.1)
+    streams, got = [torch.cuda.Stream() for _ in range(3)], []
+    for _ in range(10):
+        for stream in streams[:2]:
+            with torch.cuda.stream(stream):
+                got.append(ro.rowops_add_rmsnorm_bwd(x, gamma, h, rms, dh=r, rng=rng, p=0.1))
+        with torch.cuda.stream(streams[2]):
+            graph.replay()
+    torch.cuda.synchronize()
+    for out in [captured, *got]:
+        assert all(torch.equal(a, b) for a, b in zip(out, want))
+    assert ro.library().rowops_pipeline_timeouts() == 0
+
+
 def test_leading_dimensions(ro):
     x, r, gamma, _ = inputs(2, (24, 136), ("f16", "f32"))
     flat = ro.rowops_add_rmsnorm_fwd(x, gamma, residual=r, quantize="mx4")
