@@ -83,8 +83,9 @@ constexpr int kPlaces = Held<T, 32, true>::kChunks + 2 * Held<R, 32, true>::kChu
 
 // SPREAD: the CTAs of a cluster share a row.  Each warp writes its part of the row's sum to
 // every CTA, whose barrier counts the bytes (arrivals with a release would wait for the
-// results' stores, row after row), and every warp adds all parts in the same order.  A CTA
-// is at most a row ahead of another: what it writes two rows later was read by then.
+// results' stores, row after row), and every warp, whose wait acquires at the cluster's scope
+// as other CTAs wrote the parts, adds all of them in the same order.  A CTA is at most a row
+// ahead of another: what it writes two rows later was read by then.
 // Against one block a row, which reads dy and h twice: 4096 x 16384 bf16 121 and 184 us, 2048 x
 // 32768 with an fp32 stream 173 and 273, 4096 x 10000 110 and 194, 3 x 12064 fp32 6.1 and 15.7.
 constexpr int kMostSpread = 8;
@@ -122,8 +123,7 @@ __global__ void __launch_bounds__(THREADS, VEC ? 512 / THREADS : 2) add_rmsnorm_
             all.abort = 0;
             asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
         }
-        cluster_arrive_relaxed();
-        cluster_wait();
+        cluster_sync_all();  // with a release: this CTA's warps read the flag too
     }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int slot = warp / a.split.warps, w = warp % a.split.warps, g = lane % LANES;
@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(THREADS, VEC ? 512 / THREADS : 2) add_rmsnorm_
             if (threadIdx.x == 0) mbar_arrive_expect_tx(&all.bar[turn], parts * 4);
             const float part = group_sum<32>(dots.x + dots.y);
             if (lane < a.spread) spread_part(part, &all.sums[turn][cluster_rank() * a.split.warps + w], &all.bar[turn], lane);
-            if (!__all_sync(kFullMask, mbar_wait(&all.bar[turn], phase, &all.abort))) {
+            if (!__all_sync(kFullMask, mbar_wait_cluster(&all.bar[turn], phase, &all.abort))) {
                 if (lane == 0) raise_abort(&all.abort);
                 break;
             }
