@@ -383,11 +383,15 @@ template <auto kernel>
 int64_t resident_clusters(cudaLaunchConfig_t cfg, int spread) {
     static std::atomic<int> cached[64][kMostSpread + 1];
     int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return 0;
-    if (dev < 64)
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess && dev < 64)
         if (const int c = cached[dev][spread].load(std::memory_order_relaxed)) return c;
     cfg.blockDim = dim3(512);  // the most that any call takes
-    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) return 0;
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+    if (e != cudaSuccess) {
+        (void)cudaGetLastError();  // or it would be taken for the launch's
+        return 0;
+    }
     if (dev < 64) cached[dev][spread].store(n, std::memory_order_relaxed);
     return n;
 }
