@@ -744,8 +744,9 @@ def _native():
             from . import _host as module
         except ImportError as e:
             raise RuntimeError(
-                "the compiled part of the binding (_host.so) is missing: build it with "
-                "row_wise_softmax_warp_gb300.build.build() (or __graft_entry__.build())") from e
+                f"the compiled part of the binding (_host.so) cannot be loaded ({e}): build it with "
+                "row_wise_softmax_warp_gb300.build.build() (or __graft_entry__.build()), which warns where it cannot "
+                "be compiled; the other operators do without") from e
         module.load(LIB_PATH)
         _host = module
     return _host

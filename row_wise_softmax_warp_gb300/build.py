@@ -17,6 +17,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -44,14 +45,30 @@ def _sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
-def _fingerprint(extra=()) -> str:
+def _digest(paths, *rest) -> str:
     h = hashlib.sha256()
-    for p in sorted(glob.glob(os.path.join(CSRC, "*")) + [os.path.join(INCLUDE, "rowops.h")]):
+    for p in sorted(paths):
         with open(p, "rb") as f:
             h.update(p.encode() + b"\0" + f.read())
-    h.update(" ".join(ARCH + NVCC_FLAGS + list(extra)).encode())
-    h.update(f"{importlib.metadata.version('torch')} {sys.version}".encode())
+    h.update(" ".join(rest).encode())
     return h.hexdigest()
+
+
+def _fingerprint(extra=()) -> str:
+    sources = set(glob.glob(os.path.join(CSRC, "*"))) - {HOST_SOURCE}
+    return _digest([*sources, os.path.join(INCLUDE, "rowops.h")], *ARCH, *NVCC_FLAGS, *extra)
+
+
+def _current(stamp: str, out: str, fingerprint: str) -> bool:
+    if not os.path.exists(out) or not os.path.exists(stamp):
+        return False
+    with open(stamp) as f:
+        return f.read() == fingerprint
+
+
+def _stamp(stamp: str, fingerprint: str) -> None:
+    with open(stamp, "w") as f:
+        f.write(fingerprint)
 
 
 def _host_command(out: str):
@@ -64,22 +81,29 @@ def _host_command(out: str):
             "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10_cuda", "-lc10", "-ldl"]
 
 
-def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    """Compile and link librowops.so if any source changed; returns its path."""
-    os.makedirs(BUILD, exist_ok=True)
+def _build_host(force: bool) -> None:
+    """Compile _host.so if its source, the C ABI, torch or Python changed."""
+    stamp = os.path.join(BUILD, "fingerprint_host")
+    fp = _digest([HOST_SOURCE, os.path.join(INCLUDE, "rowops.h")], *_host_command(HOST), sys.version,
+                 importlib.metadata.version("torch"))
+    if not force and _current(stamp, HOST, fp):
+        return
+    tmp = HOST + f".tmp{os.getpid()}"
+    r = subprocess.run(_host_command(tmp), capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"the C++ compiler failed on {os.path.basename(HOST_SOURCE)}:\n{r.stdout}{r.stderr}")
+    os.replace(tmp, HOST)
+    _stamp(stamp, fp)
+
+
+def _build_library(ex, force: bool, verbose: bool, extra_flags) -> None:
     stamp = os.path.join(BUILD, "fingerprint")
     fp = _fingerprint(extra_flags)
-    built = os.path.exists(LIB) and os.path.exists(HOST) and os.path.exists(stamp)
-    if not force and built and open(stamp).read() == fp:
-        return LIB
+    if not force and _current(stamp, LIB, fp):
+        return
     nvcc = _nvcc()
 
     def compile_one(src):
-        if src == HOST_SOURCE:
-            r = subprocess.run(_host_command(host), capture_output=True, text=True)
-            if r.returncode != 0:
-                raise RuntimeError(f"the C++ compiler failed on {os.path.basename(src)}:\n{r.stdout}{r.stderr}")
-            return None
         obj = os.path.join(BUILD, os.path.basename(src)[:-3] + ".o")
         cmd = [nvcc, *ARCH, *NVCC_FLAGS, *extra_flags, "-c", src, "-o", obj]
         if verbose:
@@ -91,19 +115,33 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             print(r.stdout + r.stderr, file=sys.stderr)
         return obj
 
-    host = HOST + f".tmp{os.getpid()}"
-    srcs = [HOST_SOURCE, *_sources()]
-    with ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 1))) as ex:
-        objs = [o for o in ex.map(compile_one, srcs) if o]
+    objs = list(ex.map(compile_one, _sources()))
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}{r.stderr}")
     os.replace(tmp, LIB)
-    os.replace(host, HOST)
-    with open(stamp, "w") as f:
-        f.write(fp)
+    _stamp(stamp, fp)
+
+
+def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
+    """Compile and link librowops.so if any source changed; returns its path.
+
+    _host.so is compiled beside it.  The library and the operators that are called by
+    ctypes do without: where it cannot be compiled (no headers of Python, another torch), a
+    warning says why, and the calls that need it raise.
+    """
+    os.makedirs(BUILD, exist_ok=True)
+    with ThreadPoolExecutor(max_workers=max(1, min(len(_sources()) + 1, os.cpu_count() or 1))) as ex:
+        host = ex.submit(_build_host, force)
+        _build_library(ex, force, verbose, extra_flags)
+        try:
+            host.result()
+        except Exception as e:  # noqa: BLE001 - whatever it lacks, the library is there
+            if os.path.exists(HOST):
+                os.remove(HOST)  # made for other sources or another torch
+            warnings.warn(f"the compiled part of the Python binding (_host.so) was not built: {e}", RuntimeWarning, stacklevel=2)
     return LIB
 
 
