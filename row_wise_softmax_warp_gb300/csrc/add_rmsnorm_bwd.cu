@@ -34,7 +34,7 @@ struct AddNormBwdArgs {
     int64_t rows;
     int cols;
     RowSplit split;
-    bool wide;  // long rows: the sums fit in shared memory
+    bool wide;  // long rows off 16-byte boundaries: the sums fit in shared memory
     int spread, span;  // CTAs of a cluster that share a row, and columns of each
 };
 
@@ -269,9 +269,10 @@ __global__ void __launch_bounds__(kSumWarps * 32) sum_parts(const float* parts, 
     }
 }
 
-// Rows of more than 65536 values, or of more than 8192 off 16-byte boundaries: one block a row.  dy and h are read a second time,
-// from the L2, and the sums over rows lie in shared memory, or where that is too small in
-// the block's row of parts.  A thread reads and writes its own columns only.
+// Rows of more than 65536 values, or of more than 8192 off 16-byte boundaries: one block a
+// row.  dy and h are read a second time, from the L2.  The sums over rows lie in the block's
+// row of parts, which is its own and stays in the L2, or, of rows off a boundary that fit
+// (kWideCols), in shared memory.  A thread reads and writes its own columns only.
 template <typename T, typename R, bool VEC>
 __global__ void __launch_bounds__(1024) add_rmsnorm_bwd_long(const AddNormBwdArgs a) {
     extern __shared__ __align__(16) float sums[];
@@ -282,7 +283,8 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_bwd_long(const AddNormBwdArg
     const Masker masker(a.drop);
     const int64_t units = (int64_t(a.cols) + 255) / 256;
     float* parts = a.parts + int64_t(blockIdx.x) * a.cols;
-    float* mine = a.wide ? sums : parts;
+    const bool wide = !VEC && a.wide;
+    float* mine = wide ? sums : parts;
     const auto each = [&](int base, auto&& f) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -336,12 +338,12 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_bwd_long(const AddNormBwdArg
             gradients<T, R, 32, VEC>(a, masker, o, row, base, lane, dh, gy, n, inv, mean);
         }
     }
-    if (!a.wide) return;
+    if (!wide) return;
     for (int64_t u = w; u < units; u += 32) each(int(u * 256), [&](int c, int) { parts[c] = sums[c]; });
 }
 
 constexpr int64_t kRegisterCols = 8192;  // 256 or 512 columns for each of the most warps of a row
-constexpr int64_t kWideCols = 48 * 1024;  // sums in shared memory
+constexpr int64_t kWideCols = 48 * 1024;  // sums in shared memory, of long rows off 16-byte boundaries
 
 // Lanes, columns of a lane, warps and sets of warps by the row's length, and blocks by the
 // rows.
@@ -448,9 +450,8 @@ cudaError_t launch_add_rmsnorm_bwd(const void* dy, const float* gamma, const voi
             cfg.dynamicSmemBytes = smem;
             e = cudaLaunchKernelEx(&cfg, kernel, a);
         } else if (cols > kRegisterCols) {
-            const size_t wide = a.wide ? size_t(cols) * 4 : 0;
-            if (vec) go(add_rmsnorm_bwd_long<T, R, true>, wide);
-            else go(add_rmsnorm_bwd_long<T, R, false>, wide);
+            if (vec) go(add_rmsnorm_bwd_long<T, R, true>, 0);
+            else go(add_rmsnorm_bwd_long<T, R, false>, a.wide ? size_t(cols) * 4 : 0);
         } else if (!vec) {
             if (plan.nv == 1) go(add_rmsnorm_bwd_rows<T, R, 32, 1, false, 512>, smem);
             else go(add_rmsnorm_bwd_rows<T, R, 32, 2, false, 512>, smem);
