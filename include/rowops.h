@@ -583,8 +583,10 @@ int rowops_quantize_mx4(const void *x, uint8_t *q, uint8_t *scale, int64_t rows,
  * that are no multiple of 32) and timeouts as for rowops_expert_matmul.
  * The gradient with respect to x is this call on dy, quantised by rows, with the
  * weights transposed within each expert and quantised from their own values (blocks
- * run along the sum, so these bytes cannot be transposed).  The gradient with respect
- * to the weights is rowops_expert_matmul_wgrad on fp16 or bf16 rows.
+ * run along the sum, so these bytes cannot be transposed): in_cols is then out_cols,
+ * or out_cols + 1 where that is odd, for both operands' rows end in four bits of 0, and
+ * out_cols is in_cols.  The gradient with respect to the weights is
+ * rowops_expert_matmul_wgrad on fp16 or bf16 rows.
  */
 size_t rowops_expert_matmul_mx4_workspace(int64_t slots, int64_t in_cols, int64_t out_cols,
                                           int64_t experts);
