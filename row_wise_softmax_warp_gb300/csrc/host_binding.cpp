@@ -200,14 +200,18 @@ rowops_stream stream_of(const at::Tensor& t) {
     return reinterpret_cast<rowops_stream>(c10::cuda::getCurrentCUDAStream(t.get_device()).stream());
 }
 
-// The C call without the interpreter's lock, as ctypes makes it.
+// The C call without the interpreter's lock, as ctypes makes it.  What `f` throws (a tensor
+// without storage has no address to give) passes on with the lock taken again.
+struct Unlocked {
+    PyThreadState* state = PyEval_SaveThread();
+    Unlocked() = default;
+    Unlocked(const Unlocked&) = delete;
+    ~Unlocked() { PyEval_RestoreThread(state); }
+};
 template <typename F>
 int call(F&& f) {
-    int status;
-    Py_BEGIN_ALLOW_THREADS;
-    status = f();
-    Py_END_ALLOW_THREADS;
-    return status;
+    const Unlocked unlocked;
+    return f();
 }
 PyObject* tuple_of(std::initializer_list<PyObject*> items) {  // takes the references
     PyObject* t = PyTuple_New(Py_ssize_t(items.size()));
