@@ -76,7 +76,9 @@ __device__ __forceinline__ void gradients(const AddNormBwdArgs& a, const Masker&
 // an SM then do (16384 x 4096, bf16 and fp32 stream with dropout: 170 us; 1024, which have
 // half the registers, 177; without the places 181; three and four stages are no faster),
 // in two blocks where a row takes 8 warps at most (4096 x 768 fp32: 13.6 us, in one 14.3).
-// Rows that are read directly hide more behind 1024 threads (16384 x 1023: 67 us, 512: 77).
+// Rows that are read directly hide more behind 1024 threads (16384 x 1023: 67 us, 512: 77),
+// whose 64 registers do not hold what a thread keeps: 48 to 56 bytes of it are spilled with one
+// chunk a lane, 264 to 288 with two (rows of 4097 to 8192), in every row.
 constexpr int kStages = 2;
 template <typename T, typename R>
 constexpr int kPlaces = Held<T, 32, true>::kChunks + 2 * Held<R, 32, true>::kChunks;  // of 16 bytes, a row

@@ -104,6 +104,9 @@ cudaError_t launch_dropout(const void* x, const void* residual, const uint64_t* 
         with_type(y_type, [&](auto r) {
             using T = decltype(t);
             using R = decltype(r);
+            // One block of 8 values a thread as long as the SMs hold all threads at once, four where
+            // there are more (bf16, one and four: 64 x 4096 1.7 and 2.1 us, 608 x 4096, the border, 3.4
+            // and 3.8, 4096 x 4096 14.9 and 14.1).
             const bool few = a.items < 2048 * int64_t(sm_count());
             constexpr int kMany = sizeof(T) + sizeof(R) <= 4 ? 4 : 1;
             if (vec && few) dropout_run<T, R, 1><<<grid(kDropThreads), kDropThreads, 0, stream>>>(a);

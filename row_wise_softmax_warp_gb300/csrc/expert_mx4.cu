@@ -19,10 +19,14 @@
 // What bounds it: 16384 x 4096 -> 4096 takes 103 to 106 us (5200 to 5350 TFLOP/s; the bf16
 // product 299).  Variants that leave work out, when all of it took 107: products alone 66 us,
 // copies alone 73 (16 TB/s from the L2, 52 bytes a clock into an SM), both without scales 90,
-// with scales that are written but not loaded 96.  So it is what an SM takes in: operands,
-// scales (9% of their bytes: a tile's 256 columns and, in both CTAs, its rows), and the hand-
-// over of the latter.  A single tile takes 5.5 us with its launch, 64 experts of 768 x 2048 with 8192
-// rows 21 us against 14 of HBM traffic, with 32 rows 8.9 against 3.2.  Four sets of scale
+// with scales that are written but not loaded 96.  So one part grows with K: what an SM takes
+// in, operands, scales (9% of their bytes: a tile's 256 columns and, in both CTAs, its rows),
+// and the hand-over of the latter.  The other is the write-out, some 0.8 us a round of tiles
+// whatever K is, although the next tile's products run beside it: without its stores 16384 rows
+// to 4096 columns take 20, 26, 48 and 92 us for K = 512, 1024, 2048 and 4096, with them 36, 39,
+// 61 and 105, with half of them 27, 33, 57 and 100, with all but not turned 35, 39, 62 and 106.
+// A single tile takes 5.5 us with its launch, 64 experts of 768 x 2048 with 8192 rows 21 us (16
+// without stores) against 14 of HBM traffic, with 32 rows 8.9 against 3.2.  Four sets of scale
 // warps, or fewer rows a tile and more stages, are no faster; two sets take 7% longer.
 // Scales written stage by stage took 256 us: every hand-over to the other CTA has a fence
 // that a thread's loads, stores and a cluster-wide release wait for, so one hand-over
