@@ -10,8 +10,9 @@
 // Bound by HBM where the stream is fp32: x and residual are read once, h and y written
 // once (16384 x 4096, bf16 and an fp32 stream, with dropout: 120 us, 6.7 TB/s).  Where it
 // is 16-bit the instructions of a value count as well (8 bytes a value plain 88 us, 6.1
-// TB/s; 8192 x 4096 to e4m3 46 us, 5.2; 8192 x 2048 to 4 bits 23 us, 4.7), so values are
-// added, multiplied and converted in pairs.  A row lies in the registers of a group of
+// TB/s; 8192 x 4096 to e4m3 46 us, 5.2; 8192 x 2048 to 4 bits 23 us, 4.7: an SM's 16 warps
+// take 56% of its issue slots and wait on their own instructions, not on memory), so values
+// are added, multiplied and converted in pairs.  A row lies in the registers of a group of
 // lanes, of a warp, or of up to 32 warps that meet once, at a barrier of their own.
 #include "eight.cuh"
 #include "quant.cuh"
